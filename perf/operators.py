@@ -193,7 +193,6 @@ def prepare(case, seed):
         s["page_table"] = torch.from_numpy(rng.permutation(P).astype(np.int32).reshape(B, width)).cuda()
         kv = torch.randn((c["bufs"], P, c["Hkv"], page, c["D"]), generator=gen, device="cuda", dtype=torch.bfloat16)
         s["kv"] = kv if c["cache"] == "bf16" else kv.to(torch.float8_e4m3fn)
-        s["buffers"] = list(s["kv"].unbind(0))
         path = np.stack([np.sort(rng.choice(np.arange(1, N), L, replace=False)) for _ in range(B)]).astype(np.int32)
         s["path"] = torch.from_numpy(np.concatenate([path, np.full((B, 2), -1, np.int32)], 1)).cuda()
         s["count"] = _ints([L + 1] * B)
@@ -244,7 +243,7 @@ def run(state):
                 presence=s["presence"], frequency=s["frequency"], bias_tokens=s["bias_tokens"],
                 bias_values=s["bias_values"], allowed=s["allowed"], out=s["out"])
         if op == "compact":
-            sv.spec_kv_compact_paged(s["buffers"], s["page_table"], s["path"], s["count"], s["base"])
+            sv.spec_kv_compact_paged(s["kv"], s["page_table"], s["path"], s["count"], s["base"])
             return s["kv"]
         if op == "append":
             sv.spec_kv_append(s["key"], s["value"], s["k_pages"], s["v_pages"], s["page_table"], s["base"],
