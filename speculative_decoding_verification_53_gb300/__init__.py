@@ -1,6 +1,6 @@
 """GB300 (sm_103a) speculative-decoding verify/accept library -- Python binding.
 
-A thin ctypes layer over ``libspecverify.so`` (C ABI: ``include/spec_verify.h``).
+A thin ctypes layer over ``libspecverify.so`` (C ABI: the headers in ``include/``).
 Each function carries the name of the C entry point it calls and only marshals
 arguments: torch tensors become device pointers, the current torch stream
 becomes the launch stream, outputs are allocated with torch when not given.
@@ -22,17 +22,27 @@ SV_OK, SV_ERR_INVALID_ARG, SV_ERR_UNSUPPORTED, SV_ERR_CUDA, SV_ERR_TIMEOUT, SV_E
 SV_F32, SV_BF16 = 0, 1
 SV_DRAFT_PROBS, SV_DRAFT_LOGITS = 0, 1
 SV_SIBLINGS_WITHOUT_REPLACEMENT, SV_SIBLINGS_IID = 0, 1
+SV_CACHE_BF16, SV_CACHE_E4M3 = 0, 1
 
 EXPORTS = ("spec_verify_workspace_size", "spec_verify_chain", "spec_greedy_accept", "spec_verify_tree",
            "spec_verify_status_string", "spec_verify_last_cuda_error", "spec_verify_chain_noalloc",
            "spec_tree_mask", "spec_kv_compact", "spec_verify_tree_rule", "spec_sample_and_verify",
            "spec_verify_count_invalid", "spec_verify_rows_status", "spec_verify_chain_host",
-           "spec_verify_host_sizes")
+           "spec_verify_host_sizes", "spec_kv_append", "spec_kv_read", "spec_kv_compact_paged")
 
 # out_count value of a batch row whose kernel gave up a bounded device-side wait
 COUNT_TIMEOUT = -1
 
 _lib = None
+
+
+class PagedCache(ctypes.Structure):
+    """sv_paged_cache of include/spec_paged_kv.h."""
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("num_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
 
 
 class SpecVerifyError(RuntimeError):
@@ -86,6 +96,13 @@ def lib() -> ctypes.CDLL:
     L.spec_verify_chain_host.restype = ci
     L.spec_verify_host_sizes.argtypes = [ci, ci, ci, ci, ci, ci, vp, vp, vp]
     L.spec_verify_host_sizes.restype = ci
+    pc = ctypes.POINTER(PagedCache)
+    L.spec_kv_append.argtypes = [vp, vp, ci, vp, pc, vp, vp, ci, ci, vp]
+    L.spec_kv_append.restype = ci
+    L.spec_kv_read.argtypes = [pc, vp, vp, ci, ci, vp, vp, ci, vp]
+    L.spec_kv_read.restype = ci
+    L.spec_kv_compact_paged.argtypes = [vp, ci, i64, i64, ci, i64, i64, vp, ci, ci, ci, vp, vp, vp, ci, ci, vp]
+    L.spec_kv_compact_paged.restype = ci
     _lib = L
     return L
 
@@ -452,3 +469,205 @@ def spec_kv_compact(kv_buffers, path, count, base=None, *, stream=None):
                                _stream(stream))
     if st != SV_OK:
         raise SpecVerifyError(st, "spec_kv_compact")
+
+
+# --------------------------------------------- a verification round on a paged cache
+
+def _one_device(first, stream, **tensors):
+    """Checks that every given tensor is on the device of `first` (the first of them) and
+    contiguous; returns that device and the stream to launch on (that device's current one
+    unless given)."""
+    dev = first.device
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, other arguments on {dev}")
+    if stream is None:
+        stream = _torch().cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the arguments on {dev}")
+    return dev, stream
+
+
+def _shaped(name, t, shape, dtype):
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _launch(where, dev, stream, call, *args):
+    """call(*args, stream) with `dev` current; raises on a non-zero status."""
+    cuda = _torch().cuda
+    if dev.index == cuda.current_device():
+        st = call(*args, ctypes.c_void_p(stream.cuda_stream))
+    else:
+        with cuda.device(dev):
+            st = call(*args, ctypes.c_void_p(stream.cuda_stream))
+    if st != SV_OK:
+        raise SpecVerifyError(st, where)
+
+
+def _new(shape, dtype, dev, stream):
+    """A new tensor that belongs to `stream`."""
+    torch = _torch()
+    if stream == torch.cuda.current_stream(dev):
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, B):
+    """The sv_paged_cache of tensors [pages][heads][page_size][head_dim] (checked)."""
+    torch = _torch()
+    if k_pages.dim() != 4 or v_pages.dim() != 4:
+        raise ValueError("k_pages and v_pages must be [pages][heads][page_size][head_dim]")
+    if k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype or k_pages.stride() != v_pages.stride():
+        raise ValueError("k_pages and v_pages must have one shape, stride and dtype")
+    P, H, ps, D = k_pages.shape
+    sp, sh, sr, sd = k_pages.stride()
+    if sd != 1 and D > 1:
+        raise ValueError("the last dimension of k_pages and v_pages must be contiguous")
+    if k_pages.dtype == torch.bfloat16:
+        code, es = SV_CACHE_BF16, 2
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale and v_scale belong to float8_e4m3fn pages")
+    elif k_pages.dtype == torch.float8_e4m3fn:
+        code, es = SV_CACHE_E4M3, 1
+        if k_scale is None or v_scale is None:
+            raise ValueError("float8_e4m3fn pages need k_scale and v_scale")
+        _shaped("k_scale", k_scale, (P, H, ps), torch.float32)
+        _shaped("v_scale", v_scale, (P, H, ps), torch.float32)
+    else:
+        raise TypeError(f"pages must be bfloat16 or float8_e4m3fn, got {k_pages.dtype}")
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must be [{B}][max_pages], got {tuple(page_table.shape)}")
+    _shaped("page_table", page_table, page_table.shape, torch.int32)
+    return PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
+                      None if v_scale is None else v_scale.data_ptr(), page_table.data_ptr(), sp * es, sh * es,
+                      max(sr, D) * es if ps == 1 else sr * es, code, P, ps, page_table.shape[1], H, D)
+
+
+def _strides3(t, name):
+    """Element strides of the first three dimensions of [B][N][heads][head_dim]."""
+    if t.stride(3) != 1 and t.shape[3] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return (ctypes.c_int64 * 3)(*t.stride()[:3])
+
+
+def _src_code(dtype, name) -> int:
+    torch = _torch()
+    if dtype == torch.bfloat16:
+        return SV_BF16
+    if dtype == torch.float32:
+        return SV_F32
+    raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+
+
+def spec_kv_append(key, value, k_pages, v_pages, page_table, base, *, new_len=None, k_scale=None, v_scale=None,
+                   stream=None):
+    """Write new tokens' keys and values into a paged cache, in place.  key, value
+    [B][N][heads][head_dim] (fp32/bf16, any strides with contiguous elements, one shape,
+    stride and dtype); k_pages, v_pages [pages][heads][page_size][head_dim] bf16, or
+    float8_e4m3fn with k_scale, v_scale fp32 [pages][heads][page_size] (any strides with
+    contiguous elements: a [pages][page_size][heads][head_dim] cache is passed permuted);
+    page_table int32 [B][max_pages]; base int32 [B] (positions before token 0); new_len
+    int32 [B] or None (all N tokens are real)."""
+    torch = _torch()
+    dev, stream = _one_device(key, stream, key=key, value=value, k_pages=k_pages, v_pages=v_pages,
+                              page_table=page_table, base=base, new_len=new_len, k_scale=k_scale, v_scale=v_scale)
+    if key.dim() != 4 or key.shape != value.shape or key.dtype != value.dtype or key.stride() != value.stride():
+        raise ValueError("key and value must be [B][N][heads][head_dim] of one shape, stride and dtype")
+    B, N, H, D = key.shape
+    cache = _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, B)
+    if (cache.num_heads, cache.head_dim) != (H, D):
+        raise ValueError(f"key has {H} heads of {D}, the cache {cache.num_heads} of {cache.head_dim}")
+    _shaped("base", base, (B,), torch.int32)
+    _shaped("new_len", new_len, (B,), torch.int32)
+    _launch("spec_kv_append", dev, stream, lib().spec_kv_append, _ptr(key), _ptr(value), _src_code(key.dtype, "key"),
+            _strides3(key, "key"), cache, _ptr(base), _ptr(new_len), B, N)
+
+
+def spec_kv_read(k_pages, v_pages, page_table, base, num_tokens: int, *, new_len=None, k_scale=None, v_scale=None,
+                 out_key=None, out_value=None, dtype=None, stream=None):
+    """Read positions base[b] .. base[b] + new_len[b] - 1 (new_len None: num_tokens for every
+    row) of a paged cache into dense arrays [B][num_tokens][heads][head_dim] of dtype
+    (bf16 unless given; that of out_key where that is given).  Arguments as
+    spec_kv_append.  Rows of new outputs at and behind new_len are zero; rows of given
+    outputs there keep what they hold.  Returns (out_key, out_value)."""
+    torch = _torch()
+    dev, stream = _one_device(k_pages, stream, k_pages=k_pages, v_pages=v_pages, page_table=page_table, base=base,
+                              new_len=new_len, k_scale=k_scale, v_scale=v_scale, out_key=out_key,
+                              out_value=out_value)
+    B, N = page_table.shape[0], int(num_tokens)
+    cache = _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, B)
+    shape = (B, N, cache.num_heads, cache.head_dim)
+    given = out_key if out_key is not None else out_value
+    if dtype is None:
+        dtype = given.dtype if given is not None else torch.bfloat16
+    code = _src_code(dtype, "dtype")
+    if N < 0:
+        raise ValueError("num_tokens must not be negative")
+    _shaped("base", base, (B,), torch.int32)
+    _shaped("new_len", new_len, (B,), torch.int32)
+    _shaped("out_key", out_key, shape, dtype)
+    _shaped("out_value", out_value, shape, dtype)
+    if out_key is None or out_value is None:
+        with torch.cuda.stream(stream):
+            out_key = torch.zeros(shape, dtype=dtype, device=dev) if out_key is None else out_key
+            out_value = torch.zeros(shape, dtype=dtype, device=dev) if out_value is None else out_value
+    _launch("spec_kv_read", dev, stream, lib().spec_kv_read, cache, _ptr(base), _ptr(new_len), B, N, _ptr(out_key),
+            _ptr(out_value), code)
+    return out_key, out_value
+
+
+def spec_kv_compact_paged(kv_buffers, page_table, path, count, base=None, *, stream=None):
+    """spec_kv_compact on a paged cache, in place: every batch row's accepted tree nodes'
+    cache rows move to base[b], base[b] + 1, ... through the page table.  kv_buffers: CUDA
+    tensors [pages][planes][page_size][width] of one dtype, shape and stride with a
+    contiguous last dimension (each layer's K and V pages; their e4m3 scales in a call of
+    their own, as [pages][planes][page_size][1] views), or one tensor
+    [buffers][pages][planes][page_size][width].  page_table int32 [B][max_pages]; path,
+    count, base as spec_kv_compact."""
+    torch = _torch()
+    if isinstance(kv_buffers, torch.Tensor):
+        if kv_buffers.dim() != 5 or not kv_buffers.shape[0]:
+            raise ValueError("a single kv_buffers tensor must be [buffers][pages][planes][page_size][width]")
+        n, shape, strides, t0 = kv_buffers.shape[0], kv_buffers.shape[1:], kv_buffers.stride()[1:], kv_buffers
+        es = t0.element_size()
+        at, step = t0.data_ptr(), kv_buffers.stride(0) * es
+        ptrs = [at + k * step for k in range(n)]
+    else:
+        bufs = list(kv_buffers)
+        if not bufs:
+            raise ValueError("kv_buffers is empty")
+        t0 = bufs[0]
+        n, shape, strides, dtype, where = len(bufs), t0.shape, t0.stride(), t0.dtype, t0.device
+        for t in bufs:
+            if t.dim() != 4 or t.shape != shape or t.stride() != strides or t.dtype != dtype or t.device != where:
+                raise ValueError("kv_buffers must be tensors [pages][planes][page_size][width] of one shape, stride, "
+                                 "dtype and device")
+        es = t0.element_size()
+        ptrs = [t.data_ptr() for t in bufs]
+    dev, stream = _one_device(t0, stream, kv_buffers=t0, page_table=page_table, path=path, count=count, base=base)
+    P, H, ps, W = shape
+    if strides[3] != 1 and W > 1:
+        raise ValueError("the last dimension of every kv buffer must be contiguous")
+    if path.dim() != 2 or page_table.dim() != 2 or page_table.shape[0] != path.shape[0]:
+        raise ValueError("path must be [B][max_depth] and page_table [B][max_pages]")
+    B = path.shape[0]
+    _shaped("page_table", page_table, page_table.shape, torch.int32)
+    _shaped("path", path, path.shape, torch.int32)
+    _shaped("count", count, (B,), torch.int32)
+    _shaped("base", base, (B,), torch.int32)
+    row = max(strides[2], W) if ps == 1 else strides[2]
+    _launch("spec_kv_compact_paged", dev, stream, lib().spec_kv_compact_paged, (ctypes.c_void_p * n)(*ptrs), n,
+            strides[0] * es, strides[1] * es, H, row * es, W * es, _ptr(page_table), P, ps, page_table.shape[1],
+            _ptr(path), _ptr(count), _ptr(base), B, path.shape[1])

@@ -1,0 +1,437 @@
+// sv_paged_kv.cu -- new keys and values written into a paged cache, pages read back, and
+// the accepted tree nodes' rows moved through the page table (include/spec_paged_kv.h).
+//
+// Writing and reading are one pass over the data.  A row of one token and head is held by
+// a group of lanes, eight elements each (a power of two of lanes, so that the row's
+// largest magnitude is log2 shuffles away); a group does the key and the value of its
+// token and head, so both loads are in flight together and the page is looked up once.
+//   e4m3: scale s = max(a / 448, 2^-126), a the largest finite magnitude; code = e4m3(x *
+//   (1/s)).  The floor keeps s and 1/s normal numbers, so a row of zeros or of tiny
+//   numbers needs no case of its own.  The product with 1/s instead of a division per
+//   element moves x/s by at most 2^-23 of itself, 2^-19 of an e4m3 step.
+//
+// The paged compaction is the kernel of sv_tree_kv.cu with one more indirection: a warp
+// turns the path into byte offsets through the table, then every thread moves its piece
+// of each row, loading up to eight sources before storing them.
+#include <cstdint>
+
+#include "spec_paged_kv.h"
+#include "sv_internal.h"
+#include "sv_paged.cuh"
+
+namespace {
+
+using sv::PagedCache;
+using sv::pdl_trigger;
+using sv::pdl_wait;
+
+constexpr int kThreads = 256;
+constexpr int kMaxB = 65535;
+
+struct RowsArgs {
+    PagedCache c;
+    const int32_t* base;
+    const int32_t* new_len;
+    int N;
+    const unsigned char* key;    // append: source; read: destination (written)
+    const unsigned char* value;
+    int64_t sb, st, sh;          // element strides of key and value
+};
+
+// Elements e0 .. e0+7 of a row of `dim` elements as fp32 (zero beyond dim).
+template <typename T, bool AL>
+__device__ __forceinline__ void load_row8(const T* row, int e0, int dim, float x[8]) {
+    if (AL) {
+        if (e0 < dim) {
+            if (sizeof(T) == 2) {
+                const uint4 v = sv::ld_nc_v4(row + e0);
+                x[0] = sv::bf16_lo(v.x); x[1] = sv::bf16_hi(v.x); x[2] = sv::bf16_lo(v.y); x[3] = sv::bf16_hi(v.y);
+                x[4] = sv::bf16_lo(v.z); x[5] = sv::bf16_hi(v.z); x[6] = sv::bf16_lo(v.w); x[7] = sv::bf16_hi(v.w);
+            } else {
+                const uint4 a = sv::ld_nc_v4(row + e0), b = sv::ld_nc_v4(row + e0 + 4);
+                x[0] = __uint_as_float(a.x); x[1] = __uint_as_float(a.y);
+                x[2] = __uint_as_float(a.z); x[3] = __uint_as_float(a.w);
+                x[4] = __uint_as_float(b.x); x[5] = __uint_as_float(b.y);
+                x[6] = __uint_as_float(b.z); x[7] = __uint_as_float(b.w);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            x[j] = 0.0f;
+            if (e0 + j < dim)
+                x[j] = sizeof(T) == 2 ? __uint_as_float((uint32_t)__ldg((const unsigned short*)row + e0 + j) << 16)
+                                      : __ldg((const float*)row + e0 + j);
+        }
+    }
+}
+
+__device__ __forceinline__ float finite_abs(float x) {
+    const float a = fabsf(x);
+    return a < sv::pos_inf() ? a : 0.0f;  // false for NaN and infinity
+}
+
+// Writes eight elements of a cache row (and the row's scale).  LPR lanes hold the row.
+template <int LPR, bool E4M3, bool AL>
+__device__ __forceinline__ void store_cache_row(unsigned char* row, float* scale, int e0, int dim, bool live,
+                                                const float x[8]) {
+    if (E4M3) {
+        float a = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a = fmaxf(a, finite_abs(x[j]));
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        const float s = fmaxf(a / sv::E4M3_MAX, 1.17549435e-38f), inv = 1.0f / s;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = sv::e4m3x2(x[2 * j] * inv, x[2 * j + 1] * inv);
+        if (!live) return;
+        if (e0 == 0) *scale = s;
+        if (AL) {
+            if (e0 < dim) *reinterpret_cast<uint2*>(row + e0) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (e0 + j < dim) row[e0 + j] = (unsigned char)(w[j / 2] >> (8 * (j & 1)));
+        }
+    } else {
+        if (!live) return;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = sv::bf16x2(x[2 * j], x[2 * j + 1]);
+        if (AL) {
+            if (e0 < dim) *reinterpret_cast<uint4*>(row + 2 * e0) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (e0 + j < dim) reinterpret_cast<unsigned short*>(row)[e0 + j] = (unsigned short)(w[j / 2] >> (16 * (j & 1)));
+        }
+    }
+}
+
+// grid: x over the N * heads rows of one batch row, y the batch row.
+template <typename T, int LPR, bool E4M3, bool AL>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ RowsArgs a) {
+    pdl_trigger();
+    pdl_wait();  // nothing the previous kernel on the stream writes is read before this
+    constexpr int RPC = kThreads / LPR;
+    const int b = blockIdx.y, lane = threadIdx.x % LPR, e0 = 8 * lane;
+    const int64_t r = (int64_t)blockIdx.x * RPC + threadIdx.x / LPR;
+    int first, n;
+    if (!sv::paged_row(a.c, a.base, a.new_len, b, a.N, first, n)) return;
+    const int i = (int)(r / a.c.heads), h = (int)(r - (int64_t)i * a.c.heads);
+    if ((int64_t)blockIdx.x * RPC / a.c.heads >= n) return;  // the whole block is behind the row's tokens
+    bool live = i < n;
+    float x[8], y[8];
+    int row = 0, page = -1;
+    if (live) {
+        const int64_t off = b * a.sb + i * a.st + h * a.sh;
+        load_row8<T, AL>(reinterpret_cast<const T*>(a.key) + off, e0, a.c.dim, x);
+        load_row8<T, AL>(reinterpret_cast<const T*>(a.value) + off, e0, a.c.dim, y);
+        page = sv::paged_place(a.c, b, first + i, row);
+        live = page >= 0;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.0f;
+    }
+    const int64_t at = page * a.c.page_stride + h * a.c.head_stride + row * a.c.row_stride;
+    const int64_t sc = ((int64_t)page * a.c.heads + h) * a.c.page_size + row;
+    store_cache_row<LPR, E4M3, AL>(a.c.k + at, a.c.k_scale + sc, e0, a.c.dim, live, x);
+    store_cache_row<LPR, E4M3, AL>(a.c.v + at, a.c.v_scale + sc, e0, a.c.dim, live, y);
+}
+
+template <bool E4M3, bool AL>
+__device__ __forceinline__ void load_cache_row8(const unsigned char* row, float scale, int e0, int dim, float x[8]) {
+    if (!E4M3) {
+        load_row8<uint16_t, AL>(reinterpret_cast<const uint16_t*>(row), e0, dim, x);
+        return;
+    }
+    uint2 w = make_uint2(0u, 0u);
+    if (AL) {
+        if (e0 < dim) w = __ldg(reinterpret_cast<const uint2*>(row + e0));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (e0 + j < dim) (j < 4 ? w.x : w.y) |= (uint32_t)__ldg(row + e0 + j) << (8 * (j & 3));
+    }
+    const float2 p = sv::e4m3x2_to_f32(w.x & 0xffffu), q = sv::e4m3x2_to_f32(w.x >> 16);
+    const float2 r = sv::e4m3x2_to_f32(w.y & 0xffffu), t = sv::e4m3x2_to_f32(w.y >> 16);
+    x[0] = p.x * scale; x[1] = p.y * scale; x[2] = q.x * scale; x[3] = q.y * scale;
+    x[4] = r.x * scale; x[5] = r.y * scale; x[6] = t.x * scale; x[7] = t.y * scale;
+}
+
+template <typename T, bool AL>
+__device__ __forceinline__ void store_row8(T* row, int e0, int dim, const float x[8]) {
+    if (AL) {
+        if (e0 >= dim) return;
+        if (sizeof(T) == 2) {
+            *reinterpret_cast<uint4*>(row + e0) = make_uint4(sv::bf16x2(x[0], x[1]), sv::bf16x2(x[2], x[3]),
+                                                             sv::bf16x2(x[4], x[5]), sv::bf16x2(x[6], x[7]));
+        } else {
+            *reinterpret_cast<float4*>(row + e0) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4*>(row + e0 + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (e0 + j < dim) {
+                if (sizeof(T) == 2) reinterpret_cast<unsigned short*>(row)[e0 + j] = (unsigned short)sv::bf16x2(x[j], 0.0f);
+                else reinterpret_cast<float*>(row)[e0 + j] = x[j];
+            }
+    }
+}
+
+template <typename T, int LPR, bool E4M3, bool AL>
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant__ RowsArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    constexpr int RPC = kThreads / LPR;
+    const int b = blockIdx.y, lane = threadIdx.x % LPR, e0 = 8 * lane;
+    const int64_t r = (int64_t)blockIdx.x * RPC + threadIdx.x / LPR;
+    int first, n;
+    if (!sv::paged_row(a.c, a.base, a.new_len, b, a.N, first, n)) return;
+    const int i = (int)(r / a.c.heads), h = (int)(r - (int64_t)i * a.c.heads);
+    if (i >= n) return;
+    int row;
+    const int page = sv::paged_place(a.c, b, first + i, row);
+    float x[8], y[8];
+    if (page >= 0) {
+        const int64_t at = page * a.c.page_stride + h * a.c.head_stride + row * a.c.row_stride;
+        const int64_t sc = ((int64_t)page * a.c.heads + h) * a.c.page_size + row;
+        const float ks = E4M3 ? __ldg(a.c.k_scale + sc) : 1.0f, vs = E4M3 ? __ldg(a.c.v_scale + sc) : 1.0f;
+        load_cache_row8<E4M3, AL>(a.c.k + at, ks, e0, a.c.dim, x);
+        load_cache_row8<E4M3, AL>(a.c.v + at, vs, e0, a.c.dim, y);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.0f;
+    }
+    const int64_t off = b * a.sb + i * a.st + h * a.sh;
+    store_row8<T, AL>(reinterpret_cast<T*>(const_cast<unsigned char*>(a.key)) + off, e0, a.c.dim, x);
+    store_row8<T, AL>(reinterpret_cast<T*>(const_cast<unsigned char*>(a.value)) + off, e0, a.c.dim, y);
+}
+
+template <bool READ, typename T, int LPR, bool E4M3, bool AL>
+cudaError_t launch_rows(const RowsArgs& a, int B, cudaStream_t stream) {
+    const int64_t rows = (int64_t)a.N * a.c.heads;
+    const dim3 grid((unsigned)((rows + kThreads / LPR - 1) / (kThreads / LPR)), (unsigned)B);
+    if (READ) return sv::launch_serial(kv_read_kernel<T, LPR, E4M3, AL>, grid, dim3(kThreads), 0, stream, a);
+    return sv::launch_serial(kv_append_kernel<T, LPR, E4M3, AL>, grid, dim3(kThreads), 0, stream, a);
+}
+
+template <bool READ, typename T, bool E4M3, bool AL>
+cudaError_t launch_lpr(const RowsArgs& a, int B, cudaStream_t stream) {
+    const int lanes = (a.c.dim + 7) / 8;
+    if (lanes <= 8) return launch_rows<READ, T, 8, E4M3, AL>(a, B, stream);
+    if (lanes <= 16) return launch_rows<READ, T, 16, E4M3, AL>(a, B, stream);
+    return launch_rows<READ, T, 32, E4M3, AL>(a, B, stream);
+}
+
+template <bool READ>
+sv_status run_rows(const RowsArgs& a, bool e4m3, int dt, bool al, int B, cudaStream_t s) {
+    cudaError_t e;
+    if (dt == SV_BF16) {
+        if (e4m3) e = al ? launch_lpr<READ, uint16_t, true, true>(a, B, s) : launch_lpr<READ, uint16_t, true, false>(a, B, s);
+        else e = al ? launch_lpr<READ, uint16_t, false, true>(a, B, s) : launch_lpr<READ, uint16_t, false, false>(a, B, s);
+    } else {
+        if (e4m3) e = al ? launch_lpr<READ, float, true, true>(a, B, s) : launch_lpr<READ, float, true, false>(a, B, s);
+        else e = al ? launch_lpr<READ, float, false, true>(a, B, s) : launch_lpr<READ, float, false, false>(a, B, s);
+    }
+    return sv::launch_status(e);
+}
+
+bool rows_sizes_ok(const PagedCache& c, int B, int N) {
+    return B >= 0 && B <= kMaxB && N >= 0 && (int64_t)N * c.heads < ((int64_t)1 << 31);
+}
+
+// Whether 16-byte (8-byte for codes) accesses of eight elements are aligned everywhere.
+bool rows_aligned(const RowsArgs& a, const sv_paged_cache* c, int es) {
+    const int64_t cs = c->dtype == SV_CACHE_BF16 ? 16 : 8;
+    return c->head_dim % 8 == 0 && (a.sb * es | a.st * es | a.sh * es) % 16 == 0 &&
+           ((uintptr_t)a.key | (uintptr_t)a.value) % 16 == 0 &&
+           (c->page_stride | c->head_stride | c->row_stride) % cs == 0 &&
+           ((uintptr_t)c->k_pages | (uintptr_t)c->v_pages) % cs == 0;
+}
+
+// ---------------------------------------------------------------- compaction
+
+constexpr int kKvMaxBuffers = 256;
+constexpr int kKvMaxDepth = 64;
+constexpr int kKvBatch = 8;  // sources loaded before their stores
+
+struct PagedMoveArgs {
+    unsigned char* buf[kKvMaxBuffers];
+    int64_t page_stride, plane_stride, row_stride;
+    int num_planes, pieces, D;
+    int num_pages, page_size, max_pages;
+    unsigned total;  // num_buffers * num_planes * pieces
+    const int32_t* table;
+    const int32_t* path;
+    const int32_t* count;
+    const int32_t* base;
+};
+
+template <int PW> struct Piece;
+template <> struct Piece<16> { using T = uint4; };
+template <> struct Piece<4> { using T = uint32_t; };
+template <> struct Piece<1> { using T = uint8_t; };
+
+// grid: x covers num_buffers * num_planes * pieces, y is the batch row.
+template <int PW>
+__global__ void __launch_bounds__(kThreads) kv_compact_paged_kernel(const __grid_constant__ PagedMoveArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    using T = typename Piece<PW>::T;
+    __shared__ int64_t s_dst[kKvMaxDepth], s_src[kKvMaxDepth];
+    __shared__ int s_moves;
+    const int b = blockIdx.y;
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        const int cnt = __ldg(a.count + b);
+        const int L = cnt - 1;
+        const int base = a.base ? __ldg(a.base + b) : 0;
+        const int64_t rows = (int64_t)a.max_pages * a.page_size;
+        const int32_t* table = a.table + (int64_t)b * a.max_pages;
+        bool ok = cnt >= 1 && L <= a.D && base >= 0;
+        int moves = 0;
+        for (int d0 = 0; d0 < a.D; d0 += 32) {
+            const int d = d0 + lane;
+            int s = d;
+            bool lane_ok = true;
+            if (ok && d < L) {
+                s = __ldg(a.path + (int64_t)b * a.D + d);
+                lane_ok = s >= d && (int64_t)base + s < rows;
+            }
+            bool move = ok && lane_ok && d < L && s != d;  // a row already in place is not copied
+            int64_t src = 0, dst = 0;
+            if (move) {
+                const int ps = base + s, pd = base + d;  // below rows < 2^31
+                const int is = ps / a.page_size, id = pd / a.page_size;
+                const int gs = __ldg(table + is), gd = __ldg(table + id);
+                lane_ok = (unsigned)gs < (unsigned)a.num_pages && (unsigned)gd < (unsigned)a.num_pages;
+                src = gs * a.page_stride + (ps - is * a.page_size) * a.row_stride;
+                dst = gd * a.page_stride + (pd - id * a.page_size) * a.row_stride;
+            }
+            ok = ok && __all_sync(0xffffffffu, lane_ok);
+            move = move && ok;
+            const unsigned m = __ballot_sync(0xffffffffu, move);
+            if (move) {
+                const int slot = moves + __popc(m & ((1u << lane) - 1u));
+                s_dst[slot] = dst;
+                s_src[slot] = src;
+            }
+            moves += __popc(m);
+        }
+        if (lane == 0) s_moves = ok ? moves : 0;
+    }
+    __syncthreads();
+    const int moves = s_moves;
+    const unsigned f = blockIdx.x * kThreads + threadIdx.x;
+    if (moves == 0 || f >= a.total) return;
+    const unsigned piece = f % a.pieces, rest = f / a.pieces;
+    const unsigned h = rest % a.num_planes, k = rest / a.num_planes;
+    unsigned char* p0 = a.buf[k] + (int64_t)h * a.plane_stride + (int64_t)piece * PW;
+    for (int m0 = 0; m0 < moves; m0 += kKvBatch) {
+        T v[kKvBatch];
+#pragma unroll
+        for (int j = 0; j < kKvBatch; ++j)
+            if (m0 + j < moves) v[j] = *reinterpret_cast<const T*>(p0 + s_src[m0 + j]);
+#pragma unroll
+        for (int j = 0; j < kKvBatch; ++j)
+            if (m0 + j < moves) *reinterpret_cast<T*>(p0 + s_dst[m0 + j]) = v[j];
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+sv_status spec_kv_append(const void* key, const void* value, sv_dtype src, const int64_t* src_stride,
+                         const sv_paged_cache* cache, const int32_t* base, const int32_t* new_len, int B, int N,
+                         void* stream) {
+    RowsArgs a{};
+    if (src != SV_F32 && src != SV_BF16) return SV_ERR_INVALID_ARG;
+    if (!sv::paged_cache_args(cache, a.c) || !rows_sizes_ok(a.c, B, N)) return SV_ERR_INVALID_ARG;
+    if (B == 0 || N == 0) return SV_OK;
+    const int es = src == SV_BF16 ? 2 : 4;
+    if (!key || !value || !base || !src_stride || ((uintptr_t)key | (uintptr_t)value) % es) return SV_ERR_INVALID_ARG;
+    a.base = base;
+    a.new_len = new_len;
+    a.N = N;
+    a.key = static_cast<const unsigned char*>(key);
+    a.value = static_cast<const unsigned char*>(value);
+    a.sb = src_stride[0];
+    a.st = src_stride[1];
+    a.sh = src_stride[2];
+    return run_rows<false>(a, cache->dtype == SV_CACHE_E4M3, src, rows_aligned(a, cache, es), B, (cudaStream_t)stream);
+}
+
+sv_status spec_kv_read(const sv_paged_cache* cache, const int32_t* base, const int32_t* new_len, int B, int N,
+                       void* out_key, void* out_value, sv_dtype dst, void* stream) {
+    RowsArgs a{};
+    if (dst != SV_F32 && dst != SV_BF16) return SV_ERR_INVALID_ARG;
+    if (!sv::paged_cache_args(cache, a.c) || !rows_sizes_ok(a.c, B, N)) return SV_ERR_INVALID_ARG;
+    if (B == 0 || N == 0) return SV_OK;
+    const int es = dst == SV_BF16 ? 2 : 4;
+    if (!out_key || !out_value || !base || ((uintptr_t)out_key | (uintptr_t)out_value) % es) return SV_ERR_INVALID_ARG;
+    a.base = base;
+    a.new_len = new_len;
+    a.N = N;
+    a.key = static_cast<const unsigned char*>(out_key);
+    a.value = static_cast<const unsigned char*>(out_value);
+    a.sh = a.c.dim;
+    a.st = a.sh * a.c.heads;
+    a.sb = a.st * N;
+    return run_rows<true>(a, cache->dtype == SV_CACHE_E4M3, dst, rows_aligned(a, cache, es), B, (cudaStream_t)stream);
+}
+
+sv_status spec_kv_compact_paged(void* const* kv_buffers, int num_buffers, int64_t page_stride, int64_t plane_stride,
+                                int num_planes, int64_t row_stride, int64_t row_bytes, const int32_t* page_table,
+                                int num_pages, int page_size, int max_pages, const int32_t* path,
+                                const int32_t* count, const int32_t* base, int B, int max_depth, void* stream) {
+    if (B < 0 || B > kMaxB || num_buffers < 1 || num_buffers > kKvMaxBuffers || num_planes < 1 || max_depth < 1 ||
+        max_depth > kKvMaxDepth || row_bytes < 1 || row_stride < row_bytes || page_stride < 0 || plane_stride < 0 ||
+        num_pages < 1 || page_size < 1 || page_size > 65536 || max_pages < 1 ||
+        (int64_t)max_pages * page_size >= ((int64_t)1 << 31))
+        return SV_ERR_INVALID_ARG;
+    if (B == 0) return SV_OK;
+    if (!kv_buffers || !page_table || !path || !count) return SV_ERR_INVALID_ARG;
+    PagedMoveArgs a{};
+    uint64_t align = (uint64_t)page_stride | (uint64_t)plane_stride | (uint64_t)row_stride | (uint64_t)row_bytes;
+    for (int k = 0; k < num_buffers; ++k) {
+        if (!kv_buffers[k]) return SV_ERR_INVALID_ARG;
+        a.buf[k] = static_cast<unsigned char*>(kv_buffers[k]);
+        align |= (uint64_t)(uintptr_t)kv_buffers[k];
+    }
+    const int pw = (align % 16 == 0) ? 16 : (align % 4 == 0) ? 4 : 1;
+    const int64_t pieces = row_bytes / pw;
+    const int64_t limit = (int64_t)INT32_MAX - kThreads;
+    if (pieces > limit || (int64_t)num_planes > limit / pieces || (int64_t)num_buffers > limit / (pieces * num_planes))
+        return SV_ERR_INVALID_ARG;
+    const int64_t total = (int64_t)num_buffers * num_planes * pieces;
+    a.page_stride = page_stride;
+    a.plane_stride = plane_stride;
+    a.row_stride = row_stride;
+    a.num_planes = num_planes;
+    a.pieces = (int)pieces;
+    a.D = max_depth;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    a.total = (unsigned)total;
+    a.table = page_table;
+    a.path = path;
+    a.count = count;
+    a.base = base;
+    const dim3 grid((unsigned)((total + kThreads - 1) / kThreads), (unsigned)B);
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e;
+    if (pw == 16) e = sv::launch_serial(kv_compact_paged_kernel<16>, grid, dim3(kThreads), 0, s, a);
+    else if (pw == 4) e = sv::launch_serial(kv_compact_paged_kernel<4>, grid, dim3(kThreads), 0, s, a);
+    else e = sv::launch_serial(kv_compact_paged_kernel<1>, grid, dim3(kThreads), 0, s, a);
+    return sv::launch_status(e);
+}
+
+}  // extern "C"
