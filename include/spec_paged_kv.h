@@ -1,7 +1,8 @@
 /*
  * spec_paged_kv.h -- a verification round on a paged key/value cache: the new tokens'
- * keys and values written into cache pages (as bf16, or quantised to e4m3), pages read
- * back, and the accepted tree nodes' rows moved through the page table after the verify.  Same
+ * keys and values written into cache pages (as bf16, or quantised to e4m3), their
+ * attention over the cache under the chain's or the tree's mask, pages read back, and
+ * the accepted tree nodes' rows moved through the page table after the verify.  Same
  * library, status codes and conventions as spec_verify.h (caller-owned device arrays,
  * asynchronous on `stream`, argument errors returned before any launch, SV_ERR_CUDA for
  * launch failures).
@@ -42,7 +43,7 @@ typedef enum {
  *                for SV_CACHE_BF16.
  *   page_table   device int32 [B][max_pages], dense.
  * The struct is read during the call and is not retained.
- *   1 <= num_pages, 1 <= page_size <= 65536, 1 <= max_pages, max_pages * page_size < 2^31,
+ *   1 <= num_pages, 1 <= page_size <= 65536, 1 <= max_pages, max_pages * page_size <= 2^30,
  *   1 <= num_heads <= 1024, 1 <= head_dim <= 256; strides are multiples of the element
  *   size and row_stride covers a row.
  */
@@ -94,6 +95,47 @@ SV_API sv_status spec_kv_append(const void *key, const void *value, sv_dtype src
  */
 SV_API sv_status spec_kv_read(const sv_paged_cache *cache, const int32_t *base, const int32_t *new_len, int B, int N,
                               void *out_key, void *out_value, sv_dtype dst, void *stream);
+
+/*
+ * Attention of a chunk of new tokens over the paged cache, which already holds the new
+ * tokens' own keys and values (spec_kv_append): the attention of a target's verify pass.
+ *   q            device bf16 [B][Q][num_q_heads][head_dim] with element strides
+ *                q_stride[0..2] (batch, token, head; HOST int64 array of three) and
+ *                contiguous elements.  num_q_heads is a multiple of cache->num_heads; query
+ *                head h reads cache head h / (num_q_heads / num_heads).
+ *   base, new_len  as above, with N = Q.  Query i of row b sees every position below
+ *                base[b] that is no hole, and of the new positions base[b] + j, j < new_len[b]:
+ *   tree_mask    NULL: those with j <= i (a chain, or a chunk of a prompt);
+ *                device uint32 [B][Q-1][W], W = ceil((Q-1) / 32), as spec_tree_mask writes
+ *                it for the N = Q - 1 nodes of draft trees: token 0 is the tree's root,
+ *                token i + 1 node i (the rows of spec_verify_tree).  Every query sees the
+ *                root, query i + 1 also node j where bit j of mask row i is set.
+ *   scale        factor of the scores (1 / sqrt(head_dim) as a rule), finite.
+ *   max_len      host bound on base[b] + new_len[b] over the rows, by which the work is
+ *                split; 1 <= max_len.  Rows beyond it are still right, but slower.
+ *   out          device bf16 [B][Q][num_q_heads][head_dim], dense: softmax(scale q k) v.
+ *   out_lse      device fp32 [B][Q][num_q_heads] or NULL: natural logarithm of the sum of
+ *                exponentials of the scaled scores.
+ * A query that sees no position (or only scores of -inf) gets a zero output and lse -inf.  Keys and values at
+ * positions that a query does not see never affect it, whatever they hold.  Scores,
+ * softmax sums and outputs are accumulated in fp32; the probabilities (for e4m3, times
+ * the value's scale) enter the second product rounded to bf16.
+ *   workspace    device scratch of ws_bytes, 16-byte aligned (spec_paged_attention_workspace_size;
+ *                no initialisation, free for other uses once the call has run), or NULL:
+ *                contexts are then not split, which is slower for few rows and long contexts.
+ * 1 <= Q <= 65536, Q * num_q_heads / num_heads < 2^30, head_dim a multiple of 8 (SV_ERR_UNSUPPORTED otherwise), pages, strides
+ * and q aligned to 16 bytes (SV_ERR_UNSUPPORTED otherwise).  Errors: SV_ERR_INVALID_ARG for
+ * a bad size, pointer or stride (B = 0 returns SV_OK).
+ */
+SV_API sv_status spec_paged_attention(const void *q, const int64_t *q_stride, int num_q_heads,
+                                      const sv_paged_cache *cache, const int32_t *base, const int32_t *new_len,
+                                      const uint32_t *tree_mask, float scale, int B, int Q, int max_len, void *out,
+                                      float *out_lse, void *workspace, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace that spec_paged_attention can use for such a call (0: none), a
+ * function of the sizes and of the current device. */
+SV_API size_t spec_paged_attention_workspace_size(int B, int Q, int num_q_heads, int num_heads, int head_dim,
+                                                  sv_cache_dtype dtype, int max_len);
 
 /*
  * spec_kv_compact on a paged cache: row base[b] + d <- row base[b] + path[b][d] for

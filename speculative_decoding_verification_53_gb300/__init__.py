@@ -28,7 +28,8 @@ EXPORTS = ("spec_verify_workspace_size", "spec_verify_chain", "spec_greedy_accep
            "spec_verify_status_string", "spec_verify_last_cuda_error", "spec_verify_chain_noalloc",
            "spec_tree_mask", "spec_kv_compact", "spec_verify_tree_rule", "spec_sample_and_verify",
            "spec_verify_count_invalid", "spec_verify_rows_status", "spec_verify_chain_host",
-           "spec_verify_host_sizes", "spec_kv_append", "spec_kv_read", "spec_kv_compact_paged")
+           "spec_verify_host_sizes", "spec_kv_append", "spec_kv_read", "spec_kv_compact_paged",
+           "spec_paged_attention", "spec_paged_attention_workspace_size")
 
 # out_count value of a batch row whose kernel gave up a bounded device-side wait
 COUNT_TIMEOUT = -1
@@ -103,6 +104,10 @@ def lib() -> ctypes.CDLL:
     L.spec_kv_read.restype = ci
     L.spec_kv_compact_paged.argtypes = [vp, ci, i64, i64, ci, i64, i64, vp, ci, ci, ci, vp, vp, vp, ci, ci, vp]
     L.spec_kv_compact_paged.restype = ci
+    L.spec_paged_attention.argtypes = [vp, vp, ci, pc, vp, vp, vp, ctypes.c_float, ci, ci, ci, vp, vp, vp, sz, vp]
+    L.spec_paged_attention.restype = ci
+    L.spec_paged_attention_workspace_size.argtypes = [ci, ci, ci, ci, ci, ci, ci]
+    L.spec_paged_attention_workspace_size.restype = sz
     _lib = L
     return L
 
@@ -671,3 +676,81 @@ def spec_kv_compact_paged(kv_buffers, page_table, path, count, base=None, *, str
     _launch("spec_kv_compact_paged", dev, stream, lib().spec_kv_compact_paged, (ctypes.c_void_p * n)(*ptrs), n,
             strides[0] * es, strides[1] * es, H, row * es, W * es, _ptr(page_table), P, ps, page_table.shape[1],
             _ptr(path), _ptr(count), _ptr(base), B, path.shape[1])
+
+
+def spec_paged_attention_workspace_size(B: int, Q: int, num_q_heads: int, num_heads: int, head_dim: int, cache_dtype,
+                                        max_len: int) -> int:
+    """Bytes of scratch spec_paged_attention uses for such a call on the current device;
+    cache_dtype is the pages' torch dtype."""
+    torch = _torch()
+    if cache_dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError(f"pages must be bfloat16 or float8_e4m3fn, got {cache_dtype}")
+    code = SV_CACHE_BF16 if cache_dtype == torch.bfloat16 else SV_CACHE_E4M3
+    return int(lib().spec_paged_attention_workspace_size(B, Q, num_q_heads, num_heads, head_dim, code, max_len))
+
+
+_attention_needs = {}
+
+
+def _attention_need(dev, *sizes):
+    """spec_paged_attention_workspace_size(*sizes) on a device, remembered by the sizes."""
+    key = (dev.index, *sizes)
+    need = _attention_needs.get(key)
+    if need is None:
+        with _torch().cuda.device(dev):
+            need = int(lib().spec_paged_attention_workspace_size(*sizes))
+        if len(_attention_needs) >= 4096:  # context lengths vary: keep the table small
+            _attention_needs.clear()
+        _attention_needs[key] = need
+    return need
+
+
+def spec_paged_attention(q, k_pages, v_pages, page_table, base, *, max_len=None, new_len=None, tree_mask=None,
+                         scale=None, k_scale=None, v_scale=None, out=None, out_lse=None, want_lse: bool = False,
+                         workspace="auto", stream=None):
+    """Attention of a chunk of new tokens over a paged cache that already holds their keys
+    and values (spec_kv_append).  q bf16 [B][Q][q_heads][head_dim] (any strides with
+    contiguous elements, multiples of 8); pages, scales, page_table, base and new_len as
+    spec_kv_append.  Query i sees the base[b] positions before the chunk and, of the chunk,
+    tokens 0..i; with tree_mask (int32 [B][Q-1][ceil((Q-1)/32)] from spec_tree_mask: token 0
+    is the root, token i + 1 node i) the root, itself and its ancestors.  max_len: a bound
+    on base + new_len that the caller knows (the page table's capacity unless given);
+    scale: 1 / sqrt(head_dim) unless given.  workspace: "auto" (allocated for the call), a
+    uint8 CUDA tensor, or None (long contexts are not split).
+    Returns (out bf16 [B][Q][q_heads][head_dim], lse fp32 [B][Q][q_heads] or None)."""
+    torch = _torch()
+    auto = isinstance(workspace, str)
+    dev, stream = _one_device(q, stream, q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, base=base,
+                              new_len=new_len, tree_mask=tree_mask, k_scale=k_scale, v_scale=v_scale, out=out,
+                              out_lse=out_lse, workspace=None if auto else workspace)
+    if q.dim() != 4 or q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16 [B][Q][q_heads][head_dim]")
+    B, Q, Hq, D = q.shape
+    cache = _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, B)
+    if cache.head_dim != D or Hq % cache.num_heads:
+        raise ValueError(f"q has {Hq} heads of {D}, the cache {cache.num_heads} of {cache.head_dim}")
+    if Q < 1:
+        raise ValueError("q holds no query")
+    _shaped("base", base, (B,), torch.int32)
+    _shaped("new_len", new_len, (B,), torch.int32)
+    _shaped("tree_mask", tree_mask, (B, Q - 1, (Q + 30) // 32), torch.int32)
+    _shaped("out", out, (B, Q, Hq, D), torch.bfloat16)
+    _shaped("out_lse", out_lse, (B, Q, Hq), torch.float32)
+    if max_len is None:
+        max_len = cache.max_pages * cache.page_size
+    if scale is None:
+        scale = D ** -0.5
+    if out is None:
+        out = _new((B, Q, Hq, D), torch.bfloat16, dev, stream)
+    if out_lse is None and want_lse:
+        out_lse = _new((B, Q, Hq), torch.float32, dev, stream)
+    if auto:
+        need = _attention_need(dev, B, Q, Hq, cache.num_heads, D, cache.dtype, max_len) if B else 0
+        workspace = _new((need,), torch.uint8, dev, stream) if need else None
+    elif workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _launch("spec_paged_attention", dev, stream, lib().spec_paged_attention, _ptr(q), _strides3(q, "q"), Hq, cache,
+            _ptr(base), _ptr(new_len), _ptr(tree_mask), scale, B, Q, max_len, _ptr(out), _ptr(out_lse),
+            _ptr(workspace), ws_bytes)
+    return out, out_lse

@@ -1,0 +1,110 @@
+// sv_attention.cuh -- what the paged-attention kernels share: their arguments, which rows
+// and positions a CTA works on, what a query sees, and where results go.
+//
+// A CTA works on one batch row b, one cache head h, one tile of query rows and one stretch
+// of positions ("split").  Query rows are the pairs (query i, head of h's group) in the
+// order r = i * group + g, so the queries that share a cache head share its loads.
+#pragma once
+
+#include "sv_internal.h"
+#include "sv_paged.cuh"
+
+namespace sv {
+
+struct AttnArgs {
+    PagedCache c;
+    const uint16_t* q;         // bf16, element strides below
+    int64_t q_sb, q_st, q_sh;
+    const int32_t* base;
+    const int32_t* new_len;    // or nullptr
+    const uint32_t* tree_mask; // [B][Q-1][mask_words] or nullptr
+    float scale_log2;          // scale * log2(e)
+    int Q, Hq, group, mask_words;
+    int m_tiles, splits, chunk; // chunk: positions per split (the last split takes what remains)
+    uint16_t* out;             // [B][Q][Hq][D] bf16
+    float* lse;                // [B][Q][Hq] or nullptr
+    float* part_o;             // [B][Q][Hq][splits][D] fp32, splits > 1
+    float* part_lse;           // [B][Q][Hq][splits], base 2
+};
+
+struct AttnTile {
+    int b, h, mt, split;
+    int base, n;       // positions before the chunk, real queries
+    int begin, end;    // this CTA's positions
+    int active;        // splits of this row tile that have positions
+};
+
+// End of the positions that rows [0, last query of the tile] can see.
+__host__ __device__ __forceinline__ int attn_tile_end(int base, int n, int group, int mt, int tile_rows, bool tree) {
+    if (tree) return base + n;
+    int last = ((mt + 1) * tile_rows - 1) / group;
+    if (last > n - 1) last = n - 1;
+    return base + last + 1;
+}
+
+// The work of CTA `id`; false where it has none.
+__device__ __forceinline__ bool attn_tile(const AttnArgs& a, unsigned id, int tile_rows, AttnTile& t) {
+    t.mt = (int)(id % (unsigned)a.m_tiles);
+    unsigned rest = id / (unsigned)a.m_tiles;
+    t.split = (int)(rest % (unsigned)a.splits);
+    rest /= (unsigned)a.splits;
+    t.h = (int)(rest % (unsigned)a.c.heads);
+    t.b = (int)(rest / (unsigned)a.c.heads);
+    if (!paged_row(a.c, a.base, a.new_len, t.b, a.Q, t.base, t.n)) return false;
+    if ((int64_t)t.mt * tile_rows >= (int64_t)t.n * a.group) return false;
+    const int end = attn_tile_end(t.base, t.n, a.group, t.mt, tile_rows, a.tree_mask != nullptr);
+    t.active = (end + a.chunk - 1) / a.chunk;
+    if (t.active > a.splits) t.active = a.splits;
+    if (t.split >= t.active) return false;
+    t.begin = t.split * a.chunk;
+    t.end = t.split == t.active - 1 ? end : t.begin + a.chunk;
+    return true;
+}
+
+// Bits of `count` (at most 32) positions from pos0 on that query i sees by the mask alone
+// (holes and the end of the sequence are the caller's): the context, and of the chunk
+// what the chain or the tree shows.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+__device__ __forceinline__ uint32_t attn_visible(const AttnArgs& a, const AttnTile& t, int i, int pos0) {
+    if (!a.tree_mask) return low_bits(t.base + i + 1 - pos0);
+    uint32_t bits = low_bits(t.base + 1 - pos0);  // context and root
+    const int j0 = pos0 - t.base - 1;             // node of bit 0
+    if (i > 0 && j0 > -32) {
+        const uint32_t* row = a.tree_mask + ((int64_t)t.b * (a.Q - 1) + (i - 1)) * a.mask_words;
+        if (j0 < 0) {
+            bits |= __ldg(row) << (-j0);
+        } else if ((j0 >> 5) < a.mask_words) {
+            const int w = j0 >> 5;
+            const uint32_t lo = __ldg(row + w), hi = w + 1 < a.mask_words ? __ldg(row + w + 1) : 0u;
+            bits |= __funnelshift_r(lo, hi, j0 & 31);
+        }
+    }
+    return bits;
+}
+
+// Element d of the value at a position, from the cache itself (0 in a hole).
+template <bool E4M3>
+__device__ __forceinline__ float attn_value(const AttnArgs& a, const AttnTile& t, int pos, int d) {
+    int row;
+    const int page = paged_place(a.c, t.b, pos, row);
+    if (page < 0) return 0.0f;
+    const unsigned char* p = a.c.v + page * a.c.page_stride + t.h * a.c.head_stride + row * a.c.row_stride;
+    if (!E4M3) return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + d) << 16);
+    const float s = __ldg(a.c.v_scale + ((int64_t)page * a.c.heads + t.h) * a.c.page_size + row);
+    return e4m3x2_to_f32(__ldg(p + d)).x * s;
+}
+
+// Index of query row r's (query, head) in [B][Q][Hq].
+__device__ __forceinline__ int64_t attn_row(const AttnArgs& a, const AttnTile& t, int r) {
+    return ((int64_t)t.b * a.Q + r / a.group) * a.Hq + t.h * a.group + r % a.group;
+}
+
+__device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) < pos_inf()); }
+
+// Tensor-core kernel for many query rows per cache head (sv_attention_tc.cu).
+bool attn_tc_applies(int rows, int dim);
+int attn_tc_tile_rows(int rows, int dim);
+cudaError_t launch_attn_tc(const AttnArgs& a, bool e4m3, unsigned ctas, cudaStream_t stream);
+
+}  // namespace sv

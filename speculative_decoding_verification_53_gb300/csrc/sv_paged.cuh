@@ -13,6 +13,7 @@ namespace sv {
 constexpr float E4M3_MAX = 448.0f;
 constexpr int PAGED_MAX_DIM = 256;
 constexpr int PAGED_MAX_HEADS = 1024;
+constexpr int PAGED_MAX_POS = 1 << 30;  // positions of a page table's row: index sums stay within int
 
 struct PagedCache {
     unsigned char* k;
@@ -72,13 +73,13 @@ inline bool paged_cache_args(const sv_paged_cache* c, PagedCache& out) {
     if (!c) return false;
     if (c->dtype != SV_CACHE_BF16 && c->dtype != SV_CACHE_E4M3) return false;
     if (c->num_pages < 1 || c->page_size < 1 || c->page_size > 65536 || c->max_pages < 1 ||
-        (int64_t)c->max_pages * c->page_size >= ((int64_t)1 << 31) || c->num_heads < 1 ||
+        (int64_t)c->max_pages * c->page_size > PAGED_MAX_POS || c->num_heads < 1 ||
         c->num_heads > PAGED_MAX_HEADS || c->head_dim < 1 || c->head_dim > PAGED_MAX_DIM)
         return false;
     const int64_t es = c->dtype == SV_CACHE_BF16 ? 2 : 1;
     if (c->page_stride < 0 || c->head_stride < 0 || c->row_stride < es * c->head_dim) return false;
     if ((c->page_stride | c->head_stride | c->row_stride) % es) return false;
-    if (!c->k_pages || !c->v_pages || !c->page_table) return false;
+    if (!c->k_pages || !c->v_pages) return false;  // the table may be NULL in a call on no rows
     if (((uintptr_t)c->k_pages | (uintptr_t)c->v_pages) % es) return false;
     if (c->dtype == SV_CACHE_E4M3 && (!c->k_scale || !c->v_scale)) return false;
     out = PagedCache{static_cast<unsigned char*>(c->k_pages), static_cast<unsigned char*>(c->v_pages), c->k_scale,

@@ -356,7 +356,7 @@ sv_status spec_kv_append(const void* key, const void* value, sv_dtype src, const
     if (!sv::paged_cache_args(cache, a.c) || !rows_sizes_ok(a.c, B, N)) return SV_ERR_INVALID_ARG;
     if (B == 0 || N == 0) return SV_OK;
     const int es = src == SV_BF16 ? 2 : 4;
-    if (!key || !value || !base || !src_stride || ((uintptr_t)key | (uintptr_t)value) % es) return SV_ERR_INVALID_ARG;
+    if (!cache->page_table || !key || !value || !base || !src_stride || ((uintptr_t)key | (uintptr_t)value) % es) return SV_ERR_INVALID_ARG;
     a.base = base;
     a.new_len = new_len;
     a.N = N;
@@ -375,7 +375,7 @@ sv_status spec_kv_read(const sv_paged_cache* cache, const int32_t* base, const i
     if (!sv::paged_cache_args(cache, a.c) || !rows_sizes_ok(a.c, B, N)) return SV_ERR_INVALID_ARG;
     if (B == 0 || N == 0) return SV_OK;
     const int es = dst == SV_BF16 ? 2 : 4;
-    if (!out_key || !out_value || !base || ((uintptr_t)out_key | (uintptr_t)out_value) % es) return SV_ERR_INVALID_ARG;
+    if (!cache->page_table || !out_key || !out_value || !base || ((uintptr_t)out_key | (uintptr_t)out_value) % es) return SV_ERR_INVALID_ARG;
     a.base = base;
     a.new_len = new_len;
     a.N = N;
@@ -394,7 +394,7 @@ sv_status spec_kv_compact_paged(void* const* kv_buffers, int num_buffers, int64_
     if (B < 0 || B > kMaxB || num_buffers < 1 || num_buffers > kKvMaxBuffers || num_planes < 1 || max_depth < 1 ||
         max_depth > kKvMaxDepth || row_bytes < 1 || row_stride < row_bytes || page_stride < 0 || plane_stride < 0 ||
         num_pages < 1 || page_size < 1 || page_size > 65536 || max_pages < 1 ||
-        (int64_t)max_pages * page_size >= ((int64_t)1 << 31))
+        (int64_t)max_pages * page_size > sv::PAGED_MAX_POS)
         return SV_ERR_INVALID_ARG;
     if (B == 0) return SV_OK;
     if (!kv_buffers || !page_table || !path || !count) return SV_ERR_INVALID_ARG;

@@ -31,7 +31,7 @@ def _cache(**kw):
 
 
 BAD_CACHES = [dict(dtype=2), dict(num_pages=0), dict(page_size=0), dict(page_size=65537), dict(max_pages=0),
-              dict(page_size=65536, max_pages=32768), dict(num_heads=0), dict(num_heads=1025), dict(head_dim=0),
+              dict(page_size=65536, max_pages=16385), dict(num_heads=0), dict(num_heads=1025), dict(head_dim=0),
               dict(head_dim=257, row_stride=1024), dict(row_stride=254), dict(row_stride=257), dict(page_stride=-2),
               dict(k_pages=None), dict(v_pages=None), dict(page_table=None), dict(k_pages=257),
               dict(dtype=1), dict(dtype=1, k_scale=256)]
@@ -68,6 +68,7 @@ def test_append_and_read_arguments(lib):
     assert r(c, vp, None, 1, 1, None, vp, 1, None) == 1
     assert r(c, vp, None, 1, 1, vp, ctypes.c_void_p(258), 0, None) == 1      # misaligned fp32
     assert r(c, None, None, 0, 1, None, None, 1, None) == 0
+    assert r(_cache(page_table=None), None, None, 0, 1, None, None, 1, None) == 0
 
 
 def test_compact_paged_arguments(lib):
@@ -81,7 +82,7 @@ def test_compact_paged_arguments(lib):
                  None, B, D, None)
 
     for bad in (dict(n=0), dict(n=257), dict(planes=0), dict(row_stride=8), dict(row_bytes=0), dict(table=None),
-                dict(pages=0), dict(ps=0), dict(ps=65537), dict(mp=0), dict(ps=65536, mp=32768), dict(path=None),
+                dict(pages=0), dict(ps=0), dict(ps=65537), dict(mp=0), dict(ps=65536, mp=16385), dict(path=None),
                 dict(count=None), dict(B=-1), dict(B=65536), dict(D=0), dict(D=65), dict(bufs=None),
                 dict(page_stride=-1), dict(plane_stride=-16), dict(planes=1 << 30, n=256),
                 dict(bufs=(ctypes.c_void_p * 2)(256, None), n=2)):
@@ -180,3 +181,28 @@ def test_plain_compact_matches_the_dense_one():
     got = paged.compact(pages, table, path, count, base)
     got = got[table].transpose(0, 2, 1, 3, 4).reshape(B * H, mp * ps, W)
     assert (got == want).all()
+
+
+def test_attention_arguments(lib):
+    vp = ctypes.c_void_p(256)
+    st = (ctypes.c_int64 * 3)(0, 0, 0)
+    f = lib.spec_paged_attention
+
+    def call(q=vp, stride=st, Hq=8, cache=None, base=vp, scale=1.0, B=1, Q=6, max_len=32, out=vp, cache_kw={}):
+        c = cache if cache is not None else _cache(**cache_kw)
+        return f(q, stride, Hq, c, base, None, None, scale, B, Q, max_len, out, None, None, 0, None)
+
+    for bad in BAD_CACHES:
+        assert call(cache_kw=bad) == 1, bad
+    for bad in (dict(q=None), dict(stride=None), dict(Hq=0), dict(Hq=7), dict(Hq=12), dict(base=None),
+                dict(scale=float("nan")), dict(scale=float("inf")), dict(B=-1), dict(B=65536), dict(Q=0),
+                dict(Q=65537), dict(max_len=0), dict(out=None), dict(Hq=65544)):
+        assert call(**bad) == 1, bad
+    for odd in (dict(cache_kw=dict(head_dim=100)), dict(q=ctypes.c_void_p(264)), dict(out=ctypes.c_void_p(258)),
+                dict(cache_kw=dict(row_stride=264)), dict(cache_kw=dict(k_pages=264)),
+                dict(stride=(ctypes.c_int64 * 3)(4, 0, 0))):
+        assert call(**odd) == 2, odd
+    assert call(B=0, q=None, base=None, out=None) == 0
+    size = lib.spec_paged_attention_workspace_size
+    assert size(0, 1, 8, 8, 128, 0, 100) == 0 and size(1, 1, 8, 3, 128, 0, 100) == 0
+    assert size(1, 1, 8, 8, 128, 5, 100) == 0 and size(1, 1, 8, 8, 128, 0, 0) == 0
