@@ -135,3 +135,47 @@ def compact(pages, table, path, count, base):
         for (p, r), (g, t) in where:
             pages[g, :, t] = pages[p, :, r]
     return pages
+
+
+def adjust_logits(logits, history=None, history_len=None, prompt_len=None, draft_tokens=None, tree_mask=None,
+                  repetition=None, presence=None, frequency=None, bias_tokens=None, bias_values=None, allowed=None):
+    """Penalties, biases and masks of logits [B][R][V], token by token from the lists."""
+    x = np.array(logits, np.float64)
+    B, R, V = x.shape
+    for b in range(B):
+        n = 0 if history is None else min(max(int(history_len[b]), 0), history.shape[1])
+        start = 0 if prompt_len is None else int(prompt_len[b])
+        prompt = {int(t) for t in (history[b, :n][:max(start, 0)] if n else []) if 0 <= t < V}
+        output = [int(t) for t in (history[b, :n][max(start, 0):] if n else []) if 0 <= t < V]
+        bias = {}
+        if bias_tokens is not None:
+            for t, v in zip(bias_tokens[b], bias_values[b]):
+                if 0 <= t < V:
+                    bias[int(t)] = float(v)
+        for r in range(R):
+            count = {}
+            for t in output:
+                count[t] = count.get(t, 0) + 1
+            for j in range(R - 1 if draft_tokens is not None else 0):
+                if tree_mask is None:
+                    follows = j < r
+                else:
+                    follows = r > 0 and bool((int(np.asarray(tree_mask).view(np.uint32)[b, r - 1, j // 32]) >> (j % 32)) & 1)
+                t = int(draft_tokens[b, j])
+                if follows and 0 <= t < V:
+                    count[t] = count.get(t, 0) + 1
+            for t in prompt | set(count):
+                v, c = x[b, r, t], count.get(t, 0)
+                if repetition is not None:
+                    v = v / repetition[b] if v > 0 else v * repetition[b]
+                if frequency is not None:
+                    v -= c * frequency[b]
+                if presence is not None and c:
+                    v -= presence[b]
+                x[b, r, t] = v
+            for t, v in bias.items():
+                x[b, r, t] += v
+            if allowed is not None:
+                bits = np.unpackbits(np.ascontiguousarray(allowed[b, r]).view(np.uint8), bitorder="little")[:V]
+                x[b, r, bits == 0] = -np.inf
+    return x

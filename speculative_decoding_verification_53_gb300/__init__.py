@@ -29,7 +29,7 @@ EXPORTS = ("spec_verify_workspace_size", "spec_verify_chain", "spec_greedy_accep
            "spec_tree_mask", "spec_kv_compact", "spec_verify_tree_rule", "spec_sample_and_verify",
            "spec_verify_count_invalid", "spec_verify_rows_status", "spec_verify_chain_host",
            "spec_verify_host_sizes", "spec_kv_append", "spec_kv_read", "spec_kv_compact_paged",
-           "spec_paged_attention", "spec_paged_attention_workspace_size")
+           "spec_paged_attention", "spec_paged_attention_workspace_size", "spec_adjust_logits")
 
 # out_count value of a batch row whose kernel gave up a bounded device-side wait
 COUNT_TIMEOUT = -1
@@ -108,6 +108,8 @@ def lib() -> ctypes.CDLL:
     L.spec_paged_attention.restype = ci
     L.spec_paged_attention_workspace_size.argtypes = [ci, ci, ci, ci, ci, ci, ci]
     L.spec_paged_attention_workspace_size.restype = sz
+    L.spec_adjust_logits.argtypes = [vp, ci, vp, vp, vp, ci, vp, vp, vp, vp, vp, vp, vp, ci, vp, ci, ci, ci, vp, vp]
+    L.spec_adjust_logits.restype = ci
     _lib = L
     return L
 
@@ -754,3 +756,64 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, base, *, max_len=None,
             _ptr(base), _ptr(new_len), _ptr(tree_mask), scale, B, Q, max_len, _ptr(out), _ptr(out_lse),
             _ptr(workspace), ws_bytes)
     return out, out_lse
+
+
+def spec_adjust_logits(logits, *, history=None, history_len=None, prompt_len=None, draft_tokens=None, tree_mask=None,
+                       repetition=None, presence=None, frequency=None, bias_tokens=None, bias_values=None,
+                       allowed=None, out=None, stream=None):
+    """Penalties for repeated tokens, biases and grammar masks on the logits [B][R][V]
+    (fp32/bf16) of a verify call, R = K + 1 rows of a chain or N + 1 of a tree.  history
+    int32 [B][H] (history_len int32 [B], all H unless given; tokens before prompt_len int32
+    [B] are the prompt); draft_tokens int32 [B][R-1], which row r has as output so far where
+    they precede it in the chain, or with tree_mask (int32 [B][R-1][ceil((R-1)/32)] from
+    spec_tree_mask) where they are node r-1 or its ancestors; repetition, presence,
+    frequency fp32 [B]; bias_tokens int32 and bias_values fp32 [B][M]; allowed int32
+    [B][R][ceil(V/32)], bit v % 32 of word v / 32 set where token v is allowed.  Any of them
+    may be None.  Returns out (a new tensor unless given; logits itself works in place)."""
+    torch = _torch()
+    dev, stream = _one_device(logits, stream, logits=logits, history=history, history_len=history_len,
+                              prompt_len=prompt_len, draft_tokens=draft_tokens, tree_mask=tree_mask,
+                              repetition=repetition, presence=presence, frequency=frequency, bias_tokens=bias_tokens,
+                              bias_values=bias_values, allowed=allowed, out=out)
+    if logits.dim() != 3 or not logits.is_contiguous():
+        raise ValueError("logits must be contiguous [B][R][V]")
+    code = _dtype_code(logits)
+    B, R, V = logits.shape
+    i32, f32 = torch.int32, torch.float32
+    H = M = 0
+    if history is not None:
+        if history.dim() != 2:
+            raise ValueError("history must be [B][H]")
+        H = history.shape[1]
+        _shaped("history", history, (B, H), i32)
+        if history_len is None:
+            with torch.cuda.stream(stream):
+                history_len = torch.full((B,), H, dtype=i32, device=dev)
+    elif history_len is not None or prompt_len is not None:
+        raise ValueError("history_len and prompt_len belong to a history")
+    _shaped("history_len", history_len, (B,), i32)
+    _shaped("prompt_len", prompt_len, (B,), i32)
+    _shaped("draft_tokens", draft_tokens, (B, R - 1), i32)
+    if tree_mask is not None and draft_tokens is None:
+        raise ValueError("tree_mask belongs to draft_tokens")
+    _shaped("tree_mask", tree_mask, (B, R - 1, (R + 30) // 32), i32)
+    _shaped("repetition", repetition, (B,), f32)
+    _shaped("presence", presence, (B,), f32)
+    _shaped("frequency", frequency, (B,), f32)
+    if (bias_tokens is None) != (bias_values is None):
+        raise ValueError("bias_tokens and bias_values belong together")
+    if bias_tokens is not None:
+        if bias_tokens.dim() != 2:
+            raise ValueError("bias_tokens must be [B][M]")
+        M = bias_tokens.shape[1]
+        _shaped("bias_tokens", bias_tokens, (B, M), i32)
+        _shaped("bias_values", bias_values, (B, M), f32)
+    _shaped("allowed", allowed, (B, R, (V + 31) // 32), i32)
+    _shaped("out", out, (B, R, V), logits.dtype)
+    if out is None:
+        out = _new((B, R, V), logits.dtype, dev, stream)
+    _launch("spec_adjust_logits", dev, stream, lib().spec_adjust_logits, _ptr(logits), code, _ptr(history),
+            _ptr(history_len), _ptr(prompt_len), H, _ptr(draft_tokens), _ptr(tree_mask), _ptr(repetition),
+            _ptr(presence), _ptr(frequency), _ptr(bias_tokens), _ptr(bias_values), M, _ptr(allowed), B, R, V,
+            _ptr(out))
+    return out
