@@ -613,15 +613,18 @@ Plan make_plan(int B, int Q, int Hq, int H, int D, int max_len, int num_sms) {
     Plan p{};
     if (max_len > sv::PAGED_MAX_POS) max_len = sv::PAGED_MAX_POS;
     const int64_t rows = (int64_t)Q * (Hq / H);
-    p.tile_rows = rows <= 16 ? 16 : rows <= 32 || D > 128 ? 32 : 64;
+    if (D > 128) p.tile_rows = rows <= 16 ? 16 : 32;
+    else p.tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
     p.m_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
     const int64_t tiles = (int64_t)B * H * p.m_tiles;
-    int64_t splits = (4LL * num_sms + tiles - 1) / tiles;
+    const int64_t want = p.tile_rows >= 128 ? num_sms : 4LL * num_sms;  // CTAs that are at work at once
+    int64_t splits = p.tile_rows >= 128 ? want / tiles : (want + tiles - 1) / tiles;
     const int64_t most = ((int64_t)max_len + 127) / 128;
     if (splits > most) splits = most;
     if (splits > 512) splits = 512;
     if (splits < 1) splits = 1;
-    const int64_t chunk = (((int64_t)max_len + splits - 1) / splits + TN - 1) / TN * TN;
+    const int tn = p.tile_rows >= 128 ? 128 : TN;  // positions per tile of the kernel taken
+    const int64_t chunk = (((int64_t)max_len + splits - 1) / splits + tn - 1) / tn * tn;
     p.chunk = (int)chunk;
     p.splits = (int)(((int64_t)max_len + chunk - 1) / chunk);
     p.ctas = tiles * p.splits;
@@ -705,7 +708,8 @@ sv_status spec_paged_attention(const void* q, const int64_t* q_stride, int num_q
     cudaStream_t s = (cudaStream_t)stream;
     const bool e4m3 = cache->dtype == SV_CACHE_E4M3;
     cudaError_t e;
-    if (D <= 64) e = e4m3 ? launch_rows<64, true>(a, p.tile_rows, (unsigned)p.ctas, s) : launch_rows<64, false>(a, p.tile_rows, (unsigned)p.ctas, s);
+    if (p.tile_rows >= 128) e = sv::launch_attn_tc(a, e4m3, p.tile_rows, (unsigned)p.ctas, s);
+    else if (D <= 64) e = e4m3 ? launch_rows<64, true>(a, p.tile_rows, (unsigned)p.ctas, s) : launch_rows<64, false>(a, p.tile_rows, (unsigned)p.ctas, s);
     else if (D <= 128) e = e4m3 ? launch_rows<128, true>(a, p.tile_rows, (unsigned)p.ctas, s) : launch_rows<128, false>(a, p.tile_rows, (unsigned)p.ctas, s);
     else e = e4m3 ? launch_rows<256, true>(a, p.tile_rows, (unsigned)p.ctas, s) : launch_rows<256, false>(a, p.tile_rows, (unsigned)p.ctas, s);
     if (e == cudaSuccess && p.splits > 1)

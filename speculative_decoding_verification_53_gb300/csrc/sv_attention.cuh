@@ -102,9 +102,8 @@ __device__ __forceinline__ int64_t attn_row(const AttnArgs& a, const AttnTile& t
 
 __device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) < pos_inf()); }
 
-// Tensor-core kernel for many query rows per cache head (sv_attention_tc.cu).
-bool attn_tc_applies(int rows, int dim);
-int attn_tc_tile_rows(int rows, int dim);
-cudaError_t launch_attn_tc(const AttnArgs& a, bool e4m3, unsigned ctas, cudaStream_t stream);
+// The kernel for many query rows per cache head, head_dim <= 128 (sv_attention_tc.cu):
+// tile_rows 128 or 256.
+cudaError_t launch_attn_tc(const AttnArgs& a, bool e4m3, int tile_rows, unsigned ctas, cudaStream_t stream);
 
 }  // namespace sv

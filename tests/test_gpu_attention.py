@@ -111,7 +111,8 @@ CASES = [  # B, Q, Hq, H, D, page_size, ctx
     (1, 1, 1, 1, 64, 16, 0), (1, 1, 8, 1, 128, 16, 1), (3, 1, 8, 2, 128, 16, 777), (2, 6, 8, 2, 128, 24, 300),
     (3, 6, 7, 1, 64, 1, 130), (2, 2, 16, 2, 96, 64, 500), (2, 17, 4, 2, 128, 16, 129), (2, 61, 4, 1, 128, 32, 200),
     (1, 130, 2, 2, 64, 8, 70), (2, 5, 3, 3, 256, 16, 260), (1, 33, 2, 1, 200, 128, 90), (2, 64, 1, 1, 128, 64, 0),
-    (1, 9, 8, 1, 16, 5, 63), (2, 20, 8, 4, 128, 16, 640), (1, 70, 8, 2, 128, 48, 150), (1, 300, 2, 1, 128, 64, 100)]
+    (1, 9, 8, 1, 16, 5, 63), (2, 20, 8, 4, 128, 16, 640), (1, 70, 8, 2, 128, 48, 150), (1, 300, 2, 1, 128, 64, 100), (2, 30, 4, 1, 64, 16, 300), (1, 25, 8, 2, 128, 16, 500),
+    (2, 40, 4, 2, 96, 16, 130), (1, 61, 4, 1, 128, 16, 2500), (1, 150, 1, 1, 64, 8, 900), (2, 33, 7, 1, 128, 64, 40)]
 
 
 @pytest.mark.parametrize("tree", [False, True])
