@@ -617,9 +617,11 @@ Plan make_plan(int B, int Q, int Hq, int H, int D, int max_len, int num_sms) {
     else p.tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
     p.m_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
     const int64_t tiles = (int64_t)B * H * p.m_tiles;
-    const int64_t want = p.tile_rows >= 128 ? num_sms : 4LL * num_sms;  // CTAs that are at work at once
-    int64_t splits = p.tile_rows >= 128 ? want / tiles : (want + tiles - 1) / tiles;
-    const int64_t most = ((int64_t)max_len + 127) / 128;
+    // Enough CTAs that rows of unequal length even out: four per SM, or for the large tiles,
+    // one of which fills an SM, three where there are not two already.
+    const bool large = p.tile_rows >= 128;
+    int64_t splits = !large ? (4LL * num_sms + tiles - 1) / tiles : tiles < 2LL * num_sms ? 3LL * num_sms / tiles : 1;
+    const int64_t most = large ? ((int64_t)max_len + 1023) / 1024 : ((int64_t)max_len + 127) / 128;
     if (splits > most) splits = most;
     if (splits > 512) splits = 512;
     if (splits < 1) splits = 1;

@@ -54,8 +54,9 @@ struct Tc {
     //   MQ = 1: 384 x 168 = 64512 >= 128 x 216 + 128 x 136 + 128 x 40 = 50176
     static constexpr int R_SOFTMAX = MQ == 2 ? 184 : 216, R_LOAD = MQ == 2 ? 96 : 136, R_MMA = 40;
     static constexpr int MAT = (DP / 64) * BLK;   // a tile of keys, values or queries
-    static constexpr int NB = DP == 64 ? 6 : 4;   // buffers of the ring
-    static constexpr int SMEM = (MQ + NB) * MAT + 1024;  // and room to align
+    static constexpr int NB = DP == 64 ? 6 : E4M3 ? 3 : 4;   // buffers of the ring
+    static constexpr int RAW = E4M3 ? 3 : 0;      // e4m3: items whose codes are in flight
+    static constexpr int SMEM = (MQ + NB) * MAT + RAW * MAT / 2 + 1024;  // and room to align
     static constexpr int S_COL = 0, O_COL = 128 * MQ;    // TMEM columns
     static constexpr int COLS = MQ == 2 ? 512 : 256;
 };
@@ -70,27 +71,38 @@ __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
 }
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
+// One lane of a converged warp, the same one for every call.  The products' warp runs its
+// loop with all lanes, so that addresses and descriptors are uniform, and only this lane
+// issues: with one lane alone in the loop each product cost 130 cycles to issue instead of 64.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(leader)
+        : "memory");
 }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc, uint32_t leader) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(leader)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc, uint32_t leader) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(leader)
         : "memory");
 }
 
@@ -184,15 +196,16 @@ __device__ __forceinline__ bool sanitise(uint4& v) {
 template <bool E4M3, bool MASK>
 __device__ __forceinline__ void scale_scores(uint32_t v[TN], const uint32_t see[4], const float* ksc, float sc) {
 #pragma unroll
-    for (int k = 0; k < TN; k += 2) {
-        float2 f = make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-        f = fmul2(f, E4M3 ? *reinterpret_cast<const float2*>(ksc + k) : make_float2(sc, sc));
-        if (MASK) {
-            if (!((see[k >> 5] >> (k & 31)) & 1u)) f.x = neg_inf();
-            if (!((see[k >> 5] >> ((k & 31) + 1)) & 1u)) f.y = neg_inf();
-        }
-        v[k] = __float_as_uint(f.x);
-        v[k + 1] = __float_as_uint(f.y);
+    for (int k = 0; k < TN; k += 4) {
+        const float4 w = E4M3 ? *reinterpret_cast<const float4*>(ksc + k) : make_float4(sc, sc, sc, sc);
+        float2 f[2] = {make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])),
+                       make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]))};
+        f[0] = fmul2(f[0], make_float2(w.x, w.y));
+        f[1] = fmul2(f[1], make_float2(w.z, w.w));
+        const float g[4] = {f[0].x, f[0].y, f[1].x, f[1].y};
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+            v[k + z] = __float_as_uint(!MASK || ((see[k >> 5] >> ((k & 31) + z)) & 1u) ? g[z] : neg_inf());
     }
 }
 
@@ -325,13 +338,21 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             for (int c = 0; c < 4; ++c) {
                 uint32_t p[16];
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    float2 e = ffma2(make_float2(__uint_as_float(v[32 * c + k]), __uint_as_float(v[32 * c + k + 1])), mul2, sh2);
+                for (int k = 0; k < 32; k += 4) {
+                    const uint32_t* x = v + 32 * c + k;
+                    float2 e = ffma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), mul2, sh2);
+                    float2 f = ffma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), mul2, sh2);
                     e = make_float2(sv::ex2(e.x), sv::ex2(e.y));
-                    if (k & 2) sum1 = sv::fadd2(sum1, e);
-                    else sum0 = sv::fadd2(sum0, e);
-                    if (E4M3) e = fmul2(e, *reinterpret_cast<const float2*>(&sh.vsc[m][32 * c + k]));
+                    f = make_float2(sv::ex2(f.x), sv::ex2(f.y));
+                    sum0 = sv::fadd2(sum0, e);
+                    sum1 = sv::fadd2(sum1, f);
+                    if (E4M3) {
+                        const float4 w = *reinterpret_cast<const float4*>(&sh.vsc[m][32 * c + k]);
+                        e = fmul2(e, make_float2(w.x, w.y));
+                        f = fmul2(f, make_float2(w.z, w.w));
+                    }
                     p[k >> 1] = sv::bf16x2(e.x, e.y);
+                    p[(k >> 1) + 1] = sv::bf16x2(f.x, f.y);
                 }
                 tmem_st16(s_at + 16 * c, p);  // over S, which this warp has read
             }
@@ -409,7 +430,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         int page, row, page1, row1;  // of the tile at work and of the next
         look_up(0, page, row);
         look_up(1, page1, row1);
-        if (!E4M3) {
+        if constexpr (!E4M3) {
             constexpr int CH = DP / 8, RPI = 32 / CH;  // pieces of a row, rows per instruction
             const int c = lane % CH, r0 = lane / CH;
             const uint32_t place0 = piece(32 * w + r0, c);
@@ -460,25 +481,16 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             cp_wait_all();
         } else {
             constexpr int CH = DP / 16, RPI = 32 / CH, X = 32 / RPI;  // 16 codes a piece
-            uint4 kr[X], vr[X];
+            // A thread copies its pieces of an item to a place of its own, so that only it has to
+            // wait for them; RAW items ahead cover the memory's latency.
+            unsigned char* mine = gen + (MQ + S::NB) * S::MAT + 16 * (tid - 128 * MQ);
+            const uint32_t mine_at = smem_u32(mine);
+            const int c = lane % CH, r0 = lane / CH;
+            const int most = D - 16 * c < 0 ? 0 : D - 16 * c > 16 ? 16 : D - 16 * c;
+            const uint32_t place0 = piece(32 * w + r0, 2 * c);
+            // row r0 + RPI x, element 16 c + 8 y; RPI is 4 or 8 rows
+            auto place = [&](int x, int y) { return (place0 ^ (uint32_t)(((((RPI * x) & 7) ^ y)) << 4)) + x * RPI * 128; };
             float ks = 0.0f, vs = 0.0f, ks1 = 0.0f, vs1 = 0.0f;
-            auto fetch = [&](const unsigned char* src, int64_t off, uint4 (&g)[X]) {
-#pragma unroll
-                for (int x = 0; x < X; ++x) {
-                    const int r = x * RPI + lane / CH, c = lane % CH;
-                    const int64_t o = __shfl_sync(0xffffffffu, off, r);
-                    g[x] = make_uint4(0u, 0u, 0u, 0u);
-                    if (o >= 0 && 16 * c < D) {
-                        if (16 * c + 16 <= D) {
-                            g[x] = sv::ld_nc_v4(src + o + 16 * c);
-                        } else {
-                            const uint2 h = __ldg(reinterpret_cast<const uint2*>(src + o + 16 * c));
-                            g[x].x = h.x;
-                            g[x].y = h.y;
-                        }
-                    }
-                }
-            };
             auto scales = [&](int page, int row, float& k, float& v) {
                 k = v = 0.0f;
                 if (page >= 0) {
@@ -487,111 +499,136 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     v = __ldg(a.c.v_scale + at);
                 }
             };
-            auto put = [&](int n, uint4 (&g)[X]) {
-                const int buf = n % S::NB;
-                const bool clean = (n & 1) && t.begin + (n >> 1) * TN + TN > open;
+            // The copies run ahead of the conversions: tile `ahead` is the next to be copied.
+            int ahead = 0, page2 = page, row2 = row, page3 = page1, row3 = row1;
+            int64_t off = -1;
+            auto copy = [&](int n) {
+                if (n < 2 * tiles) {
+                    if (!(n & 1)) {
+                        off = offset(page2, row2);
+                        page2 = page3;
+                        row2 = row3;
+                        ++ahead;
+                        look_up(ahead + 1, page3, row3);
+                    }
+                    const unsigned char* src = mat[n & 1] + (most ? 16 * c : 0);
+                    const uint32_t dst = mine_at + (n % S::RAW) * (S::MAT / 2);
+#pragma unroll
+                    for (int x = 0; x < X; ++x) {
+                        const int64_t o = __shfl_sync(0xffffffffu, off, x * RPI + r0);
+                        cp_async16(dst + x * 2048, src + (o < 0 ? 0 : o), o < 0 ? 0 : most);
+                    }
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            copy(0);
+            copy(1);
+            scales(page, row, ks, vs);
+            for (int n = 0; n < 2 * tiles; ++n) {
+                const int j = n >> 1, buf = n % S::NB, m = j % META;
+                copy(n + 2);
+                if (n >= S::NB) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[buf], (n / S::NB - 1) & 1));
+                    if (!ok) break;
+                }
+                const bool clean = (n & 1) && t.begin + j * TN + TN > open;
+                if (!(n & 1)) {
+                    if (t.begin + j * TN + TN > open && sv::not_finite(vs)) {
+                        vs = 0.0f;
+                        bad = true;
+                    }
+                    sh.ksc[m][32 * w + lane] = ks * a.scale_log2;
+                    sh.vsc[m][32 * w + lane] = vs;
+                    const uint32_t bits = __ballot_sync(0xffffffffu, page >= 0);
+                    if (lane == 0) sh.valid[m][w] = bits;
+                    scales(page1, row1, ks1, vs1);
+                    ks = ks1;
+                    vs = vs1;
+                    page = page1;
+                    row = row1;
+                    look_up(j + 2, page1, row1);
+                }
+                asm volatile("cp.async.wait_group 2;" ::: "memory");
                 unsigned char* dst = gen + (MQ + buf) * S::MAT;
+                const unsigned char* from = mine + (n % S::RAW) * (S::MAT / 2);
 #pragma unroll
                 for (int x = 0; x < X; ++x) {
-                    const int r = 32 * w + x * RPI + lane / CH, c = lane % CH;
-                    if (clean) bad |= sanitise<true>(g[x]);
+                    uint4 g = *reinterpret_cast<const uint4*>(from + x * 2048);
+                    if (clean) bad |= sanitise<true>(g);
                     uint4 p, q;
-                    widen16(g[x], p, q);
-                    *reinterpret_cast<uint4*>(dst + piece(r, 2 * c)) = p;
-                    *reinterpret_cast<uint4*>(dst + piece(r, 2 * c + 1)) = q;
+                    widen16(g, p, q);
+                    // lanes of a row's second 64 elements, whose banks are the first's, swap halves
+                    const int y = (c >> 2) & 1;
+                    *reinterpret_cast<uint4*>(dst + place(x, y)) = y ? q : p;
+                    *reinterpret_cast<uint4*>(dst + place(x, y ^ 1)) = y ? p : q;
                 }
+                if (clean && bad) sh.bad = 1;
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.full[buf]);
-            };
-            auto room = [&](int n) {  // waits for item n's buffer
-                if (n < S::NB) return true;
-                return (bool)__all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[n % S::NB], (n / S::NB - 1) & 1));
-            };
-            scales(page, row, ks, vs);
-            fetch(mat[0], offset(page, row), kr);
-            for (int j = 0; j < tiles && ok; ++j) {
-                const int64_t off = offset(page, row), off1 = offset(page1, row1);
-                const uint32_t bits = __ballot_sync(0xffffffffu, page >= 0);
-                fetch(mat[1], off, vr);
-                scales(page1, row1, ks1, vs1);
-                ok = room(2 * j);
-                if (!ok) break;
-                const int m = j % META;
-                if (t.begin + j * TN + TN > open && sv::not_finite(vs)) {
-                    vs = 0.0f;
-                    bad = true;
-                }
-                sh.ksc[m][32 * w + lane] = ks * a.scale_log2;
-                sh.vsc[m][32 * w + lane] = vs;
-                if (lane == 0) sh.valid[m][w] = bits;
-                put(2 * j, kr);
-                if (j + 1 < tiles) fetch(mat[0], off1, kr);
-                ok = room(2 * j + 1);
-                if (!ok) break;
-                put(2 * j + 1, vr);
-                if (bad) sh.bad = 1;
-                page = page1;
-                row = row1;
-                ks = ks1;
-                vs = vs1;
-                look_up(j + 2, page1, row1);
             }
+            cp_wait_all();
         }
         if (!ok) sh.failed = 1;
     } else {
         // ------------------------------------------------------------ products
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::R_MMA));
-        if (warp == 4 * MQ + 4 && lane == 0) {
+        if (warp == 4 * MQ + 4) {
+            const uint32_t leader = elect_one();
+            // the same in every lane, and known to be
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), sm0 = __shfl_sync(0xffffffffu, smem0, 0);
+            const int todo = __shfl_sync(0xffffffffu, tiles, 0);
+            const uint32_t ring0 = sm0 + MQ * S::MAT;
             constexpr uint32_t id_s = instruction(TN, false), id_o = instruction(DP, true);
             auto full = [&](int n) {
-                const bool there = mbar_wait_bounded(&sh.full[n % S::NB], (n / S::NB) & 1);
+                const bool there = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[n % S::NB], (n / S::NB) & 1));
                 fence_proxy_async();  // copies by other threads, seen through the barrier, before the products read them
                 return there;
             };
             auto scores = [&](int q, int n) {  // S_q = Q_q K^T, K in item n
-                const uint64_t qa = operand(smem0 + q * S::MAT, 16, 1024);
-                const uint64_t ka = operand(ring + (n % S::NB) * S::MAT, 16, 1024);
+                const uint64_t qa = operand(sm0 + q * S::MAT, 16, 1024);
+                const uint64_t ka = operand(ring0 + (n % S::NB) * S::MAT, 16, 1024);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
                     const int at = ((k >> 2) * BLK + (k & 3) * 32) >> 4;
-                    mma_ss(tmem + S::S_COL + 128 * q, qa + at, ka + at, id_s, k > 0);
+                    mma_ss(tm + S::S_COL + 128 * q, qa + at, ka + at, id_s, k > 0, leader);
                 }
-                tc_commit(&sh.s_full[q]);
+                tc_commit(&sh.s_full[q], leader);
             };
             ok = full(0);
             tc_fence_after();
             if (ok) {
+                #pragma unroll
                 for (int q = 0; q < MQ; ++q) scores(q, 0);
-                tc_commit(&sh.empty[0]);
+                tc_commit(&sh.empty[0], leader);
             }
-            for (int j = 0; j < tiles && ok; ++j) {
+            for (int j = 0; j < todo && ok; ++j) {
                 const int nv = 2 * j + 1, nk = 2 * j + 2;
                 ok = full(nv);
-                const uint64_t va = operand(ring + (nv % S::NB) * S::MAT, BLK, 1024);
+                const uint64_t va = operand(ring0 + (nv % S::NB) * S::MAT, BLK, 1024);
                 for (int q = 0; q < MQ && ok; ++q) {
-                    ok = mbar_wait_bounded(&sh.p_full[q], j & 1);
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.p_full[q], j & 1));
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < TN / 16; ++k)
-                        mma_ts(tmem + S::O_COL + DP * q, tmem + S::S_COL + 128 * q + 8 * k,
-                               va + k * (2048 >> 4), id_o, j > 0 || k > 0);
-                    if (j + 1 < tiles) {
+                        mma_ts(tm + S::O_COL + DP * q, tm + S::S_COL + 128 * q + 8 * k,
+                               va + k * (2048 >> 4), id_o, j > 0 || k > 0, leader);
+                    if (j + 1 < todo) {
                         if (q == 0) ok = full(nk);
                         if (ok) scores(q, nk);
                     } else {
-                        tc_commit(&sh.o_full[q]);
+                        tc_commit(&sh.o_full[q], leader);
                     }
                 }
                 if (ok) {
-                    tc_commit(&sh.empty[nv % S::NB]);
-                    if (j + 1 < tiles) tc_commit(&sh.empty[nk % S::NB]);
+                    tc_commit(&sh.empty[nv % S::NB], leader);
+                    if (j + 1 < todo) tc_commit(&sh.empty[nk % S::NB], leader);
                 }
             }
             if (!ok) {
                 sh.failed = 1;
-                tc_commit(&sh.drain);  // whatever was issued ends before the memory is given back
+                tc_commit(&sh.drain, leader);  // whatever was issued ends before the memory is given back
                 (void)mbar_wait_bounded(&sh.drain, 0);
             }
         }
