@@ -100,7 +100,7 @@ __device__ __forceinline__ int v_piece(int r, int c) {  // eight rows are read t
 
 template <int DP, int MW, int MT, bool E4M3>
 __global__ void __launch_bounds__(MW* KW * 32, (MW * MT * 16 == 64 || DP == 256) ? 1 : 2)
-    paged_attention_kernel(const __grid_constant__ AttnArgs a) {
+    paged_attention_kernel(const __grid_constant__ AttnArgs a, const int pairs) {
     using S = Shape<DP, MW, MT, E4M3>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t s_off[RING][TN];  // byte offset of each position's row, -1: nothing there
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(MW* KW * 32, (MW * MT * 16 == 64 || DP == 256)
     pdl_trigger();
     pdl_wait();
     AttnTile t;
-    if (!sv::attn_tile(a, blockIdx.x, S::ROWS, t)) return;
+    if (!sv::attn_tile(a, pairs, blockIdx.x, S::ROWS, t)) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wk = warp % KW, wm = warp / KW;
     const int D = a.c.dim, row_bytes = D * S::ES;
     const int tiles = (t.end - t.begin + TN - 1) / TN;
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(MW* KW * 32, (MW * MT * 16 == 64 || DP == 256)
             const int R = t.mt * S::ROWS + wm * MT * 16 + 16 * m + g + 8 * y;
             if (R >= t.n * a.group) continue;
             const int64_t row = sv::attn_row(a, t, R);
-            const int64_t part = row * a.splits + t.split;
+            const int64_t part = t.part + R - t.mt * S::ROWS;
             if (t4 == 0) {
                 if (t.active > 1) a.part_lse[part] = lse2[m][y];
                 else if (a.lse) a.lse[row] = lse2[m][y] * 0.69314718055994531f;
@@ -529,41 +529,43 @@ __global__ void __launch_bounds__(MW* KW * 32, (MW * MT * 16 == 64 || DP == 256)
         }
 }
 
-// Joins the splits of a row: weights 2^(lse_s - max), one warp per (b, query, head).
-__global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_constant__ AttnArgs a, int64_t rows,
-                                                                   int tile_rows) {
+// Joins the splits of a row: weights 2^(lse_s - max), one warp per row of the split tiles.
+__global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_constant__ AttnArgs a, int pairs,
+                                                                   int tile_rows, int64_t rows) {
     pdl_trigger();
     pdl_wait();
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    if (row >= rows) return;
-    const int h = (int)(row % a.Hq), i = (int)(row / a.Hq % a.Q), b = (int)(row / ((int64_t)a.Hq * a.Q));
+    if (at >= rows) return;
+    const int rest = (int)(at / tile_rows), r = (int)(at - (int64_t)rest * tile_rows);
+    const sv::AttnPlace p = sv::attn_place(a, pairs, (unsigned)(a.whole + rest));
     int base, n;
-    if (!sv::paged_row(a.c, a.base, a.new_len, b, a.Q, base, n) || i >= n) return;
-    const int mt = (i * a.group + h % a.group) / tile_rows;
-    const int end = sv::attn_tile_end(base, n, a.group, mt, tile_rows, a.tree_mask != nullptr);
-    int active = (end + a.chunk - 1) / a.chunk;
-    if (active > a.splits) active = a.splits;
+    if (!sv::paged_row(a.c, a.base, a.new_len, p.b, a.Q, base, n)) return;
+    const int64_t R = (int64_t)p.mt * tile_rows + r;
+    if (R >= (int64_t)n * a.group) return;
+    const int active = sv::attn_active(a, sv::attn_tile_end(base, n, a.group, p.mt, tile_rows, a.tree_mask != nullptr));
     if (active <= 1) return;  // written by the one CTA that had the row
-    const float* lse = a.part_lse + row * a.splits;
+    const int64_t row = ((int64_t)p.b * a.Q + R / a.group) * a.Hq + p.h * a.group + R % a.group;
+    const int64_t part = (int64_t)rest * a.splits * tile_rows + r;  // of split 0; the next ones tile_rows apart
+    const int D = a.c.dim;
+    const float* lse = a.part_lse + part;
     float top = neg_inf();
-    for (int s = lane; s < active; s += 32) top = fmaxf(top, lse[s]);
+    for (int s = lane; s < active; s += 32) top = fmaxf(top, lse[(int64_t)s * tile_rows]);
 #pragma unroll
     for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
     const float shift = top == neg_inf() ? 0.0f : top;
     float sum = 0.0f;
-    for (int s = lane; s < active; s += 32) sum += sv::ex2(lse[s] - shift);
+    for (int s = lane; s < active; s += 32) sum += sv::ex2(lse[(int64_t)s * tile_rows] - shift);
 #pragma unroll
     for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int D = a.c.dim;
     for (int d = 4 * lane; d < D; d += 128) {
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const float* p = a.part_o + row * a.splits * D + d;
+        const float* from = a.part_o + part * D + d;
 #pragma unroll 4
         for (int s = 0; s < active; ++s) {
-            const float w = sv::ex2(lse[s] - shift) * inv;
-            const float4 v = *reinterpret_cast<const float4*>(p + (int64_t)s * D);
+            const float w = sv::ex2(lse[(int64_t)s * tile_rows] - shift) * inv;
+            const float4 v = *reinterpret_cast<const float4*>(from + (int64_t)s * tile_rows * D);
             acc.x += w * v.x;
             acc.y += w * v.y;
             acc.z += w * v.z;
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_
 }
 
 template <int DP, int MW, int MT, bool E4M3>
-cudaError_t launch_shape(const AttnArgs& a, unsigned ctas, cudaStream_t stream) {
+cudaError_t launch_shape(const AttnArgs& a, int pairs, unsigned ctas, cudaStream_t stream) {
     using S = Shape<DP, MW, MT, E4M3>;
     static sv::KernelLaunchCache cache;
     auto kern = paged_attention_kernel<DP, MW, MT, E4M3>;
@@ -584,17 +586,17 @@ cudaError_t launch_shape(const AttnArgs& a, unsigned ctas, cudaStream_t stream) 
     const cudaError_t e = cache.setup((const void*)kern, &max_dyn);
     if (e != cudaSuccess) return e;
     if (S::SMEM > max_dyn) return cudaErrorInvalidValue;
-    return sv::launch_serial(kern, dim3(ctas), dim3(S::THREADS), S::SMEM, stream, a);
+    return sv::launch_serial(kern, dim3(ctas), dim3(S::THREADS), S::SMEM, stream, a, pairs);
 }
 
 template <int DP, bool E4M3>
-cudaError_t launch_rows(const AttnArgs& a, int tile_rows, unsigned ctas, cudaStream_t stream) {
-    if (tile_rows == 16) return launch_shape<DP, 1, 1, E4M3>(a, ctas, stream);
+cudaError_t launch_rows(const AttnArgs& a, int pairs, int tile_rows, unsigned ctas, cudaStream_t stream) {
+    if (tile_rows == 16) return launch_shape<DP, 1, 1, E4M3>(a, pairs, ctas, stream);
     if constexpr (DP == 256) {
-        return launch_shape<DP, 2, 1, E4M3>(a, ctas, stream);
+        return launch_shape<DP, 2, 1, E4M3>(a, pairs, ctas, stream);
     } else {
-        if (tile_rows == 32) return launch_shape<DP, 1, 2, E4M3>(a, ctas, stream);
-        return launch_shape<DP, 2, 2, E4M3>(a, ctas, stream);
+        if (tile_rows == 32) return launch_shape<DP, 1, 2, E4M3>(a, pairs, ctas, stream);
+        return launch_shape<DP, 2, 2, E4M3>(a, pairs, ctas, stream);
     }
 }
 
@@ -603,7 +605,7 @@ constexpr int kMaxQ = 65536;
 
 struct Plan {
     int tile_rows, m_tiles, splits, chunk;
-    int64_t ctas;
+    int64_t tiles, whole, ctas;
     size_t ws;
 };
 
@@ -616,21 +618,30 @@ Plan make_plan(int B, int Q, int Hq, int H, int D, int max_len, int num_sms) {
     if (D > 128) p.tile_rows = rows <= 16 ? 16 : 32;
     else p.tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
     p.m_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
-    const int64_t tiles = (int64_t)B * H * p.m_tiles;
-    // Enough CTAs that rows of unequal length even out: four per SM, or for the large tiles,
-    // one of which fills an SM, three where there are not two already.
-    const bool large = p.tile_rows >= 128;
-    int64_t splits = !large ? (4LL * num_sms + tiles - 1) / tiles : tiles < 2LL * num_sms ? 3LL * num_sms / tiles : 1;
-    const int64_t most = large ? ((int64_t)max_len + 1023) / 1024 : ((int64_t)max_len + 127) / 128;
-    if (splits > most) splits = most;
-    if (splits > 512) splits = 512;
+    p.tiles = (int64_t)B * H * p.m_tiles;
+    const bool large = p.tile_rows >= 128;  // one such CTA fills an SM
+    const int tn = large ? 128 : TN;        // positions per tile of the kernel taken
+    // Enough CTAs that rows of unequal length even out: four per SM.  Large tiles: three per
+    // SM where there are fewer tiles than SMs; else whole waves of tiles, and what is left
+    // over split so that it fills the last wave.
+    int64_t splits;
+    if (!large) {
+        splits = (4LL * num_sms + p.tiles - 1) / p.tiles;
+    } else if (p.tiles < num_sms) {
+        splits = 3LL * num_sms / p.tiles;
+    } else {
+        p.whole = p.tiles / num_sms * num_sms;
+        splits = p.tiles > p.whole ? num_sms / (p.tiles - p.whole) : 1;
+    }
+    const int64_t least = large ? 1024 : 128;  // positions worth a CTA
+    if (splits > ((int64_t)max_len + least - 1) / least) splits = ((int64_t)max_len + least - 1) / least;
+    if (splits > 256) splits = 256;
     if (splits < 1) splits = 1;
-    const int tn = p.tile_rows >= 128 ? 128 : TN;  // positions per tile of the kernel taken
-    const int64_t chunk = (((int64_t)max_len + splits - 1) / splits + tn - 1) / tn * tn;
-    p.chunk = (int)chunk;
-    p.splits = (int)(((int64_t)max_len + chunk - 1) / chunk);
-    p.ctas = tiles * p.splits;
-    p.ws = p.splits > 1 ? (size_t)B * Q * Hq * p.splits * (D + 1) * sizeof(float) : 0;
+    p.chunk = (int)((((int64_t)max_len + splits - 1) / splits + tn - 1) / tn * tn);
+    p.splits = (int)(((int64_t)max_len + p.chunk - 1) / p.chunk);
+    if (p.splits <= 1) p.whole = p.tiles;
+    p.ctas = p.whole + (p.tiles - p.whole) * p.splits;
+    p.ws = (size_t)(p.tiles - p.whole) * p.splits * p.tile_rows * (D + 1) * sizeof(float);
     return p;
 }
 
@@ -681,10 +692,11 @@ sv_status spec_paged_attention(const void* q, const int64_t* q_stride, int num_q
     const int sms = sm_count();
     if (!sms) return sv::launch_status(cudaErrorInvalidDevice);
     Plan p = make_plan(B, Q, num_q_heads, cache->num_heads, D, max_len, sms);
-    if (p.splits > 1 && (!workspace || ws_bytes < p.ws || (uintptr_t)workspace % 16)) {
-        p.ctas /= p.splits;
+    if (p.ws && (!workspace || ws_bytes < p.ws || (uintptr_t)workspace % 16)) {
+        p.whole = p.ctas = p.tiles;
         p.splits = 1;
         p.chunk = sv::PAGED_MAX_POS;
+        p.ws = 0;
     }
     if (p.ctas >= ((int64_t)1 << 31)) return SV_ERR_UNSUPPORTED;
     a.q = static_cast<const uint16_t*>(q);
@@ -700,23 +712,26 @@ sv_status spec_paged_attention(const void* q, const int64_t* q_stride, int num_q
     a.group = num_q_heads / cache->num_heads;
     a.mask_words = (Q - 1 + 31) / 32;
     a.m_tiles = p.m_tiles;
+    a.whole = (int)p.whole;
     a.splits = p.splits;
     a.chunk = p.chunk;
     a.out = static_cast<uint16_t*>(out);
     a.lse = out_lse;
-    const int64_t rows = (int64_t)B * Q * num_q_heads;
+    const int64_t rows = p.ws ? (p.tiles - p.whole) * p.tile_rows : 0;  // of the split tiles
     a.part_o = static_cast<float*>(workspace);
-    a.part_lse = p.splits > 1 ? a.part_o + rows * p.splits * D : nullptr;
+    a.part_lse = p.ws ? a.part_o + rows * p.splits * D : nullptr;
     cudaStream_t s = (cudaStream_t)stream;
     const bool e4m3 = cache->dtype == SV_CACHE_E4M3;
+    const int pairs = B * cache->num_heads;
+    const unsigned ctas = (unsigned)p.ctas;
     cudaError_t e;
-    if (p.tile_rows >= 128) e = sv::launch_attn_tc(a, e4m3, p.tile_rows, (unsigned)p.ctas, s);
-    else if (D <= 64) e = e4m3 ? launch_rows<64, true>(a, p.tile_rows, (unsigned)p.ctas, s) : launch_rows<64, false>(a, p.tile_rows, (unsigned)p.ctas, s);
-    else if (D <= 128) e = e4m3 ? launch_rows<128, true>(a, p.tile_rows, (unsigned)p.ctas, s) : launch_rows<128, false>(a, p.tile_rows, (unsigned)p.ctas, s);
-    else e = e4m3 ? launch_rows<256, true>(a, p.tile_rows, (unsigned)p.ctas, s) : launch_rows<256, false>(a, p.tile_rows, (unsigned)p.ctas, s);
-    if (e == cudaSuccess && p.splits > 1)
-        e = sv::launch_serial(paged_attention_join_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a, rows,
-                              p.tile_rows);
+    if (p.tile_rows >= 128) e = sv::launch_attn_tc(a, pairs, e4m3, p.tile_rows, ctas, s);
+    else if (D <= 64) e = e4m3 ? launch_rows<64, true>(a, pairs, p.tile_rows, ctas, s) : launch_rows<64, false>(a, pairs, p.tile_rows, ctas, s);
+    else if (D <= 128) e = e4m3 ? launch_rows<128, true>(a, pairs, p.tile_rows, ctas, s) : launch_rows<128, false>(a, pairs, p.tile_rows, ctas, s);
+    else e = e4m3 ? launch_rows<256, true>(a, pairs, p.tile_rows, ctas, s) : launch_rows<256, false>(a, pairs, p.tile_rows, ctas, s);
+    if (e == cudaSuccess && rows)
+        e = sv::launch_serial(paged_attention_join_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a, pairs,
+                              p.tile_rows, rows);
     return sv::launch_status(e);
 }
 

@@ -20,18 +20,35 @@ struct AttnArgs {
     const uint32_t* tree_mask; // [B][Q-1][mask_words] or nullptr
     float scale_log2;          // scale * log2(e)
     int Q, Hq, group, mask_words;
-    int m_tiles, splits, chunk; // chunk: positions per split (the last split takes what remains)
+    int m_tiles;               // tiles of query rows per (batch row, cache head)
+    int whole;                 // tiles [0, whole) are not split, the others `splits` ways
+    int splits, chunk;         // chunk: positions per split (the last split takes what remains)
     uint16_t* out;             // [B][Q][Hq][D] bf16
     float* lse;                // [B][Q][Hq] or nullptr
-    float* part_o;             // [B][Q][Hq][splits][D] fp32, splits > 1
-    float* part_lse;           // [B][Q][Hq][splits], base 2
+    float* part_o;             // [split tile][split][row of the tile][D] fp32
+    float* part_lse;           // [split tile][split][row of the tile], base 2
 };
+
+// Tiles are numbered with the last row tiles first: a chain's late queries see most
+// positions, so the long tiles start first and the short ones, which are split, end.
+struct AttnPlace {
+    int b, h, mt;
+};
+__device__ __forceinline__ AttnPlace attn_place(const AttnArgs& a, int pairs, unsigned tile) {
+    AttnPlace p;
+    const int pair = (int)(tile % (unsigned)pairs);
+    p.mt = a.m_tiles - 1 - (int)(tile / (unsigned)pairs);
+    p.h = pair % a.c.heads;
+    p.b = pair / a.c.heads;
+    return p;
+}
 
 struct AttnTile {
     int b, h, mt, split;
     int base, n;       // positions before the chunk, real queries
     int begin, end;    // this CTA's positions
     int active;        // splits of this row tile that have positions
+    int64_t part;      // first row of this CTA's partial results
 };
 
 // End of the positions that rows [0, last query of the tile] can see.
@@ -42,19 +59,26 @@ __host__ __device__ __forceinline__ int attn_tile_end(int base, int n, int group
     return base + last + 1;
 }
 
-// The work of CTA `id`; false where it has none.
-__device__ __forceinline__ bool attn_tile(const AttnArgs& a, unsigned id, int tile_rows, AttnTile& t) {
-    t.mt = (int)(id % (unsigned)a.m_tiles);
-    unsigned rest = id / (unsigned)a.m_tiles;
-    t.split = (int)(rest % (unsigned)a.splits);
-    rest /= (unsigned)a.splits;
-    t.h = (int)(rest % (unsigned)a.c.heads);
-    t.b = (int)(rest / (unsigned)a.c.heads);
+// Splits of a row tile that have positions.
+__device__ __forceinline__ int attn_active(const AttnArgs& a, int end) {
+    const int n = (end + a.chunk - 1) / a.chunk;
+    return n < a.splits ? n : a.splits;
+}
+
+// The work of CTA `id` (pairs: batch rows times cache heads); false where it has none.
+__device__ __forceinline__ bool attn_tile(const AttnArgs& a, int pairs, unsigned id, int tile_rows, AttnTile& t) {
+    const bool whole = id < (unsigned)a.whole;
+    const unsigned rest = id - (unsigned)a.whole;
+    const AttnPlace p = attn_place(a, pairs, whole ? id : (unsigned)a.whole + rest / (unsigned)a.splits);
+    t.b = p.b;
+    t.h = p.h;
+    t.mt = p.mt;
+    t.split = whole ? 0 : (int)(rest % (unsigned)a.splits);
+    t.part = whole ? 0 : (int64_t)rest * tile_rows;
     if (!paged_row(a.c, a.base, a.new_len, t.b, a.Q, t.base, t.n)) return false;
     if ((int64_t)t.mt * tile_rows >= (int64_t)t.n * a.group) return false;
     const int end = attn_tile_end(t.base, t.n, a.group, t.mt, tile_rows, a.tree_mask != nullptr);
-    t.active = (end + a.chunk - 1) / a.chunk;
-    if (t.active > a.splits) t.active = a.splits;
+    t.active = whole ? 1 : attn_active(a, end);
     if (t.split >= t.active) return false;
     t.begin = t.split * a.chunk;
     t.end = t.split == t.active - 1 ? end : t.begin + a.chunk;
@@ -104,6 +128,6 @@ __device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) < pos_in
 
 // The kernel for many query rows per cache head, head_dim <= 128 (sv_attention_tc.cu):
 // tile_rows 128 or 256.
-cudaError_t launch_attn_tc(const AttnArgs& a, bool e4m3, int tile_rows, unsigned ctas, cudaStream_t stream);
+cudaError_t launch_attn_tc(const AttnArgs& a, int pairs, bool e4m3, int tile_rows, unsigned ctas, cudaStream_t stream);
 
 }  // namespace sv

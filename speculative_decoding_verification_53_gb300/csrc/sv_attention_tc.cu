@@ -7,8 +7,12 @@
 // S, and O += P V accumulates in TMEM with P read from TMEM and V from shared memory in
 // its stored order (positions x elements, "MN-major").  Roles:
 //   warps 0 .. 4 MQ - 1   softmax, one thread per query row, one warpgroup per row tile
-//   the next four warps   producers: keys and values into a ring of NB shared buffers
-//   the last four         one thread issues every tcgen05.mma (a whole warpgroup gives its registers up)
+//   the next four         keys and values into a ring of NB shared buffers, where the copy
+//                         engine cannot do it alone (odd page sizes; e4m3 codes, widened to
+//                         bf16; values that are not finite taken out where hidden in part)
+//   one warp each         the products (one lane issues every tcgen05.mma), the copy engine's
+//                         requests, and notes on each tile (holes, scales); a fourth idles to
+//                         make the warpgroup whole
 // While one row tile's softmax runs, the tensor cores work on the other's products.
 // Dependences: full/empty barriers per buffer; s_full (S is in TMEM, and so is the last
 // O, since a commit covers every earlier product); p_full (P is written, O rescaled).
@@ -20,6 +24,8 @@
 // Every wait is bounded; a CTA whose wait runs out writes NaN for its rows, which a verify
 // reports as invalid data, and frees its TMEM.
 #include <cstdint>
+
+#include <cuda.h>
 
 #include "spec_paged_kv.h"
 #include "sv_attention.cuh"
@@ -50,9 +56,11 @@ struct Tc {
     static constexpr int THREADS = SOFTMAX + 256;  // whole warpgroups, as setmaxnreg wants
     // Registers: the launch gives every thread 65536 / THREADS; softmax threads hold a row of
     // 128 scores and take what the others give back.
-    //   MQ = 2: 512 x 128 = 65536 >= 256 x 184 + 128 x 96 + 128 x 40 = 64512
-    //   MQ = 1: 384 x 168 = 64512 >= 128 x 216 + 128 x 136 + 128 x 40 = 50176
-    static constexpr int R_SOFTMAX = MQ == 2 ? 184 : 216, R_LOAD = MQ == 2 ? 96 : 136, R_MMA = 40;
+    //   MQ = 2: 512 x 128 = 65536 = 256 x 184 + 128 x 80 + 128 x 64 (bf16) = 256 x 176 + 128 x 96 + 128 x 64
+    //   MQ = 1: 384 x 168 = 64512 >= 128 x 216 + 128 x 136 + 128 x 64 = 53248
+    static constexpr int R_SOFTMAX = MQ == 1 ? 216 : E4M3 ? 176 : 184;
+    static constexpr int R_LOAD = MQ == 1 ? 136 : E4M3 ? 96 : 80, R_MMA = 64;
+    static_assert(SOFTMAX * R_SOFTMAX + 128 * (R_LOAD + R_MMA) <= (MQ == 2 ? 65536 : 64512), "registers of the launch");
     static constexpr int MAT = (DP / 64) * BLK;   // a tile of keys, values or queries
     static constexpr int NB = DP == 64 ? 6 : E4M3 ? 3 : 4;   // buffers of the ring
     static constexpr int RAW = E4M3 ? 3 : 0;      // e4m3: items whose codes are in flight
@@ -141,6 +149,18 @@ __host__ __device__ constexpr uint32_t instruction(int n, bool b_mn) {
     return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
 }
 
+// One box of a page (64 or DP elements x rows of one head) by the copy engine; a page
+// outside the cache reads as zeros.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int row, int head, int page, uint64_t* bar) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+                 "l"(map), "r"(x), "r"(row), "r"(head), "r"(page), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -165,9 +185,10 @@ __device__ __forceinline__ void widen16(uint4 w, uint4& a, uint4& b) {
     uint32_t out[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        // a code has 3 bits of mantissa: its bf16 is the upper half of its fp32 (NaN too)
         const float2 lo = sv::e4m3x2_to_f32(in[i] & 0xffffu), hi = sv::e4m3x2_to_f32(in[i] >> 16);
-        out[2 * i] = sv::bf16x2(lo.x, lo.y);
-        out[2 * i + 1] = sv::bf16x2(hi.x, hi.y);
+        out[2 * i] = __byte_perm(__float_as_uint(lo.x), __float_as_uint(lo.y), 0x7632);
+        out[2 * i + 1] = __byte_perm(__float_as_uint(hi.x), __float_as_uint(hi.y), 0x7632);
     }
     a = make_uint4(out[0], out[1], out[2], out[3]);
     b = make_uint4(out[4], out[5], out[6], out[7]);
@@ -212,12 +233,18 @@ __device__ __forceinline__ void scale_scores(uint32_t v[TN], const uint32_t see[
 __device__ __forceinline__ float largest(const uint32_t v[TN]) {
     float t[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
-    for (int k = 0; k < TN; ++k) t[k & 3] = fmaxf(t[k & 3], __uint_as_float(v[k]));
+    for (int k = 0; k < TN; k += 2) {
+        float& m = t[(k >> 1) & 3];
+        asm("max.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(__uint_as_float(v[k])), "f"(__uint_as_float(v[k + 1])));
+    }
     return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
 }
 
 struct __align__(16) Shared {
-    uint64_t full[8], empty[8], s_full[2], p_full[2], o_full[2], drain;
+    uint64_t full[8], empty[8];              // the ring's buffers
+    uint64_t q_full, s_full[2], p_full[2][2], o_full[2], drain;
+    uint64_t land[8], raw_full[4], raw_empty[4];  // copy engine: values to be looked over; e4m3 codes
+    uint64_t note_full[META], note_empty[META];   // the tiles' notes below
     uint32_t tmem;
     int bad, failed;
     uint32_t valid[META][4];       // which of the tile's positions hold something
@@ -226,14 +253,15 @@ struct __align__(16) Shared {
 };
 
 template <int DP, int MQ, bool E4M3>
-__global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap k_map,
+                              const __grid_constant__ CUtensorMap v_map, const int box_rows, const int pairs) {
     using S = Tc<DP, MQ, E4M3>;
     extern __shared__ unsigned char raw[];
     __shared__ Shared sh;
     pdl_trigger();
     pdl_wait();
     AttnTile t;
-    if (!sv::attn_tile(a, blockIdx.x, S::ROWS, t)) return;
+    if (!sv::attn_tile(a, pairs, blockIdx.x, S::ROWS, t)) return;
     const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;  // queries, then the ring
     unsigned char* gen = raw + (smem0 - smem_u32(raw));       // the same place, generic
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -245,29 +273,30 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
     if (warp == 0) tmem_alloc(&sh.tmem, S::COLS);
     if (tid == 0) {
         for (int i = 0; i < S::NB; ++i) {
-            mbar_init(&sh.full[i], E4M3 ? 4 : 128);  // warps, or threads, that fill a buffer
+            mbar_init(&sh.full[i], E4M3 || box_rows ? 4 : 128);  // warps, or threads, that fill a buffer
             mbar_init(&sh.empty[i], 1);
+            mbar_init(&sh.land[i], 1);
+        }
+        for (int i = 0; i < META; ++i) {
+            mbar_init(&sh.note_full[i], 1);
+            mbar_init(&sh.note_empty[i], 4 * MQ);
         }
         for (int i = 0; i < MQ; ++i) {
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_full[i], 4);
+            mbar_init(&sh.p_full[i][0], 4);
+            mbar_init(&sh.p_full[i][1], 4);
             mbar_init(&sh.o_full[i], 1);
         }
+        mbar_init(&sh.q_full, 4 * MQ);
         mbar_init(&sh.drain, 1);
+        for (int i = 0; i < S::RAW; ++i) {
+            mbar_init(&sh.raw_full[i], 1);
+            mbar_init(&sh.raw_empty[i], 4);
+        }
         sh.bad = 0;
         sh.failed = 0;
         sv::fence_mbar_init();
     }
-    // the queries, zero behind the last real one
-    for (int f = tid; f < S::ROWS * (DP / 8); f += S::THREADS) {
-        const int r = f / (DP / 8), c = f % (DP / 8), R = t.mt * S::ROWS + r;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (R < rows && 8 * c < D)
-            w = sv::ld_nc_v4(a.q + t.b * a.q_sb + (int64_t)(R / a.group) * a.q_st +
-                             (int64_t)(t.h * a.group + R % a.group) * a.q_sh + 8 * c);
-        *reinterpret_cast<uint4*>(gen + (r >> 7) * S::MAT + piece(r & 127, c)) = w;
-    }
-    fence_proxy_async();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -279,6 +308,24 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         // ------------------------------------------------------------ softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::R_SOFTMAX));
         const int q = warp >> 2;
+        {   // the queries of this warp's rows, zero behind the last real one
+            constexpr int CH = DP / 8, RPI = 32 / CH, X = 32 / RPI;
+            const int c = lane % CH, r0 = (warp & 3) * 32 + lane / CH;
+            uint4 w[X];  // every load in flight before the first store
+#pragma unroll
+            for (int x = 0; x < X; ++x) {
+                const int R = t.mt * S::ROWS + q * 128 + r0 + x * RPI;
+                w[x] = make_uint4(0u, 0u, 0u, 0u);
+                if (R < rows && 8 * c < D)
+                    w[x] = sv::ld_nc_v4(a.q + t.b * a.q_sb + (int64_t)(R / a.group) * a.q_st +
+                                        (int64_t)(t.h * a.group + R % a.group) * a.q_sh + 8 * c);
+            }
+#pragma unroll
+            for (int x = 0; x < X; ++x) *reinterpret_cast<uint4*>(gen + q * S::MAT + piece(r0 + x * RPI, c)) = w[x];
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.q_full);
+        }
         const int R = t.mt * S::ROWS + q * 128 + (warp & 3) * 32 + lane;
         const bool live = R < rows;
         const int i = live ? R / a.group : 0;
@@ -291,6 +338,8 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             if (!ok) break;
             tc_fence_after();
             const int tile0 = t.begin + j * TN, m = j % META;
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.note_full[m], (j / META) & 1));
+            if (!ok) break;
             uint32_t see[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) see[c] = sh.valid[m][c];
@@ -355,29 +404,39 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     p[(k >> 1) + 1] = sv::bf16x2(f.x, f.y);
                 }
                 tmem_st16(s_at + 16 * c, p);  // over S, which this warp has read
+                if (c & 1) {  // half of the row: its product may start
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.p_full[q][c >> 1]);
+                }
             }
+            if (lane == 0) mbar_arrive(&sh.note_empty[m]);
             sum0 = sv::fadd2(sum0, sum1);
             l += sum0.x + sum0.y;
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[q]);
         }
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.o_full[q], 0));
         if (!ok) sh.failed = 1;
         tc_fence_after();
         const float inv = !ok ? __int_as_float(0x7fffffff) : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
         const float lse2 = !ok ? inv : l == 0.0f ? neg_inf() : mx + log2f(l);
-        const int64_t row = live ? sv::attn_row(a, t, R) : 0, part = row * a.splits + t.split;
+        const int64_t row = live ? sv::attn_row(a, t, R) : 0, part = t.part + (R - t.mt * S::ROWS);
         if (live) {
             if (t.active > 1) a.part_lse[part] = lse2;
             else if (a.lse) a.lse[row] = lse2 * 0.69314718055994531f;
         }
         const bool patch = ok && sh.bad != 0;
-        for (int c = 0; c < DP / 32; ++c) {
-            uint32_t v[32];
+        // Rows leave through shared memory (where this row tile's queries were), so that a store
+        // covers whole rows: a lane writing its own row touched 32 lines per store and cost
+        // 15000 cycles a CTA.  Half a row at a time, 16-byte pieces swizzled by the row.
+        constexpr int CW = DP / 2, PC = CW / 4;
+        float4* stage = reinterpret_cast<float4*>(gen + q * S::MAT + (warp & 3) * (S::MAT / 4));
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+            uint32_t v[CW];
             __syncwarp();
-            tmem_ld32(o_at + 32 * c, v);
+#pragma unroll
+            for (int z = 0; z < CW; z += 32) tmem_ld32(o_at + CW * c + z, v + z);
             tc_wait_ld();
             if (live && patch) {
                 // values that are not finite, for the queries that see them
@@ -385,176 +444,186 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 if (open > t.begin) from += (open - t.begin) / TN * TN;
                 for (int pos = from; pos < t.end; ++pos) {
                     if (!(sv::attn_visible(a, t, i, pos) & 1u)) continue;
-                    for (int k = 0; k < 32 && 32 * c + k < D; ++k) {
-                        const float w = sv::attn_value<E4M3>(a, t, pos, 32 * c + k);
-                        if (sv::not_finite(w)) {
 #pragma unroll
-                            for (int z = 0; z < 32; ++z)
-                                if (z == k) v[z] = __float_as_uint(__uint_as_float(v[z]) + w);
-                        }
+                    for (int k = 0; k < CW; ++k) {
+                        if (CW * c + k >= D) break;
+                        const float w = sv::attn_value<E4M3>(a, t, pos, CW * c + k);
+                        if (sv::not_finite(w)) v[k] = __float_as_uint(__uint_as_float(v[k]) + w);
                     }
                 }
             }
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-                if (!live || 32 * c + k >= D) break;
-                float f[8];
-#pragma unroll
-                for (int z = 0; z < 8; ++z) f[z] = __uint_as_float(v[k + z]) * inv;
-                if (t.active > 1) {
-                    float4* to = reinterpret_cast<float4*>(a.part_o + part * D + 32 * c + k);
-                    to[0] = make_float4(f[0], f[1], f[2], f[3]);
-                    to[1] = make_float4(f[4], f[5], f[6], f[7]);
-                } else {
-                    *reinterpret_cast<uint4*>(a.out + row * D + 32 * c + k) = make_uint4(
-                        sv::bf16x2(f[0], f[1]), sv::bf16x2(f[2], f[3]), sv::bf16x2(f[4], f[5]), sv::bf16x2(f[6], f[7]));
+            for (int k = 0; k < PC; ++k)
+                stage[PC * lane + (k ^ (lane & (PC - 1)))] =
+                    make_float4(__uint_as_float(v[4 * k]) * inv, __uint_as_float(v[4 * k + 1]) * inv,
+                                __uint_as_float(v[4 * k + 2]) * inv, __uint_as_float(v[4 * k + 3]) * inv);
+            __syncwarp();
+            if (t.active > 1) {
+                const int k = lane % PC, d = CW * c + 4 * k;
+                for (int x = 0; x < PC; ++x) {
+                    const int r = (32 / PC) * x + lane / PC;
+                    const int64_t to = __shfl_sync(0xffffffffu, live ? part : (int64_t)-1, r);
+                    if (to >= 0 && d < D)
+                        *reinterpret_cast<float4*>(a.part_o + to * D + d) = stage[PC * r + (k ^ (r & (PC - 1)))];
+                }
+            } else {
+                const int k = 2 * (lane % (PC / 2)), d = CW * c + 4 * k;
+                for (int x = 0; x < PC / 2; ++x) {
+                    const int r = (64 / PC) * x + lane / (PC / 2);
+                    const int64_t to = __shfl_sync(0xffffffffu, live ? row : (int64_t)-1, r);
+                    if (to >= 0 && d < D) {
+                        const float4 f = stage[PC * r + (k ^ (r & (PC - 1)))], g = stage[PC * r + ((k + 1) ^ (r & (PC - 1)))];
+                        *reinterpret_cast<uint4*>(a.out + to * D + d) =
+                            make_uint4(sv::bf16x2(f.x, f.y), sv::bf16x2(f.z, f.w), sv::bf16x2(g.x, g.y), sv::bf16x2(g.z, g.w));
+                    }
                 }
             }
         }
     } else if (warp < 4 * MQ + 4) {
         // ---------------------------------------------------------- producers
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::R_LOAD));
-        // Warp w copies rows 32 w .. 32 w + 31 of every tile; a lane looks up its row's place.
+        // Warp w fills rows 32 w .. 32 w + 31 of every tile.  With the copy engine it only looks
+        // bf16 values over where some queries see them in part, or widens e4m3 codes; without,
+        // it copies the rows, a lane looking up the place of one.
         const int w = warp - 4 * MQ;
         const unsigned char* mat[2] = {a.c.k + t.h * a.c.head_stride, a.c.v + t.h * a.c.head_stride};
-        auto look_up = [&](int tile, int& page, int& row) {
+        auto look_up = [&](int tile) {
             const int pos = t.begin + tile * TN + 32 * w + lane;
-            page = -1;
-            row = 0;
-            if (tile < tiles && pos < t.end) page = sv::paged_place(a.c, t.b, pos, row);
-        };
-        auto offset = [&](int page, int row) {
+            if (box_rows || tile >= tiles || pos >= t.end) return (int64_t)-1;
+            int row;
+            const int page = sv::paged_place(a.c, t.b, pos, row);
             return page < 0 ? (int64_t)-1 : page * a.c.page_stride + row * a.c.row_stride;
         };
         bool bad = false;
-        int page, row, page1, row1;  // of the tile at work and of the next
-        look_up(0, page, row);
-        look_up(1, page1, row1);
+        int64_t off = look_up(0), off1 = look_up(1);  // rows of the tile to be copied and of the next
         if constexpr (!E4M3) {
             constexpr int CH = DP / 8, RPI = 32 / CH;  // pieces of a row, rows per instruction
             const int c = lane % CH, r0 = lane / CH;
             const uint32_t place0 = piece(32 * w + r0, c);
             // row r0 + RPI x: 128 bytes further per row, and the swizzle moves with the row
             auto place = [&](int x) { return (place0 ^ (uint32_t)(((RPI * x) & 7) << 4)) + x * RPI * 128; };
-            const int most = 2 * D - 16 * c < 0 ? 0 : 2 * D - 16 * c > 16 ? 16 : 2 * D - 16 * c;
-            int64_t off = -1;
-            for (int n = 0; n < 2 * tiles; ++n) {
-                const int tile = n >> 1, buf = n % S::NB;
-                if (n >= S::NB) {
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[buf], (n / S::NB - 1) & 1));
-                    if (!ok) break;
-                }
-                if (!(n & 1)) {
-                    off = offset(page, row);
-                    const uint32_t bits = __ballot_sync(0xffffffffu, page >= 0);
-                    if (lane == 0) sh.valid[tile % META][w] = bits;
-                    page = page1;
-                    row = row1;
-                    look_up(tile + 2, page1, row1);
-                }
-                const unsigned char* src = mat[n & 1] + (most ? 16 * c : 0);
-                const uint32_t dst = ring + buf * S::MAT;
-#pragma unroll
+            // Values that are not finite are taken out (and put back at the end for the queries
+            // that see them), and whatever a page holds behind the sequence.
+            auto look_over = [&](int tile, int buf) {
                 for (int x = 0; x < 32 / RPI; ++x) {
-                    const int64_t o = __shfl_sync(0xffffffffu, off, x * RPI + r0);
-                    cp_async16(dst + place(x), src + (o < 0 ? 0 : o), o < 0 ? 0 : most);
-                }
-                if ((n & 1) && t.begin + tile * TN + TN > open) {
-                    // some queries see this tile in part: values that are not finite are taken out
-                    // (and put back at the end for the queries that see them)
-                    cp_wait_all();
-                    for (int x = 0; x < 32 / RPI; ++x) {
-                        uint4* p = reinterpret_cast<uint4*>(gen + (MQ + buf) * S::MAT + place(x));
-                        uint4 v = *p;
-                        if (sanitise<false>(v)) {
-                            *p = v;
-                            bad = true;
-                        }
+                    uint4* p = reinterpret_cast<uint4*>(gen + (MQ + buf) * S::MAT + place(x));
+                    uint4 v = *p;
+                    if (t.begin + tile * TN + 32 * w + x * RPI + r0 >= t.end) {
+                        *p = make_uint4(0u, 0u, 0u, 0u);
+                    } else if (sanitise<false>(v)) {
+                        *p = v;
+                        bad = true;
                     }
-                    if (bad) sh.bad = 1;
-                    fence_proxy_async();
-                    mbar_arrive(&sh.full[buf]);
-                } else {
-                    cp_arrive(&sh.full[buf]);  // when this thread's copies have landed
                 }
+                if (bad) sh.bad = 1;
+                fence_proxy_async();
+            };
+            if (box_rows) {
+                uint32_t lands = 0;  // phase of each buffer's barrier
+                // the wait for the first such tile covers all tiles before it
+                const uint32_t patience = sv::WAIT_LIMIT_NS + (tiles < 150000 ? tiles * 20000u : 3000000000u);
+                int j = open > t.begin ? (open - t.begin) / TN : 0;  // the first tile that reaches beyond `open`
+                for (; j < tiles; ++j) {
+                    const int buf = (2 * j + 1) % S::NB;
+                    ok = __all_sync(0xffffffffu, sv::mbar_wait_bounded_ns(&sh.land[buf], (lands >> buf) & 1, patience));
+                    if (!ok) break;
+                    lands ^= 1u << buf;
+                    look_over(j, buf);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.full[buf]);
+                }
+            } else {
+                const int most = 2 * D - 16 * c < 0 ? 0 : 2 * D - 16 * c > 16 ? 16 : 2 * D - 16 * c;
+                for (int n = 0; n < 2 * tiles; ++n) {
+                    const int tile = n >> 1, buf = n % S::NB;
+                    if (n >= S::NB) {
+                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[buf], (n / S::NB - 1) & 1));
+                        if (!ok) break;
+                    }
+                    const unsigned char* src = mat[n & 1] + (most ? 16 * c : 0);
+                    const uint32_t dst = ring + buf * S::MAT;
+#pragma unroll
+                    for (int x = 0; x < 32 / RPI; ++x) {
+                        const int64_t o = __shfl_sync(0xffffffffu, off, x * RPI + r0);
+                        cp_async16(dst + place(x), src + (o < 0 ? 0 : o), o < 0 ? 0 : most);
+                    }
+                    if (n & 1) {
+                        off = off1;
+                        off1 = look_up(tile + 2);
+                    }
+                    if ((n & 1) && t.begin + tile * TN + TN > open) {
+                        cp_wait_all();
+                        look_over(tile, buf);
+                        mbar_arrive(&sh.full[buf]);
+                    } else {
+                        cp_arrive(&sh.full[buf]);  // when this thread's copies have landed
+                    }
+                }
+                cp_wait_all();
             }
-            cp_wait_all();
         } else {
             constexpr int CH = DP / 16, RPI = 32 / CH, X = 32 / RPI;  // 16 codes a piece
-            // A thread copies its pieces of an item to a place of its own, so that only it has to
-            // wait for them; RAW items ahead cover the memory's latency.
-            unsigned char* mine = gen + (MQ + S::NB) * S::MAT + 16 * (tid - 128 * MQ);
-            const uint32_t mine_at = smem_u32(mine);
             const int c = lane % CH, r0 = lane / CH;
             const int most = D - 16 * c < 0 ? 0 : D - 16 * c > 16 ? 16 : D - 16 * c;
+            // Codes arrive in one of RAW places: by the copy engine as rows of DP codes, else a
+            // thread copies its own pieces, so that only it has to wait for them.
+            unsigned char* raw0 = gen + (MQ + S::NB) * S::MAT;
+            const uint32_t own = 16 * (tid - 128 * MQ);
+            const unsigned char* mine = raw0 + (box_rows ? (32 * w + r0) * DP + 16 * c : own);
+            const int step = box_rows ? RPI * DP : 2048;
             const uint32_t place0 = piece(32 * w + r0, 2 * c);
             // row r0 + RPI x, element 16 c + 8 y; RPI is 4 or 8 rows
             auto place = [&](int x, int y) { return (place0 ^ (uint32_t)(((((RPI * x) & 7) ^ y)) << 4)) + x * RPI * 128; };
-            float ks = 0.0f, vs = 0.0f, ks1 = 0.0f, vs1 = 0.0f;
-            auto scales = [&](int page, int row, float& k, float& v) {
-                k = v = 0.0f;
-                if (page >= 0) {
-                    const int64_t at = ((int64_t)page * a.c.heads + t.h) * a.c.page_size + row;
-                    k = __ldg(a.c.k_scale + at);
-                    v = __ldg(a.c.v_scale + at);
-                }
-            };
-            // The copies run ahead of the conversions: tile `ahead` is the next to be copied.
-            int ahead = 0, page2 = page, row2 = row, page3 = page1, row3 = row1;
-            int64_t off = -1;
             auto copy = [&](int n) {
                 if (n < 2 * tiles) {
-                    if (!(n & 1)) {
-                        off = offset(page2, row2);
-                        page2 = page3;
-                        row2 = row3;
-                        ++ahead;
-                        look_up(ahead + 1, page3, row3);
-                    }
                     const unsigned char* src = mat[n & 1] + (most ? 16 * c : 0);
-                    const uint32_t dst = mine_at + (n % S::RAW) * (S::MAT / 2);
+                    const uint32_t dst = smem_u32(raw0) + own + (n % S::RAW) * (S::MAT / 2);
 #pragma unroll
                     for (int x = 0; x < X; ++x) {
                         const int64_t o = __shfl_sync(0xffffffffu, off, x * RPI + r0);
                         cp_async16(dst + x * 2048, src + (o < 0 ? 0 : o), o < 0 ? 0 : most);
                     }
+                    if (n & 1) {
+                        off = off1;
+                        off1 = look_up((n >> 1) + 2);
+                    }
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
             };
-            copy(0);
-            copy(1);
-            scales(page, row, ks, vs);
+            if (!box_rows) {
+                copy(0);
+                copy(1);
+            }
             for (int n = 0; n < 2 * tiles; ++n) {
-                const int j = n >> 1, buf = n % S::NB, m = j % META;
-                copy(n + 2);
+                const int j = n >> 1, buf = n % S::NB;
+                if (!box_rows) copy(n + 2);
                 if (n >= S::NB) {
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[buf], (n / S::NB - 1) & 1));
                     if (!ok) break;
                 }
-                const bool clean = (n & 1) && t.begin + j * TN + TN > open;
-                if (!(n & 1)) {
-                    if (t.begin + j * TN + TN > open && sv::not_finite(vs)) {
-                        vs = 0.0f;
-                        bad = true;
-                    }
-                    sh.ksc[m][32 * w + lane] = ks * a.scale_log2;
-                    sh.vsc[m][32 * w + lane] = vs;
-                    const uint32_t bits = __ballot_sync(0xffffffffu, page >= 0);
-                    if (lane == 0) sh.valid[m][w] = bits;
-                    scales(page1, row1, ks1, vs1);
-                    ks = ks1;
-                    vs = vs1;
-                    page = page1;
-                    row = row1;
-                    look_up(j + 2, page1, row1);
+                if (box_rows) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.raw_full[n % S::RAW], (n / S::RAW) & 1));
+                    if (!ok) break;
+                } else {
+                    asm volatile("cp.async.wait_group 2;" ::: "memory");
                 }
-                asm volatile("cp.async.wait_group 2;" ::: "memory");
+                const bool clean = (n & 1) && t.begin + j * TN + TN > open;
                 unsigned char* dst = gen + (MQ + buf) * S::MAT;
                 const unsigned char* from = mine + (n % S::RAW) * (S::MAT / 2);
+                uint4 codes[X];
+#pragma unroll
+                for (int x = 0; x < X; ++x) codes[x] = *reinterpret_cast<const uint4*>(from + x * step);
+                if (box_rows) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.raw_empty[n % S::RAW]);
+                }
 #pragma unroll
                 for (int x = 0; x < X; ++x) {
-                    uint4 g = *reinterpret_cast<const uint4*>(from + x * 2048);
-                    if (clean) bad |= sanitise<true>(g);
+                    uint4 g = codes[x];
+                    if (clean) {
+                        if (t.begin + j * TN + 32 * w + x * RPI + r0 >= t.end) g = make_uint4(0u, 0u, 0u, 0u);
+                        bad |= sanitise<true>(g);
+                    }
                     uint4 p, q;
                     widen16(g, p, q);
                     // lanes of a row's second 64 elements, whose banks are the first's, swap halves
@@ -574,6 +643,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         // ------------------------------------------------------------ products
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::R_MMA));
         if (warp == 4 * MQ + 4) {
+            // one lane issues
             const uint32_t leader = elect_one();
             // the same in every lane, and known to be
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), sm0 = __shfl_sync(0xffffffffu, smem0, 0);
@@ -595,7 +665,8 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 }
                 tc_commit(&sh.s_full[q], leader);
             };
-            ok = full(0);
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.q_full, 0));
+            ok = full(0) && ok;
             tc_fence_after();
             if (ok) {
                 #pragma unroll
@@ -607,13 +678,18 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 ok = full(nv);
                 const uint64_t va = operand(ring0 + (nv % S::NB) * S::MAT, BLK, 1024);
                 for (int q = 0; q < MQ && ok; ++q) {
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.p_full[q], j & 1));
-                    if (!ok) break;
-                    tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < TN / 16; ++k)
-                        mma_ts(tm + S::O_COL + DP * q, tm + S::S_COL + 128 * q + 8 * k,
-                               va + k * (2048 >> 4), id_o, j > 0 || k > 0, leader);
+                    for (int half = 0; half < 2; ++half) {
+                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.p_full[q][half], j & 1)) && ok;
+                        tc_fence_after();
+                        if (ok) {
+#pragma unroll
+                            for (int k = 4 * half; k < 4 * half + 4; ++k)
+                                mma_ts(tm + S::O_COL + DP * q, tm + S::S_COL + 128 * q + 8 * k,
+                                       va + k * (2048 >> 4), id_o, j > 0 || k > 0, leader);
+                        }
+                    }
+                    if (!ok) break;
                     if (j + 1 < todo) {
                         if (q == 0) ok = full(nk);
                         if (ok) scores(q, nk);
@@ -627,11 +703,120 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 }
             }
             if (!ok) {
-                sh.failed = 1;
                 tc_commit(&sh.drain, leader);  // whatever was issued ends before the memory is given back
                 (void)mbar_wait_bounded(&sh.drain, 0);
             }
+        } else if (warp == 4 * MQ + 5 && box_rows) {
+            // ---------------------------------------------------------- copies
+            // Lane l < boxes copies the box of positions l * box_rows .. of a tile, which lie in
+            // one page, into the ring, or e4m3 codes into the places before it.  bf16 values that
+            // are to be looked over land on a barrier of their own.
+            const int boxes = TN / box_rows;
+            auto box_page = [&](int tile, int& page, int& row) {
+                const int pos = t.begin + tile * TN + lane * box_rows;
+                page = a.c.num_pages;  // a page outside the cache reads as zeros
+                row = 0;
+                if (lane < boxes && tile < tiles && pos < t.end) {
+                    const int p = sv::paged_place(a.c, t.b, pos, row);
+                    if (p >= 0) page = p;
+                }
+            };
+            int page, row, page1, row1, n = 0;
+            box_page(0, page, row);
+            box_page(1, page1, row1);
+            for (; n < 2 * tiles; ++n) {
+                constexpr int PLACES = E4M3 ? S::RAW : S::NB;
+                const int slot = n % PLACES;
+                if (n >= PLACES) {
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait_bounded(E4M3 ? &sh.raw_empty[slot & 3] : &sh.empty[slot], (n / PLACES - 1) & 1));
+                    if (!ok) break;
+                }
+                const bool tail = !E4M3 && (n & 1) && t.begin + (n >> 1) * TN + TN > open;
+                uint64_t* bar = E4M3 ? &sh.raw_full[slot & 3] : tail ? &sh.land[slot] : &sh.full[slot];
+                if (lane == 0) {
+                    sv::mbar_arrive_expect_tx(bar, E4M3 ? S::MAT / 2 : S::MAT);
+                    if (!E4M3 && !tail) mbar_arrive_n(bar, 3);
+                }
+                __syncwarp();
+                const CUtensorMap* map = n & 1 ? &v_map : &k_map;
+                if (lane < boxes) {
+                    if (E4M3) {
+                        tma_box(smem0 + (MQ + S::NB) * S::MAT + slot * (S::MAT / 2) + lane * box_rows * DP, map, 0, row, t.h, page, bar);
+                    } else {
+#pragma unroll
+                        for (int z = 0; z < DP / 64; ++z)
+                            tma_box(ring + slot * S::MAT + z * BLK + lane * box_rows * 128, map, 64 * z, row, t.h, page, bar);
+                    }
+                }
+                __syncwarp();
+                if (n & 1) {
+                    page = page1;
+                    row = row1;
+                    box_page((n >> 1) + 2, page1, row1);
+                }
+            }
+            if (!ok) {  // copies in flight land before the CTA leaves
+                constexpr int PLACES = E4M3 ? S::RAW : S::NB;
+                for (int z = n > PLACES ? n - PLACES : 0; z < n; ++z)
+                    if (E4M3 || !(z & 1) || t.begin + (z >> 1) * TN + TN <= open)
+                        (void)mbar_wait_bounded(E4M3 ? &sh.raw_full[z % PLACES & 3] : &sh.full[z % PLACES], (z / PLACES) & 1);
+            }
+        } else if (warp == 4 * MQ + 6) {
+            // ----------------------------------------------------------- notes
+            // Which positions of a tile hold something, and e4m3's scales; read ahead, so that
+            // nobody else waits for a page table or a scale.
+            int64_t at1[4];  // index of the scales of the next tile's positions, -1: nothing there
+            float ks[4], vs[4];
+            uint32_t bits[4];
+            auto look_up = [&](int tile, int64_t (&at)[4]) {
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const int pos = t.begin + tile * TN + 32 * z + lane;
+                    at[z] = -1;
+                    if (tile < tiles && pos < t.end) {
+                        int row;
+                        const int page = sv::paged_place(a.c, t.b, pos, row);
+                        if (page >= 0) at[z] = ((int64_t)page * a.c.heads + t.h) * a.c.page_size + row;
+                    }
+                }
+            };
+            auto fetch = [&]() {
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    bits[z] = __ballot_sync(0xffffffffu, at1[z] >= 0);
+                    ks[z] = E4M3 && at1[z] >= 0 ? __ldg(a.c.k_scale + at1[z]) : 0.0f;
+                    vs[z] = E4M3 && at1[z] >= 0 ? __ldg(a.c.v_scale + at1[z]) : 0.0f;
+                }
+            };
+            look_up(0, at1);
+            fetch();
+            look_up(1, at1);
+            for (int j = 0; j < tiles; ++j) {
+                const int m = j % META;
+                if (j >= META) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.note_empty[m], (j / META - 1) & 1));
+                    if (!ok) break;
+                }
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    if (lane == 0) sh.valid[m][z] = bits[z];
+                    if (E4M3) {
+                        if (t.begin + j * TN + TN > open && sv::not_finite(vs[z])) {
+                            vs[z] = 0.0f;  // put back at the end, as the values are
+                            sh.bad = 1;
+                        }
+                        sh.ksc[m][32 * z + lane] = ks[z] * a.scale_log2;
+                        sh.vsc[m][32 * z + lane] = vs[z];
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.note_full[m]);
+                fetch();
+                look_up(j + 2, at1);
+            }
         }
+        if (!ok) sh.failed = 1;
     }
     __syncwarp();
     tc_fence_before();
@@ -642,8 +827,46 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
     }
 }
 
+// cuTensorMapEncodeTiled, found through the runtime (the library does not link the driver).
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+    static const EncodeTiled f = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return f;
+}
+
+// A map of pages [page][head][row][element] for boxes of `rows` rows of `width` elements.
+bool page_map(CUtensorMap* map, const void* pages, const sv::PagedCache& c, bool e4m3, int width, int rows) {
+    const EncodeTiled f = encode_tiled();
+    if (!f) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page_size, (cuuint64_t)c.heads, (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.row_stride, (cuuint64_t)c.head_stride, (cuuint64_t)c.page_stride};
+    const cuuint32_t box[4] = {(cuuint32_t)width, (cuuint32_t)rows, 1, 1}, ones[4] = {1, 1, 1, 1};
+    return f(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pages), dims,
+             strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows per box where the copy engine can fill a tile (pages of 8, 16, 32, 64 or a multiple
+// of 128 rows: a box lies in one page and starts on a swizzle atom), else 0: cp.async then
+// copies row by row.
+int box_rows_of(const sv::PagedCache& c) {
+    if (c.page_size >= TN) return c.page_size % TN == 0 ? TN : 0;
+    return c.page_size >= 8 && TN % c.page_size == 0 ? c.page_size : 0;
+}
+
 template <int DP, int MQ, bool E4M3>
-cudaError_t launch_one(const AttnArgs& a, unsigned ctas, cudaStream_t stream) {
+cudaError_t launch_one(const AttnArgs& a, int pairs, unsigned ctas, cudaStream_t stream) {
     using S = Tc<DP, MQ, E4M3>;
     static sv::KernelLaunchCache cache;
     auto kern = paged_attention_tc_kernel<DP, MQ, E4M3>;
@@ -651,21 +874,25 @@ cudaError_t launch_one(const AttnArgs& a, unsigned ctas, cudaStream_t stream) {
     const cudaError_t e = cache.setup((const void*)kern, &max_dyn);
     if (e != cudaSuccess) return e;
     if (S::SMEM > max_dyn) return cudaErrorInvalidValue;
-    return sv::launch_serial(kern, dim3(ctas), dim3(S::THREADS), S::SMEM, stream, a);
+    int rows = box_rows_of(a.c);
+    CUtensorMap k{}, v{};
+    if (rows && !(page_map(&k, a.c.k, a.c, E4M3, E4M3 ? DP : 64, rows) && page_map(&v, a.c.v, a.c, E4M3, E4M3 ? DP : 64, rows)))
+        rows = 0;
+    return sv::launch_serial(kern, dim3(ctas), dim3(S::THREADS), S::SMEM, stream, a, k, v, rows, pairs);
 }
 
 template <int DP, bool E4M3>
-cudaError_t launch_dim(const AttnArgs& a, int tile_rows, unsigned ctas, cudaStream_t stream) {
-    return tile_rows == 256 ? launch_one<DP, 2, E4M3>(a, ctas, stream) : launch_one<DP, 1, E4M3>(a, ctas, stream);
+cudaError_t launch_dim(const AttnArgs& a, int pairs, int tile_rows, unsigned ctas, cudaStream_t stream) {
+    return tile_rows == 256 ? launch_one<DP, 2, E4M3>(a, pairs, ctas, stream) : launch_one<DP, 1, E4M3>(a, pairs, ctas, stream);
 }
 
 }  // namespace
 
 namespace sv {
 
-cudaError_t launch_attn_tc(const AttnArgs& a, bool e4m3, int tile_rows, unsigned ctas, cudaStream_t stream) {
-    if (a.c.dim <= 64) return e4m3 ? launch_dim<64, true>(a, tile_rows, ctas, stream) : launch_dim<64, false>(a, tile_rows, ctas, stream);
-    return e4m3 ? launch_dim<128, true>(a, tile_rows, ctas, stream) : launch_dim<128, false>(a, tile_rows, ctas, stream);
+cudaError_t launch_attn_tc(const AttnArgs& a, int pairs, bool e4m3, int tile_rows, unsigned ctas, cudaStream_t stream) {
+    if (a.c.dim <= 64) return e4m3 ? launch_dim<64, true>(a, pairs, tile_rows, ctas, stream) : launch_dim<64, false>(a, pairs, tile_rows, ctas, stream);
+    return e4m3 ? launch_dim<128, true>(a, pairs, tile_rows, ctas, stream) : launch_dim<128, false>(a, pairs, tile_rows, ctas, stream);
 }
 
 }  // namespace sv
