@@ -165,6 +165,15 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts16(uint32_t at, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // 16-byte piece c (of 8 elements) of row r in a tile of 64-element blocks.
 __device__ __forceinline__ uint32_t piece(int r, int c) {
     return (uint32_t)((c >> 3) * BLK + r * 128 + (((c & 7) ^ (r & 7)) << 4));
@@ -263,7 +272,6 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
     AttnTile t;
     if (!sv::attn_tile(a, pairs, blockIdx.x, S::ROWS, t)) return;
     const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;  // queries, then the ring
-    unsigned char* gen = raw + (smem0 - smem_u32(raw));       // the same place, generic
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = a.c.dim, rows = t.n * a.group;
     const int tiles = (t.end - t.begin + TN - 1) / TN;
@@ -309,19 +317,17 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::R_SOFTMAX));
         const int q = warp >> 2;
         {   // the queries of this warp's rows, zero behind the last real one
-            constexpr int CH = DP / 8, RPI = 32 / CH, X = 32 / RPI;
-            const int c = lane % CH, r0 = (warp & 3) * 32 + lane / CH;
-            uint4 w[X];  // every load in flight before the first store
-#pragma unroll
-            for (int x = 0; x < X; ++x) {
-                const int R = t.mt * S::ROWS + q * 128 + r0 + x * RPI;
-                w[x] = make_uint4(0u, 0u, 0u, 0u);
-                if (R < rows && 8 * c < D)
-                    w[x] = sv::ld_nc_v4(a.q + t.b * a.q_sb + (int64_t)(R / a.group) * a.q_st +
-                                        (int64_t)(t.h * a.group + R % a.group) * a.q_sh + 8 * c);
+            constexpr int CH = DP / 8, RPI = 32 / CH;
+            const int c = lane % CH;
+            const uint16_t* from = a.q + t.b * a.q_sb + (int64_t)t.h * a.group * a.q_sh + (8 * c < D ? 8 * c : 0);
+#pragma unroll 1
+            for (int x = 0; x < 32; x += RPI) {
+                const int r = (warp & 3) * 32 + x + lane / CH, R = t.mt * S::ROWS + q * 128 + r;
+                const int y = R / a.group;
+                const bool there = R < rows && 8 * c < D;
+                cp_async16(smem0 + q * S::MAT + piece(r, c), there ? from + y * a.q_st + (R - y * a.group) * a.q_sh : a.q, there ? 16 : 0);
             }
-#pragma unroll
-            for (int x = 0; x < X; ++x) *reinterpret_cast<uint4*>(gen + q * S::MAT + piece(r0 + x * RPI, c)) = w[x];
+            cp_wait_all();
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.q_full);
@@ -430,7 +436,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         // covers whole rows: a lane writing its own row touched 32 lines per store and cost
         // 15000 cycles a CTA.  Half a row at a time, 16-byte pieces swizzled by the row.
         constexpr int CW = DP / 2, PC = CW / 4;
-        float4* stage = reinterpret_cast<float4*>(gen + q * S::MAT + (warp & 3) * (S::MAT / 4));
+        const uint32_t stage = smem0 + q * S::MAT + (warp & 3) * (S::MAT / 4);
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
             uint32_t v[CW];
@@ -454,9 +460,9 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             }
 #pragma unroll
             for (int k = 0; k < PC; ++k)
-                stage[PC * lane + (k ^ (lane & (PC - 1)))] =
-                    make_float4(__uint_as_float(v[4 * k]) * inv, __uint_as_float(v[4 * k + 1]) * inv,
-                                __uint_as_float(v[4 * k + 2]) * inv, __uint_as_float(v[4 * k + 3]) * inv);
+                sts16(stage + 16 * (PC * lane + (k ^ (lane & (PC - 1)))),
+                      make_uint4(__float_as_uint(__uint_as_float(v[4 * k]) * inv), __float_as_uint(__uint_as_float(v[4 * k + 1]) * inv),
+                                 __float_as_uint(__uint_as_float(v[4 * k + 2]) * inv), __float_as_uint(__uint_as_float(v[4 * k + 3]) * inv)));
             __syncwarp();
             if (t.active > 1) {
                 const int k = lane % PC, d = CW * c + 4 * k;
@@ -464,7 +470,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     const int r = (32 / PC) * x + lane / PC;
                     const int64_t to = __shfl_sync(0xffffffffu, live ? part : (int64_t)-1, r);
                     if (to >= 0 && d < D)
-                        *reinterpret_cast<float4*>(a.part_o + to * D + d) = stage[PC * r + (k ^ (r & (PC - 1)))];
+                        *reinterpret_cast<uint4*>(a.part_o + to * D + d) = lds16(stage + 16 * (PC * r + (k ^ (r & (PC - 1)))));
                 }
             } else {
                 const int k = 2 * (lane % (PC / 2)), d = CW * c + 4 * k;
@@ -472,9 +478,11 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     const int r = (64 / PC) * x + lane / (PC / 2);
                     const int64_t to = __shfl_sync(0xffffffffu, live ? row : (int64_t)-1, r);
                     if (to >= 0 && d < D) {
-                        const float4 f = stage[PC * r + (k ^ (r & (PC - 1)))], g = stage[PC * r + ((k + 1) ^ (r & (PC - 1)))];
+                        const uint4 f = lds16(stage + 16 * (PC * r + (k ^ (r & (PC - 1)))));
+                        const uint4 g = lds16(stage + 16 * (PC * r + ((k + 1) ^ (r & (PC - 1)))));
+                        auto pair = [](uint32_t lo, uint32_t hi) { return sv::bf16x2(__uint_as_float(lo), __uint_as_float(hi)); };
                         *reinterpret_cast<uint4*>(a.out + to * D + d) =
-                            make_uint4(sv::bf16x2(f.x, f.y), sv::bf16x2(f.z, f.w), sv::bf16x2(g.x, g.y), sv::bf16x2(g.z, g.w));
+                            make_uint4(pair(f.x, f.y), pair(f.z, f.w), pair(g.x, g.y), pair(g.z, g.w));
                     }
                 }
             }
@@ -506,12 +514,12 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             // that see them), and whatever a page holds behind the sequence.
             auto look_over = [&](int tile, int buf) {
                 for (int x = 0; x < 32 / RPI; ++x) {
-                    uint4* p = reinterpret_cast<uint4*>(gen + (MQ + buf) * S::MAT + place(x));
-                    uint4 v = *p;
+                    const uint32_t at = ring + buf * S::MAT + place(x);
+                    uint4 v = lds16(at);
                     if (t.begin + tile * TN + 32 * w + x * RPI + r0 >= t.end) {
-                        *p = make_uint4(0u, 0u, 0u, 0u);
+                        sts16(at, make_uint4(0u, 0u, 0u, 0u));
                     } else if (sanitise<false>(v)) {
-                        *p = v;
+                        sts16(at, v);
                         bad = true;
                     }
                 }
@@ -567,9 +575,9 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             const int most = D - 16 * c < 0 ? 0 : D - 16 * c > 16 ? 16 : D - 16 * c;
             // Codes arrive in one of RAW places: by the copy engine as rows of DP codes, else a
             // thread copies its own pieces, so that only it has to wait for them.
-            unsigned char* raw0 = gen + (MQ + S::NB) * S::MAT;
+            const uint32_t raw0 = ring + S::NB * S::MAT;
             const uint32_t own = 16 * (tid - 128 * MQ);
-            const unsigned char* mine = raw0 + (box_rows ? (32 * w + r0) * DP + 16 * c : own);
+            const uint32_t mine = raw0 + (box_rows ? (32 * w + r0) * DP + 16 * c : own);
             const int step = box_rows ? RPI * DP : 2048;
             const uint32_t place0 = piece(32 * w + r0, 2 * c);
             // row r0 + RPI x, element 16 c + 8 y; RPI is 4 or 8 rows
@@ -577,7 +585,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             auto copy = [&](int n) {
                 if (n < 2 * tiles) {
                     const unsigned char* src = mat[n & 1] + (most ? 16 * c : 0);
-                    const uint32_t dst = smem_u32(raw0) + own + (n % S::RAW) * (S::MAT / 2);
+                    const uint32_t dst = raw0 + own + (n % S::RAW) * (S::MAT / 2);
 #pragma unroll
                     for (int x = 0; x < X; ++x) {
                         const int64_t o = __shfl_sync(0xffffffffu, off, x * RPI + r0);
@@ -608,28 +616,31 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     asm volatile("cp.async.wait_group 2;" ::: "memory");
                 }
                 const bool clean = (n & 1) && t.begin + j * TN + TN > open;
-                unsigned char* dst = gen + (MQ + buf) * S::MAT;
-                const unsigned char* from = mine + (n % S::RAW) * (S::MAT / 2);
-                uint4 codes[X];
+                const uint32_t dst = ring + buf * S::MAT, from = mine + (n % S::RAW) * (S::MAT / 2);
+                const int y = (c >> 2) & 1;
+                // A short loop: unrolled in full, this and the softmax ran out of the instruction
+                // caches (3000 cycles an item instead of 600).
+#pragma unroll 1
+                for (int x = 0; x < X; x += 2) {
+                    uint4 g[2];
 #pragma unroll
-                for (int x = 0; x < X; ++x) codes[x] = *reinterpret_cast<const uint4*>(from + x * step);
+                    for (int z = 0; z < 2; ++z) g[z] = lds16(from + (x + z) * step);
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        if (clean) {
+                            if (t.begin + j * TN + 32 * w + (x + z) * RPI + r0 >= t.end) g[z] = make_uint4(0u, 0u, 0u, 0u);
+                            bad |= sanitise<true>(g[z]);
+                        }
+                        uint4 p, q;
+                        widen16(g[z], p, q);
+                        // lanes of a row's second 64 elements, whose banks are the first's, swap halves
+                        sts16(dst + place(x + z, y), y ? q : p);
+                        sts16(dst + place(x + z, y ^ 1), y ? p : q);
+                    }
+                }
                 if (box_rows) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.raw_empty[n % S::RAW]);
-                }
-#pragma unroll
-                for (int x = 0; x < X; ++x) {
-                    uint4 g = codes[x];
-                    if (clean) {
-                        if (t.begin + j * TN + 32 * w + x * RPI + r0 >= t.end) g = make_uint4(0u, 0u, 0u, 0u);
-                        bad |= sanitise<true>(g);
-                    }
-                    uint4 p, q;
-                    widen16(g, p, q);
-                    // lanes of a row's second 64 elements, whose banks are the first's, swap halves
-                    const int y = (c >> 2) & 1;
-                    *reinterpret_cast<uint4*>(dst + place(x, y)) = y ? q : p;
-                    *reinterpret_cast<uint4*>(dst + place(x, y ^ 1)) = y ? p : q;
                 }
                 if (clean && bad) sh.bad = 1;
                 fence_proxy_async();
