@@ -21,6 +21,15 @@
 // then reach 256 instead of 1, harmless in fp32 sums and bf16's range, and the rescale of
 // O in TMEM becomes rare.
 //
+// e4m3 pages are multiplied as fp16.  A code times its scale, over a power of two that brings
+// the tile's (keys) or the stretch's (values) largest below 2^15, is rounded once to fp16's
+// 11 bits: code * hi + code * lo with the scale as two fp16 numbers, three instructions for two
+// codes.  (Scales applied to scores and probabilities instead cost a broadcast load and two
+// products per score, and the softmax threads' time doubled.)  Queries are brought to
+// [2^14, 2^15) row by row by a power of two, exactly to 2^-39 of the row's largest element.
+// Probabilities enter as fp16 too, 2^7 times larger, so that fp16's subnormal step is 2^-31
+// of the largest.  O is held in units of the values' power of two and rescaled when it grows.
+//
 // Every wait is bounded; a CTA whose wait runs out writes NaN for its rows, which a verify
 // reports as invalid data, and frees its TMEM.
 #include <cstdint>
@@ -48,6 +57,7 @@ constexpr int TN = 128;          // positions per tile
 constexpr int BLK = 128 * 128;   // bytes of 128 rows x 64 bf16 elements, 128-byte swizzled
 constexpr int META = 4;          // tiles whose hole bits and scales are kept
 constexpr float RESCALE = 8.0f;  // log2 of how far the maximum may lag
+constexpr float RAISE = 7.0f;    // e4m3: log2 of the probabilities' factor; 2^(8 + 7) is within fp16
 
 template <int DP, int MQ, bool E4M3>
 struct Tc {
@@ -144,9 +154,9 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32
     return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-// fp32 accumulator, bf16 operands, 128 rows, n columns; b_mn: B is stored along n.
-__host__ __device__ constexpr uint32_t instruction(int n, bool b_mn) {
-    return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+// fp32 accumulator, bf16 or fp16 operands, 128 rows, n columns; b_mn: B is stored along n.
+__host__ __device__ constexpr uint32_t instruction(int n, bool b_mn, bool f16) {
+    return 1u << 4 | (f16 ? 0u : 1u << 7 | 1u << 10) | (b_mn ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
 }
 
 // One box of a page (64 or DP elements x rows of one head) by the copy engine; a page
@@ -188,19 +198,36 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Sixteen e4m3 codes to bf16 (exact), as two 16-byte pieces.
-__device__ __forceinline__ void widen16(uint4 w, uint4& a, uint4& b) {
+// Sixteen e4m3 codes times a scale (x: twice its fp16, y: twice what that leaves) in fp16, as
+// two 16-byte pieces.
+__device__ __forceinline__ void widen16(uint4 w, uint2 scale, uint4& a, uint4& b) {
     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
     uint32_t out[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        // a code has 3 bits of mantissa: its bf16 is the upper half of its fp32 (NaN too)
-        const float2 lo = sv::e4m3x2_to_f32(in[i] & 0xffffu), hi = sv::e4m3x2_to_f32(in[i] >> 16);
-        out[2 * i] = __byte_perm(__float_as_uint(lo.x), __float_as_uint(lo.y), 0x7632);
-        out[2 * i + 1] = __byte_perm(__float_as_uint(hi.x), __float_as_uint(hi.y), 0x7632);
+        asm("{.reg .b16 t, u;\n\tmov.b32 {t, u}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
+            : "=r"(out[2 * i]), "=r"(out[2 * i + 1])
+            : "r"(in[i]));
+#pragma unroll
+        for (int z = 2 * i; z < 2 * i + 2; ++z)
+            asm("{.reg .b32 t;\n\tmul.rn.f16x2 t, %0, %2;\n\tfma.rn.f16x2 %0, %0, %1, t;\n\t}"
+                : "+r"(out[z])
+                : "r"(scale.x), "r"(scale.y));
     }
     a = make_uint4(out[0], out[1], out[2], out[3]);
     b = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+// Two fp32 values rounded to fp16 (nearest even), lo in the low half.
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// 2^e as fp32 (0 or infinity beyond the normal numbers).
+__device__ __forceinline__ float power_of_two(int e) {
+    return e < -126 ? 0.0f : e > 127 ? sv::pos_inf() : __int_as_float((e + 127) << 23);
 }
 
 // Takes values that are not finite out of 16 bytes (codes, or bf16); true if there were any.
@@ -222,20 +249,12 @@ __device__ __forceinline__ bool sanitise(uint4& v) {
     return bad;
 }
 
-// Scores of a row, scaled in place (e4m3: by the keys' scales too), -inf where hidden.
-template <bool E4M3, bool MASK>
-__device__ __forceinline__ void scale_scores(uint32_t v[TN], const uint32_t see[4], const float* ksc, float sc) {
+// Scores of a row, scaled in place, -inf where hidden.
+__device__ __forceinline__ void scale_scores(uint32_t v[TN], const uint32_t see[4], float sc) {
 #pragma unroll
-    for (int k = 0; k < TN; k += 4) {
-        const float4 w = E4M3 ? *reinterpret_cast<const float4*>(ksc + k) : make_float4(sc, sc, sc, sc);
-        float2 f[2] = {make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])),
-                       make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]))};
-        f[0] = fmul2(f[0], make_float2(w.x, w.y));
-        f[1] = fmul2(f[1], make_float2(w.z, w.w));
-        const float g[4] = {f[0].x, f[0].y, f[1].x, f[1].y};
-#pragma unroll
-        for (int z = 0; z < 4; ++z)
-            v[k + z] = __float_as_uint(!MASK || ((see[k >> 5] >> ((k & 31) + z)) & 1u) ? g[z] : neg_inf());
+    for (int k = 0; k < TN; ++k) {
+        const float f = __uint_as_float(v[k]) * sc;
+        v[k] = __float_as_uint((see[k >> 5] >> (k & 31)) & 1u ? f : neg_inf());
     }
 }
 
@@ -257,8 +276,9 @@ struct __align__(16) Shared {
     uint32_t tmem;
     int bad, failed;
     uint32_t valid[META][4];       // which of the tile's positions hold something
-    __align__(16) float ksc[META][TN];  // e4m3: key scale times the score factor
-    __align__(16) float vsc[META][TN];  // value scale
+    __align__(16) uint2 ksc[META][TN];  // e4m3: a position's key scale times 2^-kexp as two fp16 numbers
+    __align__(16) uint2 vsc[META][TN];  // and its value scale times 2^-vexp
+    int kexp[META], vexp[META];
 };
 
 template <int DP, int MQ, bool E4M3>
@@ -287,7 +307,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         }
         for (int i = 0; i < META; ++i) {
             mbar_init(&sh.note_full[i], 1);
-            mbar_init(&sh.note_empty[i], 4 * MQ);
+            mbar_init(&sh.note_empty[i], E4M3 ? 4 * MQ + 4 : 4 * MQ);
         }
         for (int i = 0; i < MQ; ++i) {
             mbar_init(&sh.s_full[i], 1);
@@ -316,18 +336,44 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         // ------------------------------------------------------------ softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::R_SOFTMAX));
         const int q = warp >> 2;
+        float own = 1.0f;  // e4m3: what the row's scores are multiplied by
         {   // the queries of this warp's rows, zero behind the last real one
             constexpr int CH = DP / 8, RPI = 32 / CH;
-            const int c = lane % CH;
-            const uint16_t* from = a.q + t.b * a.q_sb + (int64_t)t.h * a.group * a.q_sh + (8 * c < D ? 8 * c : 0);
+            const int c = lane % CH, R = t.mt * S::ROWS + q * 128 + (warp & 3) * 32 + lane;
+            const int y = R / a.group;
+            const int64_t here = R < rows ? y * a.q_st + (int64_t)(t.h * a.group + R - y * a.group) * a.q_sh : -1;
+            const uint16_t* from = a.q + t.b * a.q_sb;
+            const uint32_t to = smem0 + q * S::MAT;
 #pragma unroll 1
             for (int x = 0; x < 32; x += RPI) {
-                const int r = (warp & 3) * 32 + x + lane / CH, R = t.mt * S::ROWS + q * 128 + r;
-                const int y = R / a.group;
-                const bool there = R < rows && 8 * c < D;
-                cp_async16(smem0 + q * S::MAT + piece(r, c), there ? from + y * a.q_st + (R - y * a.group) * a.q_sh : a.q, there ? 16 : 0);
+                const int64_t o = __shfl_sync(0xffffffffu, here, x + lane / CH);
+                const bool there = o >= 0 && 8 * c < D;
+                cp_async16(to + piece((warp & 3) * 32 + x + lane / CH, c), from + (there ? o + 8 * c : 0), there ? 16 : 0);
             }
             cp_wait_all();
+            if (E4M3) {  // to fp16, a lane its row
+                __syncwarp();
+                const int r = (warp & 3) * 32 + lane;
+                uint32_t top = 0u;  // largest magnitude, as bf16 bits
+#pragma unroll 2
+                for (int z = 0; z < CH; ++z) {
+                    const uint4 v = lds16(to + piece(r, z));
+                    const uint32_t m0 = max(max(v.x & 0x7fffu, v.y & 0x7fffu), max(v.z & 0x7fffu, v.w & 0x7fffu));
+                    const uint32_t m1 = max(max((v.x >> 16) & 0x7fffu, (v.y >> 16) & 0x7fffu), max((v.z >> 16) & 0x7fffu, (v.w >> 16) & 0x7fffu));
+                    top = max(top, max(m0, m1));
+                }
+                const int e = (int)(top >> 7) - 127;  // its exponent; 128: not finite, -127: 0 or subnormal
+                const int up = e == 128 ? 0 : 14 - e > 126 ? 126 : 14 - e;
+                const float f = power_of_two(up);
+#pragma unroll 2
+                for (int z = 0; z < CH; ++z) {
+                    const uint32_t at = to + piece(r, z);
+                    const uint4 v = lds16(at);
+                    sts16(at, make_uint4(f16x2(sv::bf16_lo(v.x) * f, sv::bf16_hi(v.x) * f), f16x2(sv::bf16_lo(v.y) * f, sv::bf16_hi(v.y) * f),
+                                         f16x2(sv::bf16_lo(v.z) * f, sv::bf16_hi(v.z) * f), f16x2(sv::bf16_lo(v.w) * f, sv::bf16_hi(v.w) * f)));
+                }
+                own = power_of_two(-up);
+            }
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.q_full);
@@ -337,8 +383,8 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         const int i = live ? R / a.group : 0;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes per warp, lane field at bit 16
         const uint32_t s_at = tmem + lanes + S::S_COL + 128 * q, o_at = tmem + lanes + S::O_COL + DP * q;
-        const float sc = a.scale_log2;
         float mx = neg_inf(), l = 0.0f;
+        int vexp = 0;  // e4m3: O is held times 2^-vexp
         for (int j = 0; j < tiles; ++j) {
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.s_full[q], j & 1));
             if (!ok) break;
@@ -358,14 +404,14 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, v + 32 * c);
             tc_wait_ld();
-            float top, mul = 1.0f;
-            if (!E4M3 && whole && sc >= 0.0f) {
+            const float sc = E4M3 ? a.scale_log2 * own * power_of_two(sh.kexp[m]) : a.scale_log2;
+            float top, mul = sc;
+            if (whole && sc >= 0.0f) {
                 top = largest(v) * sc;  // the factor joins the exponent's product below
-                mul = sc;
             } else {
-                if (whole) scale_scores<E4M3, false>(v, see, sh.ksc[m], sc);
-                else scale_scores<E4M3, true>(v, see, sh.ksc[m], sc);
+                scale_scores(v, see, sc);
                 top = largest(v);
+                mul = 1.0f;
             }
             // move the maximum where it grew too far
             float fac = 1.0f;
@@ -374,6 +420,11 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 fac = now == neg_inf() ? 1.0f : sv::ex2(mx - now);
                 mx = now;
                 l *= fac;
+            }
+            if (E4M3) {
+                const int e = sh.vexp[m];
+                if (j > 0) fac *= power_of_two(vexp - e);
+                vexp = e;
             }
             if (j > 0 && __any_sync(0xffffffffu, fac != 1.0f)) {
 #pragma unroll 1
@@ -386,7 +437,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     tmem_st16(o_at + 16 * c, o);
                 }
             }
-            const float shift = mx == neg_inf() ? 0.0f : mx;
+            const float shift = (mx == neg_inf() ? 0.0f : mx) - (E4M3 ? RAISE : 0.0f);
             const float2 mul2 = make_float2(mul, mul), sh2 = make_float2(-shift, -shift);
             float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
@@ -401,13 +452,8 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     f = make_float2(sv::ex2(f.x), sv::ex2(f.y));
                     sum0 = sv::fadd2(sum0, e);
                     sum1 = sv::fadd2(sum1, f);
-                    if (E4M3) {
-                        const float4 w = *reinterpret_cast<const float4*>(&sh.vsc[m][32 * c + k]);
-                        e = fmul2(e, make_float2(w.x, w.y));
-                        f = fmul2(f, make_float2(w.z, w.w));
-                    }
-                    p[k >> 1] = sv::bf16x2(e.x, e.y);
-                    p[(k >> 1) + 1] = sv::bf16x2(f.x, f.y);
+                    p[k >> 1] = E4M3 ? f16x2(e.x, e.y) : sv::bf16x2(e.x, e.y);
+                    p[(k >> 1) + 1] = E4M3 ? f16x2(f.x, f.y) : sv::bf16x2(f.x, f.y);
                 }
                 tmem_st16(s_at + 16 * c, p);  // over S, which this warp has read
                 if (c & 1) {  // half of the row: its product may start
@@ -424,13 +470,14 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.o_full[q], 0));
         if (!ok) sh.failed = 1;
         tc_fence_after();
-        const float inv = !ok ? __int_as_float(0x7fffffff) : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-        const float lse2 = !ok ? inv : l == 0.0f ? neg_inf() : mx + log2f(l);
+        float inv = !ok ? __int_as_float(0x7fffffff) : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+        const float lse2 = !ok ? inv : l == 0.0f ? neg_inf() : mx + log2f(l) - (E4M3 ? RAISE : 0.0f);
         const int64_t row = live ? sv::attn_row(a, t, R) : 0, part = t.part + (R - t.mt * S::ROWS);
         if (live) {
             if (t.active > 1) a.part_lse[part] = lse2;
             else if (a.lse) a.lse[row] = lse2 * 0.69314718055994531f;
         }
+        if (E4M3) inv *= power_of_two(vexp);
         const bool patch = ok && sh.bad != 0;
         // Rows leave through shared memory (where this row tile's queries were), so that a store
         // covers whole rows: a lane writing its own row touched 32 lines per store and cost
@@ -615,6 +662,11 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 } else {
                     asm volatile("cp.async.wait_group 2;" ::: "memory");
                 }
+                if (!(n & 1)) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.note_full[j % META], (j / META) & 1));
+                    if (!ok) break;
+                }
+                const uint2* scale = (n & 1 ? sh.vsc : sh.ksc)[j % META] + 32 * w + r0;
                 const bool clean = (n & 1) && t.begin + j * TN + TN > open;
                 const uint32_t dst = ring + buf * S::MAT, from = mine + (n % S::RAW) * (S::MAT / 2);
                 const int y = (c >> 2) & 1;
@@ -632,7 +684,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                             bad |= sanitise<true>(g[z]);
                         }
                         uint4 p, q;
-                        widen16(g[z], p, q);
+                        widen16(g[z], scale[(x + z) * RPI], p, q);
                         // lanes of a row's second 64 elements, whose banks are the first's, swap halves
                         sts16(dst + place(x + z, y), y ? q : p);
                         sts16(dst + place(x + z, y ^ 1), y ? p : q);
@@ -645,7 +697,10 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 if (clean && bad) sh.bad = 1;
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.full[buf]);
+                if (lane == 0) {
+                    mbar_arrive(&sh.full[buf]);
+                    if (n & 1) mbar_arrive(&sh.note_empty[j % META]);
+                }
             }
             cp_wait_all();
         }
@@ -660,7 +715,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), sm0 = __shfl_sync(0xffffffffu, smem0, 0);
             const int todo = __shfl_sync(0xffffffffu, tiles, 0);
             const uint32_t ring0 = sm0 + MQ * S::MAT;
-            constexpr uint32_t id_s = instruction(TN, false), id_o = instruction(DP, true);
+            constexpr uint32_t id_s = instruction(TN, false, E4M3), id_o = instruction(DP, true, E4M3);
             auto full = [&](int n) {
                 const bool there = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[n % S::NB], (n / S::NB) & 1));
                 fence_proxy_async();  // copies by other threads, seen through the barrier, before the products read them
@@ -777,6 +832,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             // ----------------------------------------------------------- notes
             // Which positions of a tile hold something, and e4m3's scales; read ahead, so that
             // nobody else waits for a page table or a scale.
+            uint32_t largest_v = 0u;  // the largest finite value scale so far, as bits
             int64_t at1[4];  // index of the scales of the next tile's positions, -1: nothing there
             float ks[4], vs[4];
             uint32_t bits[4];
@@ -809,16 +865,44 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.note_empty[m], (j / META - 1) & 1));
                     if (!ok) break;
                 }
+                if (lane == 0) {
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    if (lane == 0) sh.valid[m][z] = bits[z];
-                    if (E4M3) {
-                        if (t.begin + j * TN + TN > open && sv::not_finite(vs[z])) {
+                    for (int z = 0; z < 4; ++z) sh.valid[m][z] = bits[z];
+                }
+                if (E4M3) {
+                    uint32_t largest_k = 0u;  // of this tile, as bits
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        if (!sv::not_finite(ks[z])) largest_k = max(largest_k, __float_as_uint(fabsf(ks[z])));
+                        if (!sv::not_finite(vs[z])) {
+                            largest_v = max(largest_v, __float_as_uint(fabsf(vs[z])));
+                        } else if (t.begin + j * TN + TN > open) {
                             vs[z] = 0.0f;  // put back at the end, as the values are
                             sh.bad = 1;
                         }
-                        sh.ksc[m][32 * z + lane] = ks[z] * a.scale_log2;
-                        sh.vsc[m][32 * z + lane] = vs[z];
+                    }
+                    largest_k = __reduce_max_sync(0xffffffffu, largest_k);
+                    largest_v = __reduce_max_sync(0xffffffffu, largest_v);
+                    // scales below 2^6, times codes of at most 448: below 2^15
+                    auto exponent = [](uint32_t top) {
+                        const int e = (int)(top >> 23) - 127 + 1 - 6;
+                        return e < -118 ? -118 : e;
+                    };
+                    const int ke = exponent(largest_k), ve = exponent(largest_v);
+                    auto halves = [](float s) {  // as two fp16 numbers, each twice
+                        const uint32_t hi = f16x2(s, s);
+                        float back;
+                        asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, a;\n\t}" : "=f"(back) : "r"(hi));
+                        return make_uint2(hi, f16x2(s - back, s - back));
+                    };
+                    if (lane == 0) {
+                        sh.kexp[m] = ke;
+                        sh.vexp[m] = ve;
+                    }
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        sh.ksc[m][32 * z + lane] = halves(ks[z] * power_of_two(-ke));
+                        sh.vsc[m][32 * z + lane] = halves(vs[z] * power_of_two(-ve));
                     }
                 }
                 __syncwarp();

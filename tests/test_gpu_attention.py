@@ -6,6 +6,15 @@ products and sums, the tensor cores' own rounding included; the exponential's 2^
 below), which moves a weight by at most 2e + the same for the sum.  So with A the weighted
 mean of |v|, |out - want| <= (2^-8 + 4 e) A, plus the output's own half step 2^-8 |want|.
 lse moves by at most 2 e, plus fp32 roundings of its own value.
+
+e4m3 calls of more than 64 query rows per cache head multiply in fp16, half step 2^-11: an
+element of a key is rounded once, which moves a score by up to 2^-11 scale sum|q k| (it joins
+e); an element of a value and a probability are rounded once each, together below bf16's 2^-8.
+Probabilities are held times 2^7, where fp16 steps by 2^-24 below 2^-14: a position whose weight
+is tiny is off by up to 2^-32 of the largest weight, and the sum they are divided by is at
+least 1: n positions add at most n 2^-32 V, V = 448 vmax the largest |v| that the scales allow.
+A value element far below V is off by up to 2^-25 2^E with 2^E <= 2^-5 vmax, below 2^-38 V.  Both
+are within n 2^-31 V.
 """
 import numpy as np
 import pytest
@@ -33,9 +42,13 @@ def check(got, lse, q, k, v, ks, vs, table, base, new_len, mask, scale, keep_out
     ka = np.where(np.isfinite(kv), np.abs(kv), 0).transpose(1, 0, 2, 3).reshape(H, -1, D)
     qa = np.abs(qh).reshape(B * Q, H, Hq // H, D).transpose(1, 0, 2, 3).reshape(H, -1, D)
     reach = abs(scale) * max((qa[h] @ ka[h].T).max() for h in range(H))  # largest sum |q k|
-    e = (D + 16) * 2.0 ** -22 * reach
+    half = vs is not None and Q * Hq // H > 64 and D <= 128  # multiplied as fp16
+    e = ((D + 16) * 2.0 ** -22 + (2.0 ** -11 if half else 0)) * reach
     g, gl = host(got), host(lse)
     tol = (2.0 ** -8 + 4 * e) * np.abs(size) + 2.0 ** -8 * np.abs(want) + 1e-30
+    if half:
+        scales = host(vs)
+        tol = tol + (int(base.max()) + Q) * 2.0 ** -31 * 448 * scales[np.isfinite(scales)].max()
     assert np.isfinite(g).all()
     worst = (np.abs(g - want) / tol).max()
     assert worst <= 1, f"output off by {worst:.3g} tolerances"
@@ -144,6 +157,25 @@ def test_split_and_unsplit_agree_with_the_plain_form(sv, cache, Q):  # noqa: F81
     c = case(rng, 3, Q, 8, 2, 128, 16, 1500, cache, Q == 61, False)
     for kw in (dict(), dict(workspace=None), dict(max_len=1), dict(max_len=200), dict(max_len=1 << 30)):
         both(sv, c, **kw)
+
+
+@pytest.mark.parametrize("Q,ps", [(6, 16), (61, 16), (61, 24), (30, 64)])
+def test_e4m3_scales_of_very_different_sizes(sv, Q, ps):  # noqa: F811
+    """Value scales over a factor of 2^18 that grow and shrink along the context, key scales over
+    2^6, a row of zeros (the smallest scale there is), queries from tiny to large."""
+    import torch
+    rng = np.random.default_rng([Q, ps])
+    c = case(rng, 2, Q, 4, 1, 128, ps, 700, "e4m3", Q > 7, False, ragged=False)
+    q, k, v, ks, vs, table, base, new_len, mask = c
+    P, H, _ = vs.shape
+    vs.copy_(torch.from_numpy(2.0 ** rng.uniform(-9, 9, (P, H, ps))).float())
+    ks.copy_(torch.from_numpy(0.01 * 2.0 ** rng.uniform(-3, 3, (P, H, ps))).float())
+    page, row = int(table[0, 5]), 3
+    vs[page, :, row] = 2.0 ** -126
+    v[page, :, row] = 0
+    poison(k, v, ks, vs, table, base, new_len, ps)
+    q *= torch.from_numpy(2.0 ** rng.uniform(-20, 3, (2, Q, 4, 1))).cuda()
+    both(sv, c)
 
 
 def test_rows_that_see_nothing_holes_and_invalid_rows(sv):  # noqa: F811
