@@ -21,14 +21,15 @@
 // then reach 256 instead of 1, harmless in fp32 sums and bf16's range, and the rescale of
 // O in TMEM becomes rare.
 //
-// e4m3 pages are multiplied as fp16.  A code times its scale, over a power of two that brings
-// the tile's (keys) or the stretch's (values) largest below 2^15, is rounded once to fp16's
-// 11 bits: code * hi + code * lo with the scale as two fp16 numbers, three instructions for two
-// codes.  (Scales applied to scores and probabilities instead cost a broadcast load and two
-// products per score, and the softmax threads' time doubled.)  Queries are brought to
-// [2^14, 2^15) row by row by a power of two, exactly to 2^-39 of the row's largest element.
-// Probabilities enter as fp16 too, 2^7 times larger, so that fp16's subnormal step is 2^-31
-// of the largest.  O is held in units of the values' power of two and rescaled when it grows.
+// e4m3 pages are multiplied as fp16, which holds every code exactly and converts two in one
+// instruction (bf16 takes four).  A position's key scale multiplies its scores, in fp32: rounding
+// scaled keys to 11 bits moved lse by 10^-4.  A value's code times its scale, over a power of two
+// that brings the stretch's largest below 2^15, is rounded once to 11 bits, below what rounding the
+// scaled probabilities to bf16 cost: code * hi + code * lo with the scale as two fp16 numbers,
+// three instructions for two codes.  Queries are brought to [2^14, 2^15) row by row by a power
+// of two, exactly to 2^-39 of the row's largest element.  Probabilities enter as fp16 too, 2^7
+// times larger, so that fp16's subnormal step is 2^-31 of the largest.  O is held in units of
+// the values' power of two and rescaled when it grows.
 //
 // Every wait is bounded; a CTA whose wait runs out writes NaN for its rows, which a verify
 // reports as invalid data, and frees its TMEM.
@@ -198,8 +199,9 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Sixteen e4m3 codes times a scale (x: twice its fp16, y: twice what that leaves) in fp16, as
-// two 16-byte pieces.
+// Sixteen e4m3 codes in fp16, times a scale (x: twice its fp16, y: twice what that leaves) if
+// asked, as two 16-byte pieces.
+template <bool SCALE>
 __device__ __forceinline__ void widen16(uint4 w, uint2 scale, uint4& a, uint4& b) {
     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
     uint32_t out[8];
@@ -208,6 +210,7 @@ __device__ __forceinline__ void widen16(uint4 w, uint2 scale, uint4& a, uint4& b
         asm("{.reg .b16 t, u;\n\tmov.b32 {t, u}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
             : "=r"(out[2 * i]), "=r"(out[2 * i + 1])
             : "r"(in[i]));
+        if (!SCALE) continue;
 #pragma unroll
         for (int z = 2 * i; z < 2 * i + 2; ++z)
             asm("{.reg .b32 t;\n\tmul.rn.f16x2 t, %0, %2;\n\tfma.rn.f16x2 %0, %0, %1, t;\n\t}"
@@ -249,12 +252,18 @@ __device__ __forceinline__ bool sanitise(uint4& v) {
     return bad;
 }
 
-// Scores of a row, scaled in place, -inf where hidden.
-__device__ __forceinline__ void scale_scores(uint32_t v[TN], const uint32_t see[4], float sc) {
+// Scores of a row, scaled in place (by sc, and each by its own factor where given), -inf where hidden.
+template <bool OWN, bool MASK>
+__device__ __forceinline__ void scale_scores(uint32_t v[TN], const uint32_t see[4], const float* ksc, float sc) {
 #pragma unroll
-    for (int k = 0; k < TN; ++k) {
-        const float f = __uint_as_float(v[k]) * sc;
-        v[k] = __float_as_uint((see[k >> 5] >> (k & 31)) & 1u ? f : neg_inf());
+    for (int k = 0; k < TN; k += 4) {
+        const float4 w = OWN ? *reinterpret_cast<const float4*>(ksc + k) : make_float4(sc, sc, sc, sc);
+        const float2 f = fmul2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), make_float2(w.x, w.y));
+        const float2 h = fmul2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), make_float2(w.z, w.w));
+        const float g[4] = {f.x, f.y, h.x, h.y};
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+            v[k + z] = __float_as_uint(!MASK || ((see[k >> 5] >> ((k & 31) + z)) & 1u) ? g[z] : neg_inf());
     }
 }
 
@@ -276,9 +285,9 @@ struct __align__(16) Shared {
     uint32_t tmem;
     int bad, failed;
     uint32_t valid[META][4];       // which of the tile's positions hold something
-    __align__(16) uint2 ksc[META][TN];  // e4m3: a position's key scale times 2^-kexp as two fp16 numbers
-    __align__(16) uint2 vsc[META][TN];  // and its value scale times 2^-vexp
-    int kexp[META], vexp[META];
+    __align__(16) float ksc[META][TN];  // e4m3: a position's key scale times the score factor
+    __align__(16) uint2 vsc[META][TN];  // its value scale times 2^-vexp, as two fp16 numbers
+    int vexp[META];
 };
 
 template <int DP, int MQ, bool E4M3>
@@ -383,6 +392,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         const int i = live ? R / a.group : 0;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes per warp, lane field at bit 16
         const uint32_t s_at = tmem + lanes + S::S_COL + 128 * q, o_at = tmem + lanes + S::O_COL + DP * q;
+        const float sc = a.scale_log2;
         float mx = neg_inf(), l = 0.0f;
         int vexp = 0;  // e4m3: O is held times 2^-vexp
         for (int j = 0; j < tiles; ++j) {
@@ -404,14 +414,14 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, v + 32 * c);
             tc_wait_ld();
-            const float sc = E4M3 ? a.scale_log2 * own * power_of_two(sh.kexp[m]) : a.scale_log2;
-            float top, mul = sc;
-            if (whole && sc >= 0.0f) {
+            float top, mul = own;
+            if (!E4M3 && whole && sc >= 0.0f) {
                 top = largest(v) * sc;  // the factor joins the exponent's product below
+                mul = sc;
             } else {
-                scale_scores(v, see, sc);
-                top = largest(v);
-                mul = 1.0f;
+                if (E4M3 && whole) scale_scores<E4M3, false>(v, see, sh.ksc[m], sc);
+                else scale_scores<E4M3, true>(v, see, sh.ksc[m], sc);
+                top = largest(v) * own;
             }
             // move the maximum where it grew too far
             float fac = 1.0f;
@@ -666,7 +676,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.note_full[j % META], (j / META) & 1));
                     if (!ok) break;
                 }
-                const uint2* scale = (n & 1 ? sh.vsc : sh.ksc)[j % META] + 32 * w + r0;
+                const uint2* scale = sh.vsc[j % META] + 32 * w + r0;
                 const bool clean = (n & 1) && t.begin + j * TN + TN > open;
                 const uint32_t dst = ring + buf * S::MAT, from = mine + (n % S::RAW) * (S::MAT / 2);
                 const int y = (c >> 2) & 1;
@@ -684,7 +694,8 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                             bad |= sanitise<true>(g[z]);
                         }
                         uint4 p, q;
-                        widen16(g[z], scale[(x + z) * RPI], p, q);
+                        if (n & 1) widen16<true>(g[z], scale[(x + z) * RPI], p, q);
+                        else widen16<false>(g[z], make_uint2(0u, 0u), p, q);
                         // lanes of a row's second 64 elements, whose banks are the first's, swap halves
                         sts16(dst + place(x + z, y), y ? q : p);
                         sts16(dst + place(x + z, y ^ 1), y ? p : q);
@@ -870,10 +881,8 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     for (int z = 0; z < 4; ++z) sh.valid[m][z] = bits[z];
                 }
                 if (E4M3) {
-                    uint32_t largest_k = 0u;  // of this tile, as bits
 #pragma unroll
                     for (int z = 0; z < 4; ++z) {
-                        if (!sv::not_finite(ks[z])) largest_k = max(largest_k, __float_as_uint(fabsf(ks[z])));
                         if (!sv::not_finite(vs[z])) {
                             largest_v = max(largest_v, __float_as_uint(fabsf(vs[z])));
                         } else if (t.begin + j * TN + TN > open) {
@@ -881,27 +890,19 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                             sh.bad = 1;
                         }
                     }
-                    largest_k = __reduce_max_sync(0xffffffffu, largest_k);
                     largest_v = __reduce_max_sync(0xffffffffu, largest_v);
                     // scales below 2^6, times codes of at most 448: below 2^15
-                    auto exponent = [](uint32_t top) {
-                        const int e = (int)(top >> 23) - 127 + 1 - 6;
-                        return e < -118 ? -118 : e;
-                    };
-                    const int ke = exponent(largest_k), ve = exponent(largest_v);
+                    const int e = (int)(largest_v >> 23) - 127 + 1 - 6, ve = e < -118 ? -118 : e;
                     auto halves = [](float s) {  // as two fp16 numbers, each twice
                         const uint32_t hi = f16x2(s, s);
                         float back;
                         asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, a;\n\t}" : "=f"(back) : "r"(hi));
                         return make_uint2(hi, f16x2(s - back, s - back));
                     };
-                    if (lane == 0) {
-                        sh.kexp[m] = ke;
-                        sh.vexp[m] = ve;
-                    }
+                    if (lane == 0) sh.vexp[m] = ve;
 #pragma unroll
                     for (int z = 0; z < 4; ++z) {
-                        sh.ksc[m][32 * z + lane] = halves(ks[z] * power_of_two(-ke));
+                        sh.ksc[m][32 * z + lane] = ks[z] * a.scale_log2;
                         sh.vsc[m][32 * z + lane] = halves(vs[z] * power_of_two(-ve));
                     }
                 }
