@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(MW* KW * 32, (MW * MT * 16 == 64 || DP == 256)
     pdl_trigger();
     pdl_wait();
     AttnTile t;
-    if (!sv::attn_tile(a, pairs, blockIdx.x, S::ROWS, t)) return;
+    if (!sv::attn_tile(a, pairs, blockIdx.x, S::ROWS, 1, t)) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wk = warp % KW, wm = warp / KW;
     const int D = a.c.dim, row_bytes = D * S::ES;
     const int tiles = (t.end - t.begin + TN - 1) / TN;
@@ -591,13 +591,9 @@ cudaError_t launch_shape(const AttnArgs& a, int pairs, unsigned ctas, cudaStream
 
 template <int DP, bool E4M3>
 cudaError_t launch_rows(const AttnArgs& a, int pairs, int tile_rows, unsigned ctas, cudaStream_t stream) {
-    if (tile_rows == 16) return launch_shape<DP, 1, 1, E4M3>(a, pairs, ctas, stream);
-    if constexpr (DP == 256) {
-        return launch_shape<DP, 2, 1, E4M3>(a, pairs, ctas, stream);
-    } else {
-        if (tile_rows == 32) return launch_shape<DP, 1, 2, E4M3>(a, pairs, ctas, stream);
-        return launch_shape<DP, 2, 2, E4M3>(a, pairs, ctas, stream);
-    }
+    if constexpr (DP == 256)
+        if (tile_rows == 32) return launch_shape<DP, 2, 1, E4M3>(a, pairs, ctas, stream);
+    return launch_shape<DP, 1, 1, E4M3>(a, pairs, ctas, stream);
 }
 
 constexpr int kMaxB = 65535;
@@ -606,17 +602,24 @@ constexpr int kMaxQ = 65536;
 struct Plan {
     int tile_rows, m_tiles, splits, chunk;
     int64_t tiles, whole, ctas;
+    bool dual;  // a CTA takes two splits
     size_t ws;
 };
 
 // How a call is cut: tiles of query rows, and stretches of positions where there are too
 // few tiles to fill the SMs.
-Plan make_plan(int B, int Q, int Hq, int H, int D, int max_len, int num_sms) {
+Plan make_plan(int B, int Q, int Hq, int H, int D, bool e4m3, int max_len, int num_sms) {
     Plan p{};
     if (max_len > sv::PAGED_MAX_POS) max_len = sv::PAGED_MAX_POS;
     const int64_t rows = (int64_t)Q * (Hq / H);
     if (D > 128) p.tile_rows = rows <= 16 ? 16 : 32;
-    else p.tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+    else if (rows > 128) p.tile_rows = 256;
+    // Sixteen rows or fewer waste most of a 128-row product.  On one GB300, 32 over 8 heads of
+    // 128, one query: 64 contexts of 4096 208 us (mma.sync) against 243 (tcgen05), e4m3 201
+    // against 328; one context of 2000 16.5 against 20.7, of 8000 33.5 against 24.7, of 131072
+    // 127 against 102.  17 rows and more: 64 x 300 x 24 rows 105 against 49 us.
+    else if (rows > 16 || (!e4m3 && max_len >= 4096 && (int64_t)B * H <= num_sms)) p.tile_rows = 128;
+    else p.tile_rows = 16;
     p.m_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
     p.tiles = (int64_t)B * H * p.m_tiles;
     const bool large = p.tile_rows >= 128;  // one such CTA fills an SM
@@ -624,23 +627,30 @@ Plan make_plan(int B, int Q, int Hq, int H, int D, int max_len, int num_sms) {
     // Enough CTAs that rows of unequal length even out: four per SM.  Large tiles: three per
     // SM where there are fewer tiles than SMs; else whole waves of tiles, and what is left
     // over split so that it fills the last wave.
-    int64_t splits;
-    if (!large) {
+    p.dual = p.tile_rows == 128 && max_len >= 512;
+    int64_t splits, least = 128;  // positions worth a split
+    if (p.dual) {
+        least = 256;
+        splits = 2 * ((B == 1 ? 1LL : 3LL) * num_sms / p.tiles);
+        if (splits < 2) splits = 2;
+    } else if (!large) {
         splits = (4LL * num_sms + p.tiles - 1) / p.tiles;
     } else if (p.tiles < num_sms) {
+        least = 1024;
         splits = 3LL * num_sms / p.tiles;
     } else {
+        least = 1024;
         p.whole = p.tiles / num_sms * num_sms;
         splits = p.tiles > p.whole ? num_sms / (p.tiles - p.whole) : 1;
     }
-    const int64_t least = large ? 1024 : 128;  // positions worth a CTA
     if (splits > ((int64_t)max_len + least - 1) / least) splits = ((int64_t)max_len + least - 1) / least;
     if (splits > 256) splits = 256;
     if (splits < 1) splits = 1;
     p.chunk = (int)((((int64_t)max_len + splits - 1) / splits + tn - 1) / tn * tn);
     p.splits = (int)(((int64_t)max_len + p.chunk - 1) / p.chunk);
+    if (p.dual) p.splits += p.splits & 1;
     if (p.splits <= 1) p.whole = p.tiles;
-    p.ctas = p.whole + (p.tiles - p.whole) * p.splits;
+    p.ctas = p.whole + (p.tiles - p.whole) * p.splits / (p.dual ? 2 : 1);
     p.ws = (size_t)(p.tiles - p.whole) * p.splits * p.tile_rows * (D + 1) * sizeof(float);
     return p;
 }
@@ -670,7 +680,7 @@ size_t spec_paged_attention_workspace_size(int B, int Q, int num_q_heads, int nu
     if (!sizes_ok(B, Q, num_q_heads, num_heads, head_dim, max_len) || B == 0) return 0;
     if (dtype != SV_CACHE_BF16 && dtype != SV_CACHE_E4M3) return 0;
     const int sms = sm_count();
-    return sms ? make_plan(B, Q, num_q_heads, num_heads, head_dim, max_len, sms).ws : 0;
+    return sms ? make_plan(B, Q, num_q_heads, num_heads, head_dim, dtype == SV_CACHE_E4M3, max_len, sms).ws : 0;
 }
 
 sv_status spec_paged_attention(const void* q, const int64_t* q_stride, int num_q_heads, const sv_paged_cache* cache,
@@ -691,11 +701,12 @@ sv_status spec_paged_attention(const void* q, const int64_t* q_stride, int num_q
         return SV_ERR_UNSUPPORTED;
     const int sms = sm_count();
     if (!sms) return sv::launch_status(cudaErrorInvalidDevice);
-    Plan p = make_plan(B, Q, num_q_heads, cache->num_heads, D, max_len, sms);
+    Plan p = make_plan(B, Q, num_q_heads, cache->num_heads, D, cache->dtype == SV_CACHE_E4M3, max_len, sms);
     if (p.ws && (!workspace || ws_bytes < p.ws || (uintptr_t)workspace % 16)) {
         p.whole = p.ctas = p.tiles;
         p.splits = 1;
         p.chunk = sv::PAGED_MAX_POS;
+        p.dual = false;
         p.ws = 0;
     }
     if (p.ctas >= ((int64_t)1 << 31)) return SV_ERR_UNSUPPORTED;
@@ -725,7 +736,7 @@ sv_status spec_paged_attention(const void* q, const int64_t* q_stride, int num_q
     const int pairs = B * cache->num_heads;
     const unsigned ctas = (unsigned)p.ctas;
     cudaError_t e;
-    if (p.tile_rows >= 128) e = sv::launch_attn_tc(a, pairs, e4m3, p.tile_rows, ctas, s);
+    if (p.tile_rows >= 128) e = sv::launch_attn_tc(a, pairs, e4m3, p.tile_rows, p.dual, ctas, s);
     else if (D <= 64) e = e4m3 ? launch_rows<64, true>(a, pairs, p.tile_rows, ctas, s) : launch_rows<64, false>(a, pairs, p.tile_rows, ctas, s);
     else if (D <= 128) e = e4m3 ? launch_rows<128, true>(a, pairs, p.tile_rows, ctas, s) : launch_rows<128, false>(a, pairs, p.tile_rows, ctas, s);
     else e = e4m3 ? launch_rows<256, true>(a, pairs, p.tile_rows, ctas, s) : launch_rows<256, false>(a, pairs, p.tile_rows, ctas, s);

@@ -6,6 +6,8 @@
 // order r = i * group + g, so the queries that share a cache head share its loads.
 #pragma once
 
+#include <cuda.h>
+
 #include "sv_internal.h"
 #include "sv_paged.cuh"
 
@@ -47,6 +49,7 @@ struct AttnTile {
     int b, h, mt, split;
     int base, n;       // positions before the chunk, real queries
     int begin, end;    // this CTA's positions
+    int end2;          // of a second split behind them, where a CTA takes two (end: it has none)
     int active;        // splits of this row tile that have positions
     int64_t part;      // first row of this CTA's partial results
 };
@@ -65,16 +68,18 @@ __device__ __forceinline__ int attn_active(const AttnArgs& a, int end) {
     return n < a.splits ? n : a.splits;
 }
 
-// The work of CTA `id` (pairs: batch rows times cache heads); false where it has none.
-__device__ __forceinline__ bool attn_tile(const AttnArgs& a, int pairs, unsigned id, int tile_rows, AttnTile& t) {
+// The work of CTA `id` (pairs: batch rows times cache heads; per: splits that a CTA takes);
+// false where it has none.
+__device__ __forceinline__ bool attn_tile(const AttnArgs& a, int pairs, unsigned id, int tile_rows, int per, AttnTile& t) {
     const bool whole = id < (unsigned)a.whole;
-    const unsigned rest = id - (unsigned)a.whole;
-    const AttnPlace p = attn_place(a, pairs, whole ? id : (unsigned)a.whole + rest / (unsigned)a.splits);
+    const unsigned rest = id - (unsigned)a.whole, each = (unsigned)(a.splits / per);
+    const unsigned tile = rest / each;  // among the split ones
+    const AttnPlace p = attn_place(a, pairs, whole ? id : (unsigned)a.whole + tile);
     t.b = p.b;
     t.h = p.h;
     t.mt = p.mt;
-    t.split = whole ? 0 : (int)(rest % (unsigned)a.splits);
-    t.part = whole ? 0 : (int64_t)rest * tile_rows;
+    t.split = whole ? 0 : (int)(rest % each) * per;
+    t.part = whole ? 0 : ((int64_t)tile * a.splits + t.split) * tile_rows;
     if (!paged_row(a.c, a.base, a.new_len, t.b, a.Q, t.base, t.n)) return false;
     if ((int64_t)t.mt * tile_rows >= (int64_t)t.n * a.group) return false;
     const int end = attn_tile_end(t.base, t.n, a.group, t.mt, tile_rows, a.tree_mask != nullptr);
@@ -82,6 +87,7 @@ __device__ __forceinline__ bool attn_tile(const AttnArgs& a, int pairs, unsigned
     if (t.split >= t.active) return false;
     t.begin = t.split * a.chunk;
     t.end = t.split == t.active - 1 ? end : t.begin + a.chunk;
+    t.end2 = t.split + 1 >= t.active ? t.end : t.split + 2 == t.active ? end : t.end + a.chunk;
     return true;
 }
 
@@ -126,8 +132,75 @@ __device__ __forceinline__ int64_t attn_row(const AttnArgs& a, const AttnTile& t
 
 __device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) < pos_inf()); }
 
+// One box of a page (some elements x rows of one head) by the copy engine; a page
+// outside the cache reads as zeros.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int row, int head, int page, uint64_t* bar) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+                 "l"(map), "r"(x), "r"(row), "r"(head), "r"(page), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// Takes values that are not finite out of 16 bytes (codes, or bf16); true if there were any.
+template <bool E4M3>
+__device__ __forceinline__ bool sanitise(uint4& v) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        constexpr uint32_t ones = E4M3 ? 0x7fu : 0x7f80u, all = E4M3 ? 0xffu : 0xffffu;
+#pragma unroll
+        for (int y = 0; y < 32; y += E4M3 ? 8 : 16)
+            if (((w[i] >> y) & ones) == ones) {
+                w[i] &= ~(all << y);
+                bad = true;
+            }
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+    return bad;
+}
+
+// cuTensorMapEncodeTiled, found through the runtime (the library does not link the driver).
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline EncodeTiled encode_tiled() {
+    static const EncodeTiled f = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return f;
+}
+
+// A map of pages [page][head][row][element] for boxes of `rows` rows of `width` elements.
+inline bool page_map(CUtensorMap* map, const void* pages, const PagedCache& c, bool e4m3, int width, int rows,
+                     CUtensorMapSwizzle swizzle) {
+    const EncodeTiled f = encode_tiled();
+    if (!f) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page_size, (cuuint64_t)c.heads, (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.row_stride, (cuuint64_t)c.head_stride, (cuuint64_t)c.page_stride};
+    const cuuint32_t box[4] = {(cuuint32_t)width, (cuuint32_t)rows, 1, 1}, ones[4] = {1, 1, 1, 1};
+    return f(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pages), dims,
+             strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows per box where the copy engine can fill a tile of `tile` positions (pages of 8 rows up
+// that divide it, or of a multiple of it: a box lies in one page and starts on a swizzle
+// atom), else 0: cp.async then copies row by row.
+inline int page_box_rows(const PagedCache& c, int tile) {
+    if (c.page_size >= tile) return c.page_size % tile == 0 ? tile : 0;
+    return c.page_size >= 8 && tile % c.page_size == 0 ? c.page_size : 0;
+}
+
 // The kernel for many query rows per cache head, head_dim <= 128 (sv_attention_tc.cu):
-// tile_rows 128 or 256.
-cudaError_t launch_attn_tc(const AttnArgs& a, int pairs, bool e4m3, int tile_rows, unsigned ctas, cudaStream_t stream);
+// tile_rows 128 or 256; dual (tile_rows 128): a CTA takes two splits.
+cudaError_t launch_attn_tc(const AttnArgs& a, int pairs, bool e4m3, int tile_rows, bool dual, unsigned ctas,
+                           cudaStream_t stream);
 
 }  // namespace sv

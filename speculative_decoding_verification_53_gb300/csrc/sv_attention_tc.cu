@@ -17,6 +17,11 @@
 // Dependences: full/empty barriers per buffer; s_full (S is in TMEM, and so is the last
 // O, since a commit covers every earlier product); p_full (P is written, O rescaled).
 //
+// DUAL: for 128 query rows or fewer the two warpgroups take the same rows and two stretches of
+// positions, whose tiles alternate (tile v belongs to stretch v & 1): one row tile alone leaves
+// the tensor cores and the copies waiting for its softmax (3600 cycles a tile of 64 KB; the
+// memory brings one in 3000).  The stretches' results are joined as any splits'.
+//
 // The running maximum is moved only when it grows by more than 2^8: probabilities may
 // then reach 256 instead of 1, harmless in fp32 sums and bf16's range, and the rescale of
 // O in TMEM becomes rare.
@@ -34,8 +39,6 @@
 // Every wait is bounded; a CTA whose wait runs out writes NaN for its rows, which a verify
 // reports as invalid data, and frees its TMEM.
 #include <cstdint>
-
-#include <cuda.h>
 
 #include "spec_paged_kv.h"
 #include "sv_attention.cuh"
@@ -60,9 +63,10 @@ constexpr int META = 4;          // tiles whose hole bits and scales are kept
 constexpr float RESCALE = 8.0f;  // log2 of how far the maximum may lag
 constexpr float RAISE = 7.0f;    // e4m3: log2 of the probabilities' factor; 2^(8 + 7) is within fp16
 
-template <int DP, int MQ, bool E4M3>
+template <int DP, int MQ, bool E4M3, bool DUAL>
 struct Tc {
-    static constexpr int ROWS = 128 * MQ;
+    static constexpr int QM = DUAL ? 1 : MQ;       // query matrices
+    static constexpr int ROWS = 128 * QM;
     static constexpr int SOFTMAX = 128 * MQ;
     static constexpr int THREADS = SOFTMAX + 256;  // whole warpgroups, as setmaxnreg wants
     // Registers: the launch gives every thread 65536 / THREADS; softmax threads hold a row of
@@ -73,9 +77,9 @@ struct Tc {
     static constexpr int R_LOAD = MQ == 1 ? 136 : E4M3 ? 96 : 80, R_MMA = 64;
     static_assert(SOFTMAX * R_SOFTMAX + 128 * (R_LOAD + R_MMA) <= (MQ == 2 ? 65536 : 64512), "registers of the launch");
     static constexpr int MAT = (DP / 64) * BLK;   // a tile of keys, values or queries
-    static constexpr int NB = DP == 64 ? 6 : E4M3 ? 3 : 4;   // buffers of the ring
+    static constexpr int NB = DP == 64 ? 6 : (E4M3 ? 3 : 4) + (DUAL ? 1 : 0);  // buffers of the ring
     static constexpr int RAW = E4M3 ? 3 : 0;      // e4m3: items whose codes are in flight
-    static constexpr int SMEM = (MQ + NB) * MAT + RAW * MAT / 2 + 1024;  // and room to align
+    static constexpr int SMEM = (QM + NB) * MAT + RAW * MAT / 2 + 1024;  // and room to align
     static constexpr int S_COL = 0, O_COL = 128 * MQ;    // TMEM columns
     static constexpr int COLS = MQ == 2 ? 512 : 256;
 };
@@ -160,14 +164,6 @@ __host__ __device__ constexpr uint32_t instruction(int n, bool b_mn, bool f16) {
     return 1u << 4 | (f16 ? 0u : 1u << 7 | 1u << 10) | (b_mn ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
 }
 
-// One box of a page (64 or DP elements x rows of one head) by the copy engine; a page
-// outside the cache reads as zeros.
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int row, int head, int page, uint64_t* bar) {
-    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-                 "l"(map), "r"(x), "r"(row), "r"(head), "r"(page), "r"(smem_u32(bar))
-                 : "memory");
-}
-
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
@@ -185,6 +181,12 @@ __device__ __forceinline__ void sts16(uint32_t at, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+__device__ __forceinline__ uint2 lds8(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
 // 16-byte piece c (of 8 elements) of row r in a tile of 64-element blocks.
 __device__ __forceinline__ uint32_t piece(int r, int c) {
     return (uint32_t)((c >> 3) * BLK + r * 128 + (((c & 7) ^ (r & 7)) << 4));
@@ -199,26 +201,21 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Sixteen e4m3 codes in fp16, times a scale (x: twice its fp16, y: twice what that leaves) if
-// asked, as two 16-byte pieces.
+// Eight e4m3 codes in fp16, times a scale (x: twice its fp16, y: twice what that leaves) if asked.
 template <bool SCALE>
-__device__ __forceinline__ void widen16(uint4 w, uint2 scale, uint4& a, uint4& b) {
-    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-    uint32_t out[8];
+__device__ __forceinline__ uint4 widen8(uint2 w, uint2 scale) {
+    uint32_t out[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i)
         asm("{.reg .b16 t, u;\n\tmov.b32 {t, u}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
             : "=r"(out[2 * i]), "=r"(out[2 * i + 1])
-            : "r"(in[i]));
-        if (!SCALE) continue;
+            : "r"(i ? w.y : w.x));
 #pragma unroll
-        for (int z = 2 * i; z < 2 * i + 2; ++z)
-            asm("{.reg .b32 t;\n\tmul.rn.f16x2 t, %0, %2;\n\tfma.rn.f16x2 %0, %0, %1, t;\n\t}"
-                : "+r"(out[z])
-                : "r"(scale.x), "r"(scale.y));
-    }
-    a = make_uint4(out[0], out[1], out[2], out[3]);
-    b = make_uint4(out[4], out[5], out[6], out[7]);
+    for (int z = 0; SCALE && z < 4; ++z)
+        asm("{.reg .b32 t;\n\tmul.rn.f16x2 t, %0, %2;\n\tfma.rn.f16x2 %0, %0, %1, t;\n\t}"
+            : "+r"(out[z])
+            : "r"(scale.x), "r"(scale.y));
+    return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 // Two fp32 values rounded to fp16 (nearest even), lo in the low half.
@@ -231,25 +228,6 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
 // 2^e as fp32 (0 or infinity beyond the normal numbers).
 __device__ __forceinline__ float power_of_two(int e) {
     return e < -126 ? 0.0f : e > 127 ? sv::pos_inf() : __int_as_float((e + 127) << 23);
-}
-
-// Takes values that are not finite out of 16 bytes (codes, or bf16); true if there were any.
-template <bool E4M3>
-__device__ __forceinline__ bool sanitise(uint4& v) {
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        constexpr uint32_t ones = E4M3 ? 0x7fu : 0x7f80u, all = E4M3 ? 0xffu : 0xffffu;
-#pragma unroll
-        for (int y = 0; y < 32; y += E4M3 ? 8 : 16)
-            if (((w[i] >> y) & ones) == ones) {
-                w[i] &= ~(all << y);
-                bad = true;
-            }
-    }
-    v = make_uint4(w[0], w[1], w[2], w[3]);
-    return bad;
 }
 
 // Scores of a row, scaled in place (by sc, and each by its own factor where given), -inf where hidden.
@@ -288,22 +266,29 @@ struct __align__(16) Shared {
     __align__(16) float ksc[META][TN];  // e4m3: a position's key scale times the score factor
     __align__(16) uint2 vsc[META][TN];  // its value scale times 2^-vexp, as two fp16 numbers
     int vexp[META];
+    float row_factor[128];  // DUAL: what a row's scores are multiplied by
 };
 
-template <int DP, int MQ, bool E4M3>
+template <int DP, int MQ, bool E4M3, bool DUAL>
 __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap k_map,
                               const __grid_constant__ CUtensorMap v_map, const int box_rows, const int pairs) {
-    using S = Tc<DP, MQ, E4M3>;
+    using S = Tc<DP, MQ, E4M3, DUAL>;
     extern __shared__ unsigned char raw[];
     __shared__ Shared sh;
     pdl_trigger();
     pdl_wait();
     AttnTile t;
-    if (!sv::attn_tile(a, pairs, blockIdx.x, S::ROWS, t)) return;
+    if (!sv::attn_tile(a, pairs, blockIdx.x, S::ROWS, DUAL ? 2 : 1, t)) return;
     const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;  // queries, then the ring
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = a.c.dim, rows = t.n * a.group;
-    const int tiles = (t.end - t.begin + TN - 1) / TN;
+    // DUAL: a second stretch, of as many positions, fewer or none, follows the first
+    const int mid = t.end, last_end = DUAL ? t.end2 : t.end;
+    const int longest = DUAL && last_end - mid > mid - t.begin ? last_end - mid : mid - t.begin;
+    const int tiles = (DUAL ? 2 : 1) * ((longest + TN - 1) / TN);
+    // first position of tile v, and the end of its stretch
+    auto start = [&](int v) { return DUAL ? (v & 1 ? mid : t.begin) + (v >> 1) * TN : t.begin + v * TN; };
+    auto stop = [&](int v) { return DUAL && (v & 1) ? last_end : mid; };
     // Positions below this are seen by every query of the CTA.
     const int open = a.tree_mask ? t.base + 1 : t.base + t.mt * S::ROWS / a.group + 1;
 
@@ -316,7 +301,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         }
         for (int i = 0; i < META; ++i) {
             mbar_init(&sh.note_full[i], 1);
-            mbar_init(&sh.note_empty[i], E4M3 ? 4 * MQ + 4 : 4 * MQ);
+            mbar_init(&sh.note_empty[i], 4 * S::QM + (E4M3 ? 4 : 0));
         }
         for (int i = 0; i < MQ; ++i) {
             mbar_init(&sh.s_full[i], 1);
@@ -324,7 +309,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             mbar_init(&sh.p_full[i][1], 4);
             mbar_init(&sh.o_full[i], 1);
         }
-        mbar_init(&sh.q_full, 4 * MQ);
+        mbar_init(&sh.q_full, 4 * S::QM);
         mbar_init(&sh.drain, 1);
         for (int i = 0; i < S::RAW; ++i) {
             mbar_init(&sh.raw_full[i], 1);
@@ -338,7 +323,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    const uint32_t ring = smem0 + MQ * S::MAT;
+    const uint32_t ring = smem0 + S::QM * S::MAT;
     bool ok = true;
 
     if (warp < 4 * MQ) {
@@ -346,7 +331,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::R_SOFTMAX));
         const int q = warp >> 2;
         float own = 1.0f;  // e4m3: what the row's scores are multiplied by
-        {   // the queries of this warp's rows, zero behind the last real one
+        if (!DUAL || q == 0) {  // the queries of this warp's rows, zero behind the last real one
             constexpr int CH = DP / 8, RPI = 32 / CH;
             const int c = lane % CH, R = t.mt * S::ROWS + q * 128 + (warp & 3) * 32 + lane;
             const int y = R / a.group;
@@ -382,12 +367,16 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                                          f16x2(sv::bf16_lo(v.z) * f, sv::bf16_hi(v.z) * f), f16x2(sv::bf16_lo(v.w) * f, sv::bf16_hi(v.w) * f)));
                 }
                 own = power_of_two(-up);
+                if (DUAL) sh.row_factor[r] = own;
             }
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.q_full);
+        } else if (E4M3) {
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.q_full, 0));
+            own = sh.row_factor[(warp & 3) * 32 + lane];
         }
-        const int R = t.mt * S::ROWS + q * 128 + (warp & 3) * 32 + lane;
+        const int R = t.mt * S::ROWS + (DUAL ? 0 : q * 128) + (warp & 3) * 32 + lane;
         const bool live = R < rows;
         const int i = live ? R / a.group : 0;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes per warp, lane field at bit 16
@@ -395,12 +384,24 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         const float sc = a.scale_log2;
         float mx = neg_inf(), l = 0.0f;
         int vexp = 0;  // e4m3: O is held times 2^-vexp
-        for (int j = 0; j < tiles; ++j) {
+        const bool idle = t.mt * S::ROWS + (DUAL ? 0 : q * 128) + (warp & 3) * 32 >= rows;  // no row of this warp is real
+        for (int j = 0; j < (DUAL ? tiles / 2 : tiles) && ok; ++j) {
+            const int u = DUAL ? 2 * j + q : j;  // the tile
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.s_full[q], j & 1));
             if (!ok) break;
             tc_fence_after();
-            const int tile0 = t.begin + j * TN, m = j % META;
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.note_full[m], (j / META) & 1));
+            if (idle) {  // whatever its rows of P hold stays in its rows of O
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh.p_full[q][0]);
+                    mbar_arrive(&sh.p_full[q][1]);
+                    mbar_arrive(&sh.note_empty[u % META]);
+                }
+                continue;
+            }
+            const int tile0 = start(u), m = u % META;
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.note_full[m], (u / META) & 1));
             if (!ok) break;
             uint32_t see[4];
 #pragma unroll
@@ -478,12 +479,16 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             l += sum0.x + sum0.y;
         }
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.o_full[q], 0));
+        // DUAL: rows leave through memory that the other stretch's products read until they end
+        if (DUAL && ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.o_full[q ^ 1], 0));
+        const bool mine = !DUAL || t.split + q < t.active;  // the stretch exists
+        const int first = start(DUAL ? q : 0), last = stop(DUAL ? q : 0);
         if (!ok) sh.failed = 1;
         tc_fence_after();
         float inv = !ok ? __int_as_float(0x7fffffff) : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
         const float lse2 = !ok ? inv : l == 0.0f ? neg_inf() : mx + log2f(l) - (E4M3 ? RAISE : 0.0f);
-        const int64_t row = live ? sv::attn_row(a, t, R) : 0, part = t.part + (R - t.mt * S::ROWS);
-        if (live) {
+        const int64_t row = live ? sv::attn_row(a, t, R) : 0, part = t.part + (DUAL ? q * S::ROWS : 0) + (R - t.mt * S::ROWS);
+        if (live && mine) {
             if (t.active > 1) a.part_lse[part] = lse2;
             else if (a.lse) a.lse[row] = lse2 * 0.69314718055994531f;
         }
@@ -493,53 +498,55 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         // covers whole rows: a lane writing its own row touched 32 lines per store and cost
         // 15000 cycles a CTA.  Half a row at a time, 16-byte pieces swizzled by the row.
         constexpr int CW = DP / 2, PC = CW / 4;
-        const uint32_t stage = smem0 + q * S::MAT + (warp & 3) * (S::MAT / 4);
+        if (!idle && mine) {
+            const uint32_t stage = smem0 + q * S::MAT + (warp & 3) * (S::MAT / 4);
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-            uint32_t v[CW];
-            __syncwarp();
+            for (int c = 0; c < 2; ++c) {
+                uint32_t v[CW];
+                __syncwarp();
 #pragma unroll
-            for (int z = 0; z < CW; z += 32) tmem_ld32(o_at + CW * c + z, v + z);
-            tc_wait_ld();
-            if (live && patch) {
-                // values that are not finite, for the queries that see them
-                int from = t.begin;
-                if (open > t.begin) from += (open - t.begin) / TN * TN;
-                for (int pos = from; pos < t.end; ++pos) {
-                    if (!(sv::attn_visible(a, t, i, pos) & 1u)) continue;
+                for (int z = 0; z < CW; z += 32) tmem_ld32(o_at + CW * c + z, v + z);
+                tc_wait_ld();
+                if (live && patch) {
+                    // values that are not finite, for the queries that see them
+                    int from = first;
+                    if (open > first) from += (open - first) / TN * TN;
+                    for (int pos = from; pos < last; ++pos) {
+                        if (!(sv::attn_visible(a, t, i, pos) & 1u)) continue;
 #pragma unroll
-                    for (int k = 0; k < CW; ++k) {
-                        if (CW * c + k >= D) break;
-                        const float w = sv::attn_value<E4M3>(a, t, pos, CW * c + k);
-                        if (sv::not_finite(w)) v[k] = __float_as_uint(__uint_as_float(v[k]) + w);
+                        for (int k = 0; k < CW; ++k) {
+                            if (CW * c + k >= D) break;
+                            const float w = sv::attn_value<E4M3>(a, t, pos, CW * c + k);
+                            if (sv::not_finite(w)) v[k] = __float_as_uint(__uint_as_float(v[k]) + w);
+                        }
                     }
                 }
-            }
 #pragma unroll
-            for (int k = 0; k < PC; ++k)
-                sts16(stage + 16 * (PC * lane + (k ^ (lane & (PC - 1)))),
-                      make_uint4(__float_as_uint(__uint_as_float(v[4 * k]) * inv), __float_as_uint(__uint_as_float(v[4 * k + 1]) * inv),
-                                 __float_as_uint(__uint_as_float(v[4 * k + 2]) * inv), __float_as_uint(__uint_as_float(v[4 * k + 3]) * inv)));
-            __syncwarp();
-            if (t.active > 1) {
-                const int k = lane % PC, d = CW * c + 4 * k;
-                for (int x = 0; x < PC; ++x) {
-                    const int r = (32 / PC) * x + lane / PC;
-                    const int64_t to = __shfl_sync(0xffffffffu, live ? part : (int64_t)-1, r);
-                    if (to >= 0 && d < D)
-                        *reinterpret_cast<uint4*>(a.part_o + to * D + d) = lds16(stage + 16 * (PC * r + (k ^ (r & (PC - 1)))));
-                }
-            } else {
-                const int k = 2 * (lane % (PC / 2)), d = CW * c + 4 * k;
-                for (int x = 0; x < PC / 2; ++x) {
-                    const int r = (64 / PC) * x + lane / (PC / 2);
-                    const int64_t to = __shfl_sync(0xffffffffu, live ? row : (int64_t)-1, r);
-                    if (to >= 0 && d < D) {
-                        const uint4 f = lds16(stage + 16 * (PC * r + (k ^ (r & (PC - 1)))));
-                        const uint4 g = lds16(stage + 16 * (PC * r + ((k + 1) ^ (r & (PC - 1)))));
-                        auto pair = [](uint32_t lo, uint32_t hi) { return sv::bf16x2(__uint_as_float(lo), __uint_as_float(hi)); };
-                        *reinterpret_cast<uint4*>(a.out + to * D + d) =
-                            make_uint4(pair(f.x, f.y), pair(f.z, f.w), pair(g.x, g.y), pair(g.z, g.w));
+                for (int k = 0; k < PC; ++k)
+                    sts16(stage + 16 * (PC * lane + (k ^ (lane & (PC - 1)))),
+                          make_uint4(__float_as_uint(__uint_as_float(v[4 * k]) * inv), __float_as_uint(__uint_as_float(v[4 * k + 1]) * inv),
+                                     __float_as_uint(__uint_as_float(v[4 * k + 2]) * inv), __float_as_uint(__uint_as_float(v[4 * k + 3]) * inv)));
+                __syncwarp();
+                if (t.active > 1) {
+                    const int k = lane % PC, d = CW * c + 4 * k;
+                    for (int x = 0; x < PC; ++x) {
+                        const int r = (32 / PC) * x + lane / PC;
+                        const int64_t to = __shfl_sync(0xffffffffu, live ? part : (int64_t)-1, r);
+                        if (to >= 0 && d < D)
+                            *reinterpret_cast<uint4*>(a.part_o + to * D + d) = lds16(stage + 16 * (PC * r + (k ^ (r & (PC - 1)))));
+                    }
+                } else {
+                    const int k = 2 * (lane % (PC / 2)), d = CW * c + 4 * k;
+                    for (int x = 0; x < PC / 2; ++x) {
+                        const int r = (64 / PC) * x + lane / (PC / 2);
+                        const int64_t to = __shfl_sync(0xffffffffu, live ? row : (int64_t)-1, r);
+                        if (to >= 0 && d < D) {
+                            const uint4 f = lds16(stage + 16 * (PC * r + (k ^ (r & (PC - 1)))));
+                            const uint4 g = lds16(stage + 16 * (PC * r + ((k + 1) ^ (r & (PC - 1)))));
+                            auto pair = [](uint32_t lo, uint32_t hi) { return sv::bf16x2(__uint_as_float(lo), __uint_as_float(hi)); };
+                            *reinterpret_cast<uint4*>(a.out + to * D + d) =
+                                make_uint4(pair(f.x, f.y), pair(f.z, f.w), pair(g.x, g.y), pair(g.z, g.w));
+                        }
                     }
                 }
             }
@@ -553,8 +560,8 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         const int w = warp - 4 * MQ;
         const unsigned char* mat[2] = {a.c.k + t.h * a.c.head_stride, a.c.v + t.h * a.c.head_stride};
         auto look_up = [&](int tile) {
-            const int pos = t.begin + tile * TN + 32 * w + lane;
-            if (box_rows || tile >= tiles || pos >= t.end) return (int64_t)-1;
+            const int pos = start(tile) + 32 * w + lane;
+            if (box_rows || tile >= tiles || pos >= stop(tile)) return (int64_t)-1;
             int row;
             const int page = sv::paged_place(a.c, t.b, pos, row);
             return page < 0 ? (int64_t)-1 : page * a.c.page_stride + row * a.c.row_stride;
@@ -573,9 +580,9 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 for (int x = 0; x < 32 / RPI; ++x) {
                     const uint32_t at = ring + buf * S::MAT + place(x);
                     uint4 v = lds16(at);
-                    if (t.begin + tile * TN + 32 * w + x * RPI + r0 >= t.end) {
+                    if (start(tile) + 32 * w + x * RPI + r0 >= stop(tile)) {
                         sts16(at, make_uint4(0u, 0u, 0u, 0u));
-                    } else if (sanitise<false>(v)) {
+                    } else if (sv::sanitise<false>(v)) {
                         sts16(at, v);
                         bad = true;
                     }
@@ -587,8 +594,8 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 uint32_t lands = 0;  // phase of each buffer's barrier
                 // the wait for the first such tile covers all tiles before it
                 const uint32_t patience = sv::WAIT_LIMIT_NS + (tiles < 150000 ? tiles * 20000u : 3000000000u);
-                int j = open > t.begin ? (open - t.begin) / TN : 0;  // the first tile that reaches beyond `open`
-                for (; j < tiles; ++j) {
+                for (int j = 0; j < tiles; ++j) {
+                    if (start(j) + TN <= open) continue;
                     const int buf = (2 * j + 1) % S::NB;
                     ok = __all_sync(0xffffffffu, sv::mbar_wait_bounded_ns(&sh.land[buf], (lands >> buf) & 1, patience));
                     if (!ok) break;
@@ -616,7 +623,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                         off = off1;
                         off1 = look_up(tile + 2);
                     }
-                    if ((n & 1) && t.begin + tile * TN + TN > open) {
+                    if ((n & 1) && start(tile) + TN > open) {
                         cp_wait_all();
                         look_over(tile, buf);
                         mbar_arrive(&sh.full[buf]);
@@ -677,28 +684,35 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     if (!ok) break;
                 }
                 const uint2* scale = sh.vsc[j % META] + 32 * w + r0;
-                const bool clean = (n & 1) && t.begin + j * TN + TN > open;
+                const bool clean = (n & 1) && start(j) + TN > open;
                 const uint32_t dst = ring + buf * S::MAT, from = mine + (n % S::RAW) * (S::MAT / 2);
+                // Lanes of a row's second 64 elements, whose banks are the first's, take their two
+                // halves in the other order.
                 const int y = (c >> 2) & 1;
                 // A short loop: unrolled in full, this and the softmax ran out of the instruction
                 // caches (3000 cycles an item instead of 600).
 #pragma unroll 1
-                for (int x = 0; x < X; x += 2) {
-                    uint4 g[2];
+                for (int x = 0; x < X; x += 4) {
+                    uint2 g[8];
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) g[z] = lds16(from + (x + z) * step);
+                    for (int z = 0; z < 8; ++z) g[z] = lds8(from + (x + (z >> 1)) * step + 8 * ((z & 1) ^ y));
+                    if (clean) {
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        if (clean) {
-                            if (t.begin + j * TN + 32 * w + (x + z) * RPI + r0 >= t.end) g[z] = make_uint4(0u, 0u, 0u, 0u);
-                            bad |= sanitise<true>(g[z]);
+                        for (int z = 0; z < 8; ++z) {
+                            uint4 h = make_uint4(g[z].x, g[z].y, 0u, 0u);
+                            if (start(j) + 32 * w + (x + (z >> 1)) * RPI + r0 >= stop(j)) h = make_uint4(0u, 0u, 0u, 0u);
+                            bad |= sv::sanitise<true>(h);
+                            g[z] = make_uint2(h.x, h.y);
                         }
-                        uint4 p, q;
-                        if (n & 1) widen16<true>(g[z], scale[(x + z) * RPI], p, q);
-                        else widen16<false>(g[z], make_uint2(0u, 0u), p, q);
-                        // lanes of a row's second 64 elements, whose banks are the first's, swap halves
-                        sts16(dst + place(x + z, y), y ? q : p);
-                        sts16(dst + place(x + z, y ^ 1), y ? p : q);
+                    }
+                    if (n & 1) {
+#pragma unroll
+                        for (int z = 0; z < 8; ++z)
+                            sts16(dst + place(x + (z >> 1), (z & 1) ^ y), widen8<true>(g[z], scale[(x + (z >> 1)) * RPI]));
+                    } else {
+#pragma unroll
+                        for (int z = 0; z < 8; ++z)
+                            sts16(dst + place(x + (z >> 1), (z & 1) ^ y), widen8<false>(g[z], make_uint2(0u, 0u)));
                     }
                 }
                 if (box_rows) {
@@ -725,7 +739,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             // the same in every lane, and known to be
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), sm0 = __shfl_sync(0xffffffffu, smem0, 0);
             const int todo = __shfl_sync(0xffffffffu, tiles, 0);
-            const uint32_t ring0 = sm0 + MQ * S::MAT;
+            const uint32_t ring0 = sm0 + S::QM * S::MAT;
             constexpr uint32_t id_s = instruction(TN, false, E4M3), id_o = instruction(DP, true, E4M3);
             auto full = [&](int n) {
                 const bool there = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[n % S::NB], (n / S::NB) & 1));
@@ -733,7 +747,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 return there;
             };
             auto scores = [&](int q, int n) {  // S_q = Q_q K^T, K in item n
-                const uint64_t qa = operand(sm0 + q * S::MAT, 16, 1024);
+                const uint64_t qa = operand(sm0 + (DUAL ? 0 : q * S::MAT), 16, 1024);
                 const uint64_t ka = operand(ring0 + (n % S::NB) * S::MAT, 16, 1024);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
@@ -742,41 +756,75 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 }
                 tc_commit(&sh.s_full[q], leader);
             };
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.q_full, 0));
-            ok = full(0) && ok;
-            tc_fence_after();
-            if (ok) {
-                #pragma unroll
-                for (int q = 0; q < MQ; ++q) scores(q, 0);
-                tc_commit(&sh.empty[0], leader);
-            }
-            for (int j = 0; j < todo && ok; ++j) {
-                const int nv = 2 * j + 1, nk = 2 * j + 2;
-                ok = full(nv);
-                const uint64_t va = operand(ring0 + (nv % S::NB) * S::MAT, BLK, 1024);
-                for (int q = 0; q < MQ && ok; ++q) {
+            // O_q += P_q V, V in item n, once the halves of P_q of its j-th tile are there
+            auto outputs = [&](int q, int n, int j) {
+                const uint64_t va = operand(ring0 + (n % S::NB) * S::MAT, BLK, 1024);
+                bool there = true;
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.p_full[q][half], j & 1)) && ok;
-                        tc_fence_after();
-                        if (ok) {
+                for (int half = 0; half < 2; ++half) {
+                    there = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.p_full[q][half], j & 1)) && there;
+                    tc_fence_after();
+                    if (there) {
 #pragma unroll
-                            for (int k = 4 * half; k < 4 * half + 4; ++k)
-                                mma_ts(tm + S::O_COL + DP * q, tm + S::S_COL + 128 * q + 8 * k,
-                                       va + k * (2048 >> 4), id_o, j > 0 || k > 0, leader);
-                        }
+                        for (int k = 4 * half; k < 4 * half + 4; ++k)
+                            mma_ts(tm + S::O_COL + DP * q, tm + S::S_COL + 128 * q + 8 * k, va + k * (2048 >> 4), id_o,
+                                   j > 0 || k > 0, leader);
                     }
+                }
+                return there;
+            };
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.q_full, 0));
+            if (DUAL) {
+                // tile u: keys in item 2 u, values in 2 u + 1, of stretch u & 1
+                for (int q = 0; q < 2 && ok; ++q) {
+                    ok = full(2 * q);
+                    tc_fence_after();
+                    if (ok) {
+                        scores(q, 2 * q);
+                        tc_commit(&sh.empty[2 * q % S::NB], leader);
+                    }
+                }
+                for (int u = 0; u < todo && ok; ++u) {
+                    const int q = u & 1, nv = 2 * u + 1, nk = 2 * u + 4;
+                    ok = full(nv);
+                    ok = outputs(q, nv, u >> 1) && ok;
                     if (!ok) break;
-                    if (j + 1 < todo) {
-                        if (q == 0) ok = full(nk);
-                        if (ok) scores(q, nk);
+                    tc_commit(&sh.empty[nv % S::NB], leader);
+                    if (u + 2 < todo) {
+                        ok = full(nk);
+                        if (ok) {
+                            scores(q, nk);
+                            tc_commit(&sh.empty[nk % S::NB], leader);
+                        }
                     } else {
                         tc_commit(&sh.o_full[q], leader);
                     }
                 }
+            } else {
+                ok = full(0) && ok;
+                tc_fence_after();
                 if (ok) {
-                    tc_commit(&sh.empty[nv % S::NB], leader);
-                    if (j + 1 < todo) tc_commit(&sh.empty[nk % S::NB], leader);
+#pragma unroll
+                    for (int q = 0; q < MQ; ++q) scores(q, 0);
+                    tc_commit(&sh.empty[0], leader);
+                }
+                for (int j = 0; j < todo && ok; ++j) {
+                    const int nv = 2 * j + 1, nk = 2 * j + 2;
+                    ok = full(nv);
+                    for (int q = 0; q < MQ && ok; ++q) {
+                        ok = outputs(q, nv, j);
+                        if (!ok) break;
+                        if (j + 1 < todo) {
+                            if (q == 0) ok = full(nk);
+                            if (ok) scores(q, nk);
+                        } else {
+                            tc_commit(&sh.o_full[q], leader);
+                        }
+                    }
+                    if (ok) {
+                        tc_commit(&sh.empty[nv % S::NB], leader);
+                        if (j + 1 < todo) tc_commit(&sh.empty[nk % S::NB], leader);
+                    }
                 }
             }
             if (!ok) {
@@ -790,10 +838,10 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             // are to be looked over land on a barrier of their own.
             const int boxes = TN / box_rows;
             auto box_page = [&](int tile, int& page, int& row) {
-                const int pos = t.begin + tile * TN + lane * box_rows;
+                const int pos = start(tile) + lane * box_rows;
                 page = a.c.num_pages;  // a page outside the cache reads as zeros
                 row = 0;
-                if (lane < boxes && tile < tiles && pos < t.end) {
+                if (lane < boxes && tile < tiles && pos < stop(tile)) {
                     const int p = sv::paged_place(a.c, t.b, pos, row);
                     if (p >= 0) page = p;
                 }
@@ -809,7 +857,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                                     mbar_wait_bounded(E4M3 ? &sh.raw_empty[slot & 3] : &sh.empty[slot], (n / PLACES - 1) & 1));
                     if (!ok) break;
                 }
-                const bool tail = !E4M3 && (n & 1) && t.begin + (n >> 1) * TN + TN > open;
+                const bool tail = !E4M3 && (n & 1) && start(n >> 1) + TN > open;
                 uint64_t* bar = E4M3 ? &sh.raw_full[slot & 3] : tail ? &sh.land[slot] : &sh.full[slot];
                 if (lane == 0) {
                     sv::mbar_arrive_expect_tx(bar, E4M3 ? S::MAT / 2 : S::MAT);
@@ -819,11 +867,11 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 const CUtensorMap* map = n & 1 ? &v_map : &k_map;
                 if (lane < boxes) {
                     if (E4M3) {
-                        tma_box(smem0 + (MQ + S::NB) * S::MAT + slot * (S::MAT / 2) + lane * box_rows * DP, map, 0, row, t.h, page, bar);
+                        sv::tma_box(smem0 + (S::QM + S::NB) * S::MAT + slot * (S::MAT / 2) + lane * box_rows * DP, map, 0, row, t.h, page, bar);
                     } else {
 #pragma unroll
                         for (int z = 0; z < DP / 64; ++z)
-                            tma_box(ring + slot * S::MAT + z * BLK + lane * box_rows * 128, map, 64 * z, row, t.h, page, bar);
+                            sv::tma_box(ring + slot * S::MAT + z * BLK + lane * box_rows * 128, map, 64 * z, row, t.h, page, bar);
                     }
                 }
                 __syncwarp();
@@ -836,23 +884,23 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             if (!ok) {  // copies in flight land before the CTA leaves
                 constexpr int PLACES = E4M3 ? S::RAW : S::NB;
                 for (int z = n > PLACES ? n - PLACES : 0; z < n; ++z)
-                    if (E4M3 || !(z & 1) || t.begin + (z >> 1) * TN + TN <= open)
+                    if (E4M3 || !(z & 1) || start(z >> 1) + TN <= open)
                         (void)mbar_wait_bounded(E4M3 ? &sh.raw_full[z % PLACES & 3] : &sh.full[z % PLACES], (z / PLACES) & 1);
             }
         } else if (warp == 4 * MQ + 6) {
             // ----------------------------------------------------------- notes
             // Which positions of a tile hold something, and e4m3's scales; read ahead, so that
             // nobody else waits for a page table or a scale.
-            uint32_t largest_v = 0u;  // the largest finite value scale so far, as bits
+            uint32_t largest_v = 0u, other_v = 0u;  // the stretches' largest finite value scales so far, as bits
             int64_t at1[4];  // index of the scales of the next tile's positions, -1: nothing there
             float ks[4], vs[4];
             uint32_t bits[4];
             auto look_up = [&](int tile, int64_t (&at)[4]) {
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
-                    const int pos = t.begin + tile * TN + 32 * z + lane;
+                    const int pos = start(tile) + 32 * z + lane;
                     at[z] = -1;
-                    if (tile < tiles && pos < t.end) {
+                    if (tile < tiles && pos < stop(tile)) {
                         int row;
                         const int page = sv::paged_place(a.c, t.b, pos, row);
                         if (page >= 0) at[z] = ((int64_t)page * a.c.heads + t.h) * a.c.page_size + row;
@@ -885,7 +933,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     for (int z = 0; z < 4; ++z) {
                         if (!sv::not_finite(vs[z])) {
                             largest_v = max(largest_v, __float_as_uint(fabsf(vs[z])));
-                        } else if (t.begin + j * TN + TN > open) {
+                        } else if (start(j) + TN > open) {
                             vs[z] = 0.0f;  // put back at the end, as the values are
                             sh.bad = 1;
                         }
@@ -900,6 +948,11 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                         return make_uint2(hi, f16x2(s - back, s - back));
                     };
                     if (lane == 0) sh.vexp[m] = ve;
+                    if (DUAL) {  // the next tile is the other stretch's
+                        const uint32_t x = largest_v;
+                        largest_v = other_v;
+                        other_v = x;
+                    }
 #pragma unroll
                     for (int z = 0; z < 4; ++z) {
                         sh.ksc[m][32 * z + lane] = ks[z] * a.scale_log2;
@@ -923,72 +976,39 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
     }
 }
 
-// cuTensorMapEncodeTiled, found through the runtime (the library does not link the driver).
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiled encode_tiled() {
-    static const EncodeTiled f = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-            r != cudaDriverEntryPointSuccess) {
-            (void)cudaGetLastError();
-            p = nullptr;
-        }
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return f;
-}
-
-// A map of pages [page][head][row][element] for boxes of `rows` rows of `width` elements.
-bool page_map(CUtensorMap* map, const void* pages, const sv::PagedCache& c, bool e4m3, int width, int rows) {
-    const EncodeTiled f = encode_tiled();
-    if (!f) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page_size, (cuuint64_t)c.heads, (cuuint64_t)c.num_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)c.row_stride, (cuuint64_t)c.head_stride, (cuuint64_t)c.page_stride};
-    const cuuint32_t box[4] = {(cuuint32_t)width, (cuuint32_t)rows, 1, 1}, ones[4] = {1, 1, 1, 1};
-    return f(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pages), dims,
-             strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Rows per box where the copy engine can fill a tile (pages of 8, 16, 32, 64 or a multiple
-// of 128 rows: a box lies in one page and starts on a swizzle atom), else 0: cp.async then
-// copies row by row.
-int box_rows_of(const sv::PagedCache& c) {
-    if (c.page_size >= TN) return c.page_size % TN == 0 ? TN : 0;
-    return c.page_size >= 8 && TN % c.page_size == 0 ? c.page_size : 0;
-}
-
-template <int DP, int MQ, bool E4M3>
+template <int DP, int MQ, bool E4M3, bool DUAL>
 cudaError_t launch_one(const AttnArgs& a, int pairs, unsigned ctas, cudaStream_t stream) {
-    using S = Tc<DP, MQ, E4M3>;
+    using S = Tc<DP, MQ, E4M3, DUAL>;
     static sv::KernelLaunchCache cache;
-    auto kern = paged_attention_tc_kernel<DP, MQ, E4M3>;
+    auto kern = paged_attention_tc_kernel<DP, MQ, E4M3, DUAL>;
     int max_dyn = 0;
     const cudaError_t e = cache.setup((const void*)kern, &max_dyn);
     if (e != cudaSuccess) return e;
     if (S::SMEM > max_dyn) return cudaErrorInvalidValue;
-    int rows = box_rows_of(a.c);
+    int rows = sv::page_box_rows(a.c, TN);
     CUtensorMap k{}, v{};
-    if (rows && !(page_map(&k, a.c.k, a.c, E4M3, E4M3 ? DP : 64, rows) && page_map(&v, a.c.v, a.c, E4M3, E4M3 ? DP : 64, rows)))
+    const CUtensorMapSwizzle swizzle = E4M3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+    if (rows && !(sv::page_map(&k, a.c.k, a.c, E4M3, E4M3 ? DP : 64, rows, swizzle) &&
+                  sv::page_map(&v, a.c.v, a.c, E4M3, E4M3 ? DP : 64, rows, swizzle)))
         rows = 0;
     return sv::launch_serial(kern, dim3(ctas), dim3(S::THREADS), S::SMEM, stream, a, k, v, rows, pairs);
 }
 
 template <int DP, bool E4M3>
-cudaError_t launch_dim(const AttnArgs& a, int pairs, int tile_rows, unsigned ctas, cudaStream_t stream) {
-    return tile_rows == 256 ? launch_one<DP, 2, E4M3>(a, pairs, ctas, stream) : launch_one<DP, 1, E4M3>(a, pairs, ctas, stream);
+cudaError_t launch_dim(const AttnArgs& a, int pairs, int tile_rows, bool dual, unsigned ctas, cudaStream_t stream) {
+    if (dual) return launch_one<DP, 2, E4M3, true>(a, pairs, ctas, stream);
+    return tile_rows == 256 ? launch_one<DP, 2, E4M3, false>(a, pairs, ctas, stream)
+                            : launch_one<DP, 1, E4M3, false>(a, pairs, ctas, stream);
 }
 
 }  // namespace
 
 namespace sv {
 
-cudaError_t launch_attn_tc(const AttnArgs& a, int pairs, bool e4m3, int tile_rows, unsigned ctas, cudaStream_t stream) {
-    if (a.c.dim <= 64) return e4m3 ? launch_dim<64, true>(a, pairs, tile_rows, ctas, stream) : launch_dim<64, false>(a, pairs, tile_rows, ctas, stream);
-    return e4m3 ? launch_dim<128, true>(a, pairs, tile_rows, ctas, stream) : launch_dim<128, false>(a, pairs, tile_rows, ctas, stream);
+cudaError_t launch_attn_tc(const AttnArgs& a, int pairs, bool e4m3, int tile_rows, bool dual, unsigned ctas,
+                           cudaStream_t stream) {
+    if (a.c.dim <= 64) return e4m3 ? launch_dim<64, true>(a, pairs, tile_rows, dual, ctas, stream) : launch_dim<64, false>(a, pairs, tile_rows, dual, ctas, stream);
+    return e4m3 ? launch_dim<128, true>(a, pairs, tile_rows, dual, ctas, stream) : launch_dim<128, false>(a, pairs, tile_rows, dual, ctas, stream);
 }
 
 }  // namespace sv

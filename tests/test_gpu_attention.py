@@ -7,7 +7,7 @@ below), which moves a weight by at most 2e + the same for the sum.  So with A th
 mean of |v|, |out - want| <= (2^-8 + 4 e) A, plus the output's own half step 2^-8 |want|.
 lse moves by at most 2 e, plus fp32 roundings of its own value.
 
-e4m3 calls of more than 64 query rows per cache head multiply in fp16, half step 2^-11: an
+e4m3 calls of more than 16 query rows per cache head multiply in fp16, half step 2^-11: an
 element of a value and a probability are rounded once each, together below bf16's 2^-8.
 Probabilities are held times 2^7, where fp16 steps by 2^-24 below 2^-14: a position whose weight
 is tiny is off by up to 2^-32 of the largest weight, and the sum they are divided by is at
@@ -41,7 +41,7 @@ def check(got, lse, q, k, v, ks, vs, table, base, new_len, mask, scale, keep_out
     ka = np.where(np.isfinite(kv), np.abs(kv), 0).transpose(1, 0, 2, 3).reshape(H, -1, D)
     qa = np.abs(qh).reshape(B * Q, H, Hq // H, D).transpose(1, 0, 2, 3).reshape(H, -1, D)
     reach = abs(scale) * max((qa[h] @ ka[h].T).max() for h in range(H))  # largest sum |q k|
-    half = vs is not None and Q * Hq // H > 64 and D <= 128  # multiplied as fp16
+    half = vs is not None and Q * Hq // H > 16 and D <= 128  # multiplied as fp16
     e = (D + 16) * 2.0 ** -22 * reach
     g, gl = host(got), host(lse)
     tol = (2.0 ** -8 + 4 * e) * np.abs(size) + 2.0 ** -8 * np.abs(want) + 1e-30
