@@ -1,17 +1,25 @@
 // sv_logits.cu -- penalties, biases and grammar masks on the logits of every row of a
 // verify call (include/spec_logits.h).
 //
-// A CTA takes one batch row and a slice of the vocabulary.  From the row's token lists it
+// A CTA takes one batch row and a slice of the vocabulary: every S-th block of 256 tokens, so
+// that the frequent tokens, which have low numbers in most vocabularies, are spread over the
+// slices (with contiguous slices the first one's CTA ran 5 times as long as the others).
+// From the row's token lists it
 // builds a table of its slice in shared memory, one word per token (the count in the
-// output so far, and a flag for "in the prompt") and, where biases are given, the bias;
-// the table serves all R rows.  Then each warp takes rows of the slice in turn:
-//   out of place: it streams the row's part, 16 bytes per lane, and looks the table up;
-//   in place: it visits only the table's entries, and writes -inf where the grammar says so.
-// A row's drafted tokens (the prefix of a chain, the ancestors in a tree) are few of the
-// slice's tokens: the warp lists them, and rewrites those elements after the stream from
-// the logits it kept aside.  So nothing in shared memory changes while rows are at work,
-// and no result depends on the order of atomics (counts are integers; of two biases of one
-// token the later entry holds).
+// output so far, and a flag for "in the prompt") and, where biases are given, the bias,
+// and from it the list of the tokens that have anything; both serve all R rows.  Then each
+// warp takes rows of the slice in turn:
+//   out of place it copies the row's part, 16 bytes per lane, with -inf where the grammar
+//   says so (and does not read what the grammar rules out); in place it writes those -inf only;
+//   then it goes through the list, one token per lane, and rewrites those elements;
+//   last come the row's drafted tokens (the prefix of a chain, the ancestors in a tree), whose
+//   counts are the row's own.
+// Copy and list are apart because a group of eight tokens with one listed token among a
+// warp's 32 groups is the rule: looking the table up in the copy ran the penalties' code for
+// every group (205 instructions a group, 250 us for 16 trees of 61 rows of 128256).
+// Nothing in shared memory changes while rows are at work, and no result depends on the
+// order of atomics (counts are integers; of two biases of one token the later entry holds;
+// the list's order does not matter).
 #include <cstdint>
 
 #include "spec_logits.h"
@@ -30,7 +38,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxB = 65535;
 constexpr int kMaxRows = 1025;
 constexpr int kMaxV = 1 << 24;
-constexpr int kMaxSlice = 16384;
+constexpr int kBlock = 256;       // consecutive tokens of a slice
+constexpr int kMaxSlice = 16384;  // tokens of a slice
 constexpr uint32_t kPrompt = 0x80000000u;  // table flag; the low 31 bits count
 
 struct AdjustArgs {
@@ -47,7 +56,9 @@ struct AdjustArgs {
     const int32_t* bias_tokens;
     const float* bias_values;
     const uint32_t* allowed;
-    int H, M, R, V, slice, slices;
+    int H, M, R, V;
+    int slice;      // tokens of a slice, a multiple of kBlock
+    int log_slices;  // log2 of their number
 };
 
 struct Penalty {
@@ -74,22 +85,7 @@ __device__ __forceinline__ void store_logit(void* row, int v, float x) {
     else static_cast<float*>(row)[v] = x;
 }
 
-// The 16 bytes of a group as fp32, back, and with -inf where `keep` has a 0.
-template <bool BF16>
-__device__ __forceinline__ void unpack(uint4 g, float* x) {
-    if (BF16) {
-        x[0] = sv::bf16_lo(g.x); x[1] = sv::bf16_hi(g.x); x[2] = sv::bf16_lo(g.y); x[3] = sv::bf16_hi(g.y);
-        x[4] = sv::bf16_lo(g.z); x[5] = sv::bf16_hi(g.z); x[6] = sv::bf16_lo(g.w); x[7] = sv::bf16_hi(g.w);
-    } else {
-        x[0] = __uint_as_float(g.x); x[1] = __uint_as_float(g.y);
-        x[2] = __uint_as_float(g.z); x[3] = __uint_as_float(g.w);
-    }
-}
-template <bool BF16>
-__device__ __forceinline__ uint4 pack(const float* x) {
-    if (BF16) return make_uint4(sv::bf16x2(x[0], x[1]), sv::bf16x2(x[2], x[3]), sv::bf16x2(x[4], x[5]), sv::bf16x2(x[6], x[7]));
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-}
+// The 16 bytes of a group with -inf where `keep` has a 0.
 template <bool BF16>
 __device__ __forceinline__ uint4 masked(uint4 g, uint32_t keep) {
     uint32_t w[4] = {g.x, g.y, g.z, g.w};
@@ -112,77 +108,127 @@ __device__ __forceinline__ int to_boundary(const void* p) {
 }
 
 template <bool BF16, bool BIAS>
-__global__ void __launch_bounds__(kThreads) adjust_logits_kernel(const __grid_constant__ AdjustArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) adjust_logits_kernel(const __grid_constant__ AdjustArgs a) {
     pdl_trigger();
     pdl_wait();
     extern __shared__ __align__(16) uint32_t s_table[];  // [slice] words, [slice] biases, per-warp lists
-    const int b = blockIdx.y, v0 = blockIdx.x * a.slice;
-    const int n = a.V - v0 < a.slice ? a.V - v0 : a.slice;
+    const int b = blockIdx.y, me = blockIdx.x, slices = 1 << a.log_slices;
+    // token v of this slice is entry `local` of the tables (-1: of another slice, or none)
+    auto local = [&](int v) {
+        const int blk = v >> 8;
+        return (unsigned)v < (unsigned)a.V && (blk & (slices - 1)) == me ? (blk >> a.log_slices) << 8 | (v & 255) : -1;
+    };
+    auto token = [&](int u) { return (((u >> 8) << a.log_slices) + me) << 8 | (u & 255); };
     float* s_bias = reinterpret_cast<float*>(s_table + a.slice);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int N = a.R - 1;
     const bool in_place = a.out == a.logits;
     constexpr int ES = BF16 ? 2 : 4;
 
-    __shared__ int s_nodes;  // drafted tokens of this slice
-    for (int i = tid; i < a.slice * (BIAS ? 2 : 1); i += kThreads) s_table[i] = 0u;
-    if (tid == 0) s_nodes = 0;
-    __syncthreads();
-    uint16_t* s_node = reinterpret_cast<uint16_t*>(s_table + a.slice * (BIAS ? 2 : 1));  // [N] node, then lists
-    uint16_t* s_list = s_node + N + warp * N;                                            // this warp's
-    int len = a.history ? __ldg(a.history_len + b) : 0;
-    len = len < 0 ? 0 : len > a.H ? a.H : len;
-    const int prompt = a.prompt_len ? __ldg(a.prompt_len + b) : 0;
+    __shared__ int s_nodes, s_count;  // drafted and listed tokens of this slice
+    uint16_t* s_listed = reinterpret_cast<uint16_t*>(s_table + a.slice * (BIAS ? 2 : 1));  // [slice] entries
+    uint16_t* s_node = s_listed + a.slice;    // [N] drafted nodes of the slice
+    uint16_t* s_tok = s_node + N;             // [N] their entries
+    uint16_t* s_list = s_tok + N + warp * N;  // this warp's: indices into both
+
+    // Everything the tables need is asked for at once: the first 2048 tokens of the history and
+    // the first 256 biases do not wait for the lengths or for the tables to be cleared.
+    constexpr int AHEAD = 8;
     const int32_t* hist = a.history + (int64_t)b * a.H;
-#pragma unroll 4
-    for (int i = tid; i < len; i += kThreads) {
-        const unsigned v = (unsigned)__ldg(hist + i) - (unsigned)v0;
-        if (v < (unsigned)n) {
-            if (i < prompt) atomicOr(s_table + v, kPrompt);
-            else atomicAdd(s_table + v, 1u);
-        }
+    const int32_t* bt = a.bias_tokens + (int64_t)b * a.M;
+    const float* bv = a.bias_values + (int64_t)b * a.M;
+    int ahead[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) ahead[k] = a.history && tid + k * kThreads < a.H ? __ldg(hist + tid + k * kThreads) : -1;
+    int len = a.history ? __ldg(a.history_len + b) : 0;
+    const int prompt = a.prompt_len ? __ldg(a.prompt_len + b) : 0;
+    int bias_at = -1;
+    float bias_is = 0.0f;
+    if (BIAS && tid < a.M) {
+        bias_at = __ldg(bt + tid);
+        bias_is = __ldg(bv + tid);
     }
+    Penalty pen;
+    pen.rep = a.repetition ? __ldg(a.repetition + b) : 1.0f;
+    pen.pres = a.presence ? __ldg(a.presence + b) : 0.0f;
+    pen.freq = a.frequency ? __ldg(a.frequency + b) : 0.0f;
+    for (int i = 4 * tid; i < a.slice * (BIAS ? 2 : 1); i += 4 * kThreads)
+        *reinterpret_cast<uint4*>(s_table + i) = make_uint4(0u, 0u, 0u, 0u);
+    if (tid == 0) s_nodes = s_count = 0;
+    __syncthreads();
+    len = len < 0 ? 0 : len > a.H ? a.H : len;
+    auto count = [&](int i, int v) {
+        const int u = i < len ? local(v) : -1;
+        if (u >= 0) {
+            if (i < prompt) atomicOr(s_table + u, kPrompt);
+            else atomicAdd(s_table + u, 1u);
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) count(tid + k * kThreads, ahead[k]);
+#pragma unroll 8
+    for (int i = tid + AHEAD * kThreads; i < len; i += kThreads) count(i, __ldg(hist + i));
     if (BIAS) {
-        // the last entry of a token wins: its number + 1 is the largest
+        // the last entry of a token wins: its number + 1 is the largest, and takes the word
         uint32_t* at = reinterpret_cast<uint32_t*>(s_bias);
-        const int32_t* bt = a.bias_tokens + (int64_t)b * a.M;
-        for (int i = tid; i < a.M; i += kThreads) {
-            const int t = __ldg(bt + i);
-            const unsigned v = (unsigned)t - (unsigned)v0;
-            if (t >= 0 && v < (unsigned)n) atomicMax(at + v, (uint32_t)i + 1u);
+        auto number = [&](int i, int v) {
+            const int u = local(v);
+            if (u >= 0) atomicMax(at + u, (uint32_t)i + 1u);
+        };
+        if (tid < a.M) number(tid, bias_at);
+        for (int i = tid + kThreads; i < a.M; i += kThreads) number(i, __ldg(bt + i));
+        __syncthreads();
+        // a winner knows itself; nobody else's word is its own, and no bias is taken for a number
+        // because every word is read before the barrier and written after it
+        constexpr int MOST = 256;  // 65535 entries over 256 threads
+        uint32_t won[MOST / 32] = {};
+        int k = 0;
+        for (int i = tid; i < a.M; i += kThreads, ++k) {
+            const int u = local(i == tid ? bias_at : __ldg(bt + i));
+            if (u >= 0 && at[u] == (uint32_t)i + 1u) won[k >> 5] |= 1u << (k & 31);
         }
         __syncthreads();
-        for (int i = tid; i < n; i += kThreads) {
-            const uint32_t m = at[i];
-            s_bias[i] = m ? __ldg(a.bias_values + (int64_t)b * a.M + m - 1) : 0.0f;
-        }
+        k = 0;
+        for (int i = tid; i < a.M; i += kThreads, ++k)
+            if ((won[k >> 5] >> (k & 31)) & 1u) s_bias[local(i == tid ? bias_at : __ldg(bt + i))] = i == tid ? bias_is : __ldg(bv + i);
     }
     // drafted tokens of this slice, in node order (one warp, so that the order is fixed)
     if (a.drafts && warp == 0) {
         int have = 0;
         for (int i0 = 0; i0 < N; i0 += 32) {
             const int i = i0 + lane;
-            const bool in = i < N && (unsigned)__ldg(a.drafts + (int64_t)b * N + i) - (unsigned)v0 < (unsigned)n;
+            const int u = i < N ? local(__ldg(a.drafts + (int64_t)b * N + i)) : -1;
+            const bool in = u >= 0;
             const unsigned m = __ballot_sync(0xffffffffu, in);
-            if (in) s_node[have + __popc(m & ((1u << lane) - 1u))] = (uint16_t)i;
+            if (in) {
+                const int at = have + __popc(m & ((1u << lane) - 1u));
+                s_node[at] = (uint16_t)i;
+                s_tok[at] = (uint16_t)u;
+            }
             have += __popc(m);
         }
         if (lane == 0) s_nodes = have;
     }
     __syncthreads();
+    for (int i = tid; i < a.slice; i += kThreads) {
+        const bool in = s_table[i] != 0u || (BIAS && s_bias[i] != 0.0f);
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        int at = 0;
+        if (lane == 0 && m) at = atomicAdd(&s_count, __popc(m));
+        at = __shfl_sync(0xffffffffu, at, 0);
+        if (in) s_listed[at + __popc(m & ((1u << lane) - 1u))] = (uint16_t)i;
+    }
+    __syncthreads();
+    const int listed = s_count;
     const int nodes = s_nodes;
-    Penalty pen;
-    pen.rep = a.repetition ? __ldg(a.repetition + b) : 1.0f;
-    pen.pres = a.presence ? __ldg(a.presence + b) : 0.0f;
-    pen.freq = a.frequency ? __ldg(a.frequency + b) : 0.0f;
     const int W = (a.V + 31) / 32, MW = (N + 31) / 32;
 
     for (int r = warp; r < a.R; r += kWarps) {
         const int64_t row = (int64_t)b * a.R + r;
-        const char* src = static_cast<const char*>(a.logits) + (row * a.V + v0) * ES;
-        char* dst = static_cast<char*>(a.out) + (row * a.V + v0) * ES;
+        const char* src = static_cast<const char*>(a.logits) + row * a.V * ES;
+        char* dst = static_cast<char*>(a.out) + row * a.V * ES;
         const uint32_t* ok = a.allowed ? a.allowed + row * W : nullptr;
-        auto word_ok = [&](int v) { return !ok || ((__ldg(ok + ((v0 + v) >> 5)) >> ((v0 + v) & 31)) & 1u); };
+        auto word_ok = [&](int v) { return !ok || ((__ldg(ok + (v >> 5)) >> (v & 31)) & 1u); };
 
         // the nodes this row follows
         int mine = 0;
@@ -192,121 +238,142 @@ __global__ void __launch_bounds__(kThreads) adjust_logits_kernel(const __grid_co
             if (see && a.tree_mask)
                 see = (__ldg(a.tree_mask + ((int64_t)b * N + r - 1) * MW + (node >> 5)) >> (node & 31)) & 1u;
             const unsigned m = __ballot_sync(0xffffffffu, see);
-            if (see) s_list[mine + __popc(m & ((1u << lane) - 1u))] = (uint16_t)node;
+            if (see) s_list[mine + __popc(m & ((1u << lane) - 1u))] = (uint16_t)(i0 + lane);
             mine += __popc(m);
         }
         __syncwarp();
-        auto draft_at = [&](int i) { return __ldg(a.drafts + (int64_t)b * N + s_list[i]) - v0; };
-        // lane i's drafted token: its element's new value, if it is the token's first in the list
+        auto draft_at = [&](int i) { return (int)s_tok[s_list[i]]; };
+        // lane i's drafted token and its element's new value, if it is the token's first in the list
         auto redo = [&](int i, int& v, float& x) {
-            v = draft_at(i);
-            uint32_t w = s_table[v];
+            const int u = draft_at(i);
+            uint32_t w = s_table[u];
             for (int k = 0; k < mine; ++k)
-                if (draft_at(k) == v) {
+                if (draft_at(k) == u) {
                     if (k < i) return false;
                     ++w;
                 }
+            v = token(u);
             x = penalised(load_logit<BF16>(src, v), w, pen);
-            if (BIAS) x += s_bias[v];
+            if (BIAS) x += s_bias[u];
             if (!word_ok(v)) x = neg_inf();
             return true;
         };
         int v_mine = -1;
         float x_mine = 0.0f;
         if (lane < mine && !redo(lane, v_mine, x_mine)) v_mine = -1;
-        // lists longer than a warp (deep trees whose tokens repeat): kept out of the stream
-        // below by being in the list; in place their logits are still unread then
+        // (a list longer than a warp, in deep trees whose tokens repeat, comes at the end; in place
+        // its logits are still as they were then)
 
-        if (!in_place) {
-            constexpr int VEC = 16 / ES;
-            const int head0 = to_boundary<BF16>(src);
-            const bool same = to_boundary<BF16>(dst) == head0;
-            const int head = same ? (head0 < n ? head0 : n) : n;  // element by element up to here
-            auto one = [&](int v) {
-                float x = penalised(load_logit<BF16>(src, v), s_table[v], pen);
-                if (BIAS) x += s_bias[v];
-                if (!word_ok(v)) x = neg_inf();
+        // units of 32 groups of 16 bytes; where a row starts off a 16-byte boundary a unit has one
+        // group less, and its first and last elements are left over
+        constexpr int VEC = 16 / ES, UNIT = 32 * VEC, STEP = 4;
+        constexpr uint32_t ALL = (1u << VEC) - 1u;
+        const int head = to_boundary<BF16>(dst);
+        const bool same = to_boundary<BF16>(src) == head;
+        auto one = [&](int v) {
+            if (!word_ok(v)) store_logit<BF16>(dst, v, neg_inf());
+            else if (!in_place) store_logit<BF16>(dst, v, load_logit<BF16>(src, v));
+        };
+        // The listed tokens, four a step; in place an element is written once, so those that the
+        // row drafted are left to the end.  The first step's logits are read before the copy.
+        int lu[STEP];
+        uint32_t lx[STEP], lw[STEP];  // as loaded: looking at them here would wait for them
+        auto get_listed = [&](int i0) {
+#pragma unroll
+            for (int y = 0; y < STEP; ++y) {
+                lu[y] = i0 + 32 * y < listed ? (int)s_listed[i0 + 32 * y] : -1;
+                if (in_place)
+                    for (int k = 0; k < mine; ++k)
+                        if (lu[y] == draft_at(k)) lu[y] = -1;
+                lx[y] = lw[y] = 0u;
+                if (lu[y] < 0) continue;
+                const int v = token(lu[y]);
+                lx[y] = BF16 ? (uint32_t)reinterpret_cast<const unsigned short*>(src)[v] : reinterpret_cast<const uint32_t*>(src)[v];
+                if (ok) lw[y] = __ldg(ok + (v >> 5));
+            }
+        };
+        auto put_listed = [&]() {
+#pragma unroll
+            for (int y = 0; y < STEP; ++y) {
+                if (lu[y] < 0) continue;
+                const int v = token(lu[y]);
+                if (ok && !((lw[y] >> (v & 31)) & 1u)) continue;  // -inf already
+                float x = penalised(__uint_as_float(BF16 ? lx[y] << 16 : lx[y]), s_table[lu[y]], pen);
+                if (BIAS) x += s_bias[lu[y]];
                 store_logit<BF16>(dst, v, x);
+            }
+        };
+        get_listed(lane);
+        if (!in_place || ok) {
+            // Four units a step: the logits of the groups whose mask keeps anything, and the next
+            // step's masks, are on their way together.
+            uint32_t keep[STEP], next[STEP];
+            auto masks = [&](int u0, uint32_t (&k)[STEP]) {
+#pragma unroll
+                for (int y = 0; y < STEP; ++y) {
+                    const int u = u0 + y * UNIT, at = token(u) + head + lane * VEC;
+                    k[y] = ALL;
+                    if (ok && u < a.slice && at + VEC <= a.V) {
+                        uint32_t w = __ldg(ok + (at >> 5)) >> (at & 31);
+                        if ((at & 31) + VEC > 32) w |= __ldg(ok + (at >> 5) + 1) << (32 - (at & 31));
+                        k[y] = w & ALL;
+                    }
+                }
             };
-            for (int v = lane; v < head; v += 32) one(v);
-            const int groups = (n - head) / VEC;
-            const bool wide = (head & 3) == 0;  // the table's words are read 16 bytes at a time
-#pragma unroll 4
-            for (int g = lane; g < groups; g += 32) {
-                const int v = head + g * VEC;
-                uint4 io = sv::ld_nc_v4(src + (int64_t)v * ES);
-                uint32_t w[VEC], any = 0u;
-                float bias[VEC];
-                if (wide) {
+            masks(0, keep);
+            for (int u0 = 0; u0 < a.slice; u0 += STEP * UNIT) {
+                uint4 io[STEP];
+                int v[STEP];  // this lane's group, or -1
 #pragma unroll
-                    for (int j = 0; j < VEC; j += 4) *reinterpret_cast<uint4*>(w + j) = *reinterpret_cast<const uint4*>(s_table + v + j);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) w[j] = s_table[v + j];
+                for (int y = 0; y < STEP; ++y) {
+                    const int u = u0 + y * UNIT, first = token(u);
+                    v[y] = u < a.slice && same && first + UNIT <= a.V && !(head && lane == 31) ? first + head + lane * VEC : -1;
+                    io[y] = make_uint4(0u, 0u, 0u, 0u);
+                    if (!in_place && v[y] >= 0 && keep[y]) io[y] = sv::ld_nc_v4(src + (int64_t)v[y] * ES);
                 }
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) any |= w[j];
-                if (BIAS) {
-                    if (wide) {
-#pragma unroll
-                        for (int j = 0; j < VEC; j += 4) *reinterpret_cast<float4*>(bias + j) = *reinterpret_cast<const float4*>(s_bias + v + j);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j) bias[j] = s_bias[v + j];
+                masks(u0 + STEP * UNIT, next);
+                if (!same || head || token(u0) + ((STEP * UNIT << a.log_slices) + kBlock) > a.V) {
+#pragma unroll 1
+                    for (int y = 0; y < STEP; ++y) {
+                        const int u = u0 + y * UNIT, first = token(u);
+                        if (u >= a.slice || first >= a.V) continue;
+                        if (!same || first + UNIT > a.V) {  // other alignments, and the vocabulary's end
+                            for (int e = lane; e < UNIT && first + e < a.V; e += 32) one(first + e);
+                        } else if (head && lane < VEC) {
+                            one(first + (lane < head ? lane : 31 * VEC + lane));
+                        }
                     }
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) any |= __float_as_uint(bias[j]);
                 }
-                if (any) {  // few groups hold a token of the lists
-                    float x[VEC];
-                    unpack<BF16>(io, x);
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        x[j] = penalised(x[j], w[j], pen);
-                        if (BIAS) x[j] += bias[j];
+                for (int y = 0; y < STEP; ++y) {
+                    if (v[y] < 0) continue;
+                    if (!in_place) {
+                        if (ok) io[y] = masked<BF16>(io[y], keep[y]);
+                        *reinterpret_cast<uint4*>(dst + (int64_t)v[y] * ES) = io[y];
+                    } else if (keep[y] == 0u) {
+                        *reinterpret_cast<uint4*>(dst + (int64_t)v[y] * ES) = masked<BF16>(io[y], 0u);
+                    } else if (keep[y] != ALL) {
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j)
+                            if (!((keep[y] >> j) & 1u)) store_logit<BF16>(dst, v[y] + j, neg_inf());
                     }
-                    io = pack<BF16>(x);
                 }
-                if (ok) {
-                    const int bit = v0 + v;
-                    uint32_t keep = __ldg(ok + (bit >> 5)) >> (bit & 31);
-                    if ((bit & 31) + VEC > 32) keep |= __ldg(ok + (bit >> 5) + 1) << (32 - (bit & 31));
-                    io = masked<BF16>(io, keep);
-                }
-                *reinterpret_cast<uint4*>(dst + (int64_t)v * ES) = io;
+#pragma unroll
+                for (int y = 0; y < STEP; ++y) keep[y] = next[y];
             }
-            for (int v = head + groups * VEC + lane; v < n; v += 32) one(v);
             __syncwarp();
-            if (v_mine >= 0) store_logit<BF16>(dst, v_mine, x_mine);
-            for (int i0 = 32; i0 < mine; i0 += 32) {
-                int v;
-                float x;
-                if (i0 + lane < mine && redo(i0 + lane, v, x)) store_logit<BF16>(dst, v, x);
-            }
-        } else {
-            // Entries of the table, then the row's drafted tokens: an element is written once,
-            // by the drafted token where there is one.
-            for (int v = lane; v < n; v += 32) {
-                const bool good = word_ok(v);
-                const uint32_t w = s_table[v];
-                const bool change = !good || w != 0u || (BIAS && s_bias[v] != 0.0f);
-                if (!change) continue;
-                bool drafted = false;
-                for (int k = 0; k < mine; ++k) drafted |= draft_at(k) == v;
-                if (drafted) continue;
-                float x = neg_inf();
-                if (good) {
-                    x = penalised(load_logit<BF16>(dst, v), w, pen);
-                    if (BIAS) x += s_bias[v];
-                }
-                store_logit<BF16>(dst, v, x);
-            }
-            if (v_mine >= 0) store_logit<BF16>(dst, v_mine, x_mine);
-            for (int i0 = 32; i0 < mine; i0 += 32) {
-                int v;
-                float x;
-                if (i0 + lane < mine && redo(i0 + lane, v, x)) store_logit<BF16>(dst, v, x);
-            }
+        }
+        put_listed();
+        for (int i0 = lane + 32 * STEP; i0 < listed; i0 += 32 * STEP) {
+            get_listed(i0);
+            put_listed();
+        }
+        __syncwarp();
+        if (v_mine >= 0) store_logit<BF16>(dst, v_mine, x_mine);
+        for (int i0 = 32; i0 < mine; i0 += 32) {
+            int v;
+            float x;
+            if (i0 + lane < mine && redo(i0 + lane, v, x)) store_logit<BF16>(dst, v, x);
         }
         __syncwarp();  // the list is rewritten for the next row
     }
@@ -322,12 +389,16 @@ int device_sms() {
     return sms;
 }
 
-// Tokens per slice: the largest power of two that still gives two CTAs per SM, 2048 at
-// least (a slice's CTA reads the whole history) and 16384 at most (shared memory).
-int pick_slice(int B, int V, int sms) {
-    int s = kMaxSlice;
-    while (s > 2048 && (long long)B * ((V + s - 1) / s) < 2LL * sms) s >>= 1;
-    return s;
+// Slices: the fewest (a power of two) that give two CTAs per SM with at most kMaxSlice tokens
+// each (shared memory); every slice's CTA reads the whole history, so no more than one per
+// eight blocks.
+int pick_log_slices(int B, int V, int sms) {
+    const int blocks = (V + kBlock - 1) / kBlock;
+    int k = 0;
+    while ((((int64_t)blocks + (1 << k) - 1) >> k) * kBlock > kMaxSlice ||
+           ((long long)B << k < 2LL * sms && (8 << (k + 1)) <= blocks))
+        ++k;
+    return k;
 }
 
 template <bool BF16, bool BIAS>
@@ -337,9 +408,9 @@ cudaError_t launch_adjust(const AdjustArgs& a, int B, cudaStream_t stream) {
     int max_dyn = 0;
     const cudaError_t e = cache.setup((const void*)kern, &max_dyn);
     if (e != cudaSuccess) return e;
-    const size_t smem = (size_t)a.slice * (BIAS ? 8 : 4) + (size_t)(a.R - 1) * (1 + kWarps) * sizeof(uint16_t);
+    const size_t smem = (size_t)a.slice * (BIAS ? 10 : 6) + (size_t)(a.R - 1) * (2 + kWarps) * sizeof(uint16_t);
     if (smem > (size_t)max_dyn) return cudaErrorInvalidValue;
-    return sv::launch_serial(kern, dim3((unsigned)a.slices, (unsigned)B), dim3(kThreads), smem, stream, a);
+    return sv::launch_serial(kern, dim3(1u << a.log_slices, (unsigned)B), dim3(kThreads), smem, stream, a);
 }
 
 }  // namespace
@@ -366,8 +437,9 @@ extern "C" sv_status spec_adjust_logits(const void* logits, sv_dtype dt, const i
     AdjustArgs a{logits, out, H > 0 ? history : nullptr, history_len, prompt_len, R > 1 ? draft_tokens : nullptr,
                  R > 1 && draft_tokens ? tree_mask : nullptr, repetition, presence, frequency, bias_tokens, bias_values,
                  allowed, H, M, R, V, 0, 0};
-    a.slice = pick_slice(B, V, sms);
-    a.slices = (V + a.slice - 1) / a.slice;
+    a.log_slices = pick_log_slices(B, V, sms);
+    const int blocks = (V + kBlock - 1) / kBlock;
+    a.slice = ((blocks + (1 << a.log_slices) - 1) >> a.log_slices) * kBlock;
     const bool bias = M > 0 && bias_tokens;
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
