@@ -481,22 +481,25 @@ def spec_kv_compact(kv_buffers, path, count, base=None, *, stream=None):
 # --------------------------------------------- a verification round on a paged cache
 
 def _one_device(first, stream, **tensors):
-    """Checks that every given tensor is on the device of `first` (the first of them) and
-    contiguous; returns that device and the stream to launch on (that device's current one
-    unless given)."""
-    dev = first.device
+    """Checks that every given tensor is on the device of `first` (the first of them); returns
+    that device's index, the handle of the stream to launch on (that device's current one
+    unless given), and the stream itself where it is not the current one."""
+    torch = _torch()
+    at = first.get_device()
     for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, other arguments on {dev}")
+        if t is not None and t.get_device() != at:
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            raise ValueError(f"{name} is on {t.device}, other arguments on {first.device}")
+    if at < 0:
+        raise ValueError(f"{next(iter(tensors))} must be a CUDA tensor")
+    current = torch._C._cuda_getCurrentRawStream(at)
     if stream is None:
-        stream = _torch().cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the arguments on {dev}")
-    return dev, stream
+        return at, current, None
+    if stream.device_index != at:
+        raise ValueError(f"the stream is on device {stream.device_index}, the arguments on {first.device}")
+    handle = stream.cuda_stream
+    return at, handle, None if handle == current else stream
 
 
 def _shaped(name, t, shape, dtype):
@@ -504,62 +507,66 @@ def _shaped(name, t, shape, dtype):
         return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _launch(where, dev, stream, call, *args):
-    """call(*args, stream) with `dev` current; raises on a non-zero status."""
-    cuda = _torch().cuda
-    if dev.index == cuda.current_device():
-        st = call(*args, ctypes.c_void_p(stream.cuda_stream))
+def _adr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(where, at, call, *args):
+    """call(*args) with device `at` current; raises on a non-zero status."""
+    torch = _torch()
+    if at == torch._C._cuda_getDevice():
+        st = call(*args)
     else:
-        with cuda.device(dev):
-            st = call(*args, ctypes.c_void_p(stream.cuda_stream))
+        with torch.cuda.device(at):
+            st = call(*args)
     if st != SV_OK:
         raise SpecVerifyError(st, where)
 
 
-def _new(shape, dtype, dev, stream):
-    """A new tensor that belongs to `stream`."""
-    torch = _torch()
-    if stream == torch.cuda.current_stream(dev):
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+def _new(make, shape, dtype, at, side):
+    """A new tensor (make: torch.empty or torch.zeros) that belongs to the launch's stream."""
+    if side is None:
+        return make(shape, dtype=dtype, device=at)
+    with _torch().cuda.stream(side):
+        return make(shape, dtype=dtype, device=at)
 
 
 def _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, B):
     """The sv_paged_cache of tensors [pages][heads][page_size][head_dim] (checked)."""
     torch = _torch()
-    if k_pages.dim() != 4 or v_pages.dim() != 4:
+    shape, stride, dtype = k_pages.shape, k_pages.stride(), k_pages.dtype
+    if len(shape) != 4:
         raise ValueError("k_pages and v_pages must be [pages][heads][page_size][head_dim]")
-    if k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype or k_pages.stride() != v_pages.stride():
+    if v_pages.shape != shape or v_pages.dtype != dtype or v_pages.stride() != stride:
         raise ValueError("k_pages and v_pages must have one shape, stride and dtype")
-    P, H, ps, D = k_pages.shape
-    sp, sh, sr, sd = k_pages.stride()
+    P, H, ps, D = shape
+    sp, sh, sr, sd = stride
     if sd != 1 and D > 1:
         raise ValueError("the last dimension of k_pages and v_pages must be contiguous")
-    if k_pages.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         code, es = SV_CACHE_BF16, 2
         if k_scale is not None or v_scale is not None:
             raise ValueError("k_scale and v_scale belong to float8_e4m3fn pages")
-    elif k_pages.dtype == torch.float8_e4m3fn:
+    elif dtype == torch.float8_e4m3fn:
         code, es = SV_CACHE_E4M3, 1
         if k_scale is None or v_scale is None:
             raise ValueError("float8_e4m3fn pages need k_scale and v_scale")
         _shaped("k_scale", k_scale, (P, H, ps), torch.float32)
         _shaped("v_scale", v_scale, (P, H, ps), torch.float32)
     else:
-        raise TypeError(f"pages must be bfloat16 or float8_e4m3fn, got {k_pages.dtype}")
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError(f"page_table must be [{B}][max_pages], got {tuple(page_table.shape)}")
-    _shaped("page_table", page_table, page_table.shape, torch.int32)
-    return PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
-                      None if v_scale is None else v_scale.data_ptr(), page_table.data_ptr(), sp * es, sh * es,
-                      max(sr, D) * es if ps == 1 else sr * es, code, P, ps, page_table.shape[1], H, D)
+        raise TypeError(f"pages must be bfloat16 or float8_e4m3fn, got {dtype}")
+    table = page_table.shape
+    if len(table) != 2 or table[0] != B:
+        raise ValueError(f"page_table must be [{B}][max_pages], got {tuple(table)}")
+    _shaped("page_table", page_table, table, torch.int32)
+    return PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), _adr(k_scale), _adr(v_scale), page_table.data_ptr(),
+                      sp * es, sh * es, max(sr, D) * es if ps == 1 else sr * es, code, P, ps, table[1], H, D)
 
 
 def _strides3(t, name):
@@ -588,7 +595,7 @@ def spec_kv_append(key, value, k_pages, v_pages, page_table, base, *, new_len=No
     page_table int32 [B][max_pages]; base int32 [B] (positions before token 0); new_len
     int32 [B] or None (all N tokens are real)."""
     torch = _torch()
-    dev, stream = _one_device(key, stream, key=key, value=value, k_pages=k_pages, v_pages=v_pages,
+    at, handle, side = _one_device(key, stream, key=key, value=value, k_pages=k_pages, v_pages=v_pages,
                               page_table=page_table, base=base, new_len=new_len, k_scale=k_scale, v_scale=v_scale)
     if key.dim() != 4 or key.shape != value.shape or key.dtype != value.dtype or key.stride() != value.stride():
         raise ValueError("key and value must be [B][N][heads][head_dim] of one shape, stride and dtype")
@@ -598,8 +605,8 @@ def spec_kv_append(key, value, k_pages, v_pages, page_table, base, *, new_len=No
         raise ValueError(f"key has {H} heads of {D}, the cache {cache.num_heads} of {cache.head_dim}")
     _shaped("base", base, (B,), torch.int32)
     _shaped("new_len", new_len, (B,), torch.int32)
-    _launch("spec_kv_append", dev, stream, lib().spec_kv_append, _ptr(key), _ptr(value), _src_code(key.dtype, "key"),
-            _strides3(key, "key"), cache, _ptr(base), _ptr(new_len), B, N)
+    _launch("spec_kv_append", at, lib().spec_kv_append, _adr(key), _adr(value), _src_code(key.dtype, "key"),
+            _strides3(key, "key"), cache, _adr(base), _adr(new_len), B, N, handle)
 
 
 def spec_kv_read(k_pages, v_pages, page_table, base, num_tokens: int, *, new_len=None, k_scale=None, v_scale=None,
@@ -610,7 +617,7 @@ def spec_kv_read(k_pages, v_pages, page_table, base, num_tokens: int, *, new_len
     spec_kv_append.  Rows of new outputs at and behind new_len are zero; rows of given
     outputs there keep what they hold.  Returns (out_key, out_value)."""
     torch = _torch()
-    dev, stream = _one_device(k_pages, stream, k_pages=k_pages, v_pages=v_pages, page_table=page_table, base=base,
+    at, handle, side = _one_device(k_pages, stream, k_pages=k_pages, v_pages=v_pages, page_table=page_table, base=base,
                               new_len=new_len, k_scale=k_scale, v_scale=v_scale, out_key=out_key,
                               out_value=out_value)
     B, N = page_table.shape[0], int(num_tokens)
@@ -627,11 +634,10 @@ def spec_kv_read(k_pages, v_pages, page_table, base, num_tokens: int, *, new_len
     _shaped("out_key", out_key, shape, dtype)
     _shaped("out_value", out_value, shape, dtype)
     if out_key is None or out_value is None:
-        with torch.cuda.stream(stream):
-            out_key = torch.zeros(shape, dtype=dtype, device=dev) if out_key is None else out_key
-            out_value = torch.zeros(shape, dtype=dtype, device=dev) if out_value is None else out_value
-    _launch("spec_kv_read", dev, stream, lib().spec_kv_read, cache, _ptr(base), _ptr(new_len), B, N, _ptr(out_key),
-            _ptr(out_value), code)
+        out_key = _new(torch.zeros, shape, dtype, at, side) if out_key is None else out_key
+        out_value = _new(torch.zeros, shape, dtype, at, side) if out_value is None else out_value
+    _launch("spec_kv_read", at, lib().spec_kv_read, cache, _adr(base), _adr(new_len), B, N, _adr(out_key),
+            _adr(out_value), code, handle)
     return out_key, out_value
 
 
@@ -649,8 +655,8 @@ def spec_kv_compact_paged(kv_buffers, page_table, path, count, base=None, *, str
             raise ValueError("a single kv_buffers tensor must be [buffers][pages][planes][page_size][width]")
         n, shape, strides, t0 = kv_buffers.shape[0], kv_buffers.shape[1:], kv_buffers.stride()[1:], kv_buffers
         es = t0.element_size()
-        at, step = t0.data_ptr(), kv_buffers.stride(0) * es
-        ptrs = [at + k * step for k in range(n)]
+        origin, step = t0.data_ptr(), kv_buffers.stride(0) * es
+        ptrs = range(origin, origin + n * step, step) if step else [origin] * n
     else:
         bufs = list(kv_buffers)
         if not bufs:
@@ -663,7 +669,7 @@ def spec_kv_compact_paged(kv_buffers, page_table, path, count, base=None, *, str
                                  "dtype and device")
         es = t0.element_size()
         ptrs = [t.data_ptr() for t in bufs]
-    dev, stream = _one_device(t0, stream, kv_buffers=t0, page_table=page_table, path=path, count=count, base=base)
+    at, handle, side = _one_device(t0, stream, kv_buffers=t0, page_table=page_table, path=path, count=count, base=base)
     P, H, ps, W = shape
     if strides[3] != 1 and W > 1:
         raise ValueError("the last dimension of every kv buffer must be contiguous")
@@ -675,9 +681,9 @@ def spec_kv_compact_paged(kv_buffers, page_table, path, count, base=None, *, str
     _shaped("count", count, (B,), torch.int32)
     _shaped("base", base, (B,), torch.int32)
     row = max(strides[2], W) if ps == 1 else strides[2]
-    _launch("spec_kv_compact_paged", dev, stream, lib().spec_kv_compact_paged, (ctypes.c_void_p * n)(*ptrs), n,
-            strides[0] * es, strides[1] * es, H, row * es, W * es, _ptr(page_table), P, ps, page_table.shape[1],
-            _ptr(path), _ptr(count), _ptr(base), B, path.shape[1])
+    _launch("spec_kv_compact_paged", at, lib().spec_kv_compact_paged, (ctypes.c_void_p * n)(*ptrs), n,
+            strides[0] * es, strides[1] * es, H, row * es, W * es, _adr(page_table), P, ps, page_table.shape[1],
+            _adr(path), _adr(count), _adr(base), B, path.shape[1], handle)
 
 
 def spec_paged_attention_workspace_size(B: int, Q: int, num_q_heads: int, num_heads: int, head_dim: int, cache_dtype,
@@ -694,12 +700,12 @@ def spec_paged_attention_workspace_size(B: int, Q: int, num_q_heads: int, num_he
 _attention_needs = {}
 
 
-def _attention_need(dev, *sizes):
+def _attention_need(at, *sizes):
     """spec_paged_attention_workspace_size(*sizes) on a device, remembered by the sizes."""
-    key = (dev.index, *sizes)
+    key = (at, *sizes)
     need = _attention_needs.get(key)
     if need is None:
-        with _torch().cuda.device(dev):
+        with _torch().cuda.device(at):
             need = int(lib().spec_paged_attention_workspace_size(*sizes))
         if len(_attention_needs) >= 4096:  # context lengths vary: keep the table small
             _attention_needs.clear()
@@ -722,7 +728,7 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, base, *, max_len=None,
     Returns (out bf16 [B][Q][q_heads][head_dim], lse fp32 [B][Q][q_heads] or None)."""
     torch = _torch()
     auto = isinstance(workspace, str)
-    dev, stream = _one_device(q, stream, q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, base=base,
+    at, handle, side = _one_device(q, stream, q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, base=base,
                               new_len=new_len, tree_mask=tree_mask, k_scale=k_scale, v_scale=v_scale, out=out,
                               out_lse=out_lse, workspace=None if auto else workspace)
     if q.dim() != 4 or q.dtype != torch.bfloat16:
@@ -743,18 +749,18 @@ def spec_paged_attention(q, k_pages, v_pages, page_table, base, *, max_len=None,
     if scale is None:
         scale = D ** -0.5
     if out is None:
-        out = _new((B, Q, Hq, D), torch.bfloat16, dev, stream)
+        out = _new(torch.empty, (B, Q, Hq, D), torch.bfloat16, at, side)
     if out_lse is None and want_lse:
-        out_lse = _new((B, Q, Hq), torch.float32, dev, stream)
+        out_lse = _new(torch.empty, (B, Q, Hq), torch.float32, at, side)
     if auto:
-        need = _attention_need(dev, B, Q, Hq, cache.num_heads, D, cache.dtype, max_len) if B else 0
-        workspace = _new((need,), torch.uint8, dev, stream) if need else None
+        need = _attention_need(at, B, Q, Hq, cache.num_heads, D, cache.dtype, max_len) if B else 0
+        workspace = _new(torch.empty, (need,), torch.uint8, at, side) if need else None
     elif workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _launch("spec_paged_attention", dev, stream, lib().spec_paged_attention, _ptr(q), _strides3(q, "q"), Hq, cache,
-            _ptr(base), _ptr(new_len), _ptr(tree_mask), scale, B, Q, max_len, _ptr(out), _ptr(out_lse),
-            _ptr(workspace), ws_bytes)
+    _launch("spec_paged_attention", at, lib().spec_paged_attention, _adr(q), _strides3(q, "q"), Hq, cache,
+            _adr(base), _adr(new_len), _adr(tree_mask), scale, B, Q, max_len, _adr(out), _adr(out_lse),
+            _adr(workspace), ws_bytes, handle)
     return out, out_lse
 
 
@@ -771,7 +777,7 @@ def spec_adjust_logits(logits, *, history=None, history_len=None, prompt_len=Non
     [B][R][ceil(V/32)], bit v % 32 of word v / 32 set where token v is allowed.  Any of them
     may be None.  Returns out (a new tensor unless given; logits itself works in place)."""
     torch = _torch()
-    dev, stream = _one_device(logits, stream, logits=logits, history=history, history_len=history_len,
+    at, handle, side = _one_device(logits, stream, logits=logits, history=history, history_len=history_len,
                               prompt_len=prompt_len, draft_tokens=draft_tokens, tree_mask=tree_mask,
                               repetition=repetition, presence=presence, frequency=frequency, bias_tokens=bias_tokens,
                               bias_values=bias_values, allowed=allowed, out=out)
@@ -787,8 +793,7 @@ def spec_adjust_logits(logits, *, history=None, history_len=None, prompt_len=Non
         H = history.shape[1]
         _shaped("history", history, (B, H), i32)
         if history_len is None:
-            with torch.cuda.stream(stream):
-                history_len = torch.full((B,), H, dtype=i32, device=dev)
+            history_len = _new(lambda size, **kw: torch.full(size, H, **kw), (B,), i32, at, side)
     elif history_len is not None or prompt_len is not None:
         raise ValueError("history_len and prompt_len belong to a history")
     _shaped("history_len", history_len, (B,), i32)
@@ -811,9 +816,9 @@ def spec_adjust_logits(logits, *, history=None, history_len=None, prompt_len=Non
     _shaped("allowed", allowed, (B, R, (V + 31) // 32), i32)
     _shaped("out", out, (B, R, V), logits.dtype)
     if out is None:
-        out = _new((B, R, V), logits.dtype, dev, stream)
-    _launch("spec_adjust_logits", dev, stream, lib().spec_adjust_logits, _ptr(logits), code, _ptr(history),
-            _ptr(history_len), _ptr(prompt_len), H, _ptr(draft_tokens), _ptr(tree_mask), _ptr(repetition),
-            _ptr(presence), _ptr(frequency), _ptr(bias_tokens), _ptr(bias_values), M, _ptr(allowed), B, R, V,
-            _ptr(out))
+        out = _new(torch.empty, (B, R, V), logits.dtype, at, side)
+    _launch("spec_adjust_logits", at, lib().spec_adjust_logits, _adr(logits), code, _adr(history),
+            _adr(history_len), _adr(prompt_len), H, _adr(draft_tokens), _adr(tree_mask), _adr(repetition),
+            _adr(presence), _adr(frequency), _adr(bias_tokens), _adr(bias_values), M, _adr(allowed), B, R, V,
+            _adr(out), handle)
     return out
