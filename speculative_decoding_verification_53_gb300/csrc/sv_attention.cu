@@ -4,19 +4,24 @@
 //
 // out = softmax(scale q k^T) v in one pass over the cache: each warp keeps the running
 // maximum m and sum l of its rows and rescales its fp32 accumulator when m grows.  Few
-// rows (a chain of drafts times the heads that share a cache head) are bound by the
-// cache's bytes: the kernel's work is to keep loads in flight.  So a CTA streams tiles of
-// 64 positions through a ring of shared-memory stages filled by cp.async (16 bytes per
-// thread, any page size, holes and rows behind the end filled with zeros), its warps take
-// 16 positions each of every tile, and their partial results meet once at the end.  The
-// products use mma.sync (m16n8k16, bf16): at 64 rows or fewer they stay below the time the
-// bytes take, and 16-row tiles waste less than the 128 rows of tcgen05.
+// rows (one token times the heads that share a cache head, and heads wider than 128) are
+// bound by the cache's bytes: the kernel's work is to keep loads in flight.  So a CTA
+// streams tiles of 64 positions through a ring of shared-memory stages filled by cp.async
+// (16 bytes per thread, any page size, holes and rows behind the end filled with zeros),
+// its warps take 16 positions each of every tile, and their partial results meet once at
+// the end.  The products use mma.sync (m16n8k16): 16-row tiles waste less than the 128
+// rows of tcgen05 (sv_attention_tc.cu, the kernel of longer chunks; make_plan chooses).
+// 64 contexts of 4096, one query of 32 over 8 heads of 128, one GB300: bf16 208 us
+// (5.2 TB/s), e4m3 201 us (2.8 TB/s; bound by the issue of the widening and the softmax).
+// Filling the stages by the copy engine instead of cp.async: 258 against 213 us, not kept.
 //
 // e4m3 pages are copied as they are, and each warp widens its fragments to bf16 (exactly);
 // a position's key scale multiplies its scores, its value scale its probabilities.  Keys:
 // a thread reads 16 contiguous codes of a position, which fixes an order of the head's
 // elements within a product; the queries are stored in that order.  Values: ldmatrix
 // transposes pairs of codes, so two column tiles hold the even and the odd elements.
+// Multiplied as fp16 (two codes an instruction) with units that a row takes from the value
+// scales it sees, that call took 195 us: not worth the units' code, not kept.
 #include <cstdint>
 
 #include "spec_paged_kv.h"
@@ -67,18 +72,17 @@ __device__ __forceinline__ uint32_t widen(uint32_t w) {
     return sv::bf16x2(f.x, f.y);
 }
 
-template <int DP, int MW, int MT, bool E4M3>
+template <int DP, int MW, bool E4M3>
 struct Shape {
-    static constexpr int ROWS = MW * MT * 16;
+    static constexpr int ROWS = MW * 16;
     static constexpr int THREADS = MW * KW * 32;
     static constexpr int ES = E4M3 ? 1 : 2;
     static constexpr int PITCH = DP * ES;          // bytes of a staged row
     static constexpr int CH = PITCH / 16;          // 16-byte pieces of a staged row
     static constexpr int MAT = TN * PITCH;         // a tile of keys, or of values
     static constexpr int STAGE = 2 * MAT + (E4M3 ? 2 * TN * 4 : 0);
-    // One CTA of 64 rows, or of wide heads, fills an SM's registers; else two share it.
-    static constexpr bool ALONE = ROWS == 64 || DP == 256;
-    static constexpr int BUDGET = ALONE ? 160 * 1024 : 97 * 1024;
+    // One CTA of wide heads fills an SM's registers; else two share it.
+    static constexpr int BUDGET = DP == 256 ? 160 * 1024 : 97 * 1024;
     static constexpr int FIT = BUDGET / STAGE;
     static constexpr int STAGES = FIT > 6 ? 6 : FIT < 3 ? 3 : FIT;
     static constexpr int QBYTES = ROWS * DP * 2;
@@ -98,10 +102,10 @@ __device__ __forceinline__ int v_piece(int r, int c) {  // eight rows are read t
     return r * PITCH + ((PITCH >= 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
 }
 
-template <int DP, int MW, int MT, bool E4M3>
-__global__ void __launch_bounds__(MW* KW * 32, (MW * MT * 16 == 64 || DP == 256) ? 1 : 2)
+template <int DP, int MW, bool E4M3>
+__global__ void __launch_bounds__(MW* KW * 32, DP == 256 ? 1 : 2)
     paged_attention_kernel(const __grid_constant__ AttnArgs a, const int pairs) {
-    using S = Shape<DP, MW, MT, E4M3>;
+    using S = Shape<DP, MW, E4M3>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t s_off[RING][TN];  // byte offset of each position's row, -1: nothing there
     __shared__ int64_t s_sc[E4M3 ? RING : 1][E4M3 ? TN : 1];  // index of its scales
@@ -194,25 +198,20 @@ __global__ void __launch_bounds__(MW* KW * 32, (MW * MT * 16 == 64 || DP == 256)
         if (pos + TN < t.end) next_page = sv::paged_place(a.c, t.b, pos + TN, next_row);
     }
 
-    constexpr bool QREG = MT * DP <= 128;
+    constexpr bool QREG = DP <= 128;
     constexpr int KS = DP / 16;
-    uint32_t qf[QREG ? MT : 1][QREG ? KS : 1][4];
-    const int q_r = wm * MT * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), q_c = lane >> 4;
+    uint32_t qf[QREG ? KS : 1][4];
+    const int q_r = wm * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), q_c = lane >> 4;
     if (QREG) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int k = 0; k < KS; ++k) ldsm4(q0 + v_piece<2 * DP>(q_r + 16 * m, 2 * k + q_c), qf[m][k]);
+        for (int k = 0; k < KS; ++k) ldsm4(q0 + v_piece<2 * DP>(q_r, 2 * k + q_c), qf[k]);
     }
-    float o[MT][DP / 8][4];
-    float mx[MT][2], l[MT][2];
+    float o[DP / 8][4];
+    float mx[2], l[2];
+    mx[0] = mx[1] = neg_inf();
+    l[0] = l[1] = 0.0f;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        mx[m][0] = mx[m][1] = neg_inf();
-        l[m][0] = l[m][1] = 0.0f;
-#pragma unroll
-        for (int n = 0; n < DP / 8; ++n) o[m][n][0] = o[m][n][1] = o[m][n][2] = o[m][n][3] = 0.0f;
-    }
+    for (int n = 0; n < DP / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
 
     const int g = lane >> 2, t4 = lane & 3;
     for (int j = 0; j < tiles; ++j) {
@@ -265,25 +264,20 @@ __global__ void __launch_bounds__(MW* KW * 32, (MW * MT * 16 == 64 || DP == 256)
         const uint32_t ks0 = smem_u32(stage), vs0 = ks0 + S::MAT;
         const float* k_sc = reinterpret_cast<const float*>(stage + 2 * S::MAT);
 
-        float s[MT][2][4];
+        float s[2][4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int n = 0; n < 2; ++n) s[m][n][0] = s[m][n][1] = s[m][n][2] = s[m][n][3] = 0.0f;
+        for (int n = 0; n < 2; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
         if (!E4M3) {
             const int kr = wk * 16 + (lane >> 4) * 8 + (lane & 7), kc = (lane >> 3) & 1;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 uint32_t b[4];
                 ldsm4(ks0 + v_piece<S::PITCH>(kr, 2 * k + kc), b);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    uint32_t qa[4];
-                    if (!QREG) ldsm4(q0 + v_piece<2 * DP>(q_r + 16 * m, 2 * k + q_c), qa);
-                    const uint32_t* q = QREG ? qf[QREG ? m : 0][QREG ? k : 0] : qa;
-                    mma16816(s[m][0], q, b[0], b[1]);
-                    mma16816(s[m][1], q, b[2], b[3]);
-                }
+                uint32_t qa[4];
+                if (!QREG) ldsm4(q0 + v_piece<2 * DP>(q_r, 2 * k + q_c), qa);
+                const uint32_t* q = QREG ? qf[QREG ? k : 0] : qa;
+                mma16816(s[0], q, b[0], b[1]);
+                mma16816(s[1], q, b[2], b[3]);
             }
         } else {
 #pragma unroll
@@ -302,14 +296,11 @@ __global__ void __launch_bounds__(MW* KW * 32, (MW * MT * 16 == 64 || DP == 256)
                         b[2 * n] = widen(x & 0xffffu);
                         b[2 * n + 1] = widen(x >> 16);
                     }
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        uint32_t qa[4];
-                        if (!QREG) ldsm4(q0 + v_piece<2 * DP>(q_r + 16 * m, 2 * k + q_c), qa);
-                        const uint32_t* q = QREG ? qf[QREG ? m : 0][QREG ? k : 0] : qa;
-                        mma16816(s[m][0], q, b[0], b[1]);
-                        mma16816(s[m][1], q, b[2], b[3]);
-                    }
+                    uint32_t qa[4];
+                    if (!QREG) ldsm4(q0 + v_piece<2 * DP>(q_r, 2 * k + q_c), qa);
+                    const uint32_t* q = QREG ? qf[QREG ? k : 0] : qa;
+                    mma16816(s[0], q, b[0], b[1]);
+                    mma16816(s[1], q, b[2], b[3]);
                 }
             }
         }
@@ -322,60 +313,57 @@ __global__ void __launch_bounds__(MW* KW * 32, (MW * MT * 16 == 64 || DP == 256)
                 ksc[n][z] = E4M3 ? k_sc[p] * a.scale_log2 : a.scale_log2;
                 vsc[n][z] = E4M3 ? k_sc[TN + p] : 1.0f;
             }
-        uint32_t pf[MT][4];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            uint32_t see[2] = {valid, valid};
-            if (tail) {
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const int R = t.mt * S::ROWS + wm * MT * 16 + 16 * m + g + 8 * y;
-                    see[y] &= R < t.n * a.group ? sv::attn_visible(a, t, R / a.group, tile0 + wk * 16) : 0u;
-                }
-            }
-            float top[2] = {neg_inf(), neg_inf()};
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    float v = s[m][n][x] * ksc[n][x & 1];
-                    if (!((see[x >> 1] >> (n * 8 + 2 * t4 + (x & 1))) & 1u)) v = neg_inf();
-                    s[m][n][x] = v;
-                    top[x >> 1] = fmaxf(top[x >> 1], v);
-                }
-            float shift[2], fac[2];
+        uint32_t pf[4];
+        uint32_t see[2] = {valid, valid};
+        if (tail) {
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 1));
-                top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 2));
-                const float now = fmaxf(mx[m][y], top[y]);
-                shift[y] = now == neg_inf() ? 0.0f : now;
-                fac[y] = sv::ex2(mx[m][y] - shift[y]);  // 0 while the row has seen nothing
-                mx[m][y] = now;
+                const int R = t.mt * S::ROWS + wm * 16 + g + 8 * y;
+                see[y] &= R < t.n * a.group ? sv::attn_visible(a, t, R / a.group, tile0 + wk * 16) : 0u;
             }
-            if (__any_sync(0xffffffffu, fac[0] != 1.0f || fac[1] != 1.0f)) {
-                l[m][0] *= fac[0];
-                l[m][1] *= fac[1];
+        }
+        float top[2] = {neg_inf(), neg_inf()};
 #pragma unroll
-                for (int n = 0; n < DP / 8; ++n) {
-                    o[m][n][0] *= fac[0];
-                    o[m][n][1] *= fac[0];
-                    o[m][n][2] *= fac[1];
-                    o[m][n][3] *= fac[1];
-                }
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                float v = s[n][x] * ksc[n][x & 1];
+                if (!((see[x >> 1] >> (n * 8 + 2 * t4 + (x & 1))) & 1u)) v = neg_inf();
+                s[n][x] = v;
+                top[x >> 1] = fmaxf(top[x >> 1], v);
             }
+        float shift[2], fac[2];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                float p[4];
+        for (int y = 0; y < 2; ++y) {
+            top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 1));
+            top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 2));
+            const float now = fmaxf(mx[y], top[y]);
+            shift[y] = now == neg_inf() ? 0.0f : now;
+            fac[y] = sv::ex2(mx[y] - shift[y]);  // 0 while the row has seen nothing
+            mx[y] = now;
+        }
+        if (__any_sync(0xffffffffu, fac[0] != 1.0f || fac[1] != 1.0f)) {
+            l[0] *= fac[0];
+            l[1] *= fac[1];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    p[x] = sv::ex2(s[m][n][x] - shift[x >> 1]);
-                    l[m][x >> 1] += p[x];
-                    if (E4M3) p[x] *= vsc[n][x & 1];
-                }
-                pf[m][2 * n] = sv::bf16x2(p[0], p[1]);
-                pf[m][2 * n + 1] = sv::bf16x2(p[2], p[3]);
+            for (int n = 0; n < DP / 8; ++n) {
+                o[n][0] *= fac[0];
+                o[n][1] *= fac[0];
+                o[n][2] *= fac[1];
+                o[n][3] *= fac[1];
             }
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            float p[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                p[x] = sv::ex2(s[n][x] - shift[x >> 1]);
+                l[x >> 1] += p[x];
+                if (E4M3) p[x] *= vsc[n][x & 1];
+            }
+            pf[2 * n] = sv::bf16x2(p[0], p[1]);
+            pf[2 * n + 1] = sv::bf16x2(p[2], p[3]);
         }
         if (!E4M3) {
             const int vr = wk * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), vc = lane >> 4;
@@ -383,11 +371,8 @@ __global__ void __launch_bounds__(MW* KW * 32, (MW * MT * 16 == 64 || DP == 256)
             for (int n = 0; n < DP / 16; ++n) {
                 uint32_t b[4];
                 ldsm4t(vs0 + v_piece<S::PITCH>(vr, 2 * n + vc), b);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    mma16816(o[m][2 * n], pf[m], b[0], b[1]);
-                    mma16816(o[m][2 * n + 1], pf[m], b[2], b[3]);
-                }
+                mma16816(o[2 * n], pf, b[0], b[1]);
+                mma16816(o[2 * n + 1], pf, b[2], b[3]);
             }
         } else {
             const int vr = wk * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), vc = lane >> 4;
@@ -400,11 +385,8 @@ __global__ void __launch_bounds__(MW* KW * 32, (MW * MT * 16 == 64 || DP == 256)
                     const uint32_t lo = __byte_perm(b[2 * z], 0u, 0x3120), hi = __byte_perm(b[2 * z + 1], 0u, 0x3120);
                     const uint32_t e0 = widen(lo & 0xffffu), e1 = widen(hi & 0xffffu);
                     const uint32_t f0 = widen(lo >> 16), f1 = widen(hi >> 16);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        mma16816(o[m][4 * n + 2 * z], pf[m], e0, e1);      // even elements
-                        mma16816(o[m][4 * n + 2 * z + 1], pf[m], f0, f1);  // odd elements
-                    }
+                    mma16816(o[4 * n + 2 * z], pf, e0, e1);      // even elements
+                    mma16816(o[4 * n + 2 * z + 1], pf, f0, f1);  // odd elements
                 }
             }
         }
@@ -413,120 +395,110 @@ __global__ void __launch_bounds__(MW* KW * 32, (MW * MT * 16 == 64 || DP == 256)
     // ---- the four warps of a row tile join
     cp_wait<0>();
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            l[m][y] += __shfl_xor_sync(0xffffffffu, l[m][y], 1);
-            l[m][y] += __shfl_xor_sync(0xffffffffu, l[m][y], 2);
-            const int r = wm * MT * 16 + 16 * m + g + 8 * y;
-            if (t4 == 0) {
-                s_m[wk][r] = mx[m][y];
-                s_l[wk][r] = l[m][y];
-            }
+    for (int y = 0; y < 2; ++y) {
+        l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
+        l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
+        const int r = wm * 16 + g + 8 * y;
+        if (t4 == 0) {
+            s_m[wk][r] = mx[y];
+            s_l[wk][r] = l[y];
         }
+    }
     __syncthreads();
-    float inv[MT][2], lse2[MT][2];
+    float inv[2], lse2[2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int y = 0; y < 2; ++y) {
+        const int r = wm * 16 + g + 8 * y;
+        float top = s_m[0][r];
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const int r = wm * MT * 16 + 16 * m + g + 8 * y;
-            float top = s_m[0][r];
+        for (int w = 1; w < KW; ++w) top = fmaxf(top, s_m[w][r]);
+        const float shift = top == neg_inf() ? 0.0f : top;
+        float sum = 0.0f;
 #pragma unroll
-            for (int w = 1; w < KW; ++w) top = fmaxf(top, s_m[w][r]);
-            const float shift = top == neg_inf() ? 0.0f : top;
-            float sum = 0.0f;
+        for (int w = 0; w < KW; ++w) sum += s_l[w][r] * sv::ex2(s_m[w][r] - shift);
+        const float fac = sv::ex2(mx[y] - shift);
+        inv[y] = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // NaN stays
+        lse2[y] = sum == 0.0f ? neg_inf() : shift + log2f(sum);
 #pragma unroll
-            for (int w = 0; w < KW; ++w) sum += s_l[w][r] * sv::ex2(s_m[w][r] - shift);
-            const float fac = sv::ex2(mx[m][y] - shift);
-            inv[m][y] = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // NaN stays
-            lse2[m][y] = sum == 0.0f ? neg_inf() : shift + log2f(sum);
-#pragma unroll
-            for (int n = 0; n < DP / 8; ++n) {
-                o[m][n][2 * y] *= fac;
-                o[m][n][2 * y + 1] *= fac;
-            }
+        for (int n = 0; n < DP / 8; ++n) {
+            o[n][2 * y] *= fac;
+            o[n][2 * y + 1] *= fac;
         }
-    float4* join = reinterpret_cast<float4*>(smem) + (size_t)wm * 2 * MT * (DP / 8) * 32 + lane;
+    }
+    float4* join = reinterpret_cast<float4*>(smem) + (size_t)wm * 2 * (DP / 8) * 32 + lane;
 #pragma unroll
     for (int half = 2; half >= 1; half >>= 1) {
         if (wk >= half && wk < 2 * half) {
-            float4* to = join + (size_t)(wk - half) * MT * (DP / 8) * 32;
+            float4* to = join + (size_t)(wk - half) * (DP / 8) * 32;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int n = 0; n < DP / 8; ++n)
-                    to[(m * (DP / 8) + n) * 32] = make_float4(o[m][n][0], o[m][n][1], o[m][n][2], o[m][n][3]);
+            for (int n = 0; n < DP / 8; ++n)
+                to[n * 32] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
         }
         __syncthreads();
         if (wk < half) {
-            const float4* from = join + (size_t)wk * MT * (DP / 8) * 32;
+            const float4* from = join + (size_t)wk * (DP / 8) * 32;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int n = 0; n < DP / 8; ++n) {
-                    const float4 v = from[(m * (DP / 8) + n) * 32];
-                    o[m][n][0] += v.x;
-                    o[m][n][1] += v.y;
-                    o[m][n][2] += v.z;
-                    o[m][n][3] += v.w;
-                }
+            for (int n = 0; n < DP / 8; ++n) {
+                const float4 v = from[n * 32];
+                o[n][0] += v.x;
+                o[n][1] += v.y;
+                o[n][2] += v.z;
+                o[n][3] += v.w;
+            }
         }
         __syncthreads();
     }
     if (wk != 0) return;
 
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int y = 0; y < 2; ++y) {
+        const int R = t.mt * S::ROWS + wm * 16 + g + 8 * y;
+        if (R >= t.n * a.group) continue;
+        const int64_t row = sv::attn_row(a, t, R);
+        const int64_t part = t.part + R - t.mt * S::ROWS;
+        if (t4 == 0) {
+            if (t.active > 1) a.part_lse[part] = lse2[y];
+            else if (a.lse) a.lse[row] = lse2[y] * 0.69314718055994531f;
+        }
+        // a thread's elements of each 16: bf16 pages 2 t4, 2 t4 + 1 and 8 more; e4m3 4 t4 .. 4 t4 + 3
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const int R = t.mt * S::ROWS + wm * MT * 16 + 16 * m + g + 8 * y;
-            if (R >= t.n * a.group) continue;
-            const int64_t row = sv::attn_row(a, t, R);
-            const int64_t part = t.part + R - t.mt * S::ROWS;
-            if (t4 == 0) {
-                if (t.active > 1) a.part_lse[part] = lse2[m][y];
-                else if (a.lse) a.lse[row] = lse2[m][y] * 0.69314718055994531f;
+        for (int n = 0; n < DP / 16; ++n) {
+            float v[4];
+            int d[2];
+            if (!E4M3) {
+                d[0] = 16 * n + 2 * t4;
+                d[1] = d[0] + 8;
+                v[0] = o[2 * n][2 * y]; v[1] = o[2 * n][2 * y + 1];
+                v[2] = o[2 * n + 1][2 * y]; v[3] = o[2 * n + 1][2 * y + 1];
+            } else {
+                d[0] = 16 * n + 4 * t4;
+                d[1] = d[0] + 2;
+                v[0] = o[2 * n][2 * y]; v[1] = o[2 * n + 1][2 * y];
+                v[2] = o[2 * n][2 * y + 1]; v[3] = o[2 * n + 1][2 * y + 1];
             }
-            // a thread's elements of each 16: bf16 pages 2 t4, 2 t4 + 1 and 8 more; e4m3 4 t4 .. 4 t4 + 3
 #pragma unroll
-            for (int n = 0; n < DP / 16; ++n) {
-                float v[4];
-                int d[2];
-                if (!E4M3) {
-                    d[0] = 16 * n + 2 * t4;
-                    d[1] = d[0] + 8;
-                    v[0] = o[m][2 * n][2 * y]; v[1] = o[m][2 * n][2 * y + 1];
-                    v[2] = o[m][2 * n + 1][2 * y]; v[3] = o[m][2 * n + 1][2 * y + 1];
-                } else {
-                    d[0] = 16 * n + 4 * t4;
-                    d[1] = d[0] + 2;
-                    v[0] = o[m][2 * n][2 * y]; v[1] = o[m][2 * n + 1][2 * y];
-                    v[2] = o[m][2 * n][2 * y + 1]; v[3] = o[m][2 * n + 1][2 * y + 1];
-                }
+            for (int x = 0; x < 4; ++x) v[x] *= inv[y];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) v[x] *= inv[m][y];
+            for (int z = 0; z < 2; ++z) {
+                if (d[z] >= D) continue;
+                if (s_bad) {
+                    const int from = t.begin + (t.base > t.begin ? (t.base - t.begin) / TN * TN : 0);
+                    for (int pos = from; pos < t.end; ++pos) {
+                        if (!(sv::attn_visible(a, t, R / a.group, pos) & 1u)) continue;
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    if (d[z] >= D) continue;
-                    if (s_bad) {
-                        const int from = t.begin + (t.base > t.begin ? (t.base - t.begin) / TN * TN : 0);
-                        for (int pos = from; pos < t.end; ++pos) {
-                            if (!(sv::attn_visible(a, t, R / a.group, pos) & 1u)) continue;
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const float w = sv::attn_value<E4M3>(a, t, pos, d[z] + x);
-                                if (sv::not_finite(w)) v[2 * z + x] += w;
-                            }
+                        for (int x = 0; x < 2; ++x) {
+                            const float w = sv::attn_value<E4M3>(a, t, pos, d[z] + x);
+                            if (sv::not_finite(w)) v[2 * z + x] += w;
                         }
                     }
-                    if (t.active > 1)
-                        *reinterpret_cast<float2*>(a.part_o + part * D + d[z]) = make_float2(v[2 * z], v[2 * z + 1]);
-                    else
-                        *reinterpret_cast<uint32_t*>(a.out + row * D + d[z]) = sv::bf16x2(v[2 * z], v[2 * z + 1]);
                 }
+                if (t.active > 1)
+                    *reinterpret_cast<float2*>(a.part_o + part * D + d[z]) = make_float2(v[2 * z], v[2 * z + 1]);
+                else
+                    *reinterpret_cast<uint32_t*>(a.out + row * D + d[z]) = sv::bf16x2(v[2 * z], v[2 * z + 1]);
             }
         }
+    }
 }
 
 // Joins the splits of a row: weights 2^(lse_s - max), one warp per row of the split tiles.
@@ -577,11 +549,11 @@ __global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_
     if (a.lse && lane == 0) a.lse[row] = sum == 0.0f ? neg_inf() : (shift + log2f(sum)) * 0.69314718055994531f;
 }
 
-template <int DP, int MW, int MT, bool E4M3>
+template <int DP, int MW, bool E4M3>
 cudaError_t launch_shape(const AttnArgs& a, int pairs, unsigned ctas, cudaStream_t stream) {
-    using S = Shape<DP, MW, MT, E4M3>;
+    using S = Shape<DP, MW, E4M3>;
     static sv::KernelLaunchCache cache;
-    auto kern = paged_attention_kernel<DP, MW, MT, E4M3>;
+    auto kern = paged_attention_kernel<DP, MW, E4M3>;
     int max_dyn = 0;
     const cudaError_t e = cache.setup((const void*)kern, &max_dyn);
     if (e != cudaSuccess) return e;
@@ -592,8 +564,8 @@ cudaError_t launch_shape(const AttnArgs& a, int pairs, unsigned ctas, cudaStream
 template <int DP, bool E4M3>
 cudaError_t launch_rows(const AttnArgs& a, int pairs, int tile_rows, unsigned ctas, cudaStream_t stream) {
     if constexpr (DP == 256)
-        if (tile_rows == 32) return launch_shape<DP, 2, 1, E4M3>(a, pairs, ctas, stream);
-    return launch_shape<DP, 1, 1, E4M3>(a, pairs, ctas, stream);
+        if (tile_rows == 32) return launch_shape<DP, 2, E4M3>(a, pairs, ctas, stream);
+    return launch_shape<DP, 1, E4M3>(a, pairs, ctas, stream);
 }
 
 constexpr int kMaxB = 65535;
@@ -616,8 +588,9 @@ Plan make_plan(int B, int Q, int Hq, int H, int D, bool e4m3, int max_len, int n
     else if (rows > 128) p.tile_rows = 256;
     // Sixteen rows or fewer waste most of a 128-row product.  On one GB300, 32 over 8 heads of
     // 128, one query: 64 contexts of 4096 208 us (mma.sync) against 243 (tcgen05), e4m3 201
-    // against 328; one context of 2000 16.5 against 20.7, of 8000 33.5 against 24.7, of 131072
-    // 127 against 102.  17 rows and more: 64 x 300 x 24 rows 105 against 49 us.
+    // against 304; one context of 2000 16.5 against 20.7, of 8000 33.5 against 24.7 (e4m3 35
+    // against 29), of 131072 127 against 102 (e4m3 118 against 127).  17 rows and more: 64 x
+    // 300 x 24 rows 105 against 49 us.
     else if (rows > 16 || (!e4m3 && max_len >= 4096 && (int64_t)B * H <= num_sms)) p.tile_rows = 128;
     else p.tile_rows = 16;
     p.m_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);

@@ -266,6 +266,7 @@ struct __align__(16) Shared {
     __align__(16) float ksc[META][TN];  // e4m3: a position's key scale times the score factor
     __align__(16) uint2 vsc[META][TN];  // its value scale times 2^-vexp, as two fp16 numbers
     int vexp[META];
+    float limit[2];  // by stretch: larger value scales of new tokens are left to the end
     float row_factor[128];  // DUAL: what a row's scores are multiplied by
 };
 
@@ -317,6 +318,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         }
         sh.bad = 0;
         sh.failed = 0;
+        sh.limit[0] = sh.limit[1] = sv::pos_inf();
         sv::fence_mbar_init();
     }
     tc_fence_before();
@@ -492,6 +494,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             if (t.active > 1) a.part_lse[part] = lse2;
             else if (a.lse) a.lse[row] = lse2 * 0.69314718055994531f;
         }
+        const float weight = inv;
         if (E4M3) inv *= power_of_two(vexp);
         const bool patch = ok && sh.bad != 0;
         // Rows leave through shared memory (where this row tile's queries were), so that a store
@@ -508,24 +511,51 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 for (int z = 0; z < CW; z += 32) tmem_ld32(o_at + CW * c + z, v + z);
                 tc_wait_ld();
                 if (live && patch) {
-                    // values that are not finite, for the queries that see them
+                    // values that were left out, for the queries that see them
+#pragma unroll
+                    for (int k = 0; k < CW; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * inv);
                     int from = first;
                     if (open > first) from += (open - first) / TN * TN;
                     for (int pos = from; pos < last; ++pos) {
                         if (!(sv::attn_visible(a, t, i, pos) & 1u)) continue;
+                        if (!E4M3) {
 #pragma unroll
-                        for (int k = 0; k < CW; ++k) {
-                            if (CW * c + k >= D) break;
-                            const float w = sv::attn_value<E4M3>(a, t, pos, CW * c + k);
-                            if (sv::not_finite(w)) v[k] = __float_as_uint(__uint_as_float(v[k]) + w);
+                            for (int k = 0; k < CW; ++k) {
+                                if (CW * c + k >= D) break;
+                                const float w = sv::attn_value<E4M3>(a, t, pos, CW * c + k);
+                                if (sv::not_finite(w)) v[k] = __float_as_uint(__uint_as_float(v[k]) + w);
+                            }
+                        } else {
+                            int r;
+                            const int page = sv::paged_place(a.c, t.b, pos, r);
+                            if (page < 0) continue;
+                            const int64_t at = page * a.c.page_stride + t.h * a.c.head_stride + r * a.c.row_stride;
+                            const int64_t sc_at = ((int64_t)page * a.c.heads + t.h) * a.c.page_size + r;
+                            const float vs = __ldg(a.c.v_scale + sc_at);
+                            const bool large = pos >= open && !sv::not_finite(vs) && fabsf(vs) > sh.limit[DUAL ? q : 0];
+                            float p = 0.0f;
+                            if (large) {  // its probability, from the cache
+                                const uint16_t* qr = a.q + t.b * a.q_sb + i * a.q_st + (int64_t)(t.h * a.group + R - i * a.group) * a.q_sh;
+                                for (int d = 0; d < D; ++d)
+                                    p += __uint_as_float((uint32_t)__ldg(qr + d) << 16) * sv::e4m3x2_to_f32(__ldg(a.c.k + at + d)).x;
+                                p = sv::ex2(p * (__ldg(a.c.k_scale + sc_at) * a.scale_log2) - mx + RAISE) * weight;
+                            }
+#pragma unroll
+                            for (int k = 0; k < CW; ++k) {
+                                if (CW * c + k >= D) break;
+                                const float w = sv::e4m3x2_to_f32(__ldg(a.c.v + at + CW * c + k)).x;
+                                if (large) v[k] = __float_as_uint(__uint_as_float(v[k]) + p * w * vs);
+                                else if (sv::not_finite(w * vs)) v[k] = __float_as_uint(__uint_as_float(v[k]) + w * vs);
+                            }
                         }
                     }
                 }
+                const float by = patch ? 1.0f : inv;
 #pragma unroll
                 for (int k = 0; k < PC; ++k)
                     sts16(stage + 16 * (PC * lane + (k ^ (lane & (PC - 1)))),
-                          make_uint4(__float_as_uint(__uint_as_float(v[4 * k]) * inv), __float_as_uint(__uint_as_float(v[4 * k + 1]) * inv),
-                                     __float_as_uint(__uint_as_float(v[4 * k + 2]) * inv), __float_as_uint(__uint_as_float(v[4 * k + 3]) * inv)));
+                          make_uint4(__float_as_uint(__uint_as_float(v[4 * k]) * by), __float_as_uint(__uint_as_float(v[4 * k + 1]) * by),
+                                     __float_as_uint(__uint_as_float(v[4 * k + 2]) * by), __float_as_uint(__uint_as_float(v[4 * k + 3]) * by)));
                 __syncwarp();
                 if (t.active > 1) {
                     const int k = lane % PC, d = CW * c + 4 * k;
@@ -891,7 +921,20 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             // ----------------------------------------------------------- notes
             // Which positions of a tile hold something, and e4m3's scales; read ahead, so that
             // nobody else waits for a page table or a scale.
-            uint32_t largest_v = 0u, other_v = 0u;  // the stretches' largest finite value scales so far, as bits
+            // The stretches' largest finite value scales so far, as bits, and those of positions that
+            // every query sees (the last such position is one for both).  A new token's scale far
+            // above the latter would push the values of queries that do not see it out of fp16's
+            // range: its value is left to the end, as values that are not finite are.  Up to 2^12
+            // above, rounding to the unit costs the others at most 2^-27 of their own largest.
+            uint32_t largest_v = 0u, other_v = 0u, seen = 0u, other_seen = 0u;
+            if (E4M3) {
+                int row;
+                const int page = sv::paged_place(a.c, t.b, open - 1, row);
+                if (page >= 0) {
+                    const float s = fabsf(__ldg(a.c.v_scale + ((int64_t)page * a.c.heads + t.h) * a.c.page_size + row));
+                    if (!sv::not_finite(s)) seen = other_seen = __float_as_uint(s);
+                }
+            }
             int64_t at1[4];  // index of the scales of the next tile's positions, -1: nothing there
             float ks[4], vs[4];
             uint32_t bits[4];
@@ -929,15 +972,24 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     for (int z = 0; z < 4; ++z) sh.valid[m][z] = bits[z];
                 }
                 if (E4M3) {
+                    const bool tail = start(j) + TN > open;
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        if (!sv::not_finite(vs[z])) {
-                            largest_v = max(largest_v, __float_as_uint(fabsf(vs[z])));
-                        } else if (start(j) + TN > open) {
-                            vs[z] = 0.0f;  // put back at the end, as the values are
-                            sh.bad = 1;
-                        }
+                    for (int z = 0; z < 4; ++z)
+                        if (start(j) + 32 * z + lane < open && !sv::not_finite(vs[z])) seen = max(seen, __float_as_uint(fabsf(vs[z])));
+                    if (tail) {
+                        seen = __reduce_max_sync(0xffffffffu, seen);
+                        const float limit = 4096.0f * __uint_as_float(seen);
+                        if (lane == 0) sh.limit[DUAL ? j & 1 : 0] = limit;
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            if (sv::not_finite(vs[z]) || (start(j) + 32 * z + lane >= open && fabsf(vs[z]) > limit)) {
+                                vs[z] = 0.0f;  // put back at the end, as the values are
+                                sh.bad = 1;
+                            }
                     }
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        if (!sv::not_finite(vs[z])) largest_v = max(largest_v, __float_as_uint(fabsf(vs[z])));
                     largest_v = __reduce_max_sync(0xffffffffu, largest_v);
                     // scales below 2^6, times codes of at most 448: below 2^15
                     const int e = (int)(largest_v >> 23) - 127 + 1 - 6, ve = e < -118 ? -118 : e;
@@ -949,9 +1001,11 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     };
                     if (lane == 0) sh.vexp[m] = ve;
                     if (DUAL) {  // the next tile is the other stretch's
-                        const uint32_t x = largest_v;
+                        const uint32_t x = largest_v, y = seen;
                         largest_v = other_v;
+                        seen = other_seen;
                         other_v = x;
+                        other_seen = y;
                     }
 #pragma unroll
                     for (int z = 0; z < 4; ++z) {

@@ -74,44 +74,6 @@ __device__ __forceinline__ float finite_abs(float x) {
     return a < sv::pos_inf() ? a : 0.0f;  // false for NaN and infinity
 }
 
-// Writes eight elements of a cache row (and the row's scale).  LPR lanes hold the row.
-template <int LPR, bool E4M3, bool AL>
-__device__ __forceinline__ void store_cache_row(unsigned char* row, float* scale, int e0, int dim, bool live,
-                                                const float x[8]) {
-    if (E4M3) {
-        float a = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) a = fmaxf(a, finite_abs(x[j]));
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        const float s = fmaxf(a / sv::E4M3_MAX, 1.17549435e-38f), inv = 1.0f / s;
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = sv::e4m3x2(x[2 * j] * inv, x[2 * j + 1] * inv);
-        if (!live) return;
-        if (e0 == 0) *scale = s;
-        if (AL) {
-            if (e0 < dim) *reinterpret_cast<uint2*>(row + e0) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (e0 + j < dim) row[e0 + j] = (unsigned char)(w[j / 2] >> (8 * (j & 1)));
-        }
-    } else {
-        if (!live) return;
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = sv::bf16x2(x[2 * j], x[2 * j + 1]);
-        if (AL) {
-            if (e0 < dim) *reinterpret_cast<uint4*>(row + 2 * e0) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (e0 + j < dim) reinterpret_cast<unsigned short*>(row)[e0 + j] = (unsigned short)(w[j / 2] >> (16 * (j & 1)));
-        }
-    }
-}
-
 // Eight elements of a row as they lie in memory (AL), or widened one by one.
 template <typename T, bool AL>
 struct Eight {
@@ -126,6 +88,21 @@ struct Eight {
         } else {
             w[0] = w[sizeof(T) == 4 ? 1 : 0] = make_uint4(0u, 0u, 0u, 0u);
         }
+    }
+    // Bits of the largest magnitude; at 0x7f800000 or beyond where one is not finite.
+    __device__ __forceinline__ uint32_t largest() const {
+        if (AL && sizeof(T) == 2) {  // two bf16 at a time: as integers magnitudes are in order
+            const uint32_t a = __vmaxu2(w[0].x & 0x7fff7fffu, w[0].y & 0x7fff7fffu);
+            const uint32_t b = __vmaxu2(w[0].z & 0x7fff7fffu, w[0].w & 0x7fff7fffu);
+            const uint32_t c = __vmaxu2(a, b);
+            return max(c << 16, c & 0xffff0000u);
+        }
+        float x[8];
+        widen(x);
+        uint32_t m = 0u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7fffffffu);
+        return m;
     }
     __device__ __forceinline__ void widen(float x[8]) const {
         if (!AL) {
@@ -143,6 +120,59 @@ struct Eight {
         }
     }
 };
+
+// Writes eight elements of a cache row (and the row's scale).  LPR lanes hold the row.
+template <typename T, int LPR, bool E4M3, bool AL>
+__device__ __forceinline__ void store_cache_row(unsigned char* row, float* scale, int e0, int dim, bool live,
+                                                const Eight<T, AL>& v) {
+    if (E4M3) {
+        uint32_t top = v.largest();
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float a = __uint_as_float(top);
+        if (__any_sync(0xffffffffu, top >= 0x7f800000u)) {  // rare: the largest finite magnitude
+            float x[8];
+            v.widen(x);
+            a = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a = fmaxf(a, finite_abs(x[j]));
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        }
+        const float s = fmaxf(a / sv::E4M3_MAX, 1.17549435e-38f), inv = 1.0f / s;
+        if (!live) return;
+        float x[8];
+        v.widen(x);
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 y = sv::fmul2(make_float2(x[2 * j], x[2 * j + 1]), make_float2(inv, inv));
+            w[j] = sv::e4m3x2(y.x, y.y);
+        }
+        if (e0 == 0) *scale = s;
+        if (AL) {
+            if (e0 < dim) *reinterpret_cast<uint2*>(row + e0) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (e0 + j < dim) row[e0 + j] = (unsigned char)(w[j / 2] >> (8 * (j & 1)));
+        }
+    } else {
+        if (!live) return;
+        float x[8];
+        v.widen(x);
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = sv::bf16x2(x[2 * j], x[2 * j + 1]);
+        if (AL) {
+            if (e0 < dim) *reinterpret_cast<uint4*>(row + 2 * e0) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (e0 + j < dim) reinterpret_cast<unsigned short*>(row)[e0 + j] = (unsigned short)(w[j / 2] >> (16 * (j & 1)));
+        }
+    }
+}
 
 // Rows (of one token and head) that a group of lanes does where there are blocks to spare: all
 // their loads are in flight before the first is looked at, as they lie in memory (widened they
@@ -181,11 +211,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
         const unsigned h = (block0 + threadIdx.x / LPR + k * RPC) % heads;
         const int64_t at = page[k] * a.c.page_stride + h * a.c.head_stride + row[k] * a.c.row_stride;
         const int64_t sc = ((int64_t)page[k] * heads + h) * a.c.page_size + row[k];
-        float f[8];
-        x[k].widen(f);
-        store_cache_row<LPR, E4M3, AL>(a.c.k + at, a.c.k_scale + sc, e0, a.c.dim, page[k] >= 0, f);
-        y[k].widen(f);
-        store_cache_row<LPR, E4M3, AL>(a.c.v + at, a.c.v_scale + sc, e0, a.c.dim, page[k] >= 0, f);
+        store_cache_row<T, LPR, E4M3, AL>(a.c.k + at, a.c.k_scale + sc, e0, a.c.dim, page[k] >= 0, x[k]);
+        store_cache_row<T, LPR, E4M3, AL>(a.c.v + at, a.c.v_scale + sc, e0, a.c.dim, page[k] >= 0, y[k]);
     }
 }
 

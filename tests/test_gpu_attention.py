@@ -11,9 +11,9 @@ e4m3 calls of more than 16 query rows per cache head multiply in fp16, half step
 element of a value and a probability are rounded once each, together below bf16's 2^-8.
 Probabilities are held times 2^7, where fp16 steps by 2^-24 below 2^-14: a position whose weight
 is tiny is off by up to 2^-32 of the largest weight, and the sum they are divided by is at
-least 1: n positions add at most n 2^-32 V, V = 448 vmax the largest |v| that the scales allow.
-A value element far below V is off by up to 2^-25 2^E with 2^E <= 2^-5 vmax, below 2^-38 V.  Both
-are within n 2^-31 V.
+least 1: n positions add at most n 2^-32 V, V = 448 vmax the largest |v| that the scales allow.  A value element far below V is
+off by up to 2^-25 2^E with 2^E <= 2^-5 vmax, below 2^-38 V (both are within n 2^-31 V); a hidden
+scale of up to 2^12 vmax takes that to 2^-26 V, which the test of such scales adds.
 """
 import numpy as np
 import pytest
@@ -26,8 +26,9 @@ from test_gpu_paged_kv import host, ints, make_cache, sv, values  # noqa: F401
 pytestmark = pytest.mark.gpu
 
 
-def check(got, lse, q, k, v, ks, vs, table, base, new_len, mask, scale, keep_out, keep_lse, rows=None):
-    """Compares whole outputs; keep_out and keep_lse fill what must not be written."""
+def check(got, lse, q, k, v, ks, vs, table, base, new_len, mask, scale, keep_out, keep_lse, rows=None, vmax=None):
+    """Compares whole outputs, or the queries `rows`, for which `vmax` is the largest value scale;
+    keep_out and keep_lse fill what must not be written."""
     B, Q, Hq, D = q.shape
     kv, vv = values(k), values(v)
     if ks is not None:
@@ -47,7 +48,12 @@ def check(got, lse, q, k, v, ks, vs, table, base, new_len, mask, scale, keep_out
     tol = (2.0 ** -8 + 4 * e) * np.abs(size) + 2.0 ** -8 * np.abs(want) + 1e-30
     if half:
         scales = host(vs)
-        tol = tol + (int(base.max()) + Q) * 2.0 ** -31 * 448 * scales[np.isfinite(scales)].max()
+        vmax = scales[np.isfinite(scales)].max() if vmax is None else vmax
+        tol = tol + (int(base.max()) + Q) * 2.0 ** -31 * 448 * vmax
+        if rows is not None:
+            tol = tol + 2.0 ** -26 * 448 * vmax
+    if rows is not None:
+        g, gl, want, want_lse, tol = (x[:, rows] for x in (g, gl, want, want_lse, tol))
     assert np.isfinite(g).all()
     worst = (np.abs(g - want) / tol).max()
     assert worst <= 1, f"output off by {worst:.3g} tolerances"
@@ -235,6 +241,52 @@ def test_bad_values_reach_only_who_sees_them(sv, cache, Q):  # noqa: F811
                 vs[page, 0, row] = keep[1]
     again, _ = run(sv, c)
     assert torch.equal(again, clean)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("Q,ctx", [(3, 0), (3, 90), (4, 700), (6, 100), (40, 0), (40, 128), (61, 700), (200, 20), (300, 600)])
+def test_large_values_reach_only_who_sees_them(sv, cache, tree, Q, ctx):  # noqa: F811
+    """Finite but huge drafted values and keys, and what a page holds behind the last token."""
+    import torch
+    rng = np.random.default_rng([Q, ctx, tree])
+    c = case(rng, 2, Q, 4, 1, 128, 16, ctx, cache, tree, False, ragged=False)
+    q, k, v, ks, vs, table, base, new_len, mask = c
+    node = Q // 2 - 1                             # token node + 1
+    last = int(base[0]) + Q                       # behind the last token
+    for pos in (int(base[0]) + node + 1, last):
+        page, row = (int(table[0, pos // 16]), pos % 16) if pos // 16 < table.shape[1] else (None, None)
+        if page is None:
+            continue
+        if cache == "e4m3":
+            vs[page, 0, row] = 1e30
+            v[page, 0, row].view(torch.uint8).fill_(0x55)
+        else:
+            v[page, 0, row] = 1e30
+        if pos == last:
+            k[page, 0, row].view(torch.uint8).fill_(0x55) if cache == "e4m3" else k[page, 0, row].fill_(1e30)
+            if cache == "e4m3":
+                ks[page, 0, row] = 1e30
+    sees = np.array([False] + [(bool((int(mask[0, i, node // 32]) >> (node % 32)) & 1) if tree else i >= node)
+                               for i in range(Q - 1)])
+    o, l = run(sv, c)
+    scale = q.shape[3] ** -0.5
+    vmax = None
+    if cache == "e4m3":
+        f = host(vs)
+        vmax = f[np.isfinite(f) & (f < 1e29)].max()
+        ks = ks.clone()
+        ks[ks == 1e30] = float("nan")             # no query reaches it: out of the tolerance's sums
+    else:
+        k = k.clone()
+        k[k > 1e29] = float("nan")
+    def some(rows, vmax):
+        check(o[:1], l[:1], q[:1], k, v, ks, vs, table[:1], base[:1], new_len[:1], None if mask is None else mask[:1],
+              scale, 5.0, 6.0, rows, vmax)
+    some(~sees, vmax)
+    some(sees, None)
+    check(o[1:], l[1:], q[1:], k, v, ks, vs, table[1:], base[1:], new_len[1:], None if mask is None else mask[1:],
+          scale, 5.0, 6.0, None, vmax)
 
 
 def test_a_long_context_in_pages_beyond_32_bits(sv):  # noqa: F811
