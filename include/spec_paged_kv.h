@@ -118,8 +118,13 @@ SV_API sv_status spec_kv_read(const sv_paged_cache *cache, const int32_t *base, 
  *                exponentials of the scaled scores.
  * A query that sees no position (or only scores of -inf) gets a zero output and lse -inf.  Keys and values at
  * positions that a query does not see never affect it, whatever they hold.  Scores,
- * softmax sums and outputs are accumulated in fp32; the probabilities (for e4m3, times
- * the value's scale) enter the second product rounded to bf16.
+ * softmax sums and outputs are accumulated in fp32; the probabilities enter the second
+ * product rounded to bf16 (for e4m3, times the value's scale).  e4m3 calls of more than 16
+ * query rows per cache head and head_dim <= 128 multiply as fp16 instead: a value's code
+ * times its scale and a probability are rounded once each to 11 bits, and what a position
+ * adds below 2^-31 of 448 times the largest value scale may be lost.
+ * out must not overlap q or the cache.  Every wait inside the kernels is bounded; where one
+ * runs out, the rows concerned are written as NaN, which a verify reports as invalid data.
  *   workspace    device scratch of ws_bytes, 16-byte aligned (spec_paged_attention_workspace_size;
  *                no initialisation, free for other uses once the call has run), or NULL:
  *                contexts are then not split, which is slower for few rows and long contexts.
@@ -144,6 +149,7 @@ SV_API size_t spec_paged_attention_workspace_size(int B, int Q, int num_q_heads,
  *                layer's K and V pages; their scales in a call of their own, as rows of 4
  *                bytes); row r of page p and plane h (a KV head) of buffer k starts at
  *                kv_buffers[k] + p*page_stride + h*plane_stride + r*row_stride (bytes).
+ *                Buffers must not overlap one another.
  *   page_table   device int32 [B][max_pages]; num_pages, page_size as in sv_paged_cache.
  *   path, count, base, row_bytes, B, max_depth  as spec_kv_compact.  base is the cache row
  *                of tree node 0 (one behind the root's).

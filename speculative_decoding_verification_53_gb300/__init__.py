@@ -669,6 +669,8 @@ def spec_kv_compact_paged(kv_buffers, page_table, path, count, base=None, *, str
                                  "dtype and device")
         es = t0.element_size()
         ptrs = [t.data_ptr() for t in bufs]
+    if len(set(ptrs)) != n:
+        raise ValueError("kv_buffers names a buffer twice: its rows would move twice")
     at, handle, side = _one_device(t0, stream, kv_buffers=t0, page_table=page_table, path=path, count=count, base=base)
     P, H, ps, W = shape
     if strides[3] != 1 and W > 1:

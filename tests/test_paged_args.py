@@ -206,3 +206,13 @@ def test_attention_arguments(lib):
     size = lib.spec_paged_attention_workspace_size
     assert size(0, 1, 8, 8, 128, 0, 100) == 0 and size(1, 1, 8, 3, 128, 0, 100) == 0
     assert size(1, 1, 8, 8, 128, 5, 100) == 0 and size(1, 1, 8, 8, 128, 0, 0) == 0
+
+
+def test_compaction_refuses_a_buffer_named_twice():
+    import torch
+    import speculative_decoding_verification_53_gb300 as sv
+    t = torch.zeros(2, 1, 4, 8)
+    i = torch.zeros(1, 1, dtype=torch.int32)
+    for bufs in ([t, t], t[None].expand(2, 2, 1, 4, 8)):
+        with pytest.raises(ValueError, match="twice"):
+            sv.spec_kv_compact_paged(bufs, i, i, i[0])
