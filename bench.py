@@ -126,12 +126,18 @@ KERNEL_SOURCES = {"chain_spec_kernel": "sv_chain_spec.cu", "chain_staged_kernel"
 
 def kernel_source_hash(kernel: str = None) -> str:
     """sha256 prefix of the device sources a kernel is compiled from: its translation
-    unit and the package's internal headers (.cuh, .h).  With no kernel (or one not
-    listed), every source file of the package and of include/."""
+    unit and the package's internal headers (.cuh, .h) that the listed units include.
+    With no kernel (or one not listed), every source file of the package and of include/."""
     h = hashlib.sha256()
     pkg = os.path.join(ROOT, "speculative_decoding_verification_53_gb300", "csrc")
     if kernel in KERNEL_SOURCES:
-        files = [os.path.join(pkg, f) for f in sorted(os.listdir(pkg)) if f.endswith((".cuh", ".h"))]
+        headers, todo = set(), sorted(set(KERNEL_SOURCES.values()))
+        while todo:
+            with open(os.path.join(pkg, todo.pop())) as fh:
+                found = set(re.findall(r'#include "([^"]+)"', fh.read())) & set(os.listdir(pkg))
+            todo += found - headers
+            headers |= found
+        files = [os.path.join(pkg, f) for f in sorted(headers)]
         files.append(os.path.join(pkg, KERNEL_SOURCES[kernel]))
     else:
         files = [os.path.join(d, f) for d in (pkg, os.path.join(ROOT, "include")) for f in sorted(os.listdir(d))]

@@ -69,3 +69,21 @@ def test_large_batch_at_another_temperature_is_one_workload():
         traffic, path, kernel = bench.profile_traffic(f"large_batch_T{T:g}")
         assert path is not None and path.endswith(f"_large_batch_T{T:g}.md") and kernel == "chain_staged_kernel"
     assert bench.large_batch_at(base, 0.7) is base
+
+
+def test_a_kernels_hash_covers_its_own_headers_only(tmp_path, monkeypatch):
+    """A header that no profiled kernel's unit includes leaves the committed summaries valid;
+    one that it includes, through another, does not."""
+    import shutil
+    sys.path.insert(0, ROOT)
+    import bench
+    pkg = os.path.join("speculative_decoding_verification_53_gb300", "csrc")
+    shutil.copytree(os.path.join(ROOT, pkg), tmp_path / pkg)
+    want = {k: bench.kernel_source_hash(k) for k in bench.KERNEL_SOURCES}
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    assert {k: bench.kernel_source_hash(k) for k in bench.KERNEL_SOURCES} == want
+    (tmp_path / pkg / "sv_elsewhere.cuh").write_text("// nothing includes this\n")
+    assert {k: bench.kernel_source_hash(k) for k in bench.KERNEL_SOURCES} == want
+    with open(tmp_path / pkg / "sv_common.cuh", "a") as f:
+        f.write("// a change\n")
+    assert all(bench.kernel_source_hash(k) != want[k] for k in want)
