@@ -36,6 +36,16 @@
 // times larger, so that fp16's subnormal step is 2^-31 of the largest.  O is held in units of
 // the values' power of two and rescaled when it grows.
 //
+// A new token's scale more than 2^12 above those that every query sees would push the values of
+// queries that do not see it out of that range: its values are left out of the products and put
+// back at the end for the queries that see them, as values that are not finite are.  (A unit per row
+// in the softmax loop cost 172 -> 195 us of a tree batch in instruction-cache misses.)
+//
+// Measured on one GB300, 32 over 8 heads of 128: 2 x 2048 queries over 6001 positions, bf16, 341 us
+// (1380 TFLOP/s; the exponentials take as long as the products); 16 trees of 61 over 2048 to 8192,
+// e4m3, 147 us (560 TFLOP/s; a tile takes 5700 cycles, 2048 of them products, the rest widening and
+// softmax); 8 chains of 6 over 3277 to 32768, bf16, 135 us (5.0 TB/s).
+//
 // Every wait is bounded; a CTA whose wait runs out writes NaN for its rows, which a verify
 // reports as invalid data, and frees its TMEM.
 #include <cstdint>

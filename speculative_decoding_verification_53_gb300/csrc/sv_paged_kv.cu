@@ -10,6 +10,10 @@
 //   numbers needs no case of its own.  The product with 1/s instead of a division per
 //   element moves x/s by at most 2^-23 of itself, 2^-19 of an e4m3 step.
 //
+// One GB300: writing 16 x up to 2048 tokens of 8 heads x 128 as e4m3 takes 34 us (3.7 TB/s, issue
+// 77 %: the largest magnitude, compared as pairs of bf16 bits, and one rounding per pair), as bf16
+// 31 us (5.4 TB/s); reading 8 x up to 8192 positions back from e4m3 45 us (5.6 TB/s).
+//
 // The paged compaction is the kernel of sv_tree_kv.cu with one more indirection: a warp
 // turns the path into byte offsets through the table, then every thread moves its piece
 // of each row, loading up to eight sources before storing them.
@@ -178,7 +182,7 @@ __device__ __forceinline__ void store_cache_row(unsigned char* row, float* scale
 // their loads are in flight before the first is looked at, as they lie in memory (widened they
 // cost the registers of half the resident blocks).  Reading 8 x up to 8192 positions of 8 heads
 // x 128 e4m3 with 1, 2 and 4 rows: 57.6, 50.2, 46.5 us; writing 16 x up to 2048 tokens 40.8,
-// 37.1, 39.6 us.  A chain's 48 rows want one: 5.2 against 6.3 us.
+// 37.1, 39.6 us (magnitudes compared as fp32).  A chain's 48 rows want one: 5.2 against 6.3 us.
 template <bool READ, typename T, bool AL>
 constexpr int kRows = !AL ? 1 : READ && sizeof(T) == 2 ? 4 : 2;
 
