@@ -123,6 +123,8 @@ SV_API sv_status spec_kv_read(const sv_paged_cache *cache, const int32_t *base, 
  * query rows per cache head and head_dim <= 128 multiply as fp16 instead: a value's code
  * times its scale and a probability are rounded once each to 11 bits, and what a position
  * adds below 2^-31 of 448 times the largest value scale may be lost.
+ * Weights may stand at up to 2^8 times their value while they are summed: bf16 values beyond
+ * 2^110 may overflow to infinity.
  * out must not overlap q or the cache.  Every wait inside the kernels is bounded; where one
  * runs out, the rows concerned are written as NaN, which a verify reports as invalid data.
  *   workspace    device scratch of ws_bytes, 16-byte aligned (spec_paged_attention_workspace_size;

@@ -183,6 +183,61 @@ def test_e4m3_scales_of_very_different_sizes(sv, Q, ps):  # noqa: F811
     both(sv, c)
 
 
+@pytest.mark.parametrize("cache,D,width", [("e4m3", 72, 80), ("e4m3", 40, 48), ("e4m3", 128, 144), ("bf16", 72, 80), ("bf16", 128, 136),
+                                           ("e4m3", 200, 208)])
+@pytest.mark.parametrize("Q", [2, 9, 61])
+def test_rows_that_are_slices_of_wider_ones(sv, cache, D, width, Q):  # noqa: F811
+    """Cache rows of a fused tensor: what lies beside a row is never read as part of it."""
+    import torch
+    rng = np.random.default_rng([D, Q])
+    q, k, v, ks, vs, table, base, new_len, mask = case(rng, 2, Q, 8, 2, D, 16, 150, cache, False, False)
+    wide = []
+    for t in (k, v):
+        w = torch.full((*t.shape[:3], width), float("nan"), dtype=torch.bfloat16, device="cuda") if cache == "bf16" else \
+            torch.full((*t.shape[:3], width), 0x7f, dtype=torch.uint8, device="cuda").view(t.dtype)
+        bits = torch.int16 if cache == "bf16" else torch.uint8
+        w.view(bits)[..., :D].copy_(t.view(bits))
+        wide.append(w[..., :D])
+    both(sv, (q, *wide, ks, vs, table, base, new_len, mask))
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B,Q,ctx", [(2, 3, 2600), (5, 6, 1300), (32, 5, 700), (33, 5, 700), (7, 70, 1500)])
+def test_unequal_contexts_of_many_rows(sv, cache, B, Q, ctx):  # noqa: F811
+    """Split calls of one to 33 batch rows whose contexts differ, empty and invalid rows among them."""
+    rng = np.random.default_rng([B, Q, ctx])
+    c = list(case(rng, B, Q, 8, 2, 64, 16, ctx, cache, Q == 70, False))
+    c[6] = c[6].copy()
+    c[6][1], c[7][-1] = -5, 0                  # a row that is invalid, and one without tokens
+    both(sv, c)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Q", [3, 20, 80])
+def test_a_bad_query_harms_its_own_row_only(sv, cache, Q):  # noqa: F811
+    import torch
+    rng = np.random.default_rng(Q)
+    c = case(rng, 1, Q, 4, 1, 128, 16, 700, cache, False, False, ragged=False)
+    want, want_l = run(sv, c)
+    q = c[0].clone()
+    q[0, 1, 2, 5] = float("nan")
+    q[0, Q - 1, 0, 0] = float("inf")
+    o, l = run(sv, (q, *c[1:]))
+    bad = torch.zeros(o.shape[:3], dtype=torch.bool, device="cuda")
+    bad[0, 1, 2] = bad[0, Q - 1, 0] = True
+    assert torch.equal(o[~bad], want[~bad]) and torch.equal(l[~bad], want_l[~bad])
+    assert not o[bad].isfinite().any()
+
+
+@pytest.mark.parametrize("Q", [1, 8, 60])
+def test_rows_that_share_pages(sv, Q):  # noqa: F811
+    """A common prefix whose pages are in every row's table."""
+    rng = np.random.default_rng(Q + 5)
+    c = list(case(rng, 4, Q, 8, 2, 128, 16, 640, "bf16", False, False, ragged=False))
+    c[5][1:, :40] = c[5][0, :40]               # 640 positions, 40 pages
+    both(sv, c)
+
+
 def test_rows_that_see_nothing_holes_and_invalid_rows(sv):  # noqa: F811
     import torch
     rng = np.random.default_rng(11)
