@@ -584,7 +584,7 @@ Plan make_plan(int B, int Q, int Hq, int H, int D, bool e4m3, int max_len, int n
     Plan p{};
     if (max_len > sv::PAGED_MAX_POS) max_len = sv::PAGED_MAX_POS;
     const int64_t rows = (int64_t)Q * (Hq / H);
-    if (D > 128) p.tile_rows = rows <= 16 ? 16 : 32;
+    if (D > 128) p.tile_rows = rows <= 16 ? 16 : e4m3 ? 32 : 128;
     else if (rows > 128) p.tile_rows = 256;
     // Sixteen rows or fewer waste most of a 128-row product.  On one GB300, 32 over 8 heads of
     // 128, one query: 64 contexts of 4096 208 us (mma.sync) against 243 (tcgen05), e4m3 201
@@ -600,7 +600,7 @@ Plan make_plan(int B, int Q, int Hq, int H, int D, bool e4m3, int max_len, int n
     // Enough CTAs that rows of unequal length even out: four per SM.  Large tiles: three per
     // SM where there are fewer tiles than SMs; else whole waves of tiles, and what is left
     // over split so that it fills the last wave.
-    p.dual = p.tile_rows == 128 && max_len >= 512;
+    p.dual = p.tile_rows == 128 && D <= 128 && max_len >= 512;
     int64_t splits, least = 128;  // positions worth a split
     if (p.dual) {
         least = 256;

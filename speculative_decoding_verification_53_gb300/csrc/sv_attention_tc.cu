@@ -87,11 +87,12 @@ struct Tc {
     static constexpr int R_LOAD = MQ == 1 ? 136 : E4M3 ? 96 : 80, R_MMA = 64;
     static_assert(SOFTMAX * R_SOFTMAX + 128 * (R_LOAD + R_MMA) <= (MQ == 2 ? 65536 : 64512), "registers of the launch");
     static constexpr int MAT = (DP / 64) * BLK;   // a tile of keys, values or queries
-    static constexpr int NB = DP == 64 ? 6 : (E4M3 ? 3 : 4) + (DUAL ? 1 : 0);  // buffers of the ring
+    static constexpr int NB = DP == 64 ? 6 : DP == 256 ? 2 : (E4M3 ? 3 : 4) + (DUAL ? 1 : 0);  // buffers of the ring
     static constexpr int RAW = E4M3 ? 3 : 0;      // e4m3: items whose codes are in flight
     static constexpr int SMEM = (QM + NB) * MAT + RAW * MAT / 2 + 1024;  // and room to align
     static constexpr int S_COL = 0, O_COL = 128 * MQ;    // TMEM columns
-    static constexpr int COLS = MQ == 2 ? 512 : 256;
+    static constexpr int COLS = MQ == 2 || DP == 256 ? 512 : 256;
+    static_assert(O_COL + DP * MQ <= COLS, "tensor memory");
 };
 
 // ------------------------------------------------------------ tcgen05 wrappers
@@ -509,12 +510,12 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         const bool patch = ok && sh.bad != 0;
         // Rows leave through shared memory (where this row tile's queries were), so that a store
         // covers whole rows: a lane writing its own row touched 32 lines per store and cost
-        // 15000 cycles a CTA.  Half a row at a time, 16-byte pieces swizzled by the row.
-        constexpr int CW = DP / 2, PC = CW / 4;
+        // 15000 cycles a CTA.  Part of a row at a time, 16-byte pieces swizzled by the row.
+        constexpr int PASSES = DP == 256 ? 4 : 2, CW = DP / PASSES, PC = CW / 4;
         if (!idle && mine) {
             const uint32_t stage = smem0 + q * S::MAT + (warp & 3) * (S::MAT / 4);
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < PASSES; ++c) {
                 uint32_t v[CW];
                 __syncwarp();
 #pragma unroll
@@ -1071,6 +1072,7 @@ namespace sv {
 
 cudaError_t launch_attn_tc(const AttnArgs& a, int pairs, bool e4m3, int tile_rows, bool dual, unsigned ctas,
                            cudaStream_t stream) {
+    if (a.c.dim > 128) return launch_one<256, 1, false, false>(a, pairs, ctas, stream);
     if (a.c.dim <= 64) return e4m3 ? launch_dim<64, true>(a, pairs, tile_rows, dual, ctas, stream) : launch_dim<64, false>(a, pairs, tile_rows, dual, ctas, stream);
     return e4m3 ? launch_dim<128, true>(a, pairs, tile_rows, dual, ctas, stream) : launch_dim<128, false>(a, pairs, tile_rows, dual, ctas, stream);
 }

@@ -213,6 +213,16 @@ def test_unequal_contexts_of_many_rows(sv, cache, B, Q, ctx):  # noqa: F811
 
 
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("shape", [(2, 9, 8, 2, 256, 16, 300), (1, 61, 4, 1, 256, 64, 2500), (2, 20, 2, 1, 136, 24, 100),
+                                   (1, 150, 2, 1, 192, 16, 40), (3, 40, 3, 3, 256, 1, 140), (1, 17, 1, 1, 248, 128, 0)])
+def test_wide_heads(sv, shape, cache, tree):  # noqa: F811
+    if cache == "e4m3" and shape[4] % 16:
+        pytest.skip("rows of codes would not be 16-byte aligned")
+    both(sv, case(np.random.default_rng([*shape, tree]), *shape, cache, tree, nhd=sum(shape) % 2 == 1))
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
 @pytest.mark.parametrize("Q", [3, 20, 80])
 def test_a_bad_query_harms_its_own_row_only(sv, cache, Q):  # noqa: F811
     import torch
