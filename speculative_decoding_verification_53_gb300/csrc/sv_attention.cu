@@ -4,8 +4,7 @@
 //
 // out = softmax(scale q k^T) v in one pass over the cache: each warp keeps the running
 // maximum m and sum l of its rows and rescales its fp32 accumulator when m grows.  Few
-// rows (one token times the heads that share a cache head, and heads wider than 128) are
-// bound by the cache's bytes: the kernel's work is to keep loads in flight.  So a CTA
+// rows (one token times the heads that share a cache head) are bound by the cache's bytes: the kernel's work is to keep loads in flight.  So a CTA
 // streams tiles of 64 positions through a ring of shared-memory stages filled by cp.async
 // (16 bytes per thread, any page size, holes and rows behind the end filled with zeros),
 // its warps take 16 positions each of every tile, and their partial results meet once at
@@ -72,10 +71,10 @@ __device__ __forceinline__ uint32_t widen(uint32_t w) {
     return sv::bf16x2(f.x, f.y);
 }
 
-template <int DP, int MW, bool E4M3>
+template <int DP, bool E4M3>
 struct Shape {
-    static constexpr int ROWS = MW * 16;
-    static constexpr int THREADS = MW * KW * 32;
+    static constexpr int ROWS = 16;
+    static constexpr int THREADS = KW * 32;
     static constexpr int ES = E4M3 ? 1 : 2;
     static constexpr int PITCH = DP * ES;          // bytes of a staged row
     static constexpr int CH = PITCH / 16;          // 16-byte pieces of a staged row
@@ -102,10 +101,10 @@ __device__ __forceinline__ int v_piece(int r, int c) {  // eight rows are read t
     return r * PITCH + ((PITCH >= 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
 }
 
-template <int DP, int MW, bool E4M3>
-__global__ void __launch_bounds__(MW* KW * 32, DP == 256 ? 1 : 2)
+template <int DP, bool E4M3>
+__global__ void __launch_bounds__(KW * 32, DP == 256 ? 1 : 2)
     paged_attention_kernel(const __grid_constant__ AttnArgs a, const int pairs) {
-    using S = Shape<DP, MW, E4M3>;
+    using S = Shape<DP, E4M3>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t s_off[RING][TN];  // byte offset of each position's row, -1: nothing there
     __shared__ int64_t s_sc[E4M3 ? RING : 1][E4M3 ? TN : 1];  // index of its scales
@@ -117,7 +116,7 @@ __global__ void __launch_bounds__(MW* KW * 32, DP == 256 ? 1 : 2)
     pdl_wait();
     AttnTile t;
     if (!sv::attn_tile(a, pairs, blockIdx.x, S::ROWS, 1, t)) return;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wk = warp % KW, wm = warp / KW;
+    const int tid = threadIdx.x, lane = tid & 31, wk = tid >> 5;
     const int D = a.c.dim, row_bytes = D * S::ES;
     const int tiles = (t.end - t.begin + TN - 1) / TN;
     const unsigned char* kbase = a.c.k + t.h * a.c.head_stride;
@@ -201,7 +200,7 @@ __global__ void __launch_bounds__(MW* KW * 32, DP == 256 ? 1 : 2)
     constexpr bool QREG = DP <= 128;
     constexpr int KS = DP / 16;
     uint32_t qf[QREG ? KS : 1][4];
-    const int q_r = wm * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), q_c = lane >> 4;
+    const int q_r = ((lane >> 3) & 1) * 8 + (lane & 7), q_c = lane >> 4;
     if (QREG) {
 #pragma unroll
         for (int k = 0; k < KS; ++k) ldsm4(q0 + v_piece<2 * DP>(q_r, 2 * k + q_c), qf[k]);
@@ -318,7 +317,7 @@ __global__ void __launch_bounds__(MW* KW * 32, DP == 256 ? 1 : 2)
         if (tail) {
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                const int R = t.mt * S::ROWS + wm * 16 + g + 8 * y;
+                const int R = t.mt * S::ROWS + g + 8 * y;
                 see[y] &= R < t.n * a.group ? sv::attn_visible(a, t, R / a.group, tile0 + wk * 16) : 0u;
             }
         }
@@ -398,7 +397,7 @@ __global__ void __launch_bounds__(MW* KW * 32, DP == 256 ? 1 : 2)
     for (int y = 0; y < 2; ++y) {
         l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
         l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
-        const int r = wm * 16 + g + 8 * y;
+        const int r = g + 8 * y;
         if (t4 == 0) {
             s_m[wk][r] = mx[y];
             s_l[wk][r] = l[y];
@@ -408,7 +407,7 @@ __global__ void __launch_bounds__(MW* KW * 32, DP == 256 ? 1 : 2)
     float inv[2], lse2[2];
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-        const int r = wm * 16 + g + 8 * y;
+        const int r = g + 8 * y;
         float top = s_m[0][r];
 #pragma unroll
         for (int w = 1; w < KW; ++w) top = fmaxf(top, s_m[w][r]);
@@ -425,7 +424,7 @@ __global__ void __launch_bounds__(MW* KW * 32, DP == 256 ? 1 : 2)
             o[n][2 * y + 1] *= fac;
         }
     }
-    float4* join = reinterpret_cast<float4*>(smem) + (size_t)wm * 2 * (DP / 8) * 32 + lane;
+    float4* join = reinterpret_cast<float4*>(smem) + lane;
 #pragma unroll
     for (int half = 2; half >= 1; half >>= 1) {
         if (wk >= half && wk < 2 * half) {
@@ -452,7 +451,7 @@ __global__ void __launch_bounds__(MW* KW * 32, DP == 256 ? 1 : 2)
 
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-        const int R = t.mt * S::ROWS + wm * 16 + g + 8 * y;
+        const int R = t.mt * S::ROWS + g + 8 * y;
         if (R >= t.n * a.group) continue;
         const int64_t row = sv::attn_row(a, t, R);
         const int64_t part = t.part + R - t.mt * S::ROWS;
@@ -549,23 +548,16 @@ __global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_
     if (a.lse && lane == 0) a.lse[row] = sum == 0.0f ? neg_inf() : (shift + log2f(sum)) * 0.69314718055994531f;
 }
 
-template <int DP, int MW, bool E4M3>
-cudaError_t launch_shape(const AttnArgs& a, int pairs, unsigned ctas, cudaStream_t stream) {
-    using S = Shape<DP, MW, E4M3>;
+template <int DP, bool E4M3>
+cudaError_t launch_few(const AttnArgs& a, int pairs, unsigned ctas, cudaStream_t stream) {
+    using S = Shape<DP, E4M3>;
     static sv::KernelLaunchCache cache;
-    auto kern = paged_attention_kernel<DP, MW, E4M3>;
+    auto kern = paged_attention_kernel<DP, E4M3>;
     int max_dyn = 0;
     const cudaError_t e = cache.setup((const void*)kern, &max_dyn);
     if (e != cudaSuccess) return e;
     if (S::SMEM > max_dyn) return cudaErrorInvalidValue;
     return sv::launch_serial(kern, dim3(ctas), dim3(S::THREADS), S::SMEM, stream, a, pairs);
-}
-
-template <int DP, bool E4M3>
-cudaError_t launch_rows(const AttnArgs& a, int pairs, int tile_rows, unsigned ctas, cudaStream_t stream) {
-    if constexpr (DP == 256)
-        if (tile_rows == 32) return launch_shape<DP, 2, E4M3>(a, pairs, ctas, stream);
-    return launch_shape<DP, 1, E4M3>(a, pairs, ctas, stream);
 }
 
 constexpr int kMaxB = 65535;
@@ -584,7 +576,10 @@ Plan make_plan(int B, int Q, int Hq, int H, int D, bool e4m3, int max_len, int n
     Plan p{};
     if (max_len > sv::PAGED_MAX_POS) max_len = sv::PAGED_MAX_POS;
     const int64_t rows = (int64_t)Q * (Hq / H);
-    if (D > 128) p.tile_rows = rows <= 16 ? 16 : e4m3 ? 32 : 128;
+    // Wide heads, 256 on one GB300, 32 over 8 heads, mma.sync against tcgen05: bf16, 16 contexts of
+    // 4096 with 1, 5 and 61 queries 178 and 166, 309 and 170, 1061 and 274 us, one of 8000 77 and 39,
+    // of 700 21 and 27; e4m3 174 and 252, 286 and 255, 1262 and 460, 77 and 48, 21 and 35.
+    if (D > 128) p.tile_rows = e4m3 && rows <= 16 ? 16 : 128;
     else if (rows > 128) p.tile_rows = 256;
     // Sixteen rows or fewer waste most of a 128-row product.  On one GB300, 32 over 8 heads of
     // 128, one query: 64 contexts of 4096 208 us (mma.sync) against 243 (tcgen05), e4m3 201
@@ -609,10 +604,10 @@ Plan make_plan(int B, int Q, int Hq, int H, int D, bool e4m3, int max_len, int n
     } else if (!large) {
         splits = (4LL * num_sms + p.tiles - 1) / p.tiles;
     } else if (p.tiles < num_sms) {
-        least = 1024;
+        least = D > 128 ? 512 : 1024;
         splits = 3LL * num_sms / p.tiles;
     } else {
-        least = 1024;
+        least = D > 128 ? 512 : 1024;
         p.whole = p.tiles / num_sms * num_sms;
         splits = p.tiles > p.whole ? num_sms / (p.tiles - p.whole) : 1;
     }
@@ -712,9 +707,9 @@ sv_status spec_paged_attention(const void* q, const int64_t* q_stride, int num_q
     const unsigned ctas = (unsigned)p.ctas;
     cudaError_t e;
     if (p.tile_rows >= 128) e = sv::launch_attn_tc(a, pairs, e4m3, p.tile_rows, p.dual, ctas, s);
-    else if (D <= 64) e = e4m3 ? launch_rows<64, true>(a, pairs, p.tile_rows, ctas, s) : launch_rows<64, false>(a, pairs, p.tile_rows, ctas, s);
-    else if (D <= 128) e = e4m3 ? launch_rows<128, true>(a, pairs, p.tile_rows, ctas, s) : launch_rows<128, false>(a, pairs, p.tile_rows, ctas, s);
-    else e = e4m3 ? launch_rows<256, true>(a, pairs, p.tile_rows, ctas, s) : launch_rows<256, false>(a, pairs, p.tile_rows, ctas, s);
+    else if (D <= 64) e = e4m3 ? launch_few<64, true>(a, pairs, ctas, s) : launch_few<64, false>(a, pairs, ctas, s);
+    else if (D <= 128) e = e4m3 ? launch_few<128, true>(a, pairs, ctas, s) : launch_few<128, false>(a, pairs, ctas, s);
+    else e = launch_few<256, true>(a, pairs, ctas, s);
     if (e == cudaSuccess && rows)
         e = sv::launch_serial(paged_attention_join_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a, pairs,
                               p.tile_rows, rows);

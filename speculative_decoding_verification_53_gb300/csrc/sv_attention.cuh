@@ -78,7 +78,7 @@ __device__ __forceinline__ int attn_active(const AttnArgs& a, int end) {
 // the sort and up to 4 % to the rounding.  One CTA per SM with an even share of all positions, cut
 // where it ends, took 175: a piece costs 10 us of its own, not kept.
 __device__ __forceinline__ int attn_split_begin(int end, int s, int n) {
-    return (int)((int64_t)((end + 127) / 128) * s / n) * 128;
+    return (int)((unsigned)((end + 127) / 128) * (unsigned)s / (unsigned)n) * 128;  // 2^23 units, 256 splits
 }
 
 // The batch row whose splits are the r-th longest, of at most 32 rows (more even out by

@@ -41,6 +41,10 @@
 // back at the end for the queries that see them, as values that are not finite are.  (A unit per row
 // in the softmax loop cost 172 -> 195 us of a tree batch in instruction-cache misses.)
 //
+// Heads wider than 128 take one row tile, 384 columns of TMEM and a ring of two 64 KB buffers; e4m3
+// codes then go from the cache through registers.  16 trees of 61 over 4096, 32 over 8 heads of 256,
+// bf16: 274 us (480 TFLOP/s), e4m3 460 us.
+//
 // Measured on one GB300, 32 over 8 heads of 128: 2 x 2048 queries over 6001 positions, bf16, 341 us
 // (1380 TFLOP/s; the exponentials take as long as the products); 16 trees of 61 over 2048 to 8192,
 // e4m3, 147 us (560 TFLOP/s; a tile takes 5700 cycles, 2048 of them products, the rest widening and
@@ -88,7 +92,7 @@ struct Tc {
     static_assert(SOFTMAX * R_SOFTMAX + 128 * (R_LOAD + R_MMA) <= (MQ == 2 ? 65536 : 64512), "registers of the launch");
     static constexpr int MAT = (DP / 64) * BLK;   // a tile of keys, values or queries
     static constexpr int NB = DP == 64 ? 6 : DP == 256 ? 2 : (E4M3 ? 3 : 4) + (DUAL ? 1 : 0);  // buffers of the ring
-    static constexpr int RAW = E4M3 ? 3 : 0;      // e4m3: items whose codes are in flight
+    static constexpr int RAW = E4M3 && DP != 256 ? 3 : 0;  // e4m3: items whose codes are in flight
     static constexpr int SMEM = (QM + NB) * MAT + RAW * MAT / 2 + 1024;  // and room to align
     static constexpr int S_COL = 0, O_COL = 128 * MQ;    // TMEM columns
     static constexpr int COLS = MQ == 2 || DP == 256 ? 512 : 256;
@@ -676,6 +680,11 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             }
         } else {
             constexpr int CH = DP / 16, RPI = 32 / CH, X = 32 / RPI;  // 16 codes a piece
+            constexpr int RAW = S::RAW ? S::RAW : 1;
+            // Wide heads leave no room for codes beside the ring: they come straight to registers,
+            // PER pieces a lane, asked for while the PER before them are widened.
+            constexpr bool DIRECT = S::RAW == 0;
+            constexpr int PER = DIRECT ? 8 : 4;
             const int c = lane % CH, r0 = lane / CH;
             const int most = D - 16 * c < 0 ? 0 : D - 16 * c > 16 ? 16 : D - 16 * c;
             // Codes arrive in one of RAW places: by the copy engine as rows of DP codes, else a
@@ -685,12 +694,12 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             const uint32_t mine = raw0 + (box_rows ? (32 * w + r0) * DP + 16 * c : own);
             const int step = box_rows ? RPI * DP : 2048;
             const uint32_t place0 = piece(32 * w + r0, 2 * c);
-            // row r0 + RPI x, element 16 c + 8 y; RPI is 4 or 8 rows
+            // row r0 + RPI x, element 16 c + 8 y; RPI is 2, 4 or 8 rows
             auto place = [&](int x, int y) { return (place0 ^ (uint32_t)(((((RPI * x) & 7) ^ y)) << 4)) + x * RPI * 128; };
             auto copy = [&](int n) {
                 if (n < 2 * tiles) {
                     const unsigned char* src = mat[n & 1] + (most ? 16 * c : 0);
-                    const uint32_t dst = raw0 + own + (n % S::RAW) * (S::MAT / 2);
+                    const uint32_t dst = raw0 + own + (n % RAW) * (S::MAT / 2);
 #pragma unroll
                     for (int x = 0; x < X; ++x) {
                         const int64_t o = __shfl_sync(0xffffffffu, off, x * RPI + r0);
@@ -703,21 +712,40 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
             };
-            if (!box_rows) {
+            uint4 now[DIRECT ? PER : 1], next[DIRECT ? PER : 1];
+            auto ask = [&](int n, int x0) {  // rows x0 .. x0 + PER - 1 of item n, items in turn
+                const unsigned char* src = mat[n & 1] + 16 * c;
+#pragma unroll
+                for (int x = 0; x < (DIRECT ? PER : 0); ++x) {
+                    const int64_t o = __shfl_sync(0xffffffffu, off, (x0 + x) * RPI + r0);
+                    next[x] = make_uint4(0u, 0u, 0u, 0u);
+                    if (n < 2 * tiles && o >= 0) {
+                        if (most == 16) next[x] = sv::ld_nc_v4(src + o);
+                        else if (most == 8) *reinterpret_cast<uint2*>(&next[x]) = __ldg(reinterpret_cast<const uint2*>(src + o));
+                    }
+                }
+                if ((n & 1) && x0 + PER == X) {
+                    off = off1;
+                    off1 = look_up((n >> 1) + 2);
+                }
+            };
+            if (DIRECT) {
+                ask(0, 0);
+            } else if (!box_rows) {
                 copy(0);
                 copy(1);
             }
             for (int n = 0; n < 2 * tiles; ++n) {
                 const int j = n >> 1, buf = n % S::NB;
-                if (!box_rows) copy(n + 2);
+                if (!DIRECT && !box_rows) copy(n + 2);
                 if (n >= S::NB) {
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[buf], (n / S::NB - 1) & 1));
                     if (!ok) break;
                 }
-                if (box_rows) {
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.raw_full[n % S::RAW], (n / S::RAW) & 1));
+                if (!DIRECT && box_rows) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.raw_full[n % RAW], (n / RAW) & 1));
                     if (!ok) break;
-                } else {
+                } else if (!DIRECT) {
                     asm volatile("cp.async.wait_group 2;" ::: "memory");
                 }
                 if (!(n & 1)) {
@@ -726,20 +754,32 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 }
                 const uint2* scale = sh.vsc[j % META] + 32 * w + r0;
                 const bool clean = (n & 1) && start(j) + TN > open;
-                const uint32_t dst = ring + buf * S::MAT, from = mine + (n % S::RAW) * (S::MAT / 2);
+                const uint32_t dst = ring + buf * S::MAT, from = mine + (n % RAW) * (S::MAT / 2);
                 // Lanes of a row's second 64 elements, whose banks are the first's, take their two
                 // halves in the other order.
                 const int y = (c >> 2) & 1;
                 // A short loop: unrolled in full, this and the softmax ran out of the instruction
                 // caches (3000 cycles an item instead of 600).
 #pragma unroll 1
-                for (int x = 0; x < X; x += 4) {
-                    uint2 g[8];
+                for (int x = 0; x < X; x += PER) {
+                    uint2 g[2 * PER];
+                    if (DIRECT) {
 #pragma unroll
-                    for (int z = 0; z < 8; ++z) g[z] = lds8(from + (x + (z >> 1)) * step + 8 * ((z & 1) ^ y));
+                        for (int z = 0; z < (DIRECT ? PER : 0); ++z) now[z] = next[z];
+                        ask(x + PER < X ? n : n + 1, x + PER < X ? x + PER : 0);
+                    }
+#pragma unroll
+                    for (int z = 0; z < 2 * PER; ++z) {
+                        if (DIRECT) {
+                            const uint4 v = now[DIRECT ? z >> 1 : 0];
+                            g[z] = (z & 1) ^ y ? make_uint2(v.z, v.w) : make_uint2(v.x, v.y);
+                        } else {
+                            g[z] = lds8(from + (x + (z >> 1)) * step + 8 * ((z & 1) ^ y));
+                        }
+                    }
                     if (clean) {
 #pragma unroll
-                        for (int z = 0; z < 8; ++z) {
+                        for (int z = 0; z < 2 * PER; ++z) {
                             uint4 h = make_uint4(g[z].x, g[z].y, 0u, 0u);
                             if (start(j) + 32 * w + (x + (z >> 1)) * RPI + r0 >= stop(j)) h = make_uint4(0u, 0u, 0u, 0u);
                             bad |= sv::sanitise<true>(h);
@@ -748,17 +788,17 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     }
                     if (n & 1) {
 #pragma unroll
-                        for (int z = 0; z < 8; ++z)
+                        for (int z = 0; z < 2 * PER; ++z)
                             sts16(dst + place(x + (z >> 1), (z & 1) ^ y), widen8<true>(g[z], scale[(x + (z >> 1)) * RPI]));
                     } else {
 #pragma unroll
-                        for (int z = 0; z < 8; ++z)
+                        for (int z = 0; z < 2 * PER; ++z)
                             sts16(dst + place(x + (z >> 1), (z & 1) ^ y), widen8<false>(g[z], make_uint2(0u, 0u)));
                     }
                 }
-                if (box_rows) {
+                if (!DIRECT && box_rows) {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.raw_empty[n % S::RAW]);
+                    if (lane == 0) mbar_arrive(&sh.raw_empty[n % RAW]);
                 }
                 if (clean && bad) sh.bad = 1;
                 fence_proxy_async();
@@ -891,7 +931,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             box_page(0, page, row);
             box_page(1, page1, row1);
             for (; n < 2 * tiles; ++n) {
-                constexpr int PLACES = E4M3 ? S::RAW : S::NB;
+                constexpr int PLACES = S::RAW ? S::RAW : S::NB;
                 const int slot = n % PLACES;
                 if (n >= PLACES) {
                     ok = __all_sync(0xffffffffu,
@@ -923,7 +963,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 }
             }
             if (!ok) {  // copies in flight land before the CTA leaves
-                constexpr int PLACES = E4M3 ? S::RAW : S::NB;
+                constexpr int PLACES = S::RAW ? S::RAW : S::NB;
                 for (int z = n > PLACES ? n - PLACES : 0; z < n; ++z)
                     if (E4M3 || !(z & 1) || start(z >> 1) + TN <= open)
                         (void)mbar_wait_bounded(E4M3 ? &sh.raw_full[z % PLACES & 3] : &sh.full[z % PLACES], (z / PLACES) & 1);
@@ -1050,7 +1090,7 @@ cudaError_t launch_one(const AttnArgs& a, int pairs, unsigned ctas, cudaStream_t
     const cudaError_t e = cache.setup((const void*)kern, &max_dyn);
     if (e != cudaSuccess) return e;
     if (S::SMEM > max_dyn) return cudaErrorInvalidValue;
-    int rows = sv::page_box_rows(a.c, TN);
+    int rows = E4M3 && !S::RAW ? 0 : sv::page_box_rows(a.c, TN);
     CUtensorMap k{}, v{};
     const CUtensorMapSwizzle swizzle = E4M3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
     if (rows && !(sv::page_map(&k, a.c.k, a.c, E4M3, E4M3 ? DP : 64, rows, swizzle) &&
@@ -1072,7 +1112,7 @@ namespace sv {
 
 cudaError_t launch_attn_tc(const AttnArgs& a, int pairs, bool e4m3, int tile_rows, bool dual, unsigned ctas,
                            cudaStream_t stream) {
-    if (a.c.dim > 128) return launch_one<256, 1, false, false>(a, pairs, ctas, stream);
+    if (a.c.dim > 128) return e4m3 ? launch_one<256, 1, true, false>(a, pairs, ctas, stream) : launch_one<256, 1, false, false>(a, pairs, ctas, stream);
     if (a.c.dim <= 64) return e4m3 ? launch_dim<64, true>(a, pairs, tile_rows, dual, ctas, stream) : launch_dim<64, false>(a, pairs, tile_rows, dual, ctas, stream);
     return e4m3 ? launch_dim<128, true>(a, pairs, tile_rows, dual, ctas, stream) : launch_dim<128, false>(a, pairs, tile_rows, dual, ctas, stream);
 }

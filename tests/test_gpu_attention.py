@@ -42,7 +42,7 @@ def check(got, lse, q, k, v, ks, vs, table, base, new_len, mask, scale, keep_out
     ka = np.where(np.isfinite(kv), np.abs(kv), 0).transpose(1, 0, 2, 3).reshape(H, -1, D)
     qa = np.abs(qh).reshape(B * Q, H, Hq // H, D).transpose(1, 0, 2, 3).reshape(H, -1, D)
     reach = abs(scale) * max((qa[h] @ ka[h].T).max() for h in range(H))  # largest sum |q k|
-    half = vs is not None and Q * Hq // H > 16 and D <= 128  # multiplied as fp16
+    half = vs is not None and Q * Hq // H > 16  # multiplied as fp16
     e = (D + 16) * 2.0 ** -22 * reach
     g, gl = host(got), host(lse)
     tol = (2.0 ** -8 + 4 * e) * np.abs(size) + 2.0 ** -8 * np.abs(want) + 1e-30
