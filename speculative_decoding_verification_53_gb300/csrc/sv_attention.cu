@@ -694,7 +694,8 @@ sv_status spec_paged_attention(const void* q, const int64_t* q_stride, int num_q
     a.whole = (int)p.whole;
     a.splits = p.splits;
     a.per = p.dual ? 2 : 1;
-    a.sort = B > 1 && B <= 32 && p.whole == 0 && p.ctas > sms ? B : 0;
+    a.equal = p.tile_rows >= 128;
+    a.sort = a.equal && B > 1 && B <= 32 && p.whole == 0 && p.ctas > sms ? B : 0;
     a.chunk = p.chunk;
     a.out = static_cast<uint16_t*>(out);
     a.lse = out_lse;

@@ -26,6 +26,7 @@ struct AttnArgs {
     int whole;                 // tiles [0, whole) are not split, the others `splits` ways
     int splits, chunk;         // a row tile has a split per `chunk` positions, `splits` at most
     int per;                   // splits that a CTA takes: 1 or 2
+    int equal;                 // splits are of one length
     int sort;                  // > 0: this many batch rows, taken longest splits first
     uint16_t* out;             // [B][Q][Hq][D] bf16
     float* lse;                // [B][Q][Hq] or nullptr
@@ -71,13 +72,15 @@ __device__ __forceinline__ int attn_active(const AttnArgs& a, int end) {
     return (n & (a.per - 1)) && end > 128 * n ? n + 1 : n;  // splits is a multiple of per
 }
 
-// First position of split s of n over `end` positions: splits of a row tile are of one length, in
-// units of 128, and with the longest first (below) a batch of unequal contexts ends together: 16
-// trees of 61 rows x 4 heads over 2048 to 8192 positions of 8 heads, e4m3, 172 us with splits of
+// First position of split s of n over `end` positions.  Splits of a row tile are of one length,
+// in units of 128, and with the longest first (below) a batch of unequal contexts ends together:
+// 16 trees of 61 rows x 4 heads over 2048 to 8192 positions of 8 heads, e4m3, 172 us with splits of
 // `chunk` positions and a rest, 158 of one length, 151 sorted as well; equal contexts lose 1 us to
-// the sort and up to 4 % to the rounding.  One CTA per SM with an even share of all positions, cut
-// where it ends, took 175: a piece costs 10 us of its own, not kept.
-__device__ __forceinline__ int attn_split_begin(int end, int s, int n) {
+// the sort and up to 4 % to the rounding.  16-row tiles keep `chunk`: equal contexts took 139 us
+// with it against 148 (16 x 8192, e4m3), unequal ones gained 2 %.  One CTA per SM with an even
+// share of all positions, cut where it ends, took 175: a piece costs 10 us of its own, not kept.
+__device__ __forceinline__ int attn_split_begin(const AttnArgs& a, int end, int s, int n) {
+    if (!a.equal) return s * a.chunk;
     return (int)((unsigned)((end + 127) / 128) * (unsigned)s / (unsigned)n) * 128;  // 2^23 units, 256 splits
 }
 
@@ -88,7 +91,7 @@ __device__ __forceinline__ int attn_sorted(const AttnArgs& a, int r) {
     int base, n, size = -1;
     if (lane < a.sort) {
         size = 0;
-        if (paged_row(a.c, a.base, a.new_len, lane, a.Q, base, n) && n > 0) size = attn_split_begin(base + n, 1, attn_active(a, base + n));
+        if (paged_row(a.c, a.base, a.new_len, lane, a.Q, base, n) && n > 0) size = attn_split_begin(a, base + n, 1, attn_active(a, base + n));
     }
     int before = 0;
     for (int j = 0; j < a.sort; ++j) {
@@ -120,9 +123,9 @@ __device__ __forceinline__ bool attn_tile(const AttnArgs& a, int pairs, unsigned
     const int end = attn_tile_end(t.base, t.n, a.group, t.mt, tile_rows, a.tree_mask != nullptr);
     t.active = whole ? 1 : attn_active(a, end);
     if (t.split >= t.active) return false;
-    t.begin = attn_split_begin(end, t.split, t.active);
-    t.end = t.split == t.active - 1 ? end : attn_split_begin(end, t.split + 1, t.active);
-    t.end2 = t.split + 1 >= t.active ? t.end : t.split + 2 == t.active ? end : attn_split_begin(end, t.split + 2, t.active);
+    t.begin = attn_split_begin(a, end, t.split, t.active);
+    t.end = t.split == t.active - 1 ? end : attn_split_begin(a, end, t.split + 1, t.active);
+    t.end2 = t.split + 1 >= t.active ? t.end : t.split + 2 == t.active ? end : attn_split_begin(a, end, t.split + 2, t.active);
     return true;
 }
 
