@@ -662,9 +662,11 @@ def spec_kv_compact_paged(kv_buffers, page_table, path, count, base=None, *, str
         if not bufs:
             raise ValueError("kv_buffers is empty")
         t0 = bufs[0]
-        n, shape, strides, dtype, where = len(bufs), t0.shape, t0.stride(), t0.dtype, t0.device
+        n, shape, strides, dtype, where = len(bufs), t0.shape, t0.stride(), t0.dtype, t0.get_device()
+        if len(shape) != 4:
+            raise ValueError("kv_buffers must be tensors [pages][planes][page_size][width]")
         for t in bufs:
-            if t.dim() != 4 or t.shape != shape or t.stride() != strides or t.dtype != dtype or t.device != where:
+            if t.shape != shape or t.stride() != strides or t.dtype != dtype or t.get_device() != where:
                 raise ValueError("kv_buffers must be tensors [pages][planes][page_size][width] of one shape, stride, "
                                  "dtype and device")
         es = t0.element_size()
