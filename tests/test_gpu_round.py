@@ -222,3 +222,44 @@ def test_side_stream_calls(sv):  # noqa: F811
         s.synchronize()
         assert torch.equal(out, want) and torch.equal(got_l, want_l)
         assert torch.equal(back[0], x) and torch.equal(back[1], y)
+
+
+FIRST = """
+import torch
+import speculative_decoding_verification_53_gb300 as sv
+B, Q, H, D, P, ps, V = 2, 9, 2, 64, 40, 16, 300
+torch.manual_seed(1)
+f = lambda *s: torch.randn(*s, device="cuda").to(torch.bfloat16)
+i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+k, v, x, y, q, lg = f(P, H, ps, D), f(P, H, ps, D), f(B, Q, H, D), f(B, Q, H, D), f(B, Q, 8, D), f(B, Q, V)
+table, base = torch.randperm(P, device="cuda").int().view(B, 20), i([200, 37])
+toks, path, count, rep = i([list(range(8))] * B), i([[1, 4]] * B), i([3, 1]), torch.full((B,), 1.2, device="cuda")
+k0, v0 = k.clone(), v.clone()
+def go():
+    sv.spec_kv_append(x, y, k, v, table, base)
+    o, l = sv.spec_paged_attention(q, k, v, table, base, want_lse=True)
+    a = sv.spec_adjust_logits(lg, draft_tokens=toks, repetition=rep)
+    sv.spec_kv_compact_paged([k, v], table, path, count, base)
+    return [o, l, a, *sv.spec_kv_read(k, v, table, base, Q)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = go()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got] + [k.clone(), v.clone()]
+k.copy_(k0); v.copy_(v0)
+want = go() + [k, v]
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+print("same")
+"""
+
+
+def test_the_first_calls_of_a_process_can_be_captured(sv):  # noqa: F811
+    """Nothing that a first call sets up is refused while a stream is captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
