@@ -75,8 +75,8 @@ typedef struct {
  * SV_CACHE_BF16: elements are rounded to nearest even.  SV_CACHE_E4M3: with a the largest
  * finite |x| of the row of one token and head, scale = max(a / 448, 2^-126) and each
  * element becomes the e4m3 value nearest to x / scale (even on ties), at most 448 in
- * magnitude; infinities become +-448 * scale, NaN stays NaN.  x / scale is taken as
- * x * (1 / scale) in fp32, so an element within 2^-23 of a midpoint may round either way.
+ * magnitude; infinities become +-448 * scale, NaN stays NaN.  scale and x / scale are fp32
+ * quotients, rounded to nearest even (x / scale from within 2^-46 of itself).
  * Tokens whose table entry is a hole are not written.  Two tokens must not share a cache
  * row (rows may share pages that they only read).
  * Errors: SV_ERR_INVALID_ARG for a bad size, dtype, pointer or stride (B = 0 or N = 0

@@ -168,8 +168,6 @@ __device__ __forceinline__ int64_t attn_row(const AttnArgs& a, const AttnTile& t
     return ((int64_t)t.b * a.Q + r / a.group) * a.Hq + t.h * a.group + r % a.group;
 }
 
-__device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) < pos_inf()); }
-
 // One box of a page (some elements x rows of one head) by the copy engine; a page
 // outside the cache reads as zeros.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int row, int head, int page, uint64_t* bar) {

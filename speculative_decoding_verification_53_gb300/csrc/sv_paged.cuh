@@ -42,6 +42,8 @@ __device__ __forceinline__ int paged_place(const PagedCache& c, int b, int pos, 
     return (unsigned)p < (unsigned)c.num_pages ? p : -1;
 }
 
+__device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) < pos_inf()); }
+
 // Two fp32 values to two e4m3 codes (lo in the low byte): nearest even, saturating at
 // +-448, NaN kept.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {

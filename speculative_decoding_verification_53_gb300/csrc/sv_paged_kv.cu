@@ -5,13 +5,16 @@
 // a group of lanes, eight elements each (a power of two of lanes, so that the row's
 // largest magnitude is log2 shuffles away); a group does the key and the value of its
 // token and head, so both loads are in flight together and the page is looked up once.
-//   e4m3: scale s = max(a / 448, 2^-126), a the largest finite magnitude; code = e4m3(x *
-//   (1/s)).  The floor keeps s and 1/s normal numbers, so a row of zeros or of tiny
-//   numbers needs no case of its own.  The product with 1/s instead of a division per
-//   element moves x/s by at most 2^-23 of itself, 2^-19 of an e4m3 step.
+//   e4m3: scale s = max(a / 448, 2^-126), a the largest finite magnitude; code = e4m3(x / s).
+//   The quotient is x i + x j, i = 1 / s rounded and j = (1 - s i) i what it leaves: i + j is 1 / s
+//   to 2^-47, x j is off by 2^-47 of the sum, and the fma that adds them rounds once, so the
+//   result is x / s rounded from within 2^-46 of itself; two elements an instruction.  x i
+//   alone put 5 in 10000 elements of bf16 rows, where x / s often is next to the middle of two codes,
+//   on its wrong side.
 //
-// One GB300: writing 16 x up to 2048 tokens of 8 heads x 128 as e4m3 takes 34 us (3.7 TB/s, issue
-// 77 %: the largest magnitude, compared as pairs of bf16 bits, and one rounding per pair), as bf16
+// One GB300: writing 16 x up to 2048 tokens of 8 heads x 128 as e4m3 takes 34 us (3.7 TB/s, bound by
+// issue: the largest magnitude, compared as pairs of bf16 bits, the quotient, which cost 4 us over
+// x i, and one rounding per pair), as bf16
 // 31 us (5.4 TB/s); reading 8 x up to 8192 positions back from e4m3 45 us (5.6 TB/s).
 //
 // The paged compaction is the kernel of sv_tree_kv.cu with one more indirection: a warp
@@ -134,7 +137,10 @@ __device__ __forceinline__ void store_cache_row(unsigned char* row, float* scale
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         float a = __uint_as_float(top);
-        if (__any_sync(0xffffffffu, top >= 0x7f800000u)) {  // rare: the largest finite magnitude
+        // Rare rows: not all finite, or (but for zeros) so small or large that j may be subnormal
+        // or a product may be: below 2^-80 or from 2^80 on.
+        const bool rare = __any_sync(0xffffffffu, top != 0u && (top < 0x17800000u || top >= 0x67800000u));
+        if (rare) {  // the largest finite magnitude
             float x[8];
             v.widen(x);
             a = 0.0f;
@@ -143,15 +149,25 @@ __device__ __forceinline__ void store_cache_row(unsigned char* row, float* scale
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
         }
-        const float s = fmaxf(a / sv::E4M3_MAX, 1.17549435e-38f), inv = 1.0f / s;
+        const float s = fmaxf(a / sv::E4M3_MAX, 1.17549435e-38f);
         if (!live) return;
+        // Rare rows are divided as x 2^90 and s 2^90 (or 2^-90), exact where it matters.
+        const float f = !rare || (s > 1.0e-20f && s < 1.0e20f) ? 1.0f : s < 1.0f ? 1.2379400392853803e27f : 8.0779356694631609e-28f;
+        const float i = 1.0f / (s * f), j = fmaf(-s * f, i, 1.0f) * i;
+        const float2 i2 = make_float2(i, i), j2 = make_float2(j, j);
         float x[8];
         v.widen(x);
         uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 y = sv::fmul2(make_float2(x[2 * j], x[2 * j + 1]), make_float2(inv, inv));
-            w[j] = sv::e4m3x2(y.x, y.y);
+        for (int k = 0; k < 4; ++k) {
+            float2 e = make_float2(x[2 * k], x[2 * k + 1]);
+            if (rare) e = make_float2(e.x * f, e.y * f);
+            float2 q = sv::ffma2(e, i2, sv::fmul2(e, j2));
+            if (rare) {  // infinity's x j may be of the other sign
+                if (sv::not_finite(e.x)) q.x = e.x;
+                if (sv::not_finite(e.y)) q.y = e.y;
+            }
+            w[k] = sv::e4m3x2(q.x, q.y);
         }
         if (e0 == 0) *scale = s;
         if (AL) {

@@ -2,8 +2,8 @@
 
 Tolerances: a rounding is off by at most half a step of its type, relative to the value
 2^-8 for bf16, 2^-24 for fp32.  An e4m3 code must be a nearest value, up to the 2^-22 by
-which fp32's x * (1 / scale) may differ from x / scale (two roundings of 2^-24, and the
-scale's own 2^-24, doubled).
+which fp32's x / scale may differ from the quotient in 64 bits (its own rounding and the
+scale's, 2^-24 each, doubled); one test asks for the very code of the fp32 quotient.
 """
 import numpy as np
 import pytest
@@ -159,6 +159,35 @@ def test_append_special_values(sv):
         a, _ = sv.spec_kv_read(k, v, ints([[0]]), ints([0]), 8, k_scale=ks, v_scale=vs, dtype=torch.float32)
         a = host(a)[0, :, 0]
         assert np.isnan(a[3]).all() and (a[0] == 0).all() and a[6, 0] == 448
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("D,amp", [(128, 1.0), (64, 1e30), (120, 1e-20), (7, 1e-30), (256, 1e-37)])
+def test_codes_are_of_the_rounded_quotient(sv, dtype, D, amp):
+    """Every code is e4m3 of x / scale rounded to fp32, with the scale that is stored: bf16 elements
+    over their row's largest often lie next to the middle of two codes, where x * (1 / scale) takes
+    the other one for 5 in 10000."""
+    import torch
+    rng = np.random.default_rng([D, int(amp > 1)])
+    n = 3000
+    x = rng.normal(size=(1, n, 1, D)) * np.exp(2 * rng.normal(size=(1, n, 1, 1))) * amp
+    x = torch.from_numpy(np.clip(x, -3e38, 3e38)).to(_torch_dtype(dtype))
+    x[0, 5] = 0
+    x[0, 17, 0, D // 2] = float("inf")
+    x[0, 18, 0, D // 2] = float("nan")
+    k = torch.zeros((1, 1, n, D), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    v, ks, vs = k.clone(), torch.zeros((1, 1, n), device="cuda"), torch.zeros((1, 1, n), device="cuda")
+    sv.spec_kv_append(x.cuda(), x.cuda(), k, v, ints([[0]]), ints([0]), k_scale=ks, v_scale=vs)
+    f = x[0, :, 0].float().numpy()
+    a = np.where(np.isfinite(f), np.abs(f), 0).max(-1)
+    s = np.maximum(a / np.float32(448), np.float32(2.0 ** -126))
+    assert np.array_equal(ks[0, 0].cpu().numpy(), s) and torch.equal(ks, vs)
+    y = np.clip(f / s[:, None], np.float32(-448), np.float32(448))
+    assert y.dtype == np.float32
+    want = torch.from_numpy(y).to(torch.float8_e4m3fn)
+    for pages in (k, v):
+        got = pages[0, 0].cpu()
+        assert np.array_equal(got.float().numpy(), want.float().numpy(), equal_nan=True)
 
 
 def test_read_new_outputs_are_zero_behind_the_tokens(sv):
