@@ -22,6 +22,7 @@
 // Multiplied as fp16 (two codes an instruction) with units that a row takes from the value
 // scales it sees, that call took 195 us: not worth the units' code, not kept.
 #include <cstdint>
+#include <cstdlib>
 
 #include "spec_paged_kv.h"
 #include "sv_attention.cuh"
@@ -629,6 +630,17 @@ bool sizes_ok(int B, int Q, int Hq, int H, int D, int max_len) {
            (int64_t)Q * (Hq / H) < ((int64_t)1 << 30);
 }
 
+// Test hook for the time-out path (SPEC_VERIFY_TEST_STALL_ATTENTION=<batch row>): the tcgen05
+// kernel's CTAs of that row never report one tile's notes, so the waits for it run out and the
+// row is written as NaN.  Read once; unset, nothing changes.
+int test_stall_row() {
+    static const int row = [] {
+        const char* s = std::getenv("SPEC_VERIFY_TEST_STALL_ATTENTION");
+        return s && *s ? std::atoi(s) : -1;
+    }();
+    return row;
+}
+
 int sm_count() {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -697,6 +709,7 @@ sv_status spec_paged_attention(const void* q, const int64_t* q_stride, int num_q
     a.equal = p.tile_rows >= 128;
     a.sort = a.equal && B > 1 && B <= 32 && p.whole == 0 && p.ctas > sms ? B : 0;
     a.chunk = p.chunk;
+    a.stall_row = test_stall_row();
     a.out = static_cast<uint16_t*>(out);
     a.lse = out_lse;
     const int64_t rows = p.ws ? (p.tiles - p.whole) * p.tile_rows : 0;  // of the split tiles

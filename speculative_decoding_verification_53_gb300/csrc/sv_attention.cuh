@@ -28,6 +28,7 @@ struct AttnArgs {
     int per;                   // splits that a CTA takes: 1 or 2
     int equal;                 // splits are of one length
     int sort;                  // > 0: this many batch rows, taken longest splits first
+    int stall_row;             // test hook, -1: none (sv_attention.cu)
     uint16_t* out;             // [B][Q][Hq][D] bf16
     float* lse;                // [B][Q][Hq] or nullptr
     float* part_o;             // [split tile][split][row of the tile][D] fp32

@@ -50,8 +50,10 @@
 // e4m3, 147 us (560 TFLOP/s; a tile takes 5700 cycles, 2048 of them products, the rest widening and
 // softmax); 8 chains of 6 over 3277 to 32768, bf16, 135 us (5.0 TB/s).
 //
-// Every wait is bounded; a CTA whose wait runs out writes NaN for its rows, which a verify
-// reports as invalid data, and frees its TMEM.
+// Every wait is bounded.  A role whose wait runs out stops, so that the others' waits run out too;
+// the softmax's warps then write NaN for their rows, which a verify reports as invalid data, and
+// the CTA leaves when its copies have landed and its products have ended, which their warps wait
+// for (with the same bound) whoever gave up.
 #include <cstdint>
 
 #include "spec_paged_kv.h"
@@ -276,7 +278,7 @@ struct __align__(16) Shared {
     uint64_t land[8], raw_full[4], raw_empty[4];  // copy engine: values to be looked over; e4m3 codes
     uint64_t note_full[META], note_empty[META];   // the tiles' notes below
     uint32_t tmem;
-    int bad, failed;
+    int bad;
     uint32_t valid[META][4];       // which of the tile's positions hold something
     __align__(16) float ksc[META][TN];  // e4m3: a position's key scale times the score factor
     __align__(16) uint2 vsc[META][TN];  // its value scale times 2^-vexp, as two fp16 numbers
@@ -332,7 +334,6 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             mbar_init(&sh.raw_empty[i], 4);
         }
         sh.bad = 0;
-        sh.failed = 0;
         sh.limit[0] = sh.limit[1] = sv::pos_inf();
         sv::fence_mbar_init();
     }
@@ -500,7 +501,6 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         if (DUAL && ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.o_full[q ^ 1], 0));
         const bool mine = !DUAL || t.split + q < t.active;  // the stretch exists
         const int first = start(DUAL ? q : 0), last = stop(DUAL ? q : 0);
-        if (!ok) sh.failed = 1;
         tc_fence_after();
         float inv = !ok ? __int_as_float(0x7fffffff) : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
         const float lse2 = !ok ? inv : l == 0.0f ? neg_inf() : mx + log2f(l) - (E4M3 ? RAISE : 0.0f);
@@ -511,12 +511,16 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         }
         const float weight = inv;
         if (E4M3) inv *= power_of_two(vexp);
-        const bool patch = ok && sh.bad != 0;
+        const bool patch = sh.bad != 0;
         // Rows leave through shared memory (where this row tile's queries were), so that a store
         // covers whole rows: a lane writing its own row touched 32 lines per store and cost
         // 15000 cycles a CTA.  Part of a row at a time, 16-byte pieces swizzled by the row.
         constexpr int PASSES = DP == 256 ? 4 : 2, CW = DP / PASSES, PC = CW / 4;
-        if (!idle && mine) {
+        if (!ok) {  // nothing of this CTA's memory is sure to be at rest
+            if (live && mine && t.active <= 1)
+                for (int d = 0; d < D; d += 8)
+                    *reinterpret_cast<uint4*>(a.out + row * D + d) = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+        } else if (!idle && mine) {
             const uint32_t stage = smem0 + q * S::MAT + (warp & 3) * (S::MAT / 4);
 #pragma unroll 1
             for (int c = 0; c < PASSES; ++c) {
@@ -810,7 +814,6 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             }
             cp_wait_all();
         }
-        if (!ok) sh.failed = 1;
     } else {
         // ------------------------------------------------------------ products
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::R_MMA));
@@ -908,10 +911,9 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     }
                 }
             }
-            if (!ok) {
-                tc_commit(&sh.drain, leader);  // whatever was issued ends before the memory is given back
-                (void)mbar_wait_bounded(&sh.drain, 0);
-            }
+            // whatever was issued ends before the memory is given back, whoever may have given up
+            tc_commit(&sh.drain, leader);
+            (void)mbar_wait_bounded(&sh.drain, 0);
         } else if (warp == 4 * MQ + 5 && box_rows) {
             // ---------------------------------------------------------- copies
             // Lane l < boxes copies the box of positions l * box_rows .. of a tile, which lie in
@@ -927,6 +929,8 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     if (p >= 0) page = p;
                 }
             };
+            auto look_over = [&](int item) { return !E4M3 && (item & 1) && start(item >> 1) + TN > open; };
+            uint32_t lands = 0;  // phase of each buffer's landing barrier
             int page, row, page1, row1, n = 0;
             box_page(0, page, row);
             box_page(1, page1, row1);
@@ -938,7 +942,8 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                                     mbar_wait_bounded(E4M3 ? &sh.raw_empty[slot & 3] : &sh.empty[slot], (n / PLACES - 1) & 1));
                     if (!ok) break;
                 }
-                const bool tail = !E4M3 && (n & 1) && start(n >> 1) + TN > open;
+                const bool tail = look_over(n);
+                if (tail) lands ^= 1u << slot;
                 uint64_t* bar = E4M3 ? &sh.raw_full[slot & 3] : tail ? &sh.land[slot] : &sh.full[slot];
                 if (lane == 0) {
                     sv::mbar_arrive_expect_tx(bar, E4M3 ? S::MAT / 2 : S::MAT);
@@ -962,11 +967,13 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     box_page((n >> 1) + 2, page1, row1);
                 }
             }
-            if (!ok) {  // copies in flight land before the CTA leaves
-                constexpr int PLACES = S::RAW ? S::RAW : S::NB;
-                for (int z = n > PLACES ? n - PLACES : 0; z < n; ++z)
-                    if (E4M3 || !(z & 1) || start(z >> 1) + TN <= open)
-                        (void)mbar_wait_bounded(E4M3 ? &sh.raw_full[z % PLACES & 3] : &sh.full[z % PLACES], (z / PLACES) & 1);
+            // The last copy into each place lands before the CTA leaves, whoever may have given up.
+            constexpr int PLACES = S::RAW ? S::RAW : S::NB;
+            for (int z = n > PLACES ? n - PLACES : 0; z < n; ++z) {
+                const int slot = z % PLACES;
+                if (E4M3) (void)mbar_wait_bounded(&sh.raw_full[slot & 3], (z / PLACES) & 1);
+                else if (look_over(z)) (void)mbar_wait_bounded(&sh.land[slot], (~lands >> slot) & 1);
+                else (void)mbar_wait_bounded(&sh.full[slot], (z / PLACES) & 1);
             }
         } else if (warp == 4 * MQ + 6) {
             // ----------------------------------------------------------- notes
@@ -1065,12 +1072,11 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.note_full[m]);
+                if (lane == 0 && !(t.b == a.stall_row && j == (tiles > 1))) mbar_arrive(&sh.note_full[m]);
                 fetch();
                 look_up(j + 2, at1);
             }
         }
-        if (!ok) sh.failed = 1;
     }
     __syncwarp();
     tc_fence_before();
