@@ -279,6 +279,7 @@ struct __align__(16) Shared {
     uint64_t note_full[META], note_empty[META];   // the tiles' notes below
     uint32_t tmem;
     int bad;
+    int asked;  // copies that the copy engine has been asked for
     uint32_t valid[META][4];       // which of the tile's positions hold something
     __align__(16) float ksc[META][TN];  // e4m3: a position's key scale times the score factor
     __align__(16) uint2 vsc[META][TN];  // its value scale times 2^-vexp, as two fp16 numbers
@@ -334,6 +335,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             mbar_init(&sh.raw_empty[i], 4);
         }
         sh.bad = 0;
+        sh.asked = 0;
         sh.limit[0] = sh.limit[1] = sv::pos_inf();
         sv::fence_mbar_init();
     }
@@ -641,12 +643,18 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             };
             if (box_rows) {
                 uint32_t lands = 0;  // phase of each buffer's barrier
-                // the wait for the first such tile covers all tiles before it
-                const uint32_t patience = sv::WAIT_LIMIT_NS + (tiles < 150000 ? tiles * 20000u : 3000000000u);
+                int asked = -1;      // copies asked for when a wait last ran out
                 for (int j = 0; j < tiles; ++j) {
                     if (start(j) + TN <= open) continue;
                     const int buf = (2 * j + 1) % S::NB;
-                    ok = __all_sync(0xffffffffu, sv::mbar_wait_bounded_ns(&sh.land[buf], (lands >> buf) & 1, patience));
+                    // The wait for the first such tile covers all tiles before it, however many: it
+                    // starts again while copies go on being asked for.
+                    do {
+                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.land[buf], (lands >> buf) & 1));
+                        const int now = __shfl_sync(0xffffffffu, *(volatile int*)&sh.asked, 0);
+                        if (ok || now == asked) break;
+                        asked = now;
+                    } while (true);
                     if (!ok) break;
                     lands ^= 1u << buf;
                     look_over(j, buf);
@@ -948,6 +956,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 if (lane == 0) {
                     sv::mbar_arrive_expect_tx(bar, E4M3 ? S::MAT / 2 : S::MAT);
                     if (!E4M3 && !tail) mbar_arrive_n(bar, 3);
+                    *(volatile int*)&sh.asked = n + 1;
                 }
                 __syncwarp();
                 const CUtensorMap* map = n & 1 ? &v_map : &k_map;
