@@ -121,8 +121,9 @@ SV_API sv_status spec_kv_read(const sv_paged_cache *cache, const int32_t *base, 
  * softmax sums and outputs are accumulated in fp32; the probabilities enter the second
  * product rounded to bf16 (for e4m3, times the value's scale).  e4m3 calls of more than 16
  * query rows per cache head multiply as fp16 instead: a value's code
- * times its scale and a probability are rounded once each to 11 bits, and what a position
- * adds below 2^-31 of 448 times the largest value scale may be lost.
+ * times its scale and a probability are rounded once each to 11 bits, and with V = 448 times the
+ * largest value scale of the positions that a query sees, what a position adds below 2^-31 V,
+ * and of a value what lies below 2^-25 V, may be lost.
  * Weights may stand at up to 2^8 times their value while they are summed: bf16 values beyond
  * 2^110 may overflow to infinity.
  * out must not overlap q or the cache.  Every wait inside the kernels is bounded; where one

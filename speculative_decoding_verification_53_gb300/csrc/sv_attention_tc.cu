@@ -29,17 +29,18 @@
 // e4m3 pages are multiplied as fp16, which holds every code exactly and converts two in one
 // instruction (bf16 takes four).  A position's key scale multiplies its scores, in fp32: rounding
 // scaled keys to 11 bits moved lse by 10^-4.  A value's code times its scale, over a power of two
-// that brings the stretch's largest below 2^15, is rounded once to 11 bits, below what rounding the
+// that keeps the stretch's largest below 2^15, is rounded once to 11 bits, below what rounding the
 // scaled probabilities to bf16 cost: code * hi + code * lo with the scale as two fp16 numbers,
-// three instructions for two codes.  Queries are brought to [2^14, 2^15) row by row by a power
+// four instructions for two codes.  Queries are brought to [2^14, 2^15) row by row by a power
 // of two, exactly to 2^-39 of the row's largest element.  Probabilities enter as fp16 too, 2^7
 // times larger, so that fp16's subnormal step is 2^-31 of the largest.  O is held in units of
 // the values' power of two and rescaled when it grows.
 //
-// A new token's scale more than 2^12 above those that every query sees would push the values of
-// queries that do not see it out of that range: its values are left out of the products and put
-// back at the end for the queries that see them, as values that are not finite are.  (A unit per row
-// in the softmax loop cost 172 -> 195 us of a tree batch in instruction-cache misses.)
+// That power of two follows the scales that every query of the CTA sees, never a token that some do
+// not see.  Tiles with new tokens leave room for scales of up to 2^12 above those; values with larger
+// ones are left out of the products and put back at the end for the queries that see them, as
+// values that are not finite are.  (A unit per row in the softmax loop cost 172 -> 195 us of a tree
+// batch in instruction-cache misses.)
 //
 // Heads wider than 128 take one row tile, 384 columns of TMEM and a ring of two 64 KB buffers; e4m3
 // codes then go from the cache through registers.  16 trees of 61 over 4096, 32 over 8 heads of 256,
@@ -218,7 +219,10 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Eight e4m3 codes in fp16, times a scale (x: twice its fp16, y: twice what that leaves) if asked.
+// Eight e4m3 codes in fp16, or times 2^-9 and a scale if asked (x: twice its fp16, y: twice what that
+// leaves).  The 2^-9 is exact (codes are multiples of 2^-9, below 2^9) and keeps the scale 2^9
+// further from fp16's subnormal numbers, where it would lose bits; it costs 16 trees of 61 over 2048
+// to 8192 152 -> 157 us (for the tiles that need it alone, by a branch, 163).
 template <bool SCALE>
 __device__ __forceinline__ uint4 widen8(uint2 w, uint2 scale) {
     uint32_t out[4];
@@ -227,6 +231,8 @@ __device__ __forceinline__ uint4 widen8(uint2 w, uint2 scale) {
         asm("{.reg .b16 t, u;\n\tmov.b32 {t, u}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
             : "=r"(out[2 * i]), "=r"(out[2 * i + 1])
             : "r"(i ? w.y : w.x));
+#pragma unroll
+    for (int z = 0; SCALE && z < 4; ++z) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(out[z]) : "r"(0x18001800u));
 #pragma unroll
     for (int z = 0; SCALE && z < 4; ++z)
         asm("{.reg .b32 t;\n\tmul.rn.f16x2 t, %0, %2;\n\tfma.rn.f16x2 %0, %0, %1, t;\n\t}"
@@ -282,7 +288,7 @@ struct __align__(16) Shared {
     int asked;  // copies that the copy engine has been asked for
     uint32_t valid[META][4];       // which of the tile's positions hold something
     __align__(16) float ksc[META][TN];  // e4m3: a position's key scale times the score factor
-    __align__(16) uint2 vsc[META][TN];  // its value scale times 2^-vexp, as two fp16 numbers
+    __align__(16) uint2 vsc[META][TN];  // its value scale times 2^(9 - vexp), as two fp16 numbers
     int vexp[META];
     float limit[2];  // by stretch: larger value scales of new tokens are left to the end
     float row_factor[128];  // DUAL: what a row's scores are multiplied by
@@ -988,11 +994,13 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             // ----------------------------------------------------------- notes
             // Which positions of a tile hold something, and e4m3's scales; read ahead, so that
             // nobody else waits for a page table or a scale.
-            // The stretches' largest finite value scales so far, as bits, and those of positions that
-            // every query sees (the last such position is one for both).  A new token's scale far
-            // above the latter would push the values of queries that do not see it out of fp16's
-            // range: its value is left to the end, as values that are not finite are.  Up to 2^12
-            // above, rounding to the unit costs the others at most 2^-27 of their own largest.
+            // The stretches' largest finite value scales so far of positions that every query sees, as
+            // bits; `seen` counts the last such position for both stretches.  The unit that values are
+            // rounded in comes from these alone, so that no query's roundings hang on what it does
+            // not see.  Tiles that hold new tokens keep room for scales of 2^12 times `seen`, which
+            // then is at least 2^-7 units: a value is off by at most 3 2^-25 units (the scale's two
+            // halves, the product with the lower one, the sum), 2^-25 of 448 seen, beside its 11 bits.
+            // Beyond, a new token's value is left to the end, as values that are not finite are.
             uint32_t largest_v = 0u, other_v = 0u, seen = 0u, other_seen = 0u;
             if (E4M3) {
                 int row;
@@ -1040,11 +1048,14 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 }
                 if (E4M3) {
                     const bool tail = start(j) + TN > open;
+                    uint32_t seen_here = 0u;
 #pragma unroll
                     for (int z = 0; z < 4; ++z)
-                        if (start(j) + 32 * z + lane < open && !sv::not_finite(vs[z])) seen = max(seen, __float_as_uint(fabsf(vs[z])));
+                        if (start(j) + 32 * z + lane < open && !sv::not_finite(vs[z])) seen_here = max(seen_here, __float_as_uint(fabsf(vs[z])));
+                    seen_here = __reduce_max_sync(0xffffffffu, seen_here);
+                    largest_v = max(largest_v, seen_here);
+                    seen = max(seen, seen_here);
                     if (tail) {
-                        seen = __reduce_max_sync(0xffffffffu, seen);
                         const float limit = 4096.0f * __uint_as_float(seen);
                         if (lane == 0) sh.limit[DUAL ? j & 1 : 0] = limit;
 #pragma unroll
@@ -1054,12 +1065,9 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                                 sh.bad = 1;
                             }
                     }
-#pragma unroll
-                    for (int z = 0; z < 4; ++z)
-                        if (!sv::not_finite(vs[z])) largest_v = max(largest_v, __float_as_uint(fabsf(vs[z])));
-                    largest_v = __reduce_max_sync(0xffffffffu, largest_v);
                     // scales below 2^6, times codes of at most 448: below 2^15
-                    const int e = (int)(largest_v >> 23) - 127 + 1 - 6, ve = e < -118 ? -118 : e;
+                    const int e = (int)((tail ? seen : largest_v) >> 23) - 127 + 1 - 6;
+                    const int ve = min(max(e, -118) + (tail ? 12 : 0), 126);
                     auto halves = [](float s) {  // as two fp16 numbers, each twice
                         const uint32_t hi = f16x2(s, s);
                         float back;
@@ -1077,7 +1085,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
 #pragma unroll
                     for (int z = 0; z < 4; ++z) {
                         sh.ksc[m][32 * z + lane] = ks[z] * a.scale_log2;
-                        sh.vsc[m][32 * z + lane] = halves(vs[z] * power_of_two(-ve));
+                        sh.vsc[m][32 * z + lane] = halves(vs[z] * power_of_two(9 - ve));  // see widen8
                     }
                 }
                 __syncwarp();
