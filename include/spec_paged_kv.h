@@ -129,8 +129,9 @@ SV_API sv_status spec_kv_read(const sv_paged_cache *cache, const int32_t *base, 
  * out must not overlap q or the cache.  Every wait inside the kernels is bounded; where one
  * runs out, the rows concerned are written as NaN, which a verify reports as invalid data.
  *   workspace    device scratch of ws_bytes, 16-byte aligned (spec_paged_attention_workspace_size;
- *                no initialisation, free for other uses once the call has run), or NULL:
- *                contexts are then not split, which is slower for few rows and long contexts.
+ *                no initialisation, free for other uses once the call has run), or NULL, or
+ *                less than that or not so aligned: contexts are then not split, which is slower
+ *                for few rows and long contexts.
  * 1 <= Q <= 65536, Q * num_q_heads / num_heads < 2^30, head_dim a multiple of 8 (SV_ERR_UNSUPPORTED otherwise), pages, strides
  * and q aligned to 16 bytes (SV_ERR_UNSUPPORTED otherwise).  Errors: SV_ERR_INVALID_ARG for
  * a bad size, pointer or stride (B = 0 returns SV_OK).

@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(KW * 32, DP == 256 ? 1 : 2)
         const int64_t row = sv::attn_row(a, t, R);
         const int64_t part = t.part + R - t.mt * S::ROWS;
         if (t4 == 0) {
-            if (t.active > 1) a.part_lse[part] = lse2[y];
+            if (t.parts > 1) a.part_lse[part] = lse2[y];
             else if (a.lse) a.lse[row] = lse2[y] * 0.69314718055994531f;
         }
         // a thread's elements of each 16: bf16 pages 2 t4, 2 t4 + 1 and 8 more; e4m3 4 t4 .. 4 t4 + 3
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(KW * 32, DP == 256 ? 1 : 2)
                         }
                     }
                 }
-                if (t.active > 1)
+                if (t.parts > 1)
                     *reinterpret_cast<float2*>(a.part_o + part * D + d[z]) = make_float2(v[2 * z], v[2 * z + 1]);
                 else
                     *reinterpret_cast<uint32_t*>(a.out + row * D + d[z]) = sv::bf16x2(v[2 * z], v[2 * z + 1]);
@@ -504,30 +504,31 @@ __global__ void __launch_bounds__(KW * 32, DP == 256 ? 1 : 2)
 // Joins the splits of a row: weights 2^(lse_s - max), one warp per row of the split tiles.
 __global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_constant__ AttnArgs a, int pairs,
                                                                    int tile_rows, int64_t rows) {
+    const int part_rows = a.part_rows;
     pdl_trigger();
     pdl_wait();
     const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (at >= rows) return;
-    const int rest = (int)(at / tile_rows), r = (int)(at - (int64_t)rest * tile_rows);
+    const int rest = (int)(at / part_rows), r = (int)(at - (int64_t)rest * part_rows);
     const sv::AttnPlace p = sv::attn_place(a, pairs, (unsigned)(a.whole + rest));
     int base, n;
     if (!sv::paged_row(a.c, a.base, a.new_len, p.b, a.Q, base, n)) return;
     const int64_t R = (int64_t)p.mt * tile_rows + r;
     if (R >= (int64_t)n * a.group) return;
-    const int active = sv::attn_active(a, sv::attn_tile_end(base, n, a.group, p.mt, tile_rows, a.tree_mask != nullptr));
-    if (active <= 1) return;  // written by the one CTA that had the row
+    const int parts = sv::attn_parts(a, sv::attn_active(a, sv::attn_tile_end(base, n, a.group, p.mt, tile_rows, a.tree_mask != nullptr)));
+    if (parts <= 1) return;  // written by the one CTA that had the row
     const int64_t row = ((int64_t)p.b * a.Q + R / a.group) * a.Hq + p.h * a.group + R % a.group;
-    const int64_t part = (int64_t)rest * a.splits * tile_rows + r;  // of split 0; the next ones tile_rows apart
+    const int64_t part = (int64_t)rest * (a.splits / a.per) * part_rows + r;  // the first; the next ones part_rows apart
     const int D = a.c.dim;
     const float* lse = a.part_lse + part;
     float top = neg_inf();
-    for (int s = lane; s < active; s += 32) top = fmaxf(top, lse[(int64_t)s * tile_rows]);
+    for (int s = lane; s < parts; s += 32) top = fmaxf(top, lse[(int64_t)s * part_rows]);
 #pragma unroll
     for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
     const float shift = top == neg_inf() ? 0.0f : top;
     float sum = 0.0f;
-    for (int s = lane; s < active; s += 32) sum += sv::ex2(lse[(int64_t)s * tile_rows] - shift);
+    for (int s = lane; s < parts; s += 32) sum += sv::ex2(lse[(int64_t)s * part_rows] - shift);
 #pragma unroll
     for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -535,9 +536,9 @@ __global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         const float* from = a.part_o + part * D + d;
 #pragma unroll 4
-        for (int s = 0; s < active; ++s) {
-            const float w = sv::ex2(lse[(int64_t)s * tile_rows] - shift) * inv;
-            const float4 v = *reinterpret_cast<const float4*>(from + (int64_t)s * tile_rows * D);
+        for (int s = 0; s < parts; ++s) {
+            const float w = sv::ex2(lse[(int64_t)s * part_rows] - shift) * inv;
+            const float4 v = *reinterpret_cast<const float4*>(from + (int64_t)s * part_rows * D);
             acc.x += w * v.x;
             acc.y += w * v.y;
             acc.z += w * v.z;
@@ -565,10 +566,10 @@ constexpr int kMaxB = 65535;
 constexpr int kMaxQ = 65536;
 
 struct Plan {
-    int tile_rows, m_tiles, splits, chunk;
+    int tile_rows, m_tiles, splits, chunk, per, part_rows;
     int64_t tiles, whole, ctas;
-    bool dual;  // a CTA takes two splits
-    size_t ws;
+    bool dual;  // a CTA takes two splits (per: how many), and joins them
+    size_t ws;  // of partial results: none where each row tile is one CTA's
 };
 
 // How a call is cut: tiles of query rows, and stretches of positions where there are too
@@ -619,8 +620,11 @@ Plan make_plan(int B, int Q, int Hq, int H, int D, bool e4m3, int max_len, int n
     p.splits = (int)(((int64_t)max_len + p.chunk - 1) / p.chunk);
     if (p.dual) p.splits += p.splits & 1;
     if (p.splits <= 1) p.whole = p.tiles;
-    p.ctas = p.whole + (p.tiles - p.whole) * p.splits / (p.dual ? 2 : 1);
-    p.ws = (size_t)(p.tiles - p.whole) * p.splits * p.tile_rows * (D + 1) * sizeof(float);
+    p.per = p.dual ? 2 : 1;
+    const int64_t parts = (p.tiles - p.whole) * p.splits / p.per;
+    p.ctas = p.whole + parts;
+    p.part_rows = p.m_tiles == 1 ? (int)rows : p.tile_rows;
+    p.ws = p.splits > p.per ? (size_t)parts * p.part_rows * (D + 1) * sizeof(float) : 0;
     return p;
 }
 
@@ -687,6 +691,7 @@ sv_status spec_paged_attention(const void* q, const int64_t* q_stride, int num_q
         p.splits = 1;
         p.chunk = sv::PAGED_MAX_POS;
         p.dual = false;
+        p.per = 1;
         p.ws = 0;
     }
     if (p.ctas >= ((int64_t)1 << 31)) return SV_ERR_UNSUPPORTED;
@@ -705,16 +710,17 @@ sv_status spec_paged_attention(const void* q, const int64_t* q_stride, int num_q
     a.m_tiles = p.m_tiles;
     a.whole = (int)p.whole;
     a.splits = p.splits;
-    a.per = p.dual ? 2 : 1;
+    a.per = p.per;
+    a.part_rows = p.part_rows;
     a.equal = p.tile_rows >= 128;
     a.sort = a.equal && B > 1 && B <= 32 && p.whole == 0 && p.ctas > sms ? B : 0;
     a.chunk = p.chunk;
     a.stall_row = test_stall_row();
     a.out = static_cast<uint16_t*>(out);
     a.lse = out_lse;
-    const int64_t rows = p.ws ? (p.tiles - p.whole) * p.tile_rows : 0;  // of the split tiles
+    const int64_t rows = p.ws ? (p.tiles - p.whole) * p.part_rows : 0;  // of the split tiles
     a.part_o = static_cast<float*>(workspace);
-    a.part_lse = p.ws ? a.part_o + rows * p.splits * D : nullptr;
+    a.part_lse = p.ws ? a.part_o + rows * (p.splits / p.per) * D : nullptr;
     cudaStream_t s = (cudaStream_t)stream;
     const bool e4m3 = cache->dtype == SV_CACHE_E4M3;
     const int pairs = B * cache->num_heads;

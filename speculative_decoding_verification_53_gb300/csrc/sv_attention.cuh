@@ -25,14 +25,15 @@ struct AttnArgs {
     int m_tiles;               // tiles of query rows per (batch row, cache head)
     int whole;                 // tiles [0, whole) are not split, the others `splits` ways
     int splits, chunk;         // a row tile has a split per `chunk` positions, `splits` at most
-    int per;                   // splits that a CTA takes: 1 or 2
+    int per;                   // splits that a CTA takes: 1 or 2, whose results it joins itself
+    int part_rows;             // rows of a tile in the partial results
     int equal;                 // splits are of one length
     int sort;                  // > 0: this many batch rows, taken longest splits first
     int stall_row;             // test hook, -1: none (sv_attention.cu)
     uint16_t* out;             // [B][Q][Hq][D] bf16
     float* lse;                // [B][Q][Hq] or nullptr
-    float* part_o;             // [split tile][split][row of the tile][D] fp32
-    float* part_lse;           // [split tile][split][row of the tile], base 2
+    float* part_o;             // [split tile][split / per][part_rows][D] fp32
+    float* part_lse;           // [split tile][split / per][part_rows], base 2
 };
 
 // Tiles are numbered with the last row tiles first: a chain's late queries see most
@@ -54,7 +55,7 @@ struct AttnTile {
     int base, n;       // positions before the chunk, real queries
     int begin, end;    // this CTA's positions
     int end2;          // of a second split behind them, where a CTA takes two (end: it has none)
-    int active;        // splits of this row tile that have positions
+    int parts;         // CTAs of this row tile that have positions
     int64_t part;      // first row of this CTA's partial results
 };
 
@@ -72,6 +73,9 @@ __device__ __forceinline__ int attn_active(const AttnArgs& a, int end) {
     if (n > a.splits) n = a.splits;
     return (n & (a.per - 1)) && end > 128 * n ? n + 1 : n;  // splits is a multiple of per
 }
+
+// CTAs that take n splits.
+__device__ __forceinline__ int attn_parts(const AttnArgs& a, int n) { return (n + a.per - 1) / a.per; }
 
 // First position of split s of n over `end` positions.  Splits of a row tile are of one length,
 // in units of 128, and with the longest first (below) a batch of unequal contexts ends together:
@@ -118,15 +122,16 @@ __device__ __forceinline__ bool attn_tile(const AttnArgs& a, int pairs, unsigned
     t.h = p.h;
     t.mt = p.mt;
     t.split = whole ? 0 : (int)(rest % each) * per;
-    t.part = whole ? 0 : ((int64_t)tile * a.splits + t.split) * tile_rows;
+    t.part = whole ? 0 : ((int64_t)tile * each + rest % each) * a.part_rows;
     if (!paged_row(a.c, a.base, a.new_len, t.b, a.Q, t.base, t.n)) return false;
     if ((int64_t)t.mt * tile_rows >= (int64_t)t.n * a.group) return false;
     const int end = attn_tile_end(t.base, t.n, a.group, t.mt, tile_rows, a.tree_mask != nullptr);
-    t.active = whole ? 1 : attn_active(a, end);
-    if (t.split >= t.active) return false;
-    t.begin = attn_split_begin(a, end, t.split, t.active);
-    t.end = t.split == t.active - 1 ? end : attn_split_begin(a, end, t.split + 1, t.active);
-    t.end2 = t.split + 1 >= t.active ? t.end : t.split + 2 == t.active ? end : attn_split_begin(a, end, t.split + 2, t.active);
+    const int active = whole ? 1 : attn_active(a, end);
+    if (t.split >= active) return false;
+    t.parts = attn_parts(a, active);
+    t.begin = attn_split_begin(a, end, t.split, active);
+    t.end = t.split == active - 1 ? end : attn_split_begin(a, end, t.split + 1, active);
+    t.end2 = t.split + 1 >= active ? t.end : t.split + 2 == active ? end : attn_split_begin(a, end, t.split + 2, active);
     return true;
 }
 

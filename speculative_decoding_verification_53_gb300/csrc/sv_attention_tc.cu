@@ -20,7 +20,10 @@
 // DUAL: for 128 query rows or fewer the two warpgroups take the same rows and two stretches of
 // positions, whose tiles alternate (tile v belongs to stretch v & 1): one row tile alone leaves
 // the tensor cores and the copies waiting for its softmax (3600 cycles a tile of 64 KB; the
-// memory brings one in 3000).  The stretches' results are joined as any splits'.
+// memory brings one in 3000).  The CTA joins its two stretches itself: both O are in the TMEM lanes of
+// either stretch's warps, which take half of the columns each.  As two partial results joined by the
+// second kernel 512 chains of 6 over 1000 positions took 541 MB of scratch and 640 us, now none
+// and 457 us (32 over 8 heads of 128, bf16).
 //
 // The running maximum is moved only when it grows by more than 2^8: probabilities may
 // then reach 256 instead of 1, harmless in fp32 sums and bf16's range, and the rescale of
@@ -292,6 +295,9 @@ struct __align__(16) Shared {
     int vexp[META];
     float limit[2];  // by stretch: larger value scales of new tokens are left to the end
     float row_factor[128];  // DUAL: what a row's scores are multiplied by
+    float row_max[2][128], row_sum[2][128];  // DUAL: the stretches' results, to be joined
+    int unit[2];    // DUAL: their vexp
+    int gave_up;    // DUAL: a softmax warp whose wait ran out
 };
 
 template <int DP, int MQ, bool E4M3, bool DUAL>
@@ -342,6 +348,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
         }
         sh.bad = 0;
         sh.asked = 0;
+        sh.gave_up = 0;
         sh.limit[0] = sh.limit[1] = sv::pos_inf();
         sv::fence_mbar_init();
     }
@@ -505,45 +512,80 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             l += sum0.x + sum0.y;
         }
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.o_full[q], 0));
-        // DUAL: rows leave through memory that the other stretch's products read until they end
+        // DUAL: both stretches end before their results meet and leave through their memory
         if (DUAL && ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.o_full[q ^ 1], 0));
-        const bool mine = !DUAL || t.split + q < t.active;  // the stretch exists
-        const int first = start(DUAL ? q : 0), last = stop(DUAL ? q : 0);
         tc_fence_after();
-        float inv = !ok ? __int_as_float(0x7fffffff) : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-        const float lse2 = !ok ? inv : l == 0.0f ? neg_inf() : mx + log2f(l) - (E4M3 ? RAISE : 0.0f);
-        const int64_t row = live ? sv::attn_row(a, t, R) : 0, part = t.part + (DUAL ? q * S::ROWS : 0) + (R - t.mt * S::ROWS);
-        if (live && mine) {
-            if (t.active > 1) a.part_lse[part] = lse2;
+        // What O, or each stretch's O, is multiplied by.  DUAL: a row's maximum and sum meet in shared
+        // memory; both O are in the TMEM lanes of either stretch's warp, which does half of the columns.
+        float gain0, gain1 = 0.0f, shift = mx == neg_inf() ? 0.0f : mx;
+        if (DUAL) {
+            const int r = (warp & 3) * 32 + lane;
+            sh.row_max[q][r] = mx;
+            sh.row_sum[q][r] = l;
+            if (!idle) sh.unit[q] = vexp;  // one for all rows
+            if (!ok) sh.gave_up = 1;
+            asm volatile("bar.sync 1, %0;" ::"n"(S::SOFTMAX) : "memory");
+            ok = sh.gave_up == 0;
+            const float m0 = sh.row_max[0][r], m1 = sh.row_max[1][r], most = fmaxf(m0, m1);
+            shift = most == neg_inf() ? 0.0f : most;
+            gain0 = sv::ex2(m0 - shift);
+            gain1 = sv::ex2(m1 - shift);
+            l = sh.row_sum[0][r] * gain0 + sh.row_sum[1][r] * gain1;
+        }
+        const float inv = !ok ? __int_as_float(0x7fffffff) : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+        const float lse2 = !ok ? inv : l == 0.0f ? neg_inf() : shift + log2f(l) - (E4M3 ? RAISE : 0.0f);
+        if (DUAL) {
+            gain0 *= inv;
+            gain1 *= inv;
+            if (E4M3 && !idle) {
+                gain0 *= power_of_two(sh.unit[0]);
+                gain1 *= power_of_two(sh.unit[1]);
+            }
+        } else {
+            gain0 = E4M3 ? inv * power_of_two(vexp) : inv;
+        }
+        const int64_t row = live ? sv::attn_row(a, t, R) : 0, part = t.part + (R - t.mt * S::ROWS);
+        if (live && (!DUAL || q == 0)) {
+            if (t.parts > 1) a.part_lse[part] = lse2;
             else if (a.lse) a.lse[row] = lse2 * 0.69314718055994531f;
         }
-        const float weight = inv;
-        if (E4M3) inv *= power_of_two(vexp);
         const bool patch = sh.bad != 0;
         // Rows leave through shared memory (where this row tile's queries were), so that a store
         // covers whole rows: a lane writing its own row touched 32 lines per store and cost
         // 15000 cycles a CTA.  Part of a row at a time, 16-byte pieces swizzled by the row.
         constexpr int PASSES = DP == 256 ? 4 : 2, CW = DP / PASSES, PC = CW / 4;
         if (!ok) {  // nothing of this CTA's memory is sure to be at rest
-            if (live && mine && t.active <= 1)
+            if (live && t.parts <= 1 && (!DUAL || q == 0))
                 for (int d = 0; d < D; d += 8)
                     *reinterpret_cast<uint4*>(a.out + row * D + d) = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-        } else if (!idle && mine) {
+        } else if (!idle) {
             const uint32_t stage = smem0 + q * S::MAT + (warp & 3) * (S::MAT / 4);
+            const uint32_t o0_at = tmem + lanes + S::O_COL + (DUAL ? 0 : DP * q);
+            static_assert(!DUAL || PASSES == 2, "a pass per stretch's warps");
 #pragma unroll 1
-            for (int c = 0; c < PASSES; ++c) {
+            for (int c = DUAL ? q : 0; c < (DUAL ? q + 1 : PASSES); ++c) {
                 uint32_t v[CW];
                 __syncwarp();
 #pragma unroll
-                for (int z = 0; z < CW; z += 32) tmem_ld32(o_at + CW * c + z, v + z);
+                for (int z = 0; z < CW; z += 32) tmem_ld32(o0_at + CW * c + z, v + z);
                 tc_wait_ld();
+#pragma unroll
+                for (int k = 0; k < CW; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * gain0);
+                if (DUAL) {
+#pragma unroll
+                    for (int z = 0; z < CW; z += 32) {
+                        uint32_t w[32];
+                        tmem_ld32(o0_at + DP + CW * c + z, w);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[z + k] = __float_as_uint(fmaf(__uint_as_float(w[k]), gain1, __uint_as_float(v[z + k])));
+                    }
+                }
                 if (live && patch) {
                     // values that were left out, for the queries that see them
-#pragma unroll
-                    for (int k = 0; k < CW; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * inv);
-                    int from = first;
-                    if (open > first) from += (open - first) / TN * TN;
-                    for (int pos = from; pos < last; ++pos) {
+                    int from = t.begin;  // stretches start at multiples of TN
+                    if (open > t.begin) from += (open - t.begin) / TN * TN;
+                    for (int pos = from; pos < last_end; ++pos) {
                         if (!(sv::attn_visible(a, t, i, pos) & 1u)) continue;
                         if (!E4M3) {
 #pragma unroll
@@ -559,13 +601,13 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                             const int64_t at = page * a.c.page_stride + t.h * a.c.head_stride + r * a.c.row_stride;
                             const int64_t sc_at = ((int64_t)page * a.c.heads + t.h) * a.c.page_size + r;
                             const float vs = __ldg(a.c.v_scale + sc_at);
-                            const bool large = pos >= open && !sv::not_finite(vs) && fabsf(vs) > sh.limit[DUAL ? q : 0];
+                            const bool large = pos >= open && !sv::not_finite(vs) && fabsf(vs) > sh.limit[DUAL && pos >= mid ? 1 : 0];
                             float p = 0.0f;
                             if (large) {  // its probability, from the cache
                                 const uint16_t* qr = a.q + t.b * a.q_sb + i * a.q_st + (int64_t)(t.h * a.group + R - i * a.group) * a.q_sh;
                                 for (int d = 0; d < D; ++d)
                                     p += __uint_as_float((uint32_t)__ldg(qr + d) << 16) * sv::e4m3x2_to_f32(__ldg(a.c.k + at + d)).x;
-                                p = sv::ex2(p * (__ldg(a.c.k_scale + sc_at) * a.scale_log2) - mx + RAISE) * weight;
+                                p = sv::ex2(p * (__ldg(a.c.k_scale + sc_at) * a.scale_log2) - shift + RAISE) * inv;
                             }
 #pragma unroll
                             for (int k = 0; k < CW; ++k) {
@@ -577,14 +619,11 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                         }
                     }
                 }
-                const float by = patch ? 1.0f : inv;
 #pragma unroll
                 for (int k = 0; k < PC; ++k)
-                    sts16(stage + 16 * (PC * lane + (k ^ (lane & (PC - 1)))),
-                          make_uint4(__float_as_uint(__uint_as_float(v[4 * k]) * by), __float_as_uint(__uint_as_float(v[4 * k + 1]) * by),
-                                     __float_as_uint(__uint_as_float(v[4 * k + 2]) * by), __float_as_uint(__uint_as_float(v[4 * k + 3]) * by)));
+                    sts16(stage + 16 * (PC * lane + (k ^ (lane & (PC - 1)))), make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
                 __syncwarp();
-                if (t.active > 1) {
+                if (t.parts > 1) {
                     const int k = lane % PC, d = CW * c + 4 * k;
                     for (int x = 0; x < PC; ++x) {
                         const int r = (32 / PC) * x + lane / PC;
