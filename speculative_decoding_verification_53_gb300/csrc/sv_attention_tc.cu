@@ -582,7 +582,11 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     }
                 }
                 if (live && patch) {
-                    // values that were left out, for the queries that see them
+                    // Values that were left out, for the queries that see them: position by position, which
+                    // takes long where there are many.  A prompt's first 2048 queries take 0.7 ms instead
+                    // of 76 us where its first value row is zero (32 over 8 heads of 128; 8 over 8: 2.5 ms
+                    // instead of 67 us, as a tile then has 256 new tokens; the queries' scattered reads
+                    // bound it; element by element 1.7 and 6.6 ms).
                     int from = t.begin;  // stretches start at multiples of TN
                     if (open > t.begin) from += (open - t.begin) / TN * TN;
                     for (int pos = from; pos < last_end; ++pos) {
@@ -605,16 +609,31 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                             float p = 0.0f;
                             if (large) {  // its probability, from the cache
                                 const uint16_t* qr = a.q + t.b * a.q_sb + i * a.q_st + (int64_t)(t.h * a.group + R - i * a.group) * a.q_sh;
-                                for (int d = 0; d < D; ++d)
-                                    p += __uint_as_float((uint32_t)__ldg(qr + d) << 16) * sv::e4m3x2_to_f32(__ldg(a.c.k + at + d)).x;
+#pragma unroll 8
+                                for (int d = 0; d < D; d += 8) {
+                                    const uint4 x = sv::ld_nc_v4(qr + d);
+                                    const uint2 y = __ldg(reinterpret_cast<const uint2*>(a.c.k + at + d));
+                                    auto two = [&](uint32_t u, uint32_t w) {
+                                        const float2 f = sv::e4m3x2_to_f32(w);
+                                        p = fmaf(sv::bf16_hi(u), f.y, fmaf(sv::bf16_lo(u), f.x, p));
+                                    };
+                                    two(x.x, y.x & 0xffffu);
+                                    two(x.y, y.x >> 16);
+                                    two(x.z, y.y & 0xffffu);
+                                    two(x.w, y.y >> 16);
+                                }
                                 p = sv::ex2(p * (__ldg(a.c.k_scale + sc_at) * a.scale_log2) - shift + RAISE) * inv;
                             }
 #pragma unroll
-                            for (int k = 0; k < CW; ++k) {
+                            for (int k = 0; k < CW; k += 4) {
                                 if (CW * c + k >= D) break;
-                                const float w = sv::e4m3x2_to_f32(__ldg(a.c.v + at + CW * c + k)).x;
-                                if (large) v[k] = __float_as_uint(__uint_as_float(v[k]) + p * w * vs);
-                                else if (sv::not_finite(w * vs)) v[k] = __float_as_uint(__uint_as_float(v[k]) + w * vs);
+                                const uint32_t y = __ldg(reinterpret_cast<const uint32_t*>(a.c.v + at + CW * c + k));
+#pragma unroll
+                                for (int z = 0; z < 4; ++z) {
+                                    const float w = sv::e4m3x2_to_f32((y >> 8 * z) & 0xffu).x;
+                                    if (large) v[k + z] = __float_as_uint(__uint_as_float(v[k + z]) + p * w * vs);
+                                    else if (sv::not_finite(w * vs)) v[k + z] = __float_as_uint(__uint_as_float(v[k + z]) + w * vs);
+                                }
                             }
                         }
                     }

@@ -49,3 +49,27 @@ def test_hidden_tokens_move_no_bit(sv, shape, tree, cache):  # noqa: F811
     if cache == "e4m3":  # the last one 2^60 above: out of the sums of the tolerance
         ks[page, 0, row] = float("nan")
         check(clean, clean_l, q, k, v, ks, vs, table, base, new_len, mask, D ** -0.5, 5.0, 6.0, ~sees, top)
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("first", ["zero", "hole"])
+@pytest.mark.parametrize("shape", [(20, 4, 128, 16, 0), (150, 4, 64, 16, 0), (300, 1, 128, 64, 0), (61, 4, 128, 24, 0),
+                                   (40, 4, 256, 16, 0), (200, 4, 128, 16, 600), (30, 4, 64, 16, 700)])
+def test_no_value_scale_to_go_by(sv, shape, first, tree):  # noqa: F811
+    """Nothing that every query sees has a value of any size: a prompt (or a context of zeros and new
+    tokens) whose first values are zeros of the smallest scale, or lie in a hole.  All other new
+    tokens' values are then left to the end."""
+    import torch
+    Q, Hq, D, ps, ctx = shape
+    rng = np.random.default_rng([*shape, tree])
+    c = case(rng, 2, Q, Hq, 1, D, ps, ctx, "e4m3", tree, False, ragged=False)
+    q, k, v, ks, vs, table, base, new_len, mask = c
+    for b in range(2):
+        for pos in range(ctx + 1):
+            page, row = int(table[b, pos // ps]), pos % ps
+            vs[page, 0, row] = 2.0 ** -126
+            v[page, 0, row].view(torch.uint8).fill_(0)
+        if first == "hole":
+            table[b, :ctx // ps + 1] = -1
+    o, l = run(sv, c)
+    check(o, l, *c[:9], D ** -0.5, 5.0, 6.0)
