@@ -12,6 +12,8 @@
 // rows of tcgen05 (sv_attention_tc.cu, the kernel of longer chunks; make_plan chooses).
 // 64 contexts of 4096, one query of 32 over 8 heads of 128, one GB300: bf16 208 us
 // (5.2 TB/s), e4m3 201 us (2.8 TB/s; bound by the issue of the widening and the softmax).
+// Probabilities (e4m3: times the value's scale) are rounded to bf16, the values' type in the second
+// product; a second term for what that leaves would double it.
 // Filling the stages by the copy engine instead of cp.async: 258 against 213 us, not kept.
 //
 // e4m3 pages are copied as they are, and each warp widens its fragments to bf16 (exactly);
@@ -85,6 +87,7 @@ struct Shape {
     static constexpr int BUDGET = DP == 256 ? 160 * 1024 : 97 * 1024;
     static constexpr int FIT = BUDGET / STAGE;
     static constexpr int STAGES = FIT > 6 ? 6 : FIT < 3 ? 3 : FIT;
+    static_assert(E4M3 || DP <= 128, "wide heads of bf16 take the tcgen05 kernel");
     static constexpr int QBYTES = ROWS * DP * 2;
     static constexpr int SMEM = STAGES * STAGE + QBYTES;
     static_assert(STAGES + 1 <= RING, "a tile's offsets outlive its stage");
@@ -227,23 +230,11 @@ __global__ void __launch_bounds__(KW * 32, DP == 256 ? 1 : 2)
             for (int x = 0; x < TN * S::CH / S::THREADS; ++x) {
                 const int f = tid + x * S::THREADS;
                 uint4* p = reinterpret_cast<uint4*>(stage + S::MAT + v_piece<S::PITCH>(f / S::CH, f % S::CH));
-                const uint4 v = *p;
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                bool here = false;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (E4M3) {
-#pragma unroll
-                        for (int y = 0; y < 32; y += 8)
-                            if (((w[i] >> y) & 0x7fu) == 0x7fu) { w[i] &= ~(0xffu << y); here = true; }
-                    } else {
-#pragma unroll
-                        for (int y = 0; y < 32; y += 16)
-                            if (((w[i] >> y) & 0x7f80u) == 0x7f80u) { w[i] &= ~(0xffffu << y); here = true; }
-                    }
+                uint4 v = *p;
+                if (sv::sanitise<E4M3>(v)) {
+                    *p = v;
+                    bad = true;
                 }
-                if (here) *p = make_uint4(w[0], w[1], w[2], w[3]);
-                bad |= here;
             }
             if (E4M3 && tid >= TN && tid < 2 * TN) {
                 float* p = reinterpret_cast<float*>(stage + 2 * S::MAT) + tid;
@@ -273,11 +264,8 @@ __global__ void __launch_bounds__(KW * 32, DP == 256 ? 1 : 2)
             for (int k = 0; k < KS; ++k) {
                 uint32_t b[4];
                 ldsm4(ks0 + v_piece<S::PITCH>(kr, 2 * k + kc), b);
-                uint32_t qa[4];
-                if (!QREG) ldsm4(q0 + v_piece<2 * DP>(q_r, 2 * k + q_c), qa);
-                const uint32_t* q = QREG ? qf[QREG ? k : 0] : qa;
-                mma16816(s[0], q, b[0], b[1]);
-                mma16816(s[1], q, b[2], b[3]);
+                mma16816(s[0], qf[QREG ? k : 0], b[0], b[1]);
+                mma16816(s[1], qf[QREG ? k : 0], b[2], b[3]);
             }
         } else {
 #pragma unroll
@@ -578,16 +566,23 @@ Plan make_plan(int B, int Q, int Hq, int H, int D, bool e4m3, int max_len, int n
     Plan p{};
     if (max_len > sv::PAGED_MAX_POS) max_len = sv::PAGED_MAX_POS;
     const int64_t rows = (int64_t)Q * (Hq / H);
-    // Wide heads, 256 on one GB300, 32 over 8 heads, mma.sync against tcgen05: bf16, 16 contexts of
-    // 4096 with 1, 5 and 61 queries 178 and 166, 309 and 170, 1061 and 274 us, one of 8000 77 and 39,
-    // of 700 21 and 27; e4m3 174 and 252, 286 and 255, 1262 and 460, 77 and 48, 21 and 35.
+    // One GB300, 32 over 8 heads, mma.sync against tcgen05, us.  Wide heads (256), 4 and 16 rows:
+    //   bf16: 64 contexts of 4096 464 and 381, 746 and 384; one of 8000 79 and 46, 150 and 46; of 700 25 and
+    //     31, 49 and 31: tcgen05 throughout, though a short context of 4 rows gives away a fifth;
+    //   e4m3: 64 of 4096 450 and 798, 744 and 800; 16 of 4096 169 and 258, 271 and 261; one of 8000 81
+    //     and 58, 152 and 59; of 700 27 and 48, 51 and 49: mma.sync up to 16 rows, for the batches of 4
+    //     rows; one or two long contexts, and 16 rows of few, would be faster on tcgen05.
     if (D > 128) p.tile_rows = e4m3 && rows <= 16 ? 16 : 128;
     else if (rows > 128) p.tile_rows = 256;
-    // Sixteen rows or fewer waste most of a 128-row product.  On one GB300, 32 over 8 heads of
-    // 128, one query: 64 contexts of 4096 208 us (mma.sync) against 243 (tcgen05), e4m3 201
-    // against 304; one context of 2000 16.5 against 20.7, of 8000 33.5 against 24.7 (e4m3 35
-    // against 29), of 131072 127 against 102 (e4m3 118 against 127).  17 rows and more: 64 x
-    // 300 x 24 rows 105 against 49 us.
+    // Sixteen rows or fewer waste most of a 128-row product, and e4m3 its widening besides; a few long
+    // contexts leave the mma.sync kernel's copies too little in flight.  Heads of 128, 4 rows:
+    //   bf16: 64 contexts of 4096 206 and 204, 16 of 4096 83 and 86, 8 of 32768 224 and 196, 8 of 8000 79
+    //     and 85, 4 of 8000 49 and 61; one of 2000 19 and 23, of 8000 38 and 29, of 131072 128 and 113:
+    //     tcgen05 for long contexts of no more cache heads than SMs (two to eight contexts lose up to
+    //     a quarter or win up to an eighth by it, one wins a tenth to a quarter, with 16 rows more);
+    //   e4m3: 64 of 4096 190 and 292; one of 2000 20 and 29, of 8000 39 and 31, of 32768 54 and 54, of
+    //     131072 117 and 129: mma.sync, which loses a fifth at one context of about 8000 only.
+    // 17 rows and more: 64 x 300 x 24 rows 105 and 49.
     else if (rows > 16 || (!e4m3 && max_len >= 4096 && (int64_t)B * H <= num_sms)) p.tile_rows = 128;
     else p.tile_rows = 16;
     p.m_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);

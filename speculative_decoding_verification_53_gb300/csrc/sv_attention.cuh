@@ -240,8 +240,9 @@ inline int page_box_rows(const PagedCache& c, int tile) {
     return c.page_size >= 8 && tile % c.page_size == 0 ? c.page_size : 0;
 }
 
-// The kernel for many query rows per cache head, head_dim <= 128 (sv_attention_tc.cu):
-// tile_rows 128 or 256; dual (tile_rows 128): a CTA takes two splits.
+// The kernel for many query rows per cache head, or wide heads (sv_attention_tc.cu): tile_rows
+// 128 or 256, 128 for heads wider than 128; dual (tile_rows 128, heads of up to 128): a CTA
+// takes two splits.
 cudaError_t launch_attn_tc(const AttnArgs& a, int pairs, bool e4m3, int tile_rows, bool dual, unsigned ctas,
                            cudaStream_t stream);
 
