@@ -53,10 +53,11 @@
 // codes then go from the cache through registers.  16 trees of 61 over 4096, 32 over 8 heads of 256,
 // bf16: 274 us (480 TFLOP/s), e4m3 460 us.
 //
-// Measured on one GB300, 32 over 8 heads of 128: 2 x 2048 queries over 6001 positions, bf16, 341 us
-// (1380 TFLOP/s; the exponentials, 32 per SM and clock, take half as long as the products); 16 trees of 61 over 2048 to 8192,
-// e4m3, 147 us (560 TFLOP/s; a tile takes 5700 cycles, 2048 of them products, the rest widening and
-// softmax); 8 chains of 6 over 3277 to 32768, bf16, 135 us (5.0 TB/s).
+// Measured on one GB300, 32 over 8 heads of 128: 2 x 2048 queries over 6001 positions, bf16, 347-359 us
+// (1310-1360 TFLOP/s, tensor pipe 53 %; the exponentials, 32 per SM and clock, take half as long as
+// the products); 16 trees of 61 over 2048 to 8192, e4m3, 149-153 us (550 TFLOP/s; a tile takes 5700
+// cycles, 2048 of them products, the rest widening and softmax); 8 chains of 6 over 3277 to 32768,
+// bf16, 132 us (5.1 TB/s).
 //
 // Every wait is bounded.  A role whose wait runs out stops, so that the others' waits run out too;
 // the softmax's warps then write NaN for their rows, which a verify reports as invalid data, and
@@ -228,8 +229,8 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
 
 // Eight e4m3 codes in fp16, or times 2^-9 and a scale if asked (x: twice its fp16, y: twice what that
 // leaves).  The 2^-9 is exact (codes are multiples of 2^-9, below 2^9) and keeps the scale 2^9
-// further from fp16's subnormal numbers, where it would lose bits; it costs 16 trees of 61 over 2048
-// to 8192 152 -> 157 us (for the tiles that need it alone, by a branch, 163).
+// further from fp16's subnormal numbers, where it would lose bits; by a branch
+// for the tiles that need it alone 16 trees of 61 over 2048 to 8192 took 163 instead of 157 us.
 template <bool SCALE>
 __device__ __forceinline__ uint4 widen8(uint2 w, uint2 scale) {
     uint32_t out[4];
