@@ -394,6 +394,7 @@ __global__ void __launch_bounds__(KW * 32, DP == 256 ? 1 : 2)
     }
     __syncthreads();
     float inv[2], lse2[2];
+    bool none[2];  // no weight at all: zero, whatever the values hold
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
         const int r = g + 8 * y;
@@ -407,6 +408,7 @@ __global__ void __launch_bounds__(KW * 32, DP == 256 ? 1 : 2)
         const float fac = sv::ex2(mx[y] - shift);
         inv[y] = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // NaN stays
         lse2[y] = sum == 0.0f ? neg_inf() : shift + log2f(sum);
+        none[y] = sum == 0.0f && t.parts <= 1;
 #pragma unroll
         for (int n = 0; n < DP / 8; ++n) {
             o[n][2 * y] *= fac;
@@ -465,11 +467,11 @@ __global__ void __launch_bounds__(KW * 32, DP == 256 ? 1 : 2)
                 v[2] = o[2 * n][2 * y + 1]; v[3] = o[2 * n + 1][2 * y + 1];
             }
 #pragma unroll
-            for (int x = 0; x < 4; ++x) v[x] *= inv[y];
+            for (int x = 0; x < 4; ++x) v[x] = none[y] ? 0.0f : v[x] * inv[y];
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
                 if (d[z] >= D) continue;
-                if (s_bad) {
+                if (s_bad && !none[y]) {
                     const int from = t.begin + (t.base > t.begin ? (t.base - t.begin) / TN * TN : 0);
                     for (int pos = from; pos < t.end; ++pos) {
                         if (!(sv::attn_visible(a, t, R / a.group, pos) & 1u)) continue;
@@ -532,6 +534,7 @@ __global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_
             acc.z += w * v.z;
             acc.w += w * v.w;
         }
+        if (sum == 0.0f) acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // no weight at all, whatever the values hold
         *reinterpret_cast<uint2*>(a.out + row * D + d) =
             make_uint2(sv::bf16x2(acc.x, acc.y), sv::bf16x2(acc.z, acc.w));
     }

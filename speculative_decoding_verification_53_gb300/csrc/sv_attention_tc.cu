@@ -555,6 +555,8 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             else if (a.lse) a.lse[row] = lse2 * 0.69314718055994531f;
         }
         const bool patch = sh.bad != 0;
+        // no weight at all: zero, whatever the values hold
+        const uint32_t keep = l == 0.0f && t.parts <= 1 ? 0u : 0xffffffffu;
         // Rows leave through shared memory (where this row tile's queries were), so that a store
         // covers whole rows: a lane writing its own row touched 32 lines per store and cost
         // 15000 cycles a CTA.  Part of a row at a time, 16-byte pieces swizzled by the row.
@@ -586,7 +588,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                         for (int k = 0; k < 32; ++k) v[z + k] = __float_as_uint(fmaf(__uint_as_float(w[k]), gain1, __uint_as_float(v[z + k])));
                     }
                 }
-                if (live && patch) {
+                if (keep && live && patch) {
                     // Values that were left out, for the queries that see them: position by position, which
                     // takes long where there are many.  A prompt's first 2048 queries take 0.7 ms instead
                     // of 76 us where its first value row is zero (32 over 8 heads of 128; 8 over 8: 2.5 ms
@@ -645,7 +647,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 }
 #pragma unroll
                 for (int k = 0; k < PC; ++k)
-                    sts16(stage + 16 * (PC * lane + (k ^ (lane & (PC - 1)))), make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+                    sts16(stage + 16 * (PC * lane + (k ^ (lane & (PC - 1)))), make_uint4(v[4 * k] & keep, v[4 * k + 1] & keep, v[4 * k + 2] & keep, v[4 * k + 3] & keep));
                 __syncwarp();
                 if (t.parts > 1) {
                     const int k = lane % PC, d = CW * c + 4 * k;

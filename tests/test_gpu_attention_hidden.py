@@ -73,3 +73,20 @@ def test_no_value_scale_to_go_by(sv, shape, first, tree):  # noqa: F811
             table[b, :ctx // ps + 1] = -1
     o, l = run(sv, c)
     check(o, l, *c[:9], D ** -0.5, 5.0, 6.0)
+
+
+@pytest.mark.parametrize("workspace", ["auto", None])
+@pytest.mark.parametrize("Q,ctx", [(1, 40), (3, 1500), (20, 300), (30, 1500), (61, 2500), (61, 0)])
+def test_scores_of_minus_infinity_alone_give_zero(sv, Q, ctx, workspace):  # noqa: F811
+    """Every key holds -inf: no position has any weight, whatever the values hold."""
+    import torch
+    rng = np.random.default_rng([Q, ctx])
+    c = case(rng, 1, Q, 4, 1, 128, 16, ctx, "bf16", Q == 61, False, ragged=False)
+    q, k, v, ks, vs, table, base, new_len, mask = c
+    q.abs_().clamp_(min=0.1)
+    k[..., 7].masked_fill_(~k[..., 7].isnan(), float("-inf"))
+    for pos in (ctx // 2, ctx, ctx + Q // 2):
+        v[int(table[0, pos // 16]), 0, pos % 16, 3:9] = float("nan")
+        v[int(table[0, pos // 16]), 0, pos % 16, 9:12] = float("inf")
+    o, l = run(sv, c, workspace=workspace)
+    assert (o == 0).all() and torch.isneginf(l).all()
