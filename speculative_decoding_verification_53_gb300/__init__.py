@@ -23,13 +23,16 @@ SV_F32, SV_BF16 = 0, 1
 SV_DRAFT_PROBS, SV_DRAFT_LOGITS = 0, 1
 SV_SIBLINGS_WITHOUT_REPLACEMENT, SV_SIBLINGS_IID = 0, 1
 SV_CACHE_BF16, SV_CACHE_E4M3 = 0, 1
+SV_SUMMARY_MEAN, SV_SUMMARY_BOUNDS = 0, 1
 
 EXPORTS = ("spec_verify_workspace_size", "spec_verify_chain", "spec_greedy_accept", "spec_verify_tree",
            "spec_verify_status_string", "spec_verify_last_cuda_error", "spec_verify_chain_noalloc",
            "spec_tree_mask", "spec_kv_compact", "spec_verify_tree_rule", "spec_sample_and_verify",
            "spec_verify_count_invalid", "spec_verify_rows_status", "spec_verify_chain_host",
            "spec_verify_host_sizes", "spec_kv_append", "spec_kv_read", "spec_kv_compact_paged",
-           "spec_paged_attention", "spec_paged_attention_workspace_size", "spec_adjust_logits")
+           "spec_paged_attention", "spec_paged_attention_workspace_size", "spec_adjust_logits",
+           "spec_page_resize", "spec_rotary", "spec_rotary_append", "spec_block_summary", "spec_block_select",
+           "spec_block_select_workspace_size", "spec_sparse_attention", "spec_sparse_attention_workspace_size")
 
 # out_count value of a batch row whose kernel gave up a bounded device-side wait
 COUNT_TIMEOUT = -1
@@ -44,6 +47,12 @@ class PagedCache(ctypes.Structure):
                 ("head_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("dtype", ctypes.c_int),
                 ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int),
                 ("num_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class Rotary(ctypes.Structure):
+    """sv_rotary of include/spec_rotary.h."""
+    _fields_ = [("freq", ctypes.c_void_p), ("tree_depth", ctypes.c_void_p), ("amplitude", ctypes.c_float),
+                ("num_freq", ctypes.c_int), ("interleaved", ctypes.c_int), ("inverse", ctypes.c_int)]
 
 
 class SpecVerifyError(RuntimeError):
@@ -110,6 +119,24 @@ def lib() -> ctypes.CDLL:
     L.spec_paged_attention_workspace_size.restype = sz
     L.spec_adjust_logits.argtypes = [vp, ci, vp, vp, vp, ci, vp, vp, vp, vp, vp, vp, vp, ci, vp, ci, ci, ci, vp, vp]
     L.spec_adjust_logits.restype = ci
+    L.spec_page_resize.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, vp, vp, vp, ci, ci, vp]
+    L.spec_page_resize.restype = ci
+    rot = ctypes.POINTER(Rotary)
+    L.spec_rotary.argtypes = [vp, vp, ci, vp, vp, ci, ci, rot, vp, vp, ci, ci, ci, vp, vp, vp, vp, vp]
+    L.spec_rotary.restype = ci
+    L.spec_rotary_append.argtypes = [vp, vp, ci, vp, vp, vp, ci, rot, pc, vp, vp, ci, ci, vp, vp, vp]
+    L.spec_rotary_append.restype = ci
+    L.spec_block_summary.argtypes = [pc, vp, vp, ci, ci, ci, vp, vp]
+    L.spec_block_summary.restype = ci
+    L.spec_block_select.argtypes = [vp, vp, ci, vp, ci, vp, ci, ci, ci, ci, ci, vp, vp, ci, ci, ci, ci, ci, ci, vp, vp, sz,
+                                    vp]
+    L.spec_block_select.restype = ci
+    L.spec_block_select_workspace_size.argtypes = [ci, ci, ci, ci, ci, ci]
+    L.spec_block_select_workspace_size.restype = sz
+    L.spec_sparse_attention.argtypes = [vp, vp, ci, pc, vp, vp, vp, vp, ci, ci, ctypes.c_float, ci, ci, vp, vp, vp, sz, vp]
+    L.spec_sparse_attention.restype = ci
+    L.spec_sparse_attention_workspace_size.argtypes = [ci, ci, ci, ci, ci, ci, ci, ci, ci]
+    L.spec_sparse_attention_workspace_size.restype = sz
     _lib = L
     return L
 
@@ -826,3 +853,343 @@ def spec_adjust_logits(logits, *, history=None, history_len=None, prompt_len=Non
             _adr(presence), _adr(frequency), _adr(bias_tokens), _adr(bias_values), M, _adr(allowed), B, R, V,
             _adr(out), handle)
     return out
+
+
+# ------------------------------------------------------- long contexts on a paged cache
+
+def spec_page_resize(page_table, pages, length, free_pages, free_count, page_size: int, *, base=None, num_tokens=None,
+                     out_slots=None, out_ok=None, stream=None):
+    """Bring every row of a page table to the pages that its length needs, in place, by a
+    stack of free pages.  page_table int32 [B][max_pages]; pages int32 [B], the pages that
+    each row holds; length int32 [B], the positions that it is to hold; free_pages int32
+    [num_pages], of which the first free_count (int32 [1]) are the stack.  Rows that shrink
+    give back what they hold too much, then rows that grow take from the top, in row order.
+    With base int32 [B], also the slots int64 [B][num_tokens] of positions base + i:
+    page * page_size + position % page_size, -1 where the row does not hold the position.
+    Returns (ok int32 [B], slots or None); a row whose ok is 0 found too few free pages (or had a
+    bad length) and stays as it was.  Lengths stay on the device: nothing is waited for."""
+    torch = _torch()
+    at, handle, side = _one_device(page_table, stream, page_table=page_table, pages=pages, length=length,
+                                   free_pages=free_pages, free_count=free_count, base=base, out_slots=out_slots,
+                                   out_ok=out_ok)
+    i32 = torch.int32
+    shape = page_table.shape
+    if len(shape) != 2 or free_pages.dim() != 1:
+        raise ValueError("page_table must be [B][max_pages], free_pages [num_pages]")
+    B, mp = shape
+    _shaped("page_table", page_table, shape, i32)
+    _shaped("pages", pages, (B,), i32)
+    _shaped("length", length, (B,), i32)
+    _shaped("free_pages", free_pages, free_pages.shape, i32)
+    _shaped("free_count", free_count, (1,), i32)
+    _shaped("base", base, (B,), i32)
+    _shaped("out_ok", out_ok, (B,), i32)
+    N = 0
+    if base is not None:
+        if out_slots is not None and num_tokens is None:
+            num_tokens = out_slots.shape[1] if out_slots.dim() == 2 else 0
+        if num_tokens is None or num_tokens < 0:
+            raise ValueError("base needs num_tokens or out_slots [B][num_tokens]")
+        N = int(num_tokens)
+        _shaped("out_slots", out_slots, (B, N), torch.int64)
+        if out_slots is None:
+            out_slots = _new(torch.empty, (B, N), torch.int64, at, side)
+    elif out_slots is not None or num_tokens is not None:
+        raise ValueError("out_slots and num_tokens belong to a base")
+    if out_ok is None:
+        out_ok = _new(torch.empty, (B,), i32, at, side)
+    slots = out_slots if N else None
+    _launch("spec_page_resize", at, lib().spec_page_resize, _adr(page_table), _adr(pages), _adr(length),
+            _adr(free_pages), _adr(free_count), free_pages.shape[0], page_size, mp, _adr(base) if N else None, _adr(slots),
+            _adr(out_ok), B, N, handle)
+    return out_ok, out_slots
+
+
+def rotary_frequencies(dim: int, theta: float = 10000.0, *, scaling=None, factor: float = 1.0, original_len: int = 8192,
+                       low: float = 1.0, high: float = 32.0, device=None):
+    """Radians per position, float64 [dim / 2], of the pairs of a head's first `dim` elements:
+    theta ** (-2 j / dim), for contexts `factor` times the trained length original_len with
+      "linear"  every frequency divided by factor;
+      "base"    theta raised by factor ** (dim / (dim - 2)), so that the slowest pair goes
+                factor times slower and the fastest as before;
+      "parts"   pairs that turn fewer than `low` times within original_len divided by factor,
+                those that turn more than `high` times kept, a straight line between."""
+    import math
+    torch = _torch()
+    if dim < 2 or dim % 2:
+        raise ValueError("dim must be even and positive")
+    if not (theta > 0 and factor > 0 and original_len > 0 and high > low):
+        raise ValueError("theta, factor and original_len must be positive, high above low")
+    if scaling == "base":
+        if dim == 2:
+            raise ValueError("a single pair has no base to raise")
+        theta = theta * factor ** (dim / (dim - 2))
+    f = theta ** (-torch.arange(0, dim, 2, dtype=torch.float64) / dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        keep = ((original_len * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+    elif scaling not in (None, "base"):
+        raise ValueError("scaling must be None, 'linear', 'base' or 'parts'")
+    return f if device is None else f.to(device)
+
+
+def _rotary(freq, tree_depth, amplitude, interleaved, inverse, B, N, D):
+    """The sv_rotary of tensors (checked)."""
+    torch = _torch()
+    R = freq.shape[0] if freq.dim() == 1 else -1
+    if R < 0 or 2 * R > D:
+        raise ValueError(f"freq must be [n] with 2 n <= head_dim {D}, got {tuple(freq.shape)}")
+    _shaped("freq", freq, (R,), torch.float64)
+    _shaped("tree_depth", tree_depth, (B, max(N - 1, 0)), torch.int32)
+    return Rotary(freq.data_ptr(), _adr(tree_depth), amplitude, R, int(bool(interleaved)), int(bool(inverse)))
+
+
+def _turned_out(name, out, x, at, side):
+    """A new output for x, or the given one (x itself, or of its shape and type)."""
+    if out is None:
+        return _new(_torch().empty, x.shape, x.dtype, at, side)
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError(f"{name} must have the shape and type of its input")
+    return out
+
+
+def spec_rotary(q, freq, base, *, key=None, tree_depth=None, new_len=None, interleaved: bool = False,
+                inverse: bool = False, amplitude: float = 1.0, out=None, out_key=None, stream=None):
+    """Turn pairs of elements of queries (and keys) by their tokens' positions.  q
+    [B][N][heads][head_dim] and key (fp32/bf16, any strides with contiguous elements); freq
+    float64 [R] (rotary_frequencies): pairs (j, j + R) of a head's first 2 R elements, or
+    (2 j, 2 j + 1) where interleaved, by position * freq[j], times amplitude; the other way where
+    inverse.  Token i has position base[b] + i (base int32 [B]); with tree_depth int32 [B][N-1]
+    (spec_tree_mask) token 0 is the root and token i + 1 at base[b] + tree_depth[b][i].  new_len
+    int32 [B]: tokens behind it are not written.  out may be q itself, out_key key itself.
+    Returns (out, out_key or None)."""
+    torch = _torch()
+    at, handle, side = _one_device(q, stream, q=q, freq=freq, base=base, key=key, tree_depth=tree_depth,
+                                   new_len=new_len, out=out, out_key=out_key)
+    if q.dim() != 4 or (key is not None and (key.dim() != 4 or key.shape[:2] != q.shape[:2] or key.shape[3] != q.shape[3]
+                                             or key.dtype != q.dtype)):
+        raise ValueError("q and key must be [B][N][heads][head_dim] of one type, with the same tokens and head_dim")
+    if key is None and out_key is not None:
+        raise ValueError("out_key belongs to a key")
+    B, N, Hq, D = q.shape
+    code = _src_code(q.dtype, "q")
+    _shaped("base", base, (B,), torch.int32)
+    _shaped("new_len", new_len, (B,), torch.int32)
+    rot = _rotary(freq, tree_depth, amplitude, interleaved, inverse, B, N, D)
+    out = _turned_out("out", out, q, at, side)
+    if key is None:
+        _launch("spec_rotary", at, lib().spec_rotary, _adr(q), _strides3(q, "q"), Hq, None, None, 0, code, rot, _adr(base),
+                _adr(new_len), B, N, D, _adr(out), _strides3(out, "out"), None, None, handle)
+        return out, None
+    out_key = _turned_out("out_key", out_key, key, at, side)
+    _launch("spec_rotary", at, lib().spec_rotary, _adr(q), _strides3(q, "q"), Hq, _adr(key), _strides3(key, "key"),
+            key.shape[2], code, rot, _adr(base), _adr(new_len), B, N, D, _adr(out), _strides3(out, "out"), _adr(out_key),
+            _strides3(out_key, "out_key"), handle)
+    return out, out_key
+
+
+def spec_rotary_append(q, key, value, freq, k_pages, v_pages, page_table, base, *, tree_depth=None, new_len=None,
+                       k_scale=None, v_scale=None, interleaved: bool = False, amplitude: float = 1.0, out=None,
+                       stream=None):
+    """spec_rotary of queries and keys with the keys and values written into a paged cache in
+    the same pass (spec_kv_append): the cache row of token i is base[b] + i, its position as
+    spec_rotary.  q [B][N][q_heads][head_dim] (or None), key and value [B][N][heads][head_dim] of
+    q's type and one stride; the other arguments as spec_kv_append and spec_rotary.  Returns the
+    turned queries (out, or a new tensor; out may be q itself)."""
+    torch = _torch()
+    at, handle, side = _one_device(key, stream, key=key, value=value, q=q, freq=freq, k_pages=k_pages, v_pages=v_pages,
+                                   page_table=page_table, base=base, tree_depth=tree_depth, new_len=new_len,
+                                   k_scale=k_scale, v_scale=v_scale, out=out)
+    if key.dim() != 4 or key.shape != value.shape or key.dtype != value.dtype or key.stride() != value.stride():
+        raise ValueError("key and value must be [B][N][heads][head_dim] of one shape, stride and dtype")
+    B, N, H, D = key.shape
+    cache = _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, B)
+    if (cache.num_heads, cache.head_dim) != (H, D):
+        raise ValueError(f"key has {H} heads of {D}, the cache {cache.num_heads} of {cache.head_dim}")
+    code = _src_code(key.dtype, "key")
+    _shaped("base", base, (B,), torch.int32)
+    _shaped("new_len", new_len, (B,), torch.int32)
+    rot = _rotary(freq, tree_depth, amplitude, interleaved, False, B, N, D)
+    if q is None:
+        if out is not None:
+            raise ValueError("out belongs to q")
+        _launch("spec_rotary_append", at, lib().spec_rotary_append, None, None, 0, _adr(key), _adr(value),
+                _strides3(key, "key"), code, rot, cache, _adr(base), _adr(new_len), B, N, None, None, handle)
+        return None
+    if q.dim() != 4 or q.shape[:2] != key.shape[:2] or q.shape[3] != D or q.dtype != key.dtype:
+        raise ValueError("q must be [B][N][q_heads][head_dim] of the keys' type and tokens")
+    out = _turned_out("out", out, q, at, side)
+    _launch("spec_rotary_append", at, lib().spec_rotary_append, _adr(q), _strides3(q, "q"), q.shape[2], _adr(key),
+            _adr(value), _strides3(key, "key"), code, rot, cache, _adr(base), _adr(new_len), B, N, _adr(out),
+            _strides3(out, "out"), handle)
+    return out
+
+
+def _summary_kind(kind) -> int:
+    if kind == "mean":
+        return SV_SUMMARY_MEAN
+    if kind == "bounds":
+        return SV_SUMMARY_BOUNDS
+    raise ValueError(f"kind must be 'mean' or 'bounds', got {kind!r}")
+
+
+def spec_block_summary(k_pages, page_table, base, num_tokens: int, *, kind: str = "mean", new_len=None, k_scale=None,
+                       summary=None, stream=None):
+    """Summaries of the keys of every block (page) that holds one of the positions base[b] ..
+    base[b] + new_len[b] - 1 (new_len None: num_tokens for every row), over the block's positions
+    below base[b] + new_len[b], read from the cache: after spec_kv_append, spec_rotary_append or
+    spec_kv_compact_paged.  kind "mean": the mean of each element; "bounds": the largest values,
+    then the smallest.  k_pages, k_scale, page_table, base, new_len as spec_kv_append.  summary
+    bf16 [pages][heads][head_dim, or 2 head_dim for bounds], written in place (a new one, zeros
+    elsewhere, unless given).  Returns summary."""
+    torch = _torch()
+    at, handle, side = _one_device(k_pages, stream, k_pages=k_pages, page_table=page_table, base=base, new_len=new_len,
+                                   k_scale=k_scale, summary=summary)
+    code = _summary_kind(kind)
+    B, N = page_table.shape[0], int(num_tokens)
+    cache = _paged_cache(k_pages, k_pages, page_table, k_scale, k_scale, B)
+    shape = (cache.num_pages, cache.num_heads, cache.head_dim * (1 + code))
+    if N < 0:
+        raise ValueError("num_tokens must not be negative")
+    _shaped("base", base, (B,), torch.int32)
+    _shaped("new_len", new_len, (B,), torch.int32)
+    _shaped("summary", summary, shape, torch.bfloat16)
+    if summary is None:
+        summary = _new(torch.zeros, shape, torch.bfloat16, at, side)
+    _launch("spec_block_summary", at, lib().spec_block_summary, cache, _adr(base), _adr(new_len), code, B, N,
+            _adr(summary), handle)
+    return summary
+
+
+def spec_block_select_workspace_size(B: int, Q: int, num_q_heads: int, num_heads: int, max_pages: int,
+                                     shared: bool) -> int:
+    """Bytes of scratch of such a spec_block_select."""
+    return int(lib().spec_block_select_workspace_size(B, Q, num_q_heads, num_heads, max_pages, int(bool(shared))))
+
+
+def spec_block_select(q, summary, page_table, base, page_size: int, top_k: int, *, kind: str = "mean", sink: int = 1,
+                      recent: int = 1, shared: bool = False, new_len=None, out=None, workspace="auto", stream=None):
+    """The top_k blocks of the context (the base[b] // page_size whole blocks before the chunk)
+    that each query attends to: the first `sink`, the last `recent`, and those with the largest
+    scores, q . mean or, for bounds, the largest product any key within them could have with q;
+    the largest over the heads that share a cache head and, where shared, over the row's queries.
+    q bf16 [B][Q][q_heads][head_dim] as spec_paged_attention; summary bf16 [pages][heads][head_dim
+    or 2 head_dim] from spec_block_summary; page_table, base, new_len as spec_paged_attention.
+    Scores are compared as sums in 64 bits, equal ones go to the lower block.  Returns int32
+    [B][Q (1 where shared)][heads][top_k], ascending, -1 behind the last."""
+    torch = _torch()
+    auto = isinstance(workspace, str)
+    at, handle, side = _one_device(q, stream, q=q, summary=summary, page_table=page_table, base=base, new_len=new_len,
+                                   out=out, workspace=None if auto else workspace)
+    if q.dim() != 4 or q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16 [B][Q][q_heads][head_dim]")
+    B, Q, Hq, D = q.shape
+    if Q < 1:
+        raise ValueError("q holds no query")
+    code = _summary_kind(kind)
+    if summary.dim() != 3 or summary.shape[2] != D * (1 + code):
+        raise ValueError(f"summary must be [pages][heads][{D * (1 + code)}] for kind {kind!r}, got {tuple(summary.shape)}")
+    P, H, _ = summary.shape
+    _shaped("summary", summary, summary.shape, torch.bfloat16)
+    if not H or Hq % H:
+        raise ValueError(f"q has {Hq} heads, the summary {H}")
+    table = page_table.shape
+    if len(table) != 2 or table[0] != B:
+        raise ValueError(f"page_table must be [{B}][max_pages], got {tuple(table)}")
+    _shaped("page_table", page_table, table, torch.int32)
+    _shaped("base", base, (B,), torch.int32)
+    _shaped("new_len", new_len, (B,), torch.int32)
+    shape = (B, 1 if shared else Q, H, top_k)
+    _shaped("out", out, shape, torch.int32)
+    if out is None:
+        out = _new(torch.empty, shape, torch.int32, at, side)
+    if auto:
+        need = lib().spec_block_select_workspace_size(B, Q, Hq, H, table[1], int(bool(shared)))
+        workspace = _new(torch.empty, (need,), torch.uint8, at, side) if need else None
+    elif workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _launch("spec_block_select", at, lib().spec_block_select, _adr(q), _strides3(q, "q"), Hq, _adr(summary), code,
+            _adr(page_table), P, page_size, table[1], H, D, _adr(base), _adr(new_len), int(bool(shared)), top_k, sink,
+            recent, B, Q, _adr(out), _adr(workspace), ws_bytes, handle)
+    return out
+
+
+def spec_sparse_attention_workspace_size(B: int, Q: int, num_q_heads: int, num_heads: int, head_dim: int, cache_dtype,
+                                         page_size: int, num_blocks: int, shared: bool) -> int:
+    """Bytes of scratch of such a spec_sparse_attention on the current device; cache_dtype is the
+    pages' torch dtype."""
+    torch = _torch()
+    if cache_dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError(f"pages must be bfloat16 or float8_e4m3fn, got {cache_dtype}")
+    code = SV_CACHE_BF16 if cache_dtype == torch.bfloat16 else SV_CACHE_E4M3
+    return int(lib().spec_sparse_attention_workspace_size(B, Q, num_q_heads, num_heads, head_dim, code, page_size,
+                                                          num_blocks, int(bool(shared))))
+
+
+_sparse_needs = {}
+
+
+def _sparse_need(at, *sizes):
+    """spec_sparse_attention_workspace_size(*sizes) on a device, remembered by the sizes."""
+    key = (at, *sizes)
+    need = _sparse_needs.get(key)
+    if need is None:
+        with _torch().cuda.device(at):
+            need = int(lib().spec_sparse_attention_workspace_size(*sizes))
+        if len(_sparse_needs) >= 4096:
+            _sparse_needs.clear()
+        _sparse_needs[key] = need
+    return need
+
+
+def spec_sparse_attention(q, k_pages, v_pages, page_table, base, blocks, *, new_len=None, tree_mask=None, scale=None,
+                          k_scale=None, v_scale=None, out=None, out_lse=None, want_lse: bool = False, workspace="auto",
+                          stream=None):
+    """spec_paged_attention over some blocks of the context: blocks int32 [B][Q][heads][n], a list
+    per query and cache head, or [B][1][heads][n], one that the row's queries share
+    (spec_block_select).  A query sees the positions of its listed blocks (ascending; entries that are
+    negative, not below base // page_size, or not above the last one taken are passed over) and
+    those from the block of position base on, under the chain's or the tree's mask.  Other
+    arguments and results as spec_paged_attention; workspace: "auto" or a uint8 CUDA tensor."""
+    torch = _torch()
+    auto = isinstance(workspace, str)
+    at, handle, side = _one_device(q, stream, q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, base=base,
+                                   blocks=blocks, new_len=new_len, tree_mask=tree_mask, k_scale=k_scale, v_scale=v_scale,
+                                   out=out, out_lse=out_lse, workspace=None if auto else workspace)
+    if q.dim() != 4 or q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16 [B][Q][q_heads][head_dim]")
+    B, Q, Hq, D = q.shape
+    cache = _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, B)
+    H = cache.num_heads
+    if cache.head_dim != D or Hq % H:
+        raise ValueError(f"q has {Hq} heads of {D}, the cache {H} of {cache.head_dim}")
+    if Q < 1:
+        raise ValueError("q holds no query")
+    _shaped("base", base, (B,), torch.int32)
+    _shaped("new_len", new_len, (B,), torch.int32)
+    if blocks.dim() != 4 or blocks.shape[:3] not in ((B, Q, H), (B, 1, H)):
+        raise ValueError(f"blocks must be [{B}][{Q} or 1][{H}][n], got {tuple(blocks.shape)}")
+    _shaped("blocks", blocks, blocks.shape, torch.int32)
+    shared, n = int(blocks.shape[1] != Q or Q == 1), blocks.shape[3]
+    _shaped("tree_mask", tree_mask, (B, Q - 1, (Q + 30) // 32), torch.int32)
+    _shaped("out", out, (B, Q, Hq, D), torch.bfloat16)
+    _shaped("out_lse", out_lse, (B, Q, Hq), torch.float32)
+    if scale is None:
+        scale = D ** -0.5
+    if out is None:
+        out = _new(torch.empty, (B, Q, Hq, D), torch.bfloat16, at, side)
+    if out_lse is None and want_lse:
+        out_lse = _new(torch.empty, (B, Q, Hq), torch.float32, at, side)
+    if auto:
+        need = _sparse_need(at, B, Q, Hq, H, D, cache.dtype, cache.page_size, n, shared) if B else 0
+        workspace = _new(torch.empty, (need,), torch.uint8, at, side) if need else None
+    elif workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _launch("spec_sparse_attention", at, lib().spec_sparse_attention, _adr(q), _strides3(q, "q"), Hq, cache, _adr(base),
+            _adr(new_len), _adr(tree_mask), _adr(blocks), n, shared, scale, B, Q, _adr(out), _adr(out_lse),
+            _adr(workspace), ws_bytes, handle)
+    return out, out_lse

@@ -27,6 +27,7 @@
 #include <cstdlib>
 
 #include "spec_paged_kv.h"
+#include "spec_sparse.h"
 #include "sv_attention.cuh"
 
 namespace {
@@ -87,7 +88,6 @@ struct Shape {
     static constexpr int BUDGET = DP == 256 ? 160 * 1024 : 97 * 1024;
     static constexpr int FIT = BUDGET / STAGE;
     static constexpr int STAGES = FIT > 6 ? 6 : FIT < 3 ? 3 : FIT;
-    static_assert(E4M3 || DP <= 128, "wide heads of bf16 take the tcgen05 kernel");
     static constexpr int QBYTES = ROWS * DP * 2;
     static constexpr int SMEM = STAGES * STAGE + QBYTES;
     static_assert(STAGES + 1 <= RING, "a tile's offsets outlive its stage");
@@ -162,15 +162,15 @@ __global__ void __launch_bounds__(KW * 32, DP == 256 ? 1 : 2)
     for (int f = tid; f < (S::STAGES - 1) * TN; f += S::THREADS) {
         const int tile = f / TN, p = f % TN, pos = t.begin + f;
         int row = 0, page = -1;
-        if (pos < t.end) page = sv::paged_place(a.c, t.b, pos, row);
+        if (pos < t.end) page = sv::paged_place(a.c, t.row, pos, row);
         put_place(tile, p, row, page);
     }
     if (tid == 0) s_bad = 0;
     // the queries, zero behind the last real one
     for (int f = tid; f < S::ROWS * (DP / 8); f += S::THREADS) {
-        const int r = f / (DP / 8), c = f % (DP / 8), R = t.mt * S::ROWS + r;
+        const int r = f / (DP / 8), c = f % (DP / 8), R = t.r0 + r;
         uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (R < t.n * a.group && 8 * c < D)
+        if (R < t.r1 && 8 * c < D)
             w = sv::ld_nc_v4(a.q + t.b * a.q_sb + (int64_t)(R / a.group) * a.q_st +
                              (int64_t)(t.h * a.group + R % a.group) * a.q_sh + 8 * c);
         if (!E4M3) {
@@ -195,10 +195,10 @@ __global__ void __launch_bounds__(KW * 32, DP == 256 ? 1 : 2)
     int next_row = 0, next_page = -1;
     if (tid < TN) {
         const int pos = t.begin + (S::STAGES - 1) * TN + tid;
-        if (pos < t.end) next_page = sv::paged_place(a.c, t.b, pos, next_row);
+        if (pos < t.end) next_page = sv::paged_place(a.c, t.row, pos, next_row);
         put_place(S::STAGES - 1, tid, next_row, next_page);
         next_page = -1;
-        if (pos + TN < t.end) next_page = sv::paged_place(a.c, t.b, pos + TN, next_row);
+        if (pos + TN < t.end) next_page = sv::paged_place(a.c, t.row, pos + TN, next_row);
     }
 
     constexpr bool QREG = DP <= 128;
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(KW * 32, DP == 256 ? 1 : 2)
             put_place(j + S::STAGES, tid, next_row, next_page);
             const int pos = t.begin + (j + S::STAGES + 1) * TN + tid;
             next_page = -1;
-            if (pos < t.end) next_page = sv::paged_place(a.c, t.b, pos, next_row);
+            if (pos < t.end) next_page = sv::paged_place(a.c, t.row, pos, next_row);
         }
         const uint32_t valid = (s_valid[j % RING][wk >> 1] >> (16 * (wk & 1))) & 0xffffu;
         const uint32_t ks0 = smem_u32(stage), vs0 = ks0 + S::MAT;
@@ -262,10 +262,12 @@ __global__ void __launch_bounds__(KW * 32, DP == 256 ? 1 : 2)
             const int kr = wk * 16 + (lane >> 4) * 8 + (lane & 7), kc = (lane >> 3) & 1;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                uint32_t b[4];
+                uint32_t b[4], qa[4];
                 ldsm4(ks0 + v_piece<S::PITCH>(kr, 2 * k + kc), b);
-                mma16816(s[0], qf[QREG ? k : 0], b[0], b[1]);
-                mma16816(s[1], qf[QREG ? k : 0], b[2], b[3]);
+                if (!QREG) ldsm4(q0 + v_piece<2 * DP>(q_r, 2 * k + q_c), qa);
+                const uint32_t* q = QREG ? qf[QREG ? k : 0] : qa;
+                mma16816(s[0], q, b[0], b[1]);
+                mma16816(s[1], q, b[2], b[3]);
             }
         } else {
 #pragma unroll
@@ -306,8 +308,8 @@ __global__ void __launch_bounds__(KW * 32, DP == 256 ? 1 : 2)
         if (tail) {
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                const int R = t.mt * S::ROWS + g + 8 * y;
-                see[y] &= R < t.n * a.group ? sv::attn_visible(a, t, R / a.group, tile0 + wk * 16) : 0u;
+                const int R = t.r0 + g + 8 * y;
+                see[y] &= R < t.r1 ? sv::attn_visible(a, t, R / a.group, tile0 + wk * 16) : 0u;
             }
         }
         float top[2] = {neg_inf(), neg_inf()};
@@ -442,10 +444,10 @@ __global__ void __launch_bounds__(KW * 32, DP == 256 ? 1 : 2)
 
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-        const int R = t.mt * S::ROWS + g + 8 * y;
-        if (R >= t.n * a.group) continue;
+        const int R = t.r0 + g + 8 * y;
+        if (R >= t.r1) continue;
         const int64_t row = sv::attn_row(a, t, R);
-        const int64_t part = t.part + R - t.mt * S::ROWS;
+        const int64_t part = t.part + R - t.r0;
         if (t4 == 0) {
             if (t.parts > 1) a.part_lse[part] = lse2[y];
             else if (a.lse) a.lse[row] = lse2[y] * 0.69314718055994531f;
@@ -502,11 +504,11 @@ __global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_
     if (at >= rows) return;
     const int rest = (int)(at / part_rows), r = (int)(at - (int64_t)rest * part_rows);
     const sv::AttnPlace p = sv::attn_place(a, pairs, (unsigned)(a.whole + rest));
-    int base, n;
-    if (!sv::paged_row(a.c, a.base, a.new_len, p.b, a.Q, base, n)) return;
-    const int64_t R = (int64_t)p.mt * tile_rows + r;
-    if (R >= (int64_t)n * a.group) return;
-    const int parts = sv::attn_parts(a, sv::attn_active(a, sv::attn_tile_end(base, n, a.group, p.mt, tile_rows, a.tree_mask != nullptr)));
+    sv::AttnRows rows_of;
+    if (!sv::attn_rows(a, p, tile_rows, rows_of)) return;
+    const int64_t R = (int64_t)rows_of.r0 + r;
+    if (R >= rows_of.r1) return;
+    const int parts = sv::attn_parts(a, sv::attn_active(a, rows_of.end));
     if (parts <= 1) return;  // written by the one CTA that had the row
     const int64_t row = ((int64_t)p.b * a.Q + R / a.group) * a.Hq + p.h * a.group + R % a.group;
     const int64_t part = (int64_t)rest * (a.splits / a.per) * part_rows + r;  // the first; the next ones part_rows apart
@@ -632,6 +634,15 @@ bool sizes_ok(int B, int Q, int Hq, int H, int D, int max_len) {
            (int64_t)Q * (Hq / H) < ((int64_t)1 << 30);
 }
 
+// The kernels read and write 16 bytes at a time.
+sv_status layout_ok(const sv_paged_cache* cache, const void* q, const int64_t* q_stride, const void* out) {
+    if (cache->head_dim % 8 || ((uintptr_t)q | (uintptr_t)cache->k_pages | (uintptr_t)cache->v_pages | (uintptr_t)out) % 16 ||
+        (cache->page_stride | cache->head_stride | cache->row_stride) % 16 ||
+        (q_stride[0] | q_stride[1] | q_stride[2]) % 8)
+        return SV_ERR_UNSUPPORTED;
+    return SV_OK;
+}
+
 // Test hook for the time-out path (SPEC_VERIFY_TEST_STALL_ATTENTION=<batch row>): the tcgen05
 // kernel's CTAs of that row never report one tile's notes, so the waits for it run out and the
 // row is written as NaN.  Read once; unset, nothing changes.
@@ -651,6 +662,95 @@ int sm_count() {
         return 0;
     }
     return sms;
+}
+
+// The launches of a call whose arguments have been checked: `a` has the cache, base and lists.
+cudaError_t run_attention(AttnArgs& a, const Plan& p, const uint16_t* q, const int64_t* q_stride, int num_q_heads,
+                          const int32_t* new_len, const uint32_t* tree_mask, float scale, int B, int Q, int sms, bool e4m3,
+                          uint16_t* out, float* out_lse, float* workspace, cudaStream_t s) {
+    const int D = a.c.dim;
+    a.q = q;
+    a.q_sb = q_stride[0];
+    a.q_st = q_stride[1];
+    a.q_sh = q_stride[2];
+    a.new_len = new_len;
+    a.tree_mask = Q > 1 ? tree_mask : nullptr;
+    a.scale_log2 = scale * sv::LOG2E;
+    a.Q = Q;
+    a.Hq = num_q_heads;
+    a.group = num_q_heads / a.c.heads;
+    a.mask_words = (Q - 1 + 31) / 32;
+    a.m_tiles = p.m_tiles;
+    a.whole = (int)p.whole;
+    a.splits = p.splits;
+    a.per = p.per;
+    a.part_rows = p.part_rows;
+    a.equal = p.tile_rows >= 128;
+    a.sort = a.equal && !a.lists && B > 1 && B <= 32 && p.whole == 0 && p.ctas > sms ? B : 0;
+    a.chunk = p.chunk;
+    a.stall_row = test_stall_row();
+    a.out = out;
+    a.lse = out_lse;
+    const int64_t rows = p.ws ? (p.tiles - p.whole) * p.part_rows : 0;  // of the split tiles
+    a.part_o = workspace;
+    a.part_lse = p.ws ? a.part_o + rows * (p.splits / p.per) * D : nullptr;
+    const int pairs = B * a.c.heads;
+    const unsigned ctas = (unsigned)p.ctas;
+    cudaError_t e;
+    if (p.tile_rows >= 128) e = sv::launch_attn_tc(a, pairs, e4m3, p.tile_rows, p.dual, ctas, s);
+    else if (D <= 64) e = e4m3 ? launch_few<64, true>(a, pairs, ctas, s) : launch_few<64, false>(a, pairs, ctas, s);
+    else if (D <= 128) e = e4m3 ? launch_few<128, true>(a, pairs, ctas, s) : launch_few<128, false>(a, pairs, ctas, s);
+    else e = e4m3 ? launch_few<256, true>(a, pairs, ctas, s) : launch_few<256, false>(a, pairs, ctas, s);
+    if (e == cudaSuccess && rows)
+        e = sv::launch_serial(paged_attention_join_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a, pairs,
+                              p.tile_rows, rows);
+    return e;
+}
+
+// Attention over lists of blocks: the layout of its page tables, and its plan.
+struct SparsePlan {
+    Plan p;
+    int lists, query_tiles, width;
+    int64_t rows;     // of the page tables
+    size_t tables;    // their bytes, and the bases', to a multiple of 16
+    size_t bytes;
+};
+
+constexpr int kMaxListed = 4096;
+
+bool sparse_plan(int B, int Q, int Hq, int H, int D, bool e4m3, int page_size, int num_blocks, bool shared, int sms, SparsePlan& sp) {
+    if (num_blocks < 0 || num_blocks > kMaxListed || page_size < 1 || page_size > 65536 ||
+        (int64_t)page_size * (num_blocks + 2) + Q > sv::PAGED_MAX_POS)
+        return false;
+    sp.lists = shared || Q == 1 ? 1 : Q;
+    sp.rows = (int64_t)B * H * sp.lists;
+    if (sp.rows >= ((int64_t)1 << 31)) return false;
+    sp.width = num_blocks + (int)(((int64_t)Q + 2 * page_size - 2) / page_size);
+    sp.tables = (size_t)(sp.rows * (sp.width + 1) * 4 + 15) / 16 * 16;
+    const int most = num_blocks * page_size + page_size - 1 + Q;  // positions of a list
+    Plan p{};
+    if (sp.lists == 1) {
+        p = make_plan(B, Q, Hq, H, D, e4m3, most, sms);
+    } else {  // a query's heads are a row tile: few rows, so mma.sync
+        const int g = Hq / H;
+        sp.query_tiles = (g + 15) / 16;
+        p.tile_rows = 16;
+        p.m_tiles = Q * sp.query_tiles;
+        p.tiles = (int64_t)B * H * p.m_tiles;
+        int64_t splits = (4LL * sms + p.tiles - 1) / p.tiles;
+        if (splits > (most + 127) / 128) splits = (most + 127) / 128;
+        if (splits > 256) splits = 256;
+        p.chunk = (int)(((most + splits - 1) / splits + TN - 1) / TN * TN);
+        p.splits = (most + p.chunk - 1) / p.chunk;
+        if (p.splits <= 1) p.whole = p.tiles;
+        p.per = 1;
+        p.ctas = p.whole + (p.tiles - p.whole) * p.splits;
+        p.part_rows = g < 16 ? g : 16;
+        p.ws = p.splits > 1 ? (size_t)p.tiles * p.splits * p.part_rows * (D + 1) * sizeof(float) : 0;
+    }
+    sp.p = p;
+    sp.bytes = sp.tables + p.ws;
+    return p.ctas < ((int64_t)1 << 31);
 }
 
 }  // namespace
@@ -677,10 +777,8 @@ sv_status spec_paged_attention(const void* q, const int64_t* q_stride, int num_q
     if (B == 0) return SV_OK;
     if (!cache->page_table || !q || !q_stride || !base || !out) return SV_ERR_INVALID_ARG;
     const int D = cache->head_dim;
-    if (D % 8 || ((uintptr_t)q | (uintptr_t)cache->k_pages | (uintptr_t)cache->v_pages | (uintptr_t)out) % 16 ||
-        (cache->page_stride | cache->head_stride | cache->row_stride) % 16 ||
-        (q_stride[0] | q_stride[1] | q_stride[2]) % 8)
-        return SV_ERR_UNSUPPORTED;
+    const sv_status bad = layout_ok(cache, q, q_stride, out);
+    if (bad != SV_OK) return bad;
     const int sms = sm_count();
     if (!sms) return sv::launch_status(cudaErrorInvalidDevice);
     Plan p = make_plan(B, Q, num_q_heads, cache->num_heads, D, cache->dtype == SV_CACHE_E4M3, max_len, sms);
@@ -693,45 +791,57 @@ sv_status spec_paged_attention(const void* q, const int64_t* q_stride, int num_q
         p.ws = 0;
     }
     if (p.ctas >= ((int64_t)1 << 31)) return SV_ERR_UNSUPPORTED;
-    a.q = static_cast<const uint16_t*>(q);
-    a.q_sb = q_stride[0];
-    a.q_st = q_stride[1];
-    a.q_sh = q_stride[2];
     a.base = base;
-    a.new_len = new_len;
-    a.tree_mask = Q > 1 ? tree_mask : nullptr;
-    a.scale_log2 = scale * sv::LOG2E;
-    a.Q = Q;
-    a.Hq = num_q_heads;
-    a.group = num_q_heads / cache->num_heads;
-    a.mask_words = (Q - 1 + 31) / 32;
-    a.m_tiles = p.m_tiles;
-    a.whole = (int)p.whole;
-    a.splits = p.splits;
-    a.per = p.per;
-    a.part_rows = p.part_rows;
-    a.equal = p.tile_rows >= 128;
-    a.sort = a.equal && B > 1 && B <= 32 && p.whole == 0 && p.ctas > sms ? B : 0;
-    a.chunk = p.chunk;
-    a.stall_row = test_stall_row();
-    a.out = static_cast<uint16_t*>(out);
-    a.lse = out_lse;
-    const int64_t rows = p.ws ? (p.tiles - p.whole) * p.part_rows : 0;  // of the split tiles
-    a.part_o = static_cast<float*>(workspace);
-    a.part_lse = p.ws ? a.part_o + rows * (p.splits / p.per) * D : nullptr;
-    cudaStream_t s = (cudaStream_t)stream;
+    return sv::launch_status(run_attention(a, p, static_cast<const uint16_t*>(q), q_stride, num_q_heads, new_len, tree_mask,
+                                           scale, B, Q, sms, cache->dtype == SV_CACHE_E4M3, static_cast<uint16_t*>(out),
+                                           out_lse, static_cast<float*>(workspace), (cudaStream_t)stream));
+}
+
+size_t spec_sparse_attention_workspace_size(int B, int Q, int num_q_heads, int num_heads, int head_dim,
+                                            sv_cache_dtype dtype, int page_size, int num_blocks, int shared) {
+    if (!sizes_ok(B, Q, num_q_heads, num_heads, head_dim, 1) || B == 0) return 0;
+    if (dtype != SV_CACHE_BF16 && dtype != SV_CACHE_E4M3) return 0;
+    const int sms = sm_count();
+    SparsePlan sp{};
+    return sms && sparse_plan(B, Q, num_q_heads, num_heads, head_dim, dtype == SV_CACHE_E4M3, page_size, num_blocks, shared != 0, sms, sp)
+               ? sp.bytes : 0;
+}
+
+sv_status spec_sparse_attention(const void* q, const int64_t* q_stride, int num_q_heads, const sv_paged_cache* cache,
+                                const int32_t* base, const int32_t* new_len, const uint32_t* tree_mask,
+                                const int32_t* blocks, int num_blocks, int shared, float scale, int B, int Q, void* out,
+                                float* out_lse, void* workspace, size_t ws_bytes, void* stream) {
+    AttnArgs a{};
+    if (!sv::paged_cache_args(cache, a.c) || !sizes_ok(B, Q, num_q_heads, cache->num_heads, cache->head_dim, 1))
+        return SV_ERR_INVALID_ARG;
+    if (!(scale - scale == 0.0f)) return SV_ERR_INVALID_ARG;  // NaN or infinite
+    if (num_blocks < 0 || num_blocks > kMaxListed) return SV_ERR_INVALID_ARG;
+    if (B == 0) return SV_OK;
+    if (!cache->page_table || !q || !q_stride || !base || !out || (num_blocks && !blocks) || !workspace) return SV_ERR_INVALID_ARG;
+    const int D = cache->head_dim;
+    const sv_status bad = layout_ok(cache, q, q_stride, out);
+    if (bad != SV_OK) return bad;
+    const int sms = sm_count();
+    if (!sms) return sv::launch_status(cudaErrorInvalidDevice);
     const bool e4m3 = cache->dtype == SV_CACHE_E4M3;
-    const int pairs = B * cache->num_heads;
-    const unsigned ctas = (unsigned)p.ctas;
-    cudaError_t e;
-    if (p.tile_rows >= 128) e = sv::launch_attn_tc(a, pairs, e4m3, p.tile_rows, p.dual, ctas, s);
-    else if (D <= 64) e = e4m3 ? launch_few<64, true>(a, pairs, ctas, s) : launch_few<64, false>(a, pairs, ctas, s);
-    else if (D <= 128) e = e4m3 ? launch_few<128, true>(a, pairs, ctas, s) : launch_few<128, false>(a, pairs, ctas, s);
-    else e = launch_few<256, true>(a, pairs, ctas, s);
-    if (e == cudaSuccess && rows)
-        e = sv::launch_serial(paged_attention_join_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a, pairs,
-                              p.tile_rows, rows);
-    return sv::launch_status(e);
+    SparsePlan sp{};
+    if (!sparse_plan(B, Q, num_q_heads, cache->num_heads, D, e4m3, cache->page_size, num_blocks, shared != 0, sms, sp))
+        return SV_ERR_UNSUPPORTED;
+    if (ws_bytes < sp.bytes || (uintptr_t)workspace % 16) return SV_ERR_INVALID_ARG;
+    int32_t* table = static_cast<int32_t*>(workspace);
+    int32_t* list_base = table + sp.rows * sp.width;
+    cudaStream_t s = (cudaStream_t)stream;
+    const cudaError_t e = sv::launch_block_tables(a.c, base, new_len, blocks, num_blocks, sp.lists, sp.rows, Q, table, list_base,
+                                                  sp.width, s);
+    if (e != cudaSuccess) return sv::launch_status(e);
+    a.c.table = table;
+    a.c.max_pages = sp.width;
+    a.base = list_base;
+    a.lists = sp.lists == 1 ? 1 : 2;
+    a.query_tiles = sp.query_tiles;
+    return sv::launch_status(run_attention(a, sp.p, static_cast<const uint16_t*>(q), q_stride, num_q_heads, new_len, tree_mask,
+                                           scale, B, Q, sms, e4m3, static_cast<uint16_t*>(out), out_lse,
+                                           reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + sp.tables), s));
 }
 
 }  // extern "C"

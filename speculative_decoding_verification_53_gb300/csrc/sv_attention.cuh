@@ -22,6 +22,9 @@ struct AttnArgs {
     const uint32_t* tree_mask; // [B][Q-1][mask_words] or nullptr
     float scale_log2;          // scale * log2(e)
     int Q, Hq, group, mask_words;
+    int lists;                 // 0: a page table and base per batch row; else (sparse attention) per
+                               // batch row and cache head (1), or per batch row, query and cache head (2)
+    int query_tiles;           // lists 2: tiles of 16 rows per query
     int m_tiles;               // tiles of query rows per (batch row, cache head)
     int whole;                 // tiles [0, whole) are not split, the others `splits` ways
     int splits, chunk;         // a row tile has a split per `chunk` positions, `splits` at most
@@ -50,8 +53,16 @@ __device__ __forceinline__ AttnPlace attn_place(const AttnArgs& a, int pairs, un
     return p;
 }
 
+// The rows of a tile: the row of the page table and of base, query rows [r0, r1), positions before
+// the chunk, real queries, and the end of the positions that the rows see.
+struct AttnRows {
+    int row, r0, r1, base, n, end;
+};
+
 struct AttnTile {
     int b, h, mt, split;
+    int row;           // of the page table
+    int r0, r1;        // query rows
     int base, n;       // positions before the chunk, real queries
     int begin, end;    // this CTA's positions
     int end2;          // of a second split behind them, where a CTA takes two (end: it has none)
@@ -65,6 +76,27 @@ __host__ __device__ __forceinline__ int attn_tile_end(int base, int n, int group
     int last = ((mt + 1) * tile_rows - 1) / group;
     if (last > n - 1) last = n - 1;
     return base + last + 1;
+}
+
+// False where the tile has no rows, or its batch row is left untouched.
+__device__ __forceinline__ bool attn_rows(const AttnArgs& a, const AttnPlace& p, int tile_rows, AttnRows& r) {
+    const int i = a.lists == 2 ? p.mt / a.query_tiles : 0;
+    r.row = a.lists == 0 ? p.b : a.lists == 1 ? p.b * a.c.heads + p.h : (p.b * a.Q + i) * a.c.heads + p.h;
+    r.base = __ldg(a.base + r.row);
+    r.n = a.new_len ? __ldg(a.new_len + p.b) : a.Q;
+    if (r.base < 0 || r.n < 0 || r.n > a.Q || (int64_t)r.base + r.n > (int64_t)a.c.max_pages * a.c.page_size) return false;
+    if (a.lists == 2) {
+        if (i >= r.n) return false;
+        r.r0 = i * a.group + (p.mt - i * a.query_tiles) * tile_rows;
+        r.r1 = (i + 1) * a.group;
+        r.end = a.tree_mask ? r.base + r.n : r.base + i + 1;
+        return true;
+    }
+    if ((int64_t)p.mt * tile_rows >= (int64_t)r.n * a.group) return false;
+    r.r0 = p.mt * tile_rows;
+    r.r1 = r.n * a.group;
+    r.end = attn_tile_end(r.base, r.n, a.group, p.mt, tile_rows, a.tree_mask != nullptr);
+    return true;
 }
 
 // Splits of a row tile that have positions.
@@ -123,9 +155,14 @@ __device__ __forceinline__ bool attn_tile(const AttnArgs& a, int pairs, unsigned
     t.mt = p.mt;
     t.split = whole ? 0 : (int)(rest % each) * per;
     t.part = whole ? 0 : ((int64_t)tile * each + rest % each) * a.part_rows;
-    if (!paged_row(a.c, a.base, a.new_len, t.b, a.Q, t.base, t.n)) return false;
-    if ((int64_t)t.mt * tile_rows >= (int64_t)t.n * a.group) return false;
-    const int end = attn_tile_end(t.base, t.n, a.group, t.mt, tile_rows, a.tree_mask != nullptr);
+    AttnRows r;
+    if (!attn_rows(a, p, tile_rows, r)) return false;
+    t.row = r.row;
+    t.r0 = r.r0;
+    t.r1 = r.r1;
+    t.base = r.base;
+    t.n = r.n;
+    const int end = r.end;
     const int active = whole ? 1 : attn_active(a, end);
     if (t.split >= active) return false;
     t.parts = attn_parts(a, active);
@@ -161,7 +198,7 @@ __device__ __forceinline__ uint32_t attn_visible(const AttnArgs& a, const AttnTi
 template <bool E4M3>
 __device__ __forceinline__ float attn_value(const AttnArgs& a, const AttnTile& t, int pos, int d) {
     int row;
-    const int page = paged_place(a.c, t.b, pos, row);
+    const int page = paged_place(a.c, t.row, pos, row);
     if (page < 0) return 0.0f;
     const unsigned char* p = a.c.v + page * a.c.page_stride + t.h * a.c.head_stride + row * a.c.row_stride;
     if (!E4M3) return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + d) << 16);
@@ -245,5 +282,11 @@ inline int page_box_rows(const PagedCache& c, int tile) {
 // takes two splits.
 cudaError_t launch_attn_tc(const AttnArgs& a, int pairs, bool e4m3, int tile_rows, bool dual, unsigned ctas,
                            cudaStream_t stream);
+
+// Page tables [rows][width] and positions before the chunk of lists of blocks (sv_sparse.cu);
+// `lists` of them per batch row and cache head, in the order (batch row, list, cache head).
+cudaError_t launch_block_tables(const PagedCache& c, const int32_t* base, const int32_t* new_len, const int32_t* blocks,
+                                int num_blocks, int lists, int64_t rows, int Q, int32_t* table, int32_t* out_base,
+                                int width, cudaStream_t stream);
 
 }  // namespace sv
