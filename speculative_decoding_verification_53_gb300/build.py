@@ -21,7 +21,8 @@ LIB = os.path.join(PKG, "libspecverify.so")
 SOURCES = ["sv_api.cu", "sv_chain.cu", "sv_chain_staged.cu", "sv_chain_spec.cu", "sv_chain_eager.cu", "sv_chain_ring.cu",
            "sv_tree.cu", "sv_tree_staged.cu", "sv_noalloc.cu", "sv_host.cu", "sv_tree_kv.cu", "sv_sample.cu", "sv_status.cu",
            "sv_launch.cu", "sv_paged_kv.cu", "sv_attention.cu", "sv_attention_tc.cu",
-           "sv_logits.cu", "sv_pages.cu", "sv_rotary.cu", "sv_select.cu", "sv_sparse.cu"]
+           "sv_logits.cu", "sv_pages.cu", "sv_rotary.cu", "sv_select.cu", "sv_sparse.cu",
+           "sv_attention_lists.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", INCLUDE, "-I", CSRC]

@@ -667,7 +667,7 @@ int sm_count() {
 // The launches of a call whose arguments have been checked: `a` has the cache, base and lists.
 cudaError_t run_attention(AttnArgs& a, const Plan& p, const uint16_t* q, const int64_t* q_stride, int num_q_heads,
                           const int32_t* new_len, const uint32_t* tree_mask, float scale, int B, int Q, int sms, bool e4m3,
-                          uint16_t* out, float* out_lse, float* workspace, cudaStream_t s) {
+                          uint16_t* out, float* out_lse, float* workspace, const uint32_t* bits, cudaStream_t s) {
     const int D = a.c.dim;
     a.q = q;
     a.q_sb = q_stride[0];
@@ -685,7 +685,7 @@ cudaError_t run_attention(AttnArgs& a, const Plan& p, const uint16_t* q, const i
     a.splits = p.splits;
     a.per = p.per;
     a.part_rows = p.part_rows;
-    a.equal = p.tile_rows >= 128;
+    a.equal = p.tile_rows >= 128 || a.lists == 3;
     a.sort = a.equal && !a.lists && B > 1 && B <= 32 && p.whole == 0 && p.ctas > sms ? B : 0;
     a.chunk = p.chunk;
     a.stall_row = test_stall_row();
@@ -697,7 +697,8 @@ cudaError_t run_attention(AttnArgs& a, const Plan& p, const uint16_t* q, const i
     const int pairs = B * a.c.heads;
     const unsigned ctas = (unsigned)p.ctas;
     cudaError_t e;
-    if (p.tile_rows >= 128) e = sv::launch_attn_tc(a, pairs, e4m3, p.tile_rows, p.dual, ctas, s);
+    if (a.lists == 3) e = sv::launch_list_attention(a, pairs, p.part_rows, ctas, bits, s);
+    else if (p.tile_rows >= 128) e = sv::launch_attn_tc(a, pairs, e4m3, p.tile_rows, p.dual, ctas, s);
     else if (D <= 64) e = e4m3 ? launch_few<64, true>(a, pairs, ctas, s) : launch_few<64, false>(a, pairs, ctas, s);
     else if (D <= 128) e = e4m3 ? launch_few<128, true>(a, pairs, ctas, s) : launch_few<128, false>(a, pairs, ctas, s);
     else e = e4m3 ? launch_few<256, true>(a, pairs, ctas, s) : launch_few<256, false>(a, pairs, ctas, s);
@@ -710,29 +711,84 @@ cudaError_t run_attention(AttnArgs& a, const Plan& p, const uint16_t* q, const i
 // Attention over lists of blocks: the layout of its page tables, and its plan.
 struct SparsePlan {
     Plan p;
-    int lists, query_tiles, width;
+    int mode;         // AttnArgs::lists
+    int lists;        // page tables per batch row and cache head
+    int query_tiles;  // as in AttnArgs
+    int width, most;  // of a page table; blocks of a union
     int64_t rows;     // of the page tables
-    size_t tables;    // their bytes, and the bases', to a multiple of 16
+    size_t tables;    // bytes of the page tables, bases and bits, to a multiple of 16
     size_t bytes;
 };
 
 constexpr int kMaxListed = 4096;
+constexpr int kMaxUnion = 8192;      // blocks of a union, whose bits are built in shared memory
+constexpr int kMaxUnionOf = 65536;   // blocks of the context it is built over
 
-bool sparse_plan(int B, int Q, int Hq, int H, int D, bool e4m3, int page_size, int num_blocks, bool shared, int sms, SparsePlan& sp) {
+// Splits of large row tiles over lists of one length: the number that is cheapest by a model of what was
+// measured (us): a tile's positions 0.0144 each (e4m3 0.0235), a split 10 of its own, the join 8 and the partial
+// results' bytes at 2 TB/s.  16 trees of 61 over 64 pages of 64 (128 tiles): 67 in one piece, 122 in 3 as
+// make_plan cuts contexts of unequal length (e4m3 110 and 160); 9 trees 64 and 87 in 5, 5 trees 63 and 59 in 5,
+// 1 tree 60 and 29; 5 trees over 200 pages 168 and 105 in 11.
+void split_lists(Plan& p, int most, int64_t rows, int D, bool e4m3, int sms) {
+    double best = 0.0;
+    int splits = 1;
+    for (int s = 1; s <= 16; ++s) {
+        if (s > 1 && most / s < 512) break;
+        const double waves = (double)((p.tiles * s + sms - 1) / sms);
+        double us = waves * (most * (e4m3 ? 0.0235 : 0.0144) / s + 10.0);
+        if (s > 1) us += 8.0 + (double)p.tiles * s * (p.m_tiles == 1 ? rows : p.tile_rows) * (D + 1) * 8.0 / 2.0e6;
+        if (s == 1 || us < best) {
+            best = us;
+            splits = s;
+        }
+    }
+    p.whole = splits > 1 ? 0 : p.tiles;
+    p.splits = splits;
+    p.chunk = splits > 1 ? (most + splits - 1) / splits + 127 & ~127 : sv::PAGED_MAX_POS;
+    p.splits = splits > 1 ? (most + p.chunk - 1) / p.chunk : 1;
+    p.ctas = p.whole + (p.tiles - p.whole) * p.splits;
+    p.ws = p.splits > 1 ? (size_t)p.tiles * p.splits * p.part_rows * (D + 1) * sizeof(float) : 0;
+}
+
+bool sparse_plan(int B, int Q, int Hq, int H, int D, bool e4m3, int page_size, int num_blocks, bool shared, bool unite, int sms, SparsePlan& sp) {
     if (num_blocks < 0 || num_blocks > kMaxListed || page_size < 1 || page_size > 65536 ||
         (int64_t)page_size * (num_blocks + 2) + Q > sv::PAGED_MAX_POS)
         return false;
-    sp.lists = shared || Q == 1 ? 1 : Q;
+    const int g = Hq / H;
+    // Queries whose lists are united: as many as 32 rows hold, in tiles of one size.
+    int tile = g <= 32 ? 32 / g : 0, tiles = tile ? (Q + tile - 1) / tile : 0;
+    if (tile) tile = (Q + tiles - 1) / tiles;
+    sp.mode = shared || Q == 1 ? 1 : unite && !e4m3 && D <= 128 && tile && (int64_t)tile * num_blocks <= kMaxUnion &&
+              (int64_t)page_size * (tile * num_blocks + 2) + Q <= sv::PAGED_MAX_POS ? 3 : 2;
+    sp.lists = sp.mode == 1 ? 1 : sp.mode == 2 ? Q : tiles;
+    sp.most = sp.mode == 3 ? tile * num_blocks : num_blocks;
     sp.rows = (int64_t)B * H * sp.lists;
     if (sp.rows >= ((int64_t)1 << 31)) return false;
-    sp.width = num_blocks + (int)(((int64_t)Q + 2 * page_size - 2) / page_size);
-    sp.tables = (size_t)(sp.rows * (sp.width + 1) * 4 + 15) / 16 * 16;
-    const int most = num_blocks * page_size + page_size - 1 + Q;  // positions of a list
+    sp.width = sp.most + (int)(((int64_t)Q + 2 * page_size - 2) / page_size);
+    sp.tables = (size_t)(sp.rows * (sp.width * (sp.mode == 3 ? 2 : 1) + 1) * 4 + 15) / 16 * 16;
+    const int most = sp.most * page_size + page_size - 1 + Q;  // positions of a list
     Plan p{};
-    if (sp.lists == 1) {
+    if (sp.mode == 1) {
         p = make_plan(B, Q, Hq, H, D, e4m3, most, sms);
+        if (p.tile_rows >= 128 && !p.dual && p.tiles < sms) split_lists(p, most, (int64_t)Q * g, D, e4m3, sms);
+    } else if (sp.mode == 3) {
+        // Unions are as long as the lists differ, which is not known here: every tile is split the same
+        // number of times, into parts of one length of 256 positions or more, as often as all CTAs fit on the
+        // SMs at once (64 tiles of 24 rows: 7 splits 43 us, 5 50, 8, which leave a second wave, 58).
+        sp.query_tiles = tile;
+        p.tile_rows = p.part_rows = tile * g;
+        p.m_tiles = tiles;
+        p.tiles = (int64_t)B * H * tiles;
+        int64_t splits = (int64_t)(p.part_rows <= 24 ? 3 : 2) * sms / p.tiles;
+        if (splits < 1) splits = 1;
+        p.chunk = 256;
+        if (splits > (most + p.chunk - 1) / p.chunk) splits = (most + p.chunk - 1) / p.chunk;
+        p.splits = splits > 256 ? 256 : (int)splits;
+        if (p.splits <= 1) p.whole = p.tiles;
+        p.per = 1;
+        p.ctas = p.whole + (p.tiles - p.whole) * p.splits;
+        p.ws = p.splits > 1 ? (size_t)p.tiles * p.splits * p.part_rows * (D + 1) * sizeof(float) : 0;
     } else {  // a query's heads are a row tile: few rows, so mma.sync
-        const int g = Hq / H;
         sp.query_tiles = (g + 15) / 16;
         p.tile_rows = 16;
         p.m_tiles = Q * sp.query_tiles;
@@ -794,7 +850,7 @@ sv_status spec_paged_attention(const void* q, const int64_t* q_stride, int num_q
     a.base = base;
     return sv::launch_status(run_attention(a, p, static_cast<const uint16_t*>(q), q_stride, num_q_heads, new_len, tree_mask,
                                            scale, B, Q, sms, cache->dtype == SV_CACHE_E4M3, static_cast<uint16_t*>(out),
-                                           out_lse, static_cast<float*>(workspace), (cudaStream_t)stream));
+                                           out_lse, static_cast<float*>(workspace), nullptr, (cudaStream_t)stream));
 }
 
 size_t spec_sparse_attention_workspace_size(int B, int Q, int num_q_heads, int num_heads, int head_dim,
@@ -802,9 +858,14 @@ size_t spec_sparse_attention_workspace_size(int B, int Q, int num_q_heads, int n
     if (!sizes_ok(B, Q, num_q_heads, num_heads, head_dim, 1) || B == 0) return 0;
     if (dtype != SV_CACHE_BF16 && dtype != SV_CACHE_E4M3) return 0;
     const int sms = sm_count();
-    SparsePlan sp{};
-    return sms && sparse_plan(B, Q, num_q_heads, num_heads, head_dim, dtype == SV_CACHE_E4M3, page_size, num_blocks, shared != 0, sms, sp)
-               ? sp.bytes : 0;
+    size_t bytes = 0;
+    for (int unite = 0; sms && unite < 2; ++unite) {  // the page table's width, which decides, is not known here
+        SparsePlan sp{};
+        if (sparse_plan(B, Q, num_q_heads, num_heads, head_dim, dtype == SV_CACHE_E4M3, page_size, num_blocks, shared != 0, unite, sms, sp) &&
+            sp.bytes > bytes)
+            bytes = sp.bytes;
+    }
+    return bytes;
 }
 
 sv_status spec_sparse_attention(const void* q, const int64_t* q_stride, int num_q_heads, const sv_paged_cache* cache,
@@ -825,23 +886,29 @@ sv_status spec_sparse_attention(const void* q, const int64_t* q_stride, int num_
     if (!sms) return sv::launch_status(cudaErrorInvalidDevice);
     const bool e4m3 = cache->dtype == SV_CACHE_E4M3;
     SparsePlan sp{};
-    if (!sparse_plan(B, Q, num_q_heads, cache->num_heads, D, e4m3, cache->page_size, num_blocks, shared != 0, sms, sp))
+    if (!sparse_plan(B, Q, num_q_heads, cache->num_heads, D, e4m3, cache->page_size, num_blocks, shared != 0,
+                     cache->max_pages <= kMaxUnionOf, sms, sp))
         return SV_ERR_UNSUPPORTED;
     if (ws_bytes < sp.bytes || (uintptr_t)workspace % 16) return SV_ERR_INVALID_ARG;
     int32_t* table = static_cast<int32_t*>(workspace);
     int32_t* list_base = table + sp.rows * sp.width;
     cudaStream_t s = (cudaStream_t)stream;
-    const cudaError_t e = sv::launch_block_tables(a.c, base, new_len, blocks, num_blocks, sp.lists, sp.rows, Q, table, list_base,
-                                                  sp.width, s);
+    uint32_t* bits = reinterpret_cast<uint32_t*>(list_base + sp.rows);
+    cudaError_t e;
+    if (sp.mode == 3)
+        e = sv::launch_list_unions(a.c, base, new_len, blocks, num_blocks, Q, sp.query_tiles, sp.lists, sp.rows, table, bits, list_base,
+                                   sp.width, sp.most < cache->max_pages ? sp.most : cache->max_pages, s);
+    else
+        e = sv::launch_block_tables(a.c, base, new_len, blocks, num_blocks, sp.lists, sp.rows, Q, table, list_base, sp.width, s);
     if (e != cudaSuccess) return sv::launch_status(e);
     a.c.table = table;
     a.c.max_pages = sp.width;
     a.base = list_base;
-    a.lists = sp.lists == 1 ? 1 : 2;
+    a.lists = sp.mode;
     a.query_tiles = sp.query_tiles;
     return sv::launch_status(run_attention(a, sp.p, static_cast<const uint16_t*>(q), q_stride, num_q_heads, new_len, tree_mask,
                                            scale, B, Q, sms, e4m3, static_cast<uint16_t*>(out), out_lse,
-                                           reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + sp.tables), s));
+                                           reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + sp.tables), bits, s));
 }
 
 }  // extern "C"

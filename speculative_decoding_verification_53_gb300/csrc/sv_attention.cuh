@@ -23,8 +23,9 @@ struct AttnArgs {
     float scale_log2;          // scale * log2(e)
     int Q, Hq, group, mask_words;
     int lists;                 // 0: a page table and base per batch row; else (sparse attention) per
-                               // batch row and cache head (1), or per batch row, query and cache head (2)
-    int query_tiles;           // lists 2: tiles of 16 rows per query
+                               // batch row and cache head (1), per batch row, query and cache head (2), or
+                               // per batch row, tile of queries and cache head (3)
+    int query_tiles;           // lists 2: tiles of 16 rows per query; 3: queries per tile
     int m_tiles;               // tiles of query rows per (batch row, cache head)
     int whole;                 // tiles [0, whole) are not split, the others `splits` ways
     int splits, chunk;         // a row tile has a split per `chunk` positions, `splits` at most
@@ -81,7 +82,8 @@ __host__ __device__ __forceinline__ int attn_tile_end(int base, int n, int group
 // False where the tile has no rows, or its batch row is left untouched.
 __device__ __forceinline__ bool attn_rows(const AttnArgs& a, const AttnPlace& p, int tile_rows, AttnRows& r) {
     const int i = a.lists == 2 ? p.mt / a.query_tiles : 0;
-    r.row = a.lists == 0 ? p.b : a.lists == 1 ? p.b * a.c.heads + p.h : (p.b * a.Q + i) * a.c.heads + p.h;
+    r.row = a.lists == 0 ? p.b : a.lists == 1 ? p.b * a.c.heads + p.h
+            : (p.b * (a.lists == 2 ? a.Q : a.m_tiles) + (a.lists == 2 ? i : p.mt)) * a.c.heads + p.h;
     r.base = __ldg(a.base + r.row);
     r.n = a.new_len ? __ldg(a.new_len + p.b) : a.Q;
     if (r.base < 0 || r.n < 0 || r.n > a.Q || (int64_t)r.base + r.n > (int64_t)a.c.max_pages * a.c.page_size) return false;
@@ -90,6 +92,14 @@ __device__ __forceinline__ bool attn_rows(const AttnArgs& a, const AttnPlace& p,
         r.r0 = i * a.group + (p.mt - i * a.query_tiles) * tile_rows;
         r.r1 = (i + 1) * a.group;
         r.end = a.tree_mask ? r.base + r.n : r.base + i + 1;
+        return true;
+    }
+    if (a.lists == 3) {
+        const int first = p.mt * a.query_tiles, end = min(r.n, first + a.query_tiles);
+        if (first >= r.n) return false;
+        r.r0 = first * a.group;
+        r.r1 = end * a.group;
+        r.end = r.base + (a.tree_mask ? r.n : end);
         return true;
     }
     if ((int64_t)p.mt * tile_rows >= (int64_t)r.n * a.group) return false;
@@ -288,5 +298,13 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int pairs, bool e4m3, int tile_row
 cudaError_t launch_block_tables(const PagedCache& c, const int32_t* base, const int32_t* new_len, const int32_t* blocks,
                                 int num_blocks, int lists, int64_t rows, int Q, int32_t* table, int32_t* out_base,
                                 int width, cudaStream_t stream);
+
+// The kernel for queries with a list each (sv_attention_lists.cu): bf16, heads of up to 128, tiles of up to
+// 32 rows; and the unions of the lists of a tile's queries, of at most `most` blocks, with a bit for each
+// query that listed a block.
+cudaError_t launch_list_attention(const AttnArgs& a, int pairs, int rows, unsigned ctas, const uint32_t* bits, cudaStream_t stream);
+cudaError_t launch_list_unions(const PagedCache& c, const int32_t* base, const int32_t* new_len, const int32_t* blocks,
+                               int num_blocks, int Q, int query_tile, int tiles, int64_t rows, int32_t* table, uint32_t* bits,
+                               int32_t* out_base, int width, int most, cudaStream_t stream);
 
 }  // namespace sv

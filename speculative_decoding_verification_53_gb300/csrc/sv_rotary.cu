@@ -27,6 +27,7 @@ constexpr int kMaxTokens = 8;  // of a block
 constexpr int kMaxFreq = 128;
 constexpr int kMaxB = 65535;
 constexpr int kMaxN = 1 << 20;
+constexpr int kDepth = 4;  // groups of rows in flight per warp, less one
 
 enum { DENSE, CACHE_BF16, CACHE_E4M3 };
 
@@ -36,7 +37,8 @@ struct RotaryArgs {
     void* dst[2];        // queries, keys (DENSE)
     int64_t ss[3][3];    // element strides of the sources (batch, token, head)
     int64_t ds[2][3];    // and of the destinations
-    int end[3];          // rows of a token: [0, end[0]) queries, then keys, then values
+    int heads[3];        // of queries, keys, values
+    int groups[3];       // groups of rows of a token: [0, groups[0]) queries, then keys, then values
     const double* freq;
     const int32_t* depth;
     const int32_t* base;
@@ -45,7 +47,7 @@ struct RotaryArgs {
     int R, interleaved, inverse;
     int B, N, D;
     int tile;   // tokens of a block: 1, 2, 4 or 8
-    int chunk;  // rows of a token that a block does
+    int chunk;  // groups of a token that a block does
 };
 
 // Position of token i of row b; false where the token is not written.
@@ -81,52 +83,82 @@ __device__ __forceinline__ float2 turn(int64_t pos, float fh, float fl) {
     return make_float2(c, s);
 }
 
+// Eight elements of a row as they lie in memory (AL), or widened one by one; zero where there is no row.
+// Plain loads: in place the same kernel writes the row.
 template <typename T, bool AL>
-__device__ __forceinline__ void read8(const T* row, int e0, int dim, float x[8]) {
-    if (AL) {
-        uint4 w[sizeof(T) / 2];
+struct Raw {
+    static constexpr int W = AL ? (int)sizeof(T) * 2 : 8;  // words
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const T* row, int e0, int dim) {
+        if (AL) {
 #pragma unroll
-        for (int k = 0; k < (int)sizeof(T) / 2; ++k)
-            w[k] = e0 < dim ? *reinterpret_cast<const uint4*>(row + e0 + 4 * k) : make_uint4(0u, 0u, 0u, 0u);
-        if (sizeof(T) == 2) {
-            x[0] = sv::bf16_lo(w[0].x); x[1] = sv::bf16_hi(w[0].x); x[2] = sv::bf16_lo(w[0].y); x[3] = sv::bf16_hi(w[0].y);
-            x[4] = sv::bf16_lo(w[0].z); x[5] = sv::bf16_hi(w[0].z); x[6] = sv::bf16_lo(w[0].w); x[7] = sv::bf16_hi(w[0].w);
+            for (int k = 0; k < W / 4; ++k) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (e0 < dim) v = *reinterpret_cast<const uint4*>(row + e0 + k * (16 / (int)sizeof(T)));
+                w[4 * k] = v.x;
+                w[4 * k + 1] = v.y;
+                w[4 * k + 2] = v.z;
+                w[4 * k + 3] = v.w;
+            }
         } else {
-            const uint4 b = w[sizeof(T) == 4 ? 1 : 0];
-            x[0] = __uint_as_float(w[0].x); x[1] = __uint_as_float(w[0].y);
-            x[2] = __uint_as_float(w[0].z); x[3] = __uint_as_float(w[0].w);
-            x[4] = __uint_as_float(b.x); x[5] = __uint_as_float(b.y);
-            x[6] = __uint_as_float(b.z); x[7] = __uint_as_float(b.w);
-        }
-    } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            x[k] = 0.0f;
-            if (e0 + k < dim)
-                x[k] = sizeof(T) == 2 ? __uint_as_float((uint32_t)reinterpret_cast<const unsigned short*>(row)[e0 + k] << 16)
-                                      : reinterpret_cast<const float*>(row)[e0 + k];
+            for (int k = 0; k < 8; ++k) w[AL ? 0 : k] = e0 + k < dim ? __float_as_uint(one(row, e0 + k)) : 0u;
         }
     }
-}
-
-template <typename T>
-__device__ __forceinline__ float read1(const T* row, int e) {
-    return sizeof(T) == 2 ? __uint_as_float((uint32_t)reinterpret_cast<const unsigned short*>(row)[e] << 16)
-                          : reinterpret_cast<const float*>(row)[e];
-}
+    static __device__ __forceinline__ float one(const T* row, int e) {
+        return sizeof(T) == 2 ? __uint_as_float((uint32_t)reinterpret_cast<const unsigned short*>(row)[e] << 16)
+                              : reinterpret_cast<const float*>(row)[e];
+    }
+    __device__ __forceinline__ float at(int k) const {
+        if (AL && sizeof(T) == 2) return k & 1 ? sv::bf16_hi(w[AL ? k / 2 : 0]) : sv::bf16_lo(w[AL ? k / 2 : 0]);
+        return __uint_as_float(w[k]);
+    }
+};
 
 // grid: x over tiles of tokens, y over chunks of a token's rows.  LPR lanes hold a row.
-template <typename T, int LPR, int MODE, bool AL, int ROWS>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
-    extern __shared__ float2 s_turn[];  // [tile][R]
+template <typename T, int LPR, int MODE, bool AL>
+__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ RotaryArgs a) {
+    extern __shared__ uint4 s_raw[];  // AL: the ring; then [tile][R] cosines and sines
+    float2* s_turn = reinterpret_cast<float2*>(s_raw + (AL ? kDepth * ((int)sizeof(T) / 2) * kThreads : 0));
     __shared__ float2 s_freq[kMaxFreq];
     __shared__ int64_t s_pos[kMaxTokens];
     __shared__ int s_first[kMaxTokens];  // the row's base; -1: token not written
     constexpr int G = 32 / LPR;
     sv::pdl_trigger();
     sv::pdl_wait();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const unsigned total = (unsigned)a.B * (unsigned)a.N;
+    const int e0 = 8 * (lane % LPR);
+    // This warp's token, and the groups of rows that it takes of it (a group is of one kind, so
+    // the warp decides on it as one); the first ones are asked for ahead of the angles.
+    const int each = kWarps / a.tile, t = warp / each;
+    const unsigned token = blockIdx.x * (unsigned)a.tile + t;
+    const int b = token < total ? (int)(token / a.N) : 0, i = token < total ? (int)(token % a.N) : 0;
+    const int last = min(a.groups[2], (int)(blockIdx.y + 1) * a.chunk);
+    int at = blockIdx.y * a.chunk + (warp - t * each);
+    auto kind_of = [&](int group) { return group < a.groups[0] ? 0 : group < a.groups[1] ? 1 : 2; };
+    auto head_of = [&](int kind, int group) { return (kind ? group - a.groups[kind - 1] : group) * G + lane / LPR; };
+    auto row_of = [&](int kind, int h) { return static_cast<const T*>(a.src[kind]) + (b * a.ss[kind][0] + i * a.ss[kind][1]) + h * a.ss[kind][2]; };
+    // Groups in flight go through a ring in shared memory, kDepth deep, where a lane copies and
+    // reads its own pieces only.
+    constexpr int PIECES = (int)sizeof(T) / 2;
+    uint4* ring = reinterpret_cast<uint4*>(s_raw) + tid;
+    auto fetch = [&](int group, int slot) {
+        if (!AL) return;
+        if (group < last) {
+            const int kind = kind_of(group), h = head_of(kind, group);
+            const bool in = h < a.heads[kind] && e0 < a.D;
+            const T* from = row_of(kind, in ? h : 0) + (in ? e0 : 0);
+#pragma unroll
+            for (int k = 0; k < PIECES; ++k)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sv::smem_u32(ring + (slot * PIECES + k) * kThreads)),
+                             "l"(from + k * 4), "r"(in ? 16 : 0)
+                             : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int k = 0; k < kDepth - 1; ++k) fetch(at + k * each, k);
     if (tid < a.tile) {
         const unsigned x = blockIdx.x * (unsigned)a.tile + tid;
         int first = -1;
@@ -147,89 +179,125 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
         s_turn[x] = make_float2(cs.x * a.amplitude, a.inverse ? -(cs.y * a.amplitude) : cs.y * a.amplitude);
     }
     __syncthreads();
-    const int each = kWarps / a.tile;  // warps of a token
-    const int t = warp / each;
     const int first = s_first[t];
     if (first < 0) return;
-    const unsigned x = blockIdx.x * (unsigned)a.tile + t;
-    const int b = (int)(x / a.N), i = (int)(x % a.N);
-    int page = -1, slot = 0;
-    if (MODE != DENSE) page = sv::paged_place(a.c, b, first + i, slot);
+    int page = -1, line = 0;
+    if (MODE != DENSE) page = sv::paged_place(a.c, b, first + i, line);
 
-    // This lane's elements: own and partner's factors (0 partner: copied).
-    const int e0 = 8 * (lane % LPR), R = a.R, turned = 2 * R;
-    float c[8], s[8];
+    // This lane's elements: own and partner's factors (elements that are copied: 1 and 0).
+    const int R = a.R, turned = 2 * R;
+    float2 c[4], s[4];
+    {
+        float cc[8], ss[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const int e = e0 + k;
-        c[k] = 1.0f;
-        s[k] = 0.0f;
-        if (e < turned) {
-            const bool second = a.interleaved ? k & 1 : e >= R;
-            const float2 cs = s_turn[t * R + (a.interleaved ? e >> 1 : second ? e - R : e)];
-            c[k] = cs.x;
-            s[k] = second ? cs.y : -cs.y;
+        for (int k = 0; k < 8; ++k) {
+            const int e = e0 + k;
+            cc[k] = 1.0f;
+            ss[k] = 0.0f;
+            if (e < turned) {
+                const bool second = a.interleaved ? k & 1 : e >= R;
+                const float2 cs = s_turn[t * R + (a.interleaved ? e >> 1 : second ? e - R : e)];
+                cc[k] = cs.x;
+                ss[k] = second ? cs.y : -cs.y;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            c[k] = make_float2(cc[2 * k], cc[2 * k + 1]);
+            s[k] = make_float2(ss[2 * k], ss[2 * k + 1]);
         }
     }
-    const bool apart = AL && !a.interleaved && R % 8 == 0;  // the partners are eight elements elsewhere
-    const int other = e0 < R ? e0 + R : e0 - R;
+    // Partners: in this lane, in another lane of the row, or (num_freq no multiple of 8) loaded one by one.
+    const bool lanes = AL && !a.interleaved && R % 8 == 0;
+    const int mate = lanes && e0 < turned ? lane + (e0 < R ? R / 8 : -(R / 8)) : lane;
+    const int same = e0 >= turned ? 0 : min(turned - e0, 8);  // elements of this lane that are turned
 
-    const int r0 = blockIdx.y * a.chunk, r1 = min(a.end[2], r0 + a.chunk);
-    for (int r = r0 + (warp - t * each) * (G * ROWS); r < r1; r += each * G * ROWS) {
-        float v[ROWS][8], p[ROWS][8];
-        int kind[ROWS], head[ROWS];
+    for (int slot = 0; at < last; slot = slot + 1 == kDepth ? 0 : slot + 1) {
+        const int kind = kind_of(at), h = head_of(kind, at);
+        const bool in = h < a.heads[kind];
+        Raw<T, AL> x;
+        if (AL) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
 #pragma unroll
-        for (int z = 0; z < ROWS; ++z) {
-            const int row = r + z * G + lane / LPR;
-            kind[z] = row >= r1 ? -1 : row < a.end[0] ? 0 : row < a.end[1] ? 1 : 2;
-            head[z] = kind[z] <= 0 ? row : row - a.end[kind[z] - 1];
-            const int kz = max(kind[z], 0);
-            const T* from = static_cast<const T*>(a.src[kz]) +
-                            (kind[z] >= 0 ? b * a.ss[kz][0] + i * a.ss[kz][1] + head[z] * a.ss[kz][2] : 0);
-            const int dim = kind[z] >= 0 ? a.D : 0;
-            read8<T, AL>(from, e0, dim, v[z]);
-            if (apart) {
-                read8<T, AL>(from, other, e0 < turned && kind[z] != 2 ? dim : 0, p[z]);
-            } else if (a.interleaved) {
+            for (int k = 0; k < PIECES; ++k) {
+                const uint4 w = ring[(slot * PIECES + k) * kThreads];
+                x.w[4 * k] = w.x;
+                x.w[4 * k + 1] = w.y;
+                x.w[4 * k + 2] = w.z;
+                x.w[4 * k + 3] = w.w;
+            }
+        } else {
+            x.load(row_of(kind, in ? h : 0), e0, in ? a.D : 0);
+        }
+        fetch(at + (kDepth - 1) * each, slot ? slot - 1 : kDepth - 1);  // into the place of the group before
+        at += each;
+        __syncwarp();  // in place: a row's elements are read before any is written
+        float v[8];
+        if (kind != 2) {
+            float p[8];
+            if (a.interleaved) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) p[z][k] = v[z][k ^ 1];
+                for (int k = 0; k < 8; ++k) p[k] = x.at(k ^ 1);
+            } else if (lanes) {
+                Raw<T, AL> y;
+#pragma unroll
+                for (int k = 0; k < Raw<T, AL>::W; ++k) y.w[k] = __shfl_sync(0xffffffffu, x.w[k], mate);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) p[k] = y.at(k);
             } else {
+                const T* from = row_of(kind, in ? h : 0);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const int e = e0 + k;
-                    p[z][k] = e < turned && e < dim ? read1(from, e < R ? e + R : e - R) : 0.0f;
+                    p[k] = in && e < turned && e < a.D ? Raw<T, AL>::one(from, e < R ? e + R : e - R) : 0.0f;
                 }
+                __syncwarp();
             }
-        }
-        __syncwarp();  // in place: a row's elements are read before any is written
 #pragma unroll
-        for (int z = 0; z < ROWS; ++z) {
-            if (kind[z] != 2) {
+            for (int k = 0; k < 4; ++k) {
+                const float2 f = sv::ffma2(make_float2(x.at(2 * k), x.at(2 * k + 1)), c[k], sv::fmul2(make_float2(p[2 * k], p[2 * k + 1]), s[k]));
+                v[2 * k] = f.x;
+                v[2 * k + 1] = f.y;
+            }
+            if (same < 8) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    if (e0 + k < turned) v[z][k] = fmaf(v[z][k], c[k], p[z][k] * s[k]);
+                    if (k >= same) v[k] = x.at(k);
             }
-            const bool dense = MODE == DENSE ? kind[z] >= 0 : kind[z] == 0;
-            if (dense) {
-                const int kz = MODE == DENSE ? kind[z] : 0;
-                T* to = static_cast<T*>(a.dst[kz]) + b * a.ds[kz][0] + i * a.ds[kz][1] + head[z] * a.ds[kz][2];
-                sv::store_row8<T, AL>(to, e0, a.D, v[z]);
+            if (MODE == DENSE || kind == 0) {
+                if (in) {
+                    T* to = static_cast<T*>(a.dst[kind]) + (b * a.ds[kind][0] + i * a.ds[kind][1]) + h * a.ds[kind][2];
+                    sv::store_row8<T, AL>(to, e0, a.D, v);
+                }
+                continue;
             }
-            if (MODE != DENSE && __any_sync(0xffffffffu, kind[z] > 0)) {
-                const bool live = kind[z] > 0 && page >= 0;
-                const int h = kind[z] > 0 ? head[z] : 0, at = live ? page : 0;
-                const int64_t off = at * a.c.page_stride + h * a.c.head_stride + slot * a.c.row_stride;
-                float* scales = kind[z] == 2 ? a.c.v_scale : a.c.k_scale;
-                sv::Eight<float, AL> f;
-                if (AL) {
-                    f.w[0] = make_uint4(__float_as_uint(v[z][0]), __float_as_uint(v[z][1]), __float_as_uint(v[z][2]), __float_as_uint(v[z][3]));
-                    f.w[AL ? 1 : 0] = make_uint4(__float_as_uint(v[z][4]), __float_as_uint(v[z][5]), __float_as_uint(v[z][6]), __float_as_uint(v[z][7]));
+        }
+        if constexpr (MODE != DENSE) {
+            const bool live = in && page >= 0;
+            const int head = in ? h : 0, pg = live ? page : 0;
+            unsigned char* to = (kind == 2 ? a.c.v : a.c.k) + (pg * a.c.page_stride + line * a.c.row_stride) + head * a.c.head_stride;
+            float* scale = (kind == 2 ? a.c.v_scale : a.c.k_scale) + ((int64_t)pg * a.c.heads + head) * a.c.page_size + line;
+            if (kind == 2) {  // values as they are
+                sv::Eight<T, AL> f;
+                if constexpr (AL) {
+#pragma unroll
+                    for (int k = 0; k < (int)sizeof(T) / 2; ++k) f.w[k] = make_uint4(x.w[4 * k], x.w[4 * k + 1], x.w[4 * k + 2], x.w[4 * k + 3]);
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) f.f[AL ? 0 : k] = v[z][k];
+                    for (int k = 0; k < 8; ++k) f.f[k] = x.at(k);
                 }
-                sv::store_cache_row<float, LPR, MODE == CACHE_E4M3, AL>(
-                    (kind[z] == 2 ? a.c.v : a.c.k) + off, scales + ((int64_t)at * a.c.heads + h) * a.c.page_size + slot, e0, a.D, live, f);
+                sv::store_cache_row<T, LPR, MODE == CACHE_E4M3, AL>(to, scale, e0, a.D, live, f);
+            } else {
+                sv::Eight<float, AL> f;
+                if constexpr (AL) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        f.w[k] = make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3]));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) f.f[k] = v[k];
+                }
+                sv::store_cache_row<float, LPR, MODE == CACHE_E4M3, AL>(to, scale, e0, a.D, live, f);
             }
         }
     }
@@ -238,19 +306,23 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 template <typename T, int LPR, int MODE, bool AL>
 cudaError_t launch_lpr(RotaryArgs& a, cudaStream_t stream) {
     const int64_t tokens = (int64_t)a.B * a.N;
-    const int rows = a.end[2];
-    int sms = 152;
+    constexpr int sms = 152, G = 32 / LPR;
+    for (int k = 0, n = 0; k < 3; ++k) a.groups[k] = n += (a.heads[k] + G - 1) / G;
     // Tokens of a block: as many as leave six blocks per SM, since they share the frequencies;
     // a few tokens are spread over blocks by their rows instead, one pass of a block's warps each.
     a.tile = 1;
     while (a.tile < kMaxTokens && tokens / (2 * a.tile) >= 6 * sms) a.tile *= 2;
-    constexpr int pass = kWarps * (32 / LPR);
-    a.chunk = tokens >= 2 * sms ? rows : pass;
-    if (a.chunk < 1) a.chunk = 1;
-    const dim3 grid((unsigned)((tokens + a.tile - 1) / a.tile), (unsigned)((rows + a.chunk - 1) / a.chunk));
+    a.chunk = tokens >= 2 * sms ? a.groups[2] : kWarps;
+    const dim3 grid((unsigned)((tokens + a.tile - 1) / a.tile), (unsigned)((a.groups[2] + a.chunk - 1) / a.chunk));
     const size_t smem = (size_t)a.tile * a.R * sizeof(float2);
-    if (tokens >= 2 * sms) return sv::launch_serial(rotary_kernel<T, LPR, MODE, AL, AL ? 2 : 1>, grid, dim3(kThreads), smem, stream, a);
-    return sv::launch_serial(rotary_kernel<T, LPR, MODE, AL, 1>, grid, dim3(kThreads), smem, stream, a);
+    constexpr size_t ring = AL ? kDepth * kThreads * sizeof(T) * 8 : 0;
+    static sv::KernelLaunchCache cache;
+    auto kern = rotary_kernel<T, LPR, MODE, AL>;
+    int max_dyn = 0;
+    const cudaError_t e = cache.setup((const void*)kern, &max_dyn);
+    if (e != cudaSuccess) return e;
+    if (ring + smem > (size_t)max_dyn) return cudaErrorInvalidValue;
+    return sv::launch_serial(kern, grid, dim3(kThreads), ring + smem, stream, a);
 }
 
 template <typename T, int MODE>
@@ -317,8 +389,8 @@ sv_status spec_rotary(const void* q, const int64_t* q_stride, int num_q_heads, c
     a.dst[0] = out_q;
     al &= take_strides(a.ss[0], q_stride, q, es);
     al &= take_strides(a.ds[0], out_q_stride, out_q, es);
-    a.end[0] = num_q_heads;
-    a.end[1] = a.end[2] = num_q_heads + num_k_heads;
+    a.heads[0] = num_q_heads;
+    a.heads[1] = num_k_heads;
     if (num_k_heads) {
         a.src[1] = k;
         a.dst[1] = out_k;
@@ -356,9 +428,8 @@ sv_status spec_rotary_append(const void* q, const int64_t* q_stride, int num_q_h
     a.src[2] = value;
     al &= take_strides(a.ss[1], kv_stride, key, es);
     al &= take_strides(a.ss[2], kv_stride, value, es);
-    a.end[0] = num_q_heads;
-    a.end[1] = num_q_heads + cache->num_heads;
-    a.end[2] = a.end[1] + cache->num_heads;
+    a.heads[0] = num_q_heads;
+    a.heads[1] = a.heads[2] = cache->num_heads;
     a.base = base;
     a.new_len = new_len;
     return sv::launch_status(launch(a, cache->dtype == SV_CACHE_BF16 ? CACHE_BF16 : CACHE_E4M3, dt, al, (cudaStream_t)stream));
