@@ -596,11 +596,20 @@ def _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, B):
                       sp * es, sh * es, max(sr, D) * es if ps == 1 else sr * es, code, P, ps, table[1], H, D)
 
 
+_strides = {}
+
+
 def _strides3(t, name):
-    """Element strides of the first three dimensions of [B][N][heads][head_dim]."""
-    if t.stride(3) != 1 and t.shape[3] > 1:
+    """Element strides of the first three dimensions of [B][N][heads][head_dim], as a C array (only read)."""
+    stride = t.stride()
+    if stride[3] != 1 and t.shape[3] > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return (ctypes.c_int64 * 3)(*t.stride()[:3])
+    got = _strides.get(stride)
+    if got is None:
+        if len(_strides) >= 4096:
+            _strides.clear()
+        got = _strides[stride] = (ctypes.c_int64 * 3)(*stride[:3])
+    return got
 
 
 def _src_code(dtype, name) -> int:
@@ -1063,6 +1072,22 @@ def spec_block_summary(k_pages, page_table, base, num_tokens: int, *, kind: str 
     return summary
 
 
+_select_needs = {}
+
+
+def _need(known, ask, at, *sizes):
+    """ask(*sizes) on a device, remembered by the sizes."""
+    key = (at, *sizes)
+    need = known.get(key)
+    if need is None:
+        with _torch().cuda.device(at):
+            need = int(ask(*sizes))
+        if len(known) >= 4096:  # sizes vary: keep the table small
+            known.clear()
+        known[key] = need
+    return need
+
+
 def spec_block_select_workspace_size(B: int, Q: int, num_q_heads: int, num_heads: int, max_pages: int,
                                      shared: bool) -> int:
     """Bytes of scratch of such a spec_block_select."""
@@ -1106,7 +1131,7 @@ def spec_block_select(q, summary, page_table, base, page_size: int, top_k: int, 
     if out is None:
         out = _new(torch.empty, shape, torch.int32, at, side)
     if auto:
-        need = lib().spec_block_select_workspace_size(B, Q, Hq, H, table[1], int(bool(shared)))
+        need = _need(_select_needs, lib().spec_block_select_workspace_size, at, B, Q, Hq, H, table[1], int(bool(shared))) if B else 0
         workspace = _new(torch.empty, (need,), torch.uint8, at, side) if need else None
     elif workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
@@ -1130,19 +1155,6 @@ def spec_sparse_attention_workspace_size(B: int, Q: int, num_q_heads: int, num_h
 
 
 _sparse_needs = {}
-
-
-def _sparse_need(at, *sizes):
-    """spec_sparse_attention_workspace_size(*sizes) on a device, remembered by the sizes."""
-    key = (at, *sizes)
-    need = _sparse_needs.get(key)
-    if need is None:
-        with _torch().cuda.device(at):
-            need = int(lib().spec_sparse_attention_workspace_size(*sizes))
-        if len(_sparse_needs) >= 4096:
-            _sparse_needs.clear()
-        _sparse_needs[key] = need
-    return need
 
 
 def spec_sparse_attention(q, k_pages, v_pages, page_table, base, blocks, *, new_len=None, tree_mask=None, scale=None,
@@ -1184,7 +1196,8 @@ def spec_sparse_attention(q, k_pages, v_pages, page_table, base, blocks, *, new_
     if out_lse is None and want_lse:
         out_lse = _new(torch.empty, (B, Q, Hq), torch.float32, at, side)
     if auto:
-        need = _sparse_need(at, B, Q, Hq, H, D, cache.dtype, cache.page_size, n, shared) if B else 0
+        need = _need(_sparse_needs, lib().spec_sparse_attention_workspace_size, at, B, Q, Hq, H, D, cache.dtype,
+                     cache.page_size, n, shared) if B else 0
         workspace = _new(torch.empty, (need,), torch.uint8, at, side) if need else None
     elif workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")

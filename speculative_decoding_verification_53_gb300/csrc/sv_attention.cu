@@ -697,7 +697,7 @@ cudaError_t run_attention(AttnArgs& a, const Plan& p, const uint16_t* q, const i
     const int pairs = B * a.c.heads;
     const unsigned ctas = (unsigned)p.ctas;
     cudaError_t e;
-    if (a.lists == 3) e = sv::launch_list_attention(a, pairs, p.part_rows, ctas, bits, s);
+    if (a.lists == 3) e = sv::launch_list_attention(a, pairs, e4m3, p.part_rows, ctas, bits, s);
     else if (p.tile_rows >= 128) e = sv::launch_attn_tc(a, pairs, e4m3, p.tile_rows, p.dual, ctas, s);
     else if (D <= 64) e = e4m3 ? launch_few<64, true>(a, pairs, ctas, s) : launch_few<64, false>(a, pairs, ctas, s);
     else if (D <= 128) e = e4m3 ? launch_few<128, true>(a, pairs, ctas, s) : launch_few<128, false>(a, pairs, ctas, s);
@@ -754,14 +754,21 @@ bool sparse_plan(int B, int Q, int Hq, int H, int D, bool e4m3, int page_size, i
     if (num_blocks < 0 || num_blocks > kMaxListed || page_size < 1 || page_size > 65536 ||
         (int64_t)page_size * (num_blocks + 2) + Q > sv::PAGED_MAX_POS)
         return false;
+    // Up to 32 query rows over a list or a union of lists: the kernel for few queries.  Lists that a row's
+    // queries share, 64 pages of 64, 32 over 8 heads of 128, against the kernels of contexts over the list's
+    // page table (us): 16 tokens bf16 57 and 77, e4m3 51 and 73; 64 tokens over 32 pages 112 and 117, 90
+    // and 114; 16 chains of 6 64 and 81, 73 and 109; one token 17 and 19, 18 and 21; but one chain of 6 24 and 20.
     const int g = Hq / H;
     // Queries whose lists are united: as many as 32 rows hold, in tiles of one size.
     int tile = g <= 32 ? 32 / g : 0, tiles = tile ? (Q + tile - 1) / tile : 0;
     if (tile) tile = (Q + tiles - 1) / tiles;
-    sp.mode = shared || Q == 1 ? 1 : unite && !e4m3 && D <= 128 && tile && (int64_t)tile * num_blocks <= kMaxUnion &&
-              (int64_t)page_size * (tile * num_blocks + 2) + Q <= sv::PAGED_MAX_POS ? 3 : 2;
+    shared |= Q == 1;
+    const int united = shared ? num_blocks : tile * num_blocks;  // blocks of a tile's union
+    const bool few = unite && D <= 128 && tile && (!shared || tiles == 1) && united <= kMaxUnion &&
+                     (int64_t)page_size * (united + 2) + Q <= sv::PAGED_MAX_POS;
+    sp.mode = few ? 3 : shared ? 1 : 2;
     sp.lists = sp.mode == 1 ? 1 : sp.mode == 2 ? Q : tiles;
-    sp.most = sp.mode == 3 ? tile * num_blocks : num_blocks;
+    sp.most = sp.mode == 3 ? united : num_blocks;
     sp.rows = (int64_t)B * H * sp.lists;
     if (sp.rows >= ((int64_t)1 << 31)) return false;
     sp.width = sp.most + (int)(((int64_t)Q + 2 * page_size - 2) / page_size);
@@ -896,7 +903,7 @@ sv_status spec_sparse_attention(const void* q, const int64_t* q_stride, int num_
     uint32_t* bits = reinterpret_cast<uint32_t*>(list_base + sp.rows);
     cudaError_t e;
     if (sp.mode == 3)
-        e = sv::launch_list_unions(a.c, base, new_len, blocks, num_blocks, Q, sp.query_tiles, sp.lists, sp.rows, table, bits, list_base,
+        e = sv::launch_list_unions(a.c, base, new_len, blocks, num_blocks, Q, sp.query_tiles, sp.lists, shared != 0 || Q == 1, sp.rows, table, bits, list_base,
                                    sp.width, sp.most < cache->max_pages ? sp.most : cache->max_pages, s);
     else
         e = sv::launch_block_tables(a.c, base, new_len, blocks, num_blocks, sp.lists, sp.rows, Q, table, list_base, sp.width, s);

@@ -299,12 +299,11 @@ cudaError_t launch_block_tables(const PagedCache& c, const int32_t* base, const 
                                 int num_blocks, int lists, int64_t rows, int Q, int32_t* table, int32_t* out_base,
                                 int width, cudaStream_t stream);
 
-// The kernel for queries with a list each (sv_attention_lists.cu): bf16, heads of up to 128, tiles of up to
-// 32 rows; and the unions of the lists of a tile's queries, of at most `most` blocks, with a bit for each
+// The kernel for few queries over lists (sv_attention_lists.cu): heads of up to 128, tiles of up to 32 rows; and the unions of the lists of a tile's queries, of at most `most` blocks, with a bit for each
 // query that listed a block.
-cudaError_t launch_list_attention(const AttnArgs& a, int pairs, int rows, unsigned ctas, const uint32_t* bits, cudaStream_t stream);
+cudaError_t launch_list_attention(const AttnArgs& a, int pairs, bool e4m3, int rows, unsigned ctas, const uint32_t* bits, cudaStream_t stream);
 cudaError_t launch_list_unions(const PagedCache& c, const int32_t* base, const int32_t* new_len, const int32_t* blocks,
-                               int num_blocks, int Q, int query_tile, int tiles, int64_t rows, int32_t* table, uint32_t* bits,
+                               int num_blocks, int Q, int query_tile, int tiles, bool shared, int64_t rows, int32_t* table, uint32_t* bits,
                                int32_t* out_base, int width, int most, cudaStream_t stream);
 
 }  // namespace sv

@@ -51,6 +51,19 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t r[4]) {
                  : "r"(addr)
                  : "memory");
 }
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+// Two e4m3 codes in the low half of w to a bf16 pair (exact).
+__device__ __forceinline__ uint32_t widen(uint32_t w) {
+    const float2 f = sv::e4m3x2_to_f32(w);
+    return sv::bf16x2(f.x, f.y);
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -62,23 +75,27 @@ __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Byte offset of 16-byte piece c of row r; the pieces of eight rows lie in different banks.
+// Byte offset of 16-byte piece c of row r; the pieces of eight rows lie in different banks (of two rows where
+// e4m3 keys are read, two rows at a time).
 template <int PITCH>
-__device__ __forceinline__ int piece(int r, int c) { return r * PITCH + ((c ^ (r & 7)) << 4); }
+__device__ __forceinline__ int piece(int r, int c) { return r * PITCH + ((PITCH >= 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4); }
+template <int PITCH>
+__device__ __forceinline__ int code_piece(int r, int c) { return r * PITCH + ((PITCH >= 128 ? c ^ ((r & 1) << 2) : c) << 4); }
 
-template <int DP, int NQ>
+template <int DP, int NQ, bool E4M3>
 struct Lists {
-    static constexpr int PITCH = 2 * DP, CH = PITCH / 16;
+    static constexpr int PITCH = (E4M3 ? 1 : 2) * DP, CH = PITCH / 16;
     static constexpr int MAT = TN * PITCH;   // a tile of keys, or of values
-    static constexpr int STAGE = 2 * MAT;
-    static constexpr int STAGES = 2;  // three CTAs an SM; with 3 stages two, 8 chains of 6: 55 us against 43
+    static constexpr int STAGE = 2 * MAT + (E4M3 ? 2 * TN * 4 : 0);
+    // Three CTAs an SM; with 3 stages of bf16 two, 8 chains of 6: 55 us against 43.
+    static constexpr int STAGES = E4M3 ? 3 : 2;
     static constexpr int RING = 4;           // places and bits of the tiles in flight
     static_assert(STAGES < RING, "a tile's places outlive its copies");
     static constexpr int ROWS = 8 * NQ;
-    static constexpr int QBYTES = ROWS * PITCH;
+    static constexpr int QBYTES = ROWS * DP * 2;
     static constexpr int OP = DP + 4;        // floats of a row where the warps meet
-    static constexpr int SMEM = STAGES * STAGE + QBYTES;
-    static_assert(KW * ROWS * OP * 4 <= SMEM, "the join of the warps reuses the stages and the queries");
+    static constexpr int JOIN = KW * ROWS * OP * 4;  // which reuses the stages and the queries
+    static constexpr int SMEM = STAGES * STAGE + QBYTES > JOIN ? STAGES * STAGE + QBYTES : JOIN;
 };
 
 // Which of the tile's queries (bit x: query first + x) see position `pos` of the list's sequence by the
@@ -95,13 +112,14 @@ __device__ __forceinline__ uint32_t who_sees(const AttnArgs& a, const AttnTile& 
     return m;
 }
 
-template <int DP, int NQ>
+template <int DP, int NQ, bool E4M3>
 __global__ void __launch_bounds__(THREADS, NQ == 4 ? 2 : 3)
     list_attention_kernel(const __grid_constant__ AttnArgs a, const int pairs, const uint32_t* bits) {
-    using S = Lists<DP, NQ>;
+    using S = Lists<DP, NQ, E4M3>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t s_off[S::RING][TN];   // byte offset of each position's row, -1: nothing there
     __shared__ uint32_t s_see[S::RING][TN];  // queries that see it
+    __shared__ int64_t s_sc[E4M3 ? S::RING : 1][E4M3 ? TN : 1];  // index of its scales
     __shared__ float s_m[KW][S::ROWS], s_l[KW][S::ROWS];
 
     sv::pdl_trigger();
@@ -109,7 +127,7 @@ __global__ void __launch_bounds__(THREADS, NQ == 4 ? 2 : 3)
     AttnTile t;
     if (!sv::attn_tile(a, pairs, blockIdx.x, S::ROWS, 1, t)) return;
     const int tid = threadIdx.x, lane = tid & 31, wk = tid >> 5, g = lane >> 2, t4 = lane & 3;
-    const int D = a.c.dim, row_bytes = 2 * D, rows = t.r1 - t.r0;
+    const int D = a.c.dim, row_bytes = (E4M3 ? 1 : 2) * D, rows = t.r1 - t.r0;
     const int tiles = (t.end - t.begin + TN - 1) / TN;
     const unsigned char* kbase = a.c.k + t.h * a.c.head_stride;
     const unsigned char* vbase = a.c.v + t.h * a.c.head_stride;
@@ -119,7 +137,7 @@ __global__ void __launch_bounds__(THREADS, NQ == 4 ? 2 : 3)
     const uint32_t* own_bits = bits + (int64_t)t.row * a.c.max_pages;
 
     // Place and bits of a position of tile j, looked up a tile ahead of its copies.
-    int64_t next_off = -1;
+    int64_t next_off = -1, next_sc = 0;
     uint32_t next_see = 0u;
     const int ps = a.c.page_size, shift = (ps & (ps - 1)) == 0 ? __ffs(ps) - 1 : -1;
     const int32_t* pages = a.c.table + (int64_t)t.row * a.c.max_pages;
@@ -132,44 +150,66 @@ __global__ void __launch_bounds__(THREADS, NQ == 4 ? 2 : 3)
             const int block = shift >= 0 ? pos >> shift : pos / ps;
             const int page = __ldg(pages + block);
             next_see = who_sees(a, t, own_bits, listed, pos, block, first, queries);
-            if ((unsigned)page < (unsigned)a.c.num_pages) next_off = page * a.c.page_stride + (pos - block * ps) * a.c.row_stride;
+            const int line = pos - block * ps;
+            if ((unsigned)page < (unsigned)a.c.num_pages) next_off = page * a.c.page_stride + line * a.c.row_stride;
             else next_see = 0u;
+            if (E4M3) next_sc = ((int64_t)page * a.c.heads + t.h) * ps + line;
         }
     };
     auto put_place = [&](int j) {
         if (tid >= TN) return;
         s_off[j % S::RING][tid] = next_off;
         s_see[j % S::RING][tid] = next_see;
+        if (E4M3) s_sc[j % S::RING][tid] = next_sc;
     };
     constexpr int RPI = THREADS / S::CH;  // rows per instruction of a copy: a thread keeps to one piece of a row
     static_assert(RPI % 8 == 0, "and to one place in the banks");
     const int my_c = tid % S::CH, my_r = tid / S::CH;
     const int most = row_bytes - 16 * my_c < 16 ? (row_bytes - 16 * my_c < 0 ? 0 : row_bytes - 16 * my_c) : 16;
-    const uint32_t my_place = smem0 + piece<S::PITCH>(my_r, my_c);
+    const uint32_t my_place = smem0 + (E4M3 ? code_piece<S::PITCH>(my_r, my_c) : piece<S::PITCH>(my_r, my_c));
+    const uint32_t my_value = smem0 + S::MAT + piece<S::PITCH>(my_r, my_c);
     const unsigned char* my_k = kbase + (most ? 16 * my_c : 0);
     const int64_t to_v = vbase - kbase;
     auto load_tile = [&](int j) {
         if (j < tiles) {
-            const uint32_t to = my_place + (j % S::STAGES) * S::STAGE;
+            const uint32_t st = (j % S::STAGES) * S::STAGE;
             const int64_t* off = s_off[j % S::RING] + my_r;
 #pragma unroll
             for (int x = 0; x < TN / RPI; ++x) {
                 const int64_t o = off[x * RPI];
                 const int bytes = o < 0 ? 0 : most;
                 const unsigned char* from = my_k + (o < 0 ? 0 : o);
-                cp_async16(to + x * RPI * S::PITCH, from, bytes);
-                cp_async16(to + x * RPI * S::PITCH + S::MAT, from + to_v, bytes);
+                cp_async16(my_place + st + x * RPI * S::PITCH, from, bytes);
+                cp_async16(my_value + st + x * RPI * S::PITCH, from + to_v, bytes);
+            }
+            if (E4M3) {  // one scale per thread: keys', then values'
+                const int p = tid & (TN - 1);
+                const bool there = s_off[j % S::RING][p] >= 0;
+                cp_async4(smem0 + st + 2 * S::MAT + 4 * tid, (tid < TN ? a.c.k_scale : a.c.v_scale) + (there ? s_sc[E4M3 ? j % S::RING : 0][E4M3 ? p : 0] : 0), there ? 4 : 0);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     // the queries, zero behind the last real row
-    for (int f = tid; f < S::ROWS * S::CH; f += THREADS) {
-        const int r = f / S::CH, c = f % S::CH, R = t.r0 + r;
+    for (int f = tid; f < S::ROWS * (DP / 8); f += THREADS) {
+        const int r = f / (DP / 8), c = f % (DP / 8), R = t.r0 + r;
         uint4 w = make_uint4(0u, 0u, 0u, 0u);
         if (r < rows && 8 * c < D)
             w = sv::ld_nc_v4(a.q + t.b * a.q_sb + (int64_t)(R / a.group) * a.q_st + (int64_t)(t.h * a.group + R % a.group) * a.q_sh + 8 * c);
-        *reinterpret_cast<uint4*>(smem + S::STAGES * S::STAGE + piece<S::PITCH>(r, c)) = w;
+        unsigned char* to = smem + S::STAGES * S::STAGE;
+        if (!E4M3) {
+            *reinterpret_cast<uint4*>(to + piece<2 * DP>(r, c)) = w;
+        } else {
+            // A lane takes 16 contiguous codes of a key, which fixes an order of elements within a product:
+            // element 64 e + 16 u + 4 s + 2 v + z goes to place 16 (4 e + s) + 8 v + 2 u + z.
+            const int e = c >> 3, u = (c >> 1) & 3, s0 = (c & 1) * 2;
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int at = 16 * (4 * e + s0 + (j >> 1)) + 8 * (j & 1) + 2 * u;
+                *reinterpret_cast<uint32_t*>(to + piece<2 * DP>(r, at >> 3) + 2 * (at & 7)) = ww[j];
+            }
+        }
     }
     // bits of this lane's two columns of each row tile (a row that is not real sees nothing)
     uint32_t col[NQ][2];
@@ -210,7 +250,11 @@ __global__ void __launch_bounds__(THREADS, NQ == 4 ? 2 : 3)
                 for (int f = tid; f < TN * S::CH; f += THREADS) {
                     uint4* p = reinterpret_cast<uint4*>(stage + S::MAT + piece<S::PITCH>(f / S::CH, f % S::CH));
                     uint4 v = *p;
-                    if (sv::sanitise<false>(v)) *p = v;
+                    if (sv::sanitise<E4M3>(v)) *p = v;
+                }
+                if (E4M3 && tid >= TN) {
+                    float* p = reinterpret_cast<float*>(stage + 2 * S::MAT) + tid;
+                    if (sv::not_finite(*p)) *p = 0.0f;
                 }
             }
             __syncthreads();  // tile j is whole; tile j - 1 is no longer read
@@ -226,24 +270,57 @@ __global__ void __launch_bounds__(THREADS, NQ == 4 ? 2 : 3)
             for (int n = 0; n < NQ; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
             const int kr = 16 * wk + (lane & 15), kc = lane >> 4;  // 16 positions by 16 elements
             const int qr = lane & 7, qc = lane >> 3;               // 8 rows by 32 elements
-#pragma unroll
-            for (int k = 0; k < DP / 32; ++k) {
-                uint32_t x[2][4];
-                ldsm4(ks0 + piece<S::PITCH>(kr, 4 * k + kc), x[0]);
-                ldsm4(ks0 + piece<S::PITCH>(kr, 4 * k + 2 + kc), x[1]);
+            auto multiply = [&](int k, const uint32_t x[2][4]) {   // 32 elements
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
                     uint32_t q[4];
-                    ldsm4(q0 + piece<S::PITCH>(8 * n + qr, 4 * k + qc), q);
+                    ldsm4(q0 + piece<2 * DP>(8 * n + qr, 4 * k + qc), q);
                     mma16816(s[n], x[0], q[0], q[1]);
                     mma16816(s[n], x[1], q[2], q[3]);
                 }
+            };
+            if constexpr (!E4M3) {
+#pragma unroll
+                for (int k = 0; k < DP / 32; ++k) {
+                    uint32_t x[2][4];
+                    ldsm4(ks0 + piece<S::PITCH>(kr, 4 * k + kc), x[0]);
+                    ldsm4(ks0 + piece<S::PITCH>(kr, 4 * k + 2 + kc), x[1]);
+                    multiply(k, x);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < DP / 64; ++e) {
+                    const uint4 w0 = lds16(ks0 + code_piece<S::PITCH>(16 * wk + g, 4 * e + t4));
+                    const uint4 w1 = lds16(ks0 + code_piece<S::PITCH>(16 * wk + 8 + g, 4 * e + t4));
+                    auto codes = [&](uint32_t u0, uint32_t u1, uint32_t x[4]) {
+                        x[0] = widen(u0 & 0xffffu);
+                        x[1] = widen(u1 & 0xffffu);
+                        x[2] = widen(u0 >> 16);
+                        x[3] = widen(u1 >> 16);
+                    };
+                    uint32_t x[2][4];
+                    codes(w0.x, w1.x, x[0]);
+                    codes(w0.y, w1.y, x[1]);
+                    multiply(2 * e, x);
+                    codes(w0.z, w1.z, x[0]);
+                    codes(w0.w, w1.w, x[1]);
+                    multiply(2 * e + 1, x);
+                }
+            }
+            // scores' factors of positions g and g + 8, and values' scales, which their probabilities take
+            float ks[2] = {a.scale_log2, a.scale_log2}, vs[2];
+            if (E4M3) {
+                const float* sc = reinterpret_cast<const float*>(stage + 2 * S::MAT) + 16 * wk + g;
+                ks[0] *= sc[0];
+                ks[1] *= sc[8];
+                vs[0] = sc[TN];
+                vs[1] = sc[TN + 8];
             }
             bool grow = false;
-            const float2 sc = make_float2(a.scale_log2, a.scale_log2);
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
-                const float2 u = sv::fmul2(make_float2(s[n][0], s[n][1]), sc), w = sv::fmul2(make_float2(s[n][2], s[n][3]), sc);
+                const float2 u = sv::fmul2(make_float2(s[n][0], s[n][1]), make_float2(ks[0], ks[0]));
+                const float2 w = sv::fmul2(make_float2(s[n][2], s[n][3]), make_float2(ks[1], ks[1]));
                 s[n][0] = see0 & col[n][0] ? u.x : neg_inf();
                 s[n][1] = see0 & col[n][1] ? u.y : neg_inf();
                 s[n][2] = see1 & col[n][0] ? w.x : neg_inf();
@@ -278,17 +355,40 @@ __global__ void __launch_bounds__(THREADS, NQ == 4 ? 2 : 3)
                 for (int x = 0; x < 4; ++x) {
                     e[x] = sv::ex2(s[n][x] - mx[n][x & 1]);
                     l[n][x & 1] += e[x];
+                    if (E4M3) e[x] *= vs[x >> 1];
                 }
                 p[n][0] = transpose8x8(sv::bf16x2(e[0], e[1]));
                 p[n][1] = transpose8x8(sv::bf16x2(e[2], e[3]));
             }
-            const int vr = 16 * wk + ((lane >> 4) << 3) + (lane & 7), vc = (lane >> 3) & 1;
+            if constexpr (!E4M3) {
+                const int vr = 16 * wk + ((lane >> 4) << 3) + (lane & 7), vc = (lane >> 3) & 1;
 #pragma unroll
-            for (int d = 0; d < DP / 16; ++d) {
-                uint32_t x[4];
-                ldsm4t(vs0 + piece<S::PITCH>(vr, 2 * d + vc), x);
+                for (int d = 0; d < DP / 16; ++d) {
+                    uint32_t x[4];
+                    ldsm4t(vs0 + piece<S::PITCH>(vr, 2 * d + vc), x);
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) mma16816(o[d][n], x, p[n][0], p[n][1]);
+                    for (int n = 0; n < NQ; ++n) mma16816(o[d][n], x, p[n][0], p[n][1]);
+                }
+            } else {
+                // Transposed in pairs of codes: 32 elements are two tiles, of the even and of the odd ones.
+                const int vr = 16 * wk + (((lane >> 3) & 1) << 3) + (lane & 7), vc = lane >> 4;
+#pragma unroll
+                for (int d = 0; d < DP / 32; ++d) {
+                    uint32_t y[4], x[2][4];  // positions 0-7 and 8-15 of 16 elements, then of the next 16
+                    ldsm4t(vs0 + piece<S::PITCH>(vr, 2 * d + vc), y);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const uint32_t w = __byte_perm(y[z], 0u, 0x3120);
+                        const int to = z == 1 ? 2 : z == 2 ? 1 : z;
+                        x[0][to] = widen(w & 0xffffu);
+                        x[1][to] = widen(w >> 16);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        mma16816(o[2 * d][n], x[0], p[n][0], p[n][1]);
+                        mma16816(o[2 * d + 1][n], x[1], p[n][0], p[n][1]);
+                    }
+                }
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -319,11 +419,18 @@ __global__ void __launch_bounds__(THREADS, NQ == 4 ? 2 : 3)
                 s_m[wk][r] = lim[n][z] == neg_inf() ? neg_inf() : mx[n][z];
                 s_l[wk][r] = w;
             }
-            float* to = reinterpret_cast<float*>(smem) + (wk * S::ROWS + r) * S::OP + g;
+            float* to = reinterpret_cast<float*>(smem) + (wk * S::ROWS + r) * S::OP;
 #pragma unroll
-            for (int d = 0; d < DP / 16; ++d) {
-                to[16 * d] = o[d][n][z];
-                to[16 * d + 8] = o[d][n][2 + z];
+            for (int d = 0; d < DP / 16; d += 2) {
+                if (!E4M3) {
+                    to[16 * d + g] = o[d][n][z];
+                    to[16 * d + g + 8] = o[d][n][2 + z];
+                    to[16 * d + g + 16] = o[d + 1][n][z];
+                    to[16 * d + g + 24] = o[d + 1][n][2 + z];
+                } else {
+                    *reinterpret_cast<float2*>(to + 16 * d + 2 * g) = make_float2(o[d][n][z], o[d + 1][n][z]);
+                    *reinterpret_cast<float2*>(to + 16 * d + 2 * g + 16) = make_float2(o[d][n][2 + z], o[d + 1][n][2 + z]);
+                }
             }
         }
     __syncthreads();
@@ -358,7 +465,7 @@ __global__ void __launch_bounds__(THREADS, NQ == 4 ? 2 : 3)
                 if (!((who_sees(a, t, own_bits, listed, pos, pos / ps, first, queries) >> (i - first)) & 1u)) continue;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const float w = sv::attn_value<false>(a, t, pos, d + x);
+                    const float w = sv::attn_value<E4M3>(a, t, pos, d + x);
                     if (sv::not_finite(w)) out[x] += w;
                 }
             }
@@ -407,7 +514,7 @@ __device__ __forceinline__ void each_taken(const int32_t* list, int64_t stride, 
 // those from base / page_size on), the union's bits, and the positions before the chunk.
 __global__ void __launch_bounds__(kUnionThreads) list_union_kernel(const __grid_constant__ sv::PagedCache c, const int32_t* base,
                                                                    const int32_t* new_len, const int32_t* blocks, int num_blocks,
-                                                                   int Q, int query_tile, int tiles, int32_t* table,
+                                                                   int Q, int query_tile, int tiles, int shared, int32_t* table,
                                                                    uint32_t* bits, int32_t* out_base, int width, int most) {
     extern __shared__ uint32_t s_dyn[];  // [most] bits of each block of the union, [words] blocks, [words] how many before
     __shared__ int s_sum[kUnionWarps];
@@ -421,14 +528,15 @@ __global__ void __launch_bounds__(kUnionThreads) list_union_kernel(const __grid_
         return;
     }
     const int full = first / c.page_size, words = (full + 31) / 32;
-    const int i0 = mt * query_tile, queries = max(0, min(query_tile, n - i0));
+    // shared: one list for all queries
+    const int i0 = shared ? 0 : mt * query_tile, queries = shared ? 1 : max(0, min(query_tile, n - i0));
     uint32_t* s_mask = s_dyn;
     uint32_t* s_in = s_dyn + most;
     uint32_t* s_before = s_in + words;
     for (int w = tid; w < words; w += kUnionThreads) s_in[w] = 0u;
     for (int w = tid; w < most; w += kUnionThreads) s_mask[w] = 0u;
     __syncthreads();
-    const int32_t* list = blocks + (((int64_t)b * Q + i0) * c.heads + h) * num_blocks;
+    const int32_t* list = blocks + (((int64_t)b * (shared ? 1 : Q) + i0) * c.heads + h) * num_blocks;
     const int64_t stride = (int64_t)c.heads * num_blocks;
     each_taken(list, stride, num_blocks, queries, full, [&](int e, int) { atomicOr(&s_in[e >> 5], 1u << (e & 31)); });
     __syncthreads();
@@ -462,17 +570,17 @@ __global__ void __launch_bounds__(kUnionThreads) list_union_kernel(const __grid_
         if (atomicOr(&s_mask[rank], 1u << x) == 0u) to[rank] = __ldg(pages + e);  // the first of them
     });
     __syncthreads();
-    for (int x = tid; x < count; x += kUnionThreads) to_bits[x] = s_mask[x];
+    for (int x = tid; x < count; x += kUnionThreads) to_bits[x] = shared ? ~0u : s_mask[x];
     const int last = n ? (first + n - 1) / c.page_size : full - 1;
     for (int k = tid; full + k <= last; k += kUnionThreads) to[count + k] = __ldg(pages + full + k);
     if (tid == 0) out_base[row] = count * c.page_size + (first - full * c.page_size);
 }
 
-template <int DP, int NQ>
+template <int DP, int NQ, bool E4M3>
 cudaError_t launch_rows(const AttnArgs& a, int pairs, unsigned ctas, const uint32_t* bits, cudaStream_t stream) {
-    using S = Lists<DP, NQ>;
+    using S = Lists<DP, NQ, E4M3>;
     static sv::KernelLaunchCache cache;
-    auto kern = list_attention_kernel<DP, NQ>;
+    auto kern = list_attention_kernel<DP, NQ, E4M3>;
     int max_dyn = 0;
     const cudaError_t e = cache.setup((const void*)kern, &max_dyn);
     if (e != cudaSuccess) return e;
@@ -480,24 +588,25 @@ cudaError_t launch_rows(const AttnArgs& a, int pairs, unsigned ctas, const uint3
     return sv::launch_serial(kern, dim3(ctas), dim3(THREADS), S::SMEM, stream, a, pairs, bits);
 }
 
-template <int DP>
+template <int DP, bool E4M3>
 cudaError_t launch_dim(const AttnArgs& a, int pairs, int rows, unsigned ctas, const uint32_t* bits, cudaStream_t stream) {
-    if (rows <= 8) return launch_rows<DP, 1>(a, pairs, ctas, bits, stream);
-    if (rows <= 16) return launch_rows<DP, 2>(a, pairs, ctas, bits, stream);
-    if (rows <= 24) return launch_rows<DP, 3>(a, pairs, ctas, bits, stream);
-    return launch_rows<DP, 4>(a, pairs, ctas, bits, stream);
+    if (rows <= 8) return launch_rows<DP, 1, E4M3>(a, pairs, ctas, bits, stream);
+    if (rows <= 16) return launch_rows<DP, 2, E4M3>(a, pairs, ctas, bits, stream);
+    if (rows <= 24) return launch_rows<DP, 3, E4M3>(a, pairs, ctas, bits, stream);
+    return launch_rows<DP, 4, E4M3>(a, pairs, ctas, bits, stream);
 }
 
 }  // namespace
 
 namespace sv {
 
-cudaError_t launch_list_attention(const AttnArgs& a, int pairs, int rows, unsigned ctas, const uint32_t* bits, cudaStream_t stream) {
-    return a.c.dim <= 64 ? launch_dim<64>(a, pairs, rows, ctas, bits, stream) : launch_dim<128>(a, pairs, rows, ctas, bits, stream);
+cudaError_t launch_list_attention(const AttnArgs& a, int pairs, bool e4m3, int rows, unsigned ctas, const uint32_t* bits, cudaStream_t stream) {
+    if (a.c.dim <= 64) return e4m3 ? launch_dim<64, true>(a, pairs, rows, ctas, bits, stream) : launch_dim<64, false>(a, pairs, rows, ctas, bits, stream);
+    return e4m3 ? launch_dim<128, true>(a, pairs, rows, ctas, bits, stream) : launch_dim<128, false>(a, pairs, rows, ctas, bits, stream);
 }
 
 cudaError_t launch_list_unions(const PagedCache& c, const int32_t* base, const int32_t* new_len, const int32_t* blocks,
-                               int num_blocks, int Q, int query_tile, int tiles, int64_t rows, int32_t* table, uint32_t* bits,
+                               int num_blocks, int Q, int query_tile, int tiles, bool shared, int64_t rows, int32_t* table, uint32_t* bits,
                                int32_t* out_base, int width, int most, cudaStream_t stream) {
     const size_t smem = ((size_t)most + 2 * (((size_t)c.max_pages + 31) / 32)) * sizeof(uint32_t);
     static sv::KernelLaunchCache cache;
@@ -506,7 +615,7 @@ cudaError_t launch_list_unions(const PagedCache& c, const int32_t* base, const i
     if (e != cudaSuccess) return e;
     if (smem > (size_t)max_dyn) return cudaErrorInvalidValue;
     return launch_serial(list_union_kernel, dim3((unsigned)rows), dim3(kUnionThreads), smem, stream, c, base, new_len, blocks,
-                         num_blocks, Q, query_tile, tiles, table, bits, out_base, width, most);
+                         num_blocks, Q, query_tile, tiles, (int)shared, table, bits, out_base, width, most);
 }
 
 }  // namespace sv

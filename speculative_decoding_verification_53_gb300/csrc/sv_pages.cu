@@ -18,7 +18,6 @@
 
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxRows = 16384;
 constexpr int kBad = INT_MIN;              // a unit of a row that is left untouched
 constexpr uint32_t kMost = 0x7fffffffu;    // sums saturate
@@ -35,6 +34,7 @@ struct PagesArgs {
     int32_t* ok;
     int num_pages, page_size, max_pages, B, N;
     int parts;  // units of a row
+    int shift;  // log2 of page_size, -1 where it is no power of two
 };
 
 __device__ __forceinline__ uint32_t sum_sat(uint32_t a, uint32_t b) { return min(a + b, kMost); }
@@ -56,13 +56,15 @@ __device__ __forceinline__ bool pages_unit(const PagesArgs& a, int b, int part, 
 
 __device__ __forceinline__ int64_t slot_of(const PagesArgs& a, int b, int length, int64_t pos) {
     if (pos < 0 || pos >= length) return -1;
-    const int i = (int)pos / a.page_size;
+    const int i = a.shift >= 0 ? (int)pos >> a.shift : (int)pos / a.page_size;
     const int p = __ldcg(a.table + (int64_t)b * a.max_pages + i);
     return (unsigned)p < (unsigned)a.num_pages ? (int64_t)p * a.page_size + ((int)pos - i * a.page_size) : -1;
 }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) page_resize_kernel(const __grid_constant__ PagesArgs a) {
     extern __shared__ int s_change[];  // of each unit: > 0 taken, < 0 given back
+    constexpr int kWarps = kThreads / 32;
     __shared__ uint32_t s_sum[2][kWarps];
     const int units = a.B * a.parts;
     uint32_t* s_take = reinterpret_cast<uint32_t*>(s_change) + units;  // [units + 1]: before each unit
@@ -73,6 +75,17 @@ __global__ void __launch_bounds__(kThreads) page_resize_kernel(const __grid_cons
     const int ranks = (int)sv::cluster_size(), rank = (int)sv::cluster_rank();
     const int first = rank * kWarps + warp, stride = ranks * kWarps;  // this warp's units
     const int start = min(max(a.count[0], 0), a.num_pages);
+
+    // Entries [e0, e0 + 256) of what a unit gives back, eight of a lane in flight.
+    int page[8];
+    auto fetch = [&](const int32_t* row, int e0, int hi) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int e = e0 + 32 * k + lane;
+            page[k] = e < hi ? __ldcg(row + e) : -1;
+        }
+    };
+    const bool one = units <= stride;  // a warp has one unit at most, and keeps the first of its entries
 
     if (ranks > 1) sv::cluster_sync_all();  // every CTA runs before its shared memory is written
     for (int u = first; u < units; u += stride) {
@@ -87,7 +100,10 @@ __global__ void __launch_bounds__(kThreads) page_resize_kernel(const __grid_cons
             const int32_t* row = a.table + (int64_t)b * a.max_pages;
             int held = 0;
 #pragma unroll 8
-            for (int e = lo + lane; e < hi; e += 32) held += (unsigned)__ldcg(row + e) < (unsigned)a.num_pages;
+            for (int e = lo + 256 + lane; e < hi; e += 32) held += (unsigned)__ldcg(row + e) < (unsigned)a.num_pages;
+            fetch(row, lo, hi);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) held += (unsigned)page[k] < (unsigned)a.num_pages;
             change = -(int)__reduce_add_sync(0xffffffffu, (unsigned)held);
         }
         if (lane < ranks) {
@@ -159,12 +175,7 @@ __global__ void __launch_bounds__(kThreads) page_resize_kernel(const __grid_cons
         int32_t* row = a.table + (int64_t)b * a.max_pages;
         uint32_t at = sum_sat((uint32_t)start, s_push[u]);
         for (int e0 = lo; e0 < hi; e0 += 256) {
-            int page[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int e = e0 + 32 * k + lane;
-                page[k] = e < hi ? __ldcg(row + e) : -1;
-            }
+            if (!one || e0 > lo) fetch(row, e0, hi);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int e = e0 + 32 * k + lane;
@@ -230,6 +241,38 @@ __global__ void __launch_bounds__(kThreads) page_resize_kernel(const __grid_cons
     }
 }
 
+// Up to `most` CTAs of one cluster.
+template <int kThreads>
+cudaError_t launch_resize(PagesArgs& a, int most, cudaStream_t stream) {
+    static sv::KernelLaunchCache cache;
+    auto kern = page_resize_kernel<kThreads>;
+    int max_dyn = 0;
+    cudaError_t e = cache.setup((const void*)kern, &max_dyn);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    auto parts_of = [&](int ranks) { return ranks * (kThreads / 32) > a.B ? ranks * (kThreads / 32) / a.B : 1; };
+    // in steps of 16 KB: what fits on the device is remembered for each size
+    auto smem_of = [&](int ranks) { return (((size_t)3 * a.B * parts_of(ranks) + 2) * sizeof(int) + 16383) / 16384 * 16384; };
+    int ranks = 1;
+    if (most > 1) e = cache.pick_cluster((const void*)kern, cfg, most, smem_of, &ranks);
+    if (e != cudaSuccess) return e;
+    if (ranks < 1 || smem_of(ranks) > (size_t)max_dyn) return cudaErrorInvalidValue;
+    a.parts = parts_of(ranks);
+    cfg.gridDim = dim3((unsigned)ranks);
+    cfg.dynamicSmemBytes = smem_of(ranks);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
 constexpr int kSlotThreads = 256, kSlotsEach = 8;
 
 // Slots of many tokens, on the whole device; grid: x over a row's tokens, y the row.
@@ -262,34 +305,17 @@ extern "C" sv_status spec_page_resize(int32_t* page_table, int32_t* pages, const
     if (B == 0) return SV_OK;
     if (!page_table || !pages || !length || (num_pages && !free_pages) || !free_count || !out_ok) return SV_ERR_INVALID_ARG;
     PagesArgs a{page_table, pages, length, free_pages, free_count, base, out_slots, out_ok,
-                num_pages, page_size, max_pages, B, N, 1};
+                num_pages, page_size, max_pages, B, N, 1, -1};
+    if ((page_size & (page_size - 1)) == 0)
+        for (a.shift = 0; 1 << a.shift < page_size;) ++a.shift;
     const bool slots = out_slots && N > 0;
     const int64_t tokens = slots ? (int64_t)B * N : 0;
-    // One CTA where little can move; else a cluster of eight, the most that is always granted.
-    const int ranks = B > 32 || tokens > 16384 ? 8 : 1;
-    a.parts = ranks * kWarps > B ? ranks * kWarps / B : 1;
     const bool apart = tokens > 32768;  // slots by a kernel of their own
     if (apart || !slots) a.slots = nullptr;
-    static sv::KernelLaunchCache cache;
-    int max_dyn = 0;
-    cudaError_t e = cache.setup((const void*)page_resize_kernel, &max_dyn);
-    if (e != cudaSuccess) return sv::launch_status(e);
-    const size_t smem = ((size_t)3 * B * a.parts + 2) * sizeof(int);
-    if (smem > (size_t)max_dyn) return SV_ERR_UNSUPPORTED;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ranks);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)ranks;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, page_resize_kernel, a);
+    // One small CTA where little can move, else the largest cluster.  For a pair of calls, 8 rows of which each gains and
+    // loses a page: 8.1 us by 256 threads, 9.1 by 512, 12 by 1024; 128 rows that move 256 to 1250 pages each, with 2^20
+    // slots: 28.8 us by 16 CTAs of 1024 threads, 32.7 by 16 of 512, 45 by 8 of 512.
+    cudaError_t e = B > 32 || tokens > 16384 ? launch_resize<1024>(a, 16, (cudaStream_t)stream) : launch_resize<256>(a, 1, (cudaStream_t)stream);
     if (e == cudaSuccess && apart) {
         a.slots = out_slots;
         const int per = kSlotThreads * kSlotsEach;

@@ -102,7 +102,7 @@ struct Kept {
 // grid: x over blocks * heads of one batch row, y the batch row.  WPU warps take one of them.
 template <int LPR, bool E4M3, bool BOUNDS, bool AL, int WPU>
 __global__ void __launch_bounds__(kThreads) block_summary_kernel(const __grid_constant__ SummaryArgs a) {
-    constexpr int G = 32 / LPR, FLY = 8;  // keys of a warp at a time, and how many a lane has in flight
+    constexpr int G = 32 / LPR, FLY = E4M3 ? 8 : 4;  // keys of a warp at a time, and how many a lane has in flight
     __shared__ Kept<BOUNDS> s_kept[WPU > 1 ? kWarps : 1][LPR];
     sv::pdl_trigger();
     sv::pdl_wait();
@@ -276,6 +276,12 @@ __global__ void __launch_bounds__(kScoreWarps * 32, KC * (BOUNDS ? 2 : 1) > 8 ? 
     sv::pdl_wait();
     const int lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
     const int y = blockIdx.y, b = y / a.H, h = y - b * a.H, unit = blockIdx.x * kScoreWarps + (threadIdx.x >> 5), j0 = 16 * unit;
+    int pages[2];  // asked for beside the row's length
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int j = j0 + 8 * x + g8;
+        pages[x] = j < a.max_pages ? __ldg(a.table + (int64_t)b * a.max_pages + j) : -1;
+    }
     int n, blocks;
     select_row(a, b, n, blocks);
     // Lists that need no scores: all blocks, or only the first and last ones.
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, KC * (BOUNDS ? 2 : 1) > 8 ? 
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int j = j0 + 8 * x + g8;
-        const int page = j < blocks ? __ldg(a.table + (int64_t)b * a.max_pages + j) : -1;
+        const int page = j < blocks ? pages[x] : -1;
         hole[x] = (unsigned)page >= (unsigned)a.num_pages;
         const uint16_t* row = a.summary + ((int64_t)(hole[x] ? 0 : page) * a.H + h) * (D * MATS) + 8 * t4;
 #pragma unroll
