@@ -28,9 +28,8 @@ extern "C" {
  *   tree_depth   NULL: token i of batch row b has position base[b] + i; device int32
  *                [B][N-1] as spec_tree_mask writes it for the N - 1 nodes of draft trees:
  *                token 0 (the root) has position base[b], token i + 1 base[b] + tree_depth[b][i].
- * Angles are reduced to a turn exactly up to 2^24 positions and 2^-24 of a turn, and up to
- * 2^30 positions within 2^-19 of a turn for frequencies of at most 1 radian.  Products are
- * fp32, results are rounded once to their type.
+ * Angles are within 2^-24 of a turn up to 2^24 positions, and within 2^-19 up to 2^30, for
+ * frequencies of at most 1 radian.  Products are fp32, results are rounded once to their type.
  * The struct is read during the call and is not retained.
  *   0 <= num_freq <= 128, 2 * num_freq <= head_dim.
  */

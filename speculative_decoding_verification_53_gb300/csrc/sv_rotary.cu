@@ -5,8 +5,13 @@
 // token and pair, shared by all heads, and a block computes them once into shared memory for
 // its tokens.  A row of one token and head is held by a group of lanes, eight elements each,
 // as in the cache's other kernels (sv_rows.cuh); a pair's other element is in the same lane
-// (neighbours paired), or num_freq elements away, read with a second 16-byte load that the
-// first level cache answers: another lane of the row has the same bytes in flight.
+// (neighbours paired), in another one (num_freq a multiple of 8: by shuffles), or anywhere in the
+// row, which lies in shared memory.  Rows in flight go through a ring there, since registers hold too
+// few: 4 x 6001 tokens, 32 + 8 heads of 128, bf16, a quarter of them in pairs: 89 us (5.5 TB/s) through the
+// ring, 95 with two rows ahead in registers, 132 with none; issue comes next (60 instructions a row of a
+// warp).  A warp decides on the kind of a group of rows as one: decided per row, 112 us.  fp32 198 us (5.0
+// TB/s); num_freq 10 129 us; few heads are bound by what a token costs a warp: 64 x 2000 tokens of 4 + 1 heads of 64
+// 90 us, four times their bytes' time.
 //
 // Angles: position * freq in fp32 would be off by whole radians at 10^7 positions.  Counted in
 // turns only the fraction matters: f = freq / 2 pi as hi + lo (fp32 each, from its 64 bits), the
@@ -27,9 +32,11 @@ constexpr int kMaxTokens = 8;  // of a block
 constexpr int kMaxFreq = 128;
 constexpr int kMaxB = 65535;
 constexpr int kMaxN = 1 << 20;
-constexpr int kDepth = 4;  // groups of rows in flight per warp, less one
+constexpr int kDepth = 4;  // places of the ring: groups of rows in flight per warp, and the one read
 
 enum { DENSE, CACHE_BF16, CACHE_E4M3 };
+// Where a pair's other element is: beside it; in another lane (num_freq a multiple of 8); or anywhere.
+enum { BESIDE, LANE, ANYWHERE };
 
 struct RotaryArgs {
     sv::PagedCache c;
@@ -116,7 +123,7 @@ struct Raw {
 };
 
 // grid: x over tiles of tokens, y over chunks of a token's rows.  LPR lanes hold a row.
-template <typename T, int LPR, int MODE, bool AL>
+template <typename T, int LPR, int MODE, bool AL, int PAIR>
 __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ RotaryArgs a) {
     extern __shared__ uint4 s_raw[];  // AL: the ring; then [tile][R] cosines and sines
     float2* s_turn = reinterpret_cast<float2*>(s_raw + (AL ? kDepth * ((int)sizeof(T) / 2) * kThreads : 0));
@@ -139,8 +146,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     auto kind_of = [&](int group) { return group < a.groups[0] ? 0 : group < a.groups[1] ? 1 : 2; };
     auto head_of = [&](int kind, int group) { return (kind ? group - a.groups[kind - 1] : group) * G + lane / LPR; };
     auto row_of = [&](int kind, int h) { return static_cast<const T*>(a.src[kind]) + (b * a.ss[kind][0] + i * a.ss[kind][1]) + h * a.ss[kind][2]; };
-    // Groups in flight go through a ring in shared memory, kDepth deep, where a lane copies and
-    // reads its own pieces only.
+    // Groups in flight go through a ring in shared memory, kDepth deep.
     constexpr int PIECES = (int)sizeof(T) / 2;
     uint4* ring = reinterpret_cast<uint4*>(s_raw) + tid;
     auto fetch = [&](int group, int slot) {
@@ -180,7 +186,10 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     }
     __syncthreads();
     const int first = s_first[t];
-    if (first < 0) return;
+    if (first < 0) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        return;
+    }
     int page = -1, line = 0;
     if (MODE != DENSE) page = sv::paged_place(a.c, b, first + i, line);
 
@@ -195,8 +204,8 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
             cc[k] = 1.0f;
             ss[k] = 0.0f;
             if (e < turned) {
-                const bool second = a.interleaved ? k & 1 : e >= R;
-                const float2 cs = s_turn[t * R + (a.interleaved ? e >> 1 : second ? e - R : e)];
+                const bool second = PAIR == BESIDE ? k & 1 : e >= R;
+                const float2 cs = s_turn[t * R + (PAIR == BESIDE ? e >> 1 : second ? e - R : e)];
                 cc[k] = cs.x;
                 ss[k] = second ? cs.y : -cs.y;
             }
@@ -207,9 +216,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
             s[k] = make_float2(ss[2 * k], ss[2 * k + 1]);
         }
     }
-    // Partners: in this lane, in another lane of the row, or (num_freq no multiple of 8) loaded one by one.
-    const bool lanes = AL && !a.interleaved && R % 8 == 0;
-    const int mate = lanes && e0 < turned ? lane + (e0 < R ? R / 8 : -(R / 8)) : lane;
+    const int mate = PAIR == LANE && e0 < turned ? lane + (e0 < R ? R / 8 : -(R / 8)) : lane;
     const int same = e0 >= turned ? 0 : min(turned - e0, 8);  // elements of this lane that are turned
 
     for (int slot = 0; at < last; slot = slot + 1 == kDepth ? 0 : slot + 1) {
@@ -218,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
         Raw<T, AL> x;
         if (AL) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+            if (PAIR == ANYWHERE) __syncwarp();  // every lane's pieces are there, and the group before is read
 #pragma unroll
             for (int k = 0; k < PIECES; ++k) {
                 const uint4 w = ring[(slot * PIECES + k) * kThreads];
@@ -231,27 +239,29 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
         }
         fetch(at + (kDepth - 1) * each, slot ? slot - 1 : kDepth - 1);  // into the place of the group before
         at += each;
-        __syncwarp();  // in place: a row's elements are read before any is written
         float v[8];
         if (kind != 2) {
             float p[8];
-            if (a.interleaved) {
+            if (PAIR == BESIDE) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) p[k] = x.at(k ^ 1);
-            } else if (lanes) {
+            } else if (PAIR == LANE) {
                 Raw<T, AL> y;
 #pragma unroll
                 for (int k = 0; k < Raw<T, AL>::W; ++k) y.w[k] = __shfl_sync(0xffffffffu, x.w[k], mate);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) p[k] = y.at(k);
             } else {
-                const T* from = row_of(kind, in ? h : 0);
+                // (AL: rows are whole in the ring, fp32 ones in two planes of four elements per lane)
+                const T* from = AL ? reinterpret_cast<const T*>(ring + slot * PIECES * kThreads - lane % LPR) : row_of(kind, in ? h : 0);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const int e = e0 + k;
-                    p[k] = in && e < turned && e < a.D ? Raw<T, AL>::one(from, e < R ? e + R : e - R) : 0.0f;
+                    const int e = e0 + k, other = e < R ? e + R : e - R;
+                    p[k] = 0.0f;
+                    if (e < turned && in)
+                        p[k] = Raw<T, AL>::one(from, AL && sizeof(T) == 4 ? ((other >> 2) & 1) * (kThreads * 4) + (other >> 3) * 4 + (other & 3) : other);
                 }
-                __syncwarp();
+                if (!AL) __syncwarp();  // in place: a row's elements are read before any is written
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -303,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     }
 }
 
-template <typename T, int LPR, int MODE, bool AL>
-cudaError_t launch_lpr(RotaryArgs& a, cudaStream_t stream) {
+template <typename T, int LPR, int MODE, bool AL, int PAIR>
+cudaError_t launch_pair(RotaryArgs& a, cudaStream_t stream) {
     const int64_t tokens = (int64_t)a.B * a.N;
     constexpr int sms = 152, G = 32 / LPR;
     for (int k = 0, n = 0; k < 3; ++k) a.groups[k] = n += (a.heads[k] + G - 1) / G;
@@ -317,12 +327,19 @@ cudaError_t launch_lpr(RotaryArgs& a, cudaStream_t stream) {
     const size_t smem = (size_t)a.tile * a.R * sizeof(float2);
     constexpr size_t ring = AL ? kDepth * kThreads * sizeof(T) * 8 : 0;
     static sv::KernelLaunchCache cache;
-    auto kern = rotary_kernel<T, LPR, MODE, AL>;
+    auto kern = rotary_kernel<T, LPR, MODE, AL, PAIR>;
     int max_dyn = 0;
     const cudaError_t e = cache.setup((const void*)kern, &max_dyn);
     if (e != cudaSuccess) return e;
     if (ring + smem > (size_t)max_dyn) return cudaErrorInvalidValue;
     return sv::launch_serial(kern, grid, dim3(kThreads), ring + smem, stream, a);
+}
+
+template <typename T, int LPR, int MODE, bool AL>
+cudaError_t launch_lpr(RotaryArgs& a, cudaStream_t stream) {
+    if (a.interleaved) return launch_pair<T, LPR, MODE, AL, BESIDE>(a, stream);
+    if (AL && a.R % 8 == 0) return launch_pair<T, LPR, MODE, AL, AL ? LANE : ANYWHERE>(a, stream);
+    return launch_pair<T, LPR, MODE, AL, ANYWHERE>(a, stream);
 }
 
 template <typename T, int MODE>

@@ -101,3 +101,61 @@ def test_rounds(sv, cache, tree, shared):  # noqa: F811
     # everybody leaves: every page is free again, once
     sv.spec_page_resize(t_table, t_pages, ints([0] * B), t_stack, t_count, PS)
     assert t_count.tolist() == [P] and sorted(t_stack.tolist()) == list(range(P)) and t_pages.tolist() == [0] * B
+
+
+FIRST = """
+import torch
+import speculative_decoding_verification_53_gb300 as sv
+B, Q, H, HQ, D, P, ps = 40, 5, 2, 8, 64, 900, 16
+torch.manual_seed(1)
+f = lambda *s: torch.randn(*s, device="cuda").to(torch.bfloat16)
+i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+k, v, qkv = f(P, H, ps, D), f(P, H, ps, D), f(B, Q, HQ + 2 * H, D)
+table, base = torch.randperm(P, device="cuda").int()[:B * 22].view(B, 22), i([320 - 5 * b for b in range(B)])
+held, stack, top = (base + 15) // ps, i(list(range(P))), i([0])
+summary, freq, zero = torch.zeros((P, H, D), dtype=torch.bfloat16, device="cuda"), sv.rotary_frequencies(D, device="cuda"), i([0] * B)
+state = [k, v, table, held, stack, top, summary]
+start = [t.clone() for t in state]
+def go():
+    sv.spec_page_resize(table, held, base - 16, stack, top, ps)
+    ok, slots = sv.spec_page_resize(table, held, base + Q, stack, top, ps, base=base, num_tokens=Q)
+    out, key = sv.spec_rotary(qkv[:, :, :HQ], freq, base, key=qkv[:, :, HQ:HQ + H])
+    q = sv.spec_rotary_append(qkv[:, :, :HQ], qkv[:, :, HQ:HQ + H], qkv[:, :, HQ + H:], freq, k, v, table, base)
+    sv.spec_block_summary(k, table, zero, 330, new_len=base, summary=summary)
+    lists = sv.spec_block_select(q, summary, table, base, ps, 6)
+    one = sv.spec_block_select(q, summary, table, base, ps, 6, shared=True)
+    return [ok, slots, out, key, q, lists, one, *sv.spec_sparse_attention(q, k, v, table, base, lists, want_lse=True),
+            *sv.spec_sparse_attention(q, k, v, table, base, one, want_lse=True)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = go()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got + state]
+for t, s in zip(state, start):
+    t.copy_(s)
+want = go() + state
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+# and on a stream of its own, again and again, while the current one is idle
+torch.cuda.synchronize()
+side = torch.cuda.Stream()
+for _ in range(10):
+    q = sv.spec_rotary(qkv[:, :, :HQ], freq, base, stream=side)[0]
+    one = sv.spec_block_select(q, summary, table, base, ps, 6, shared=True, stream=side)
+    o = sv.spec_sparse_attention(q, k, v, table, base, one, stream=side)[0]
+    m = sv.spec_block_summary(k, table, zero, 330, new_len=base, stream=side)
+    side.synchronize()
+    assert torch.equal(q, want[2]) and torch.equal(one, want[6]) and torch.equal(o, want[9]) and m.shape == summary.shape
+print("same")
+"""
+
+
+def test_the_first_calls_of_a_process_can_be_captured(sv):  # noqa: F811
+    """Nothing that a first call sets up is refused while a stream is captured; calls on another stream."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]

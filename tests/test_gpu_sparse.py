@@ -133,13 +133,14 @@ def test_select(sv, kind, shared, B, Q, Hq, H, D, ps, blocks, top, sink, recent)
 @pytest.mark.parametrize("kind", ["mean", "bounds"])
 @pytest.mark.parametrize("shared", [False, True])
 @pytest.mark.parametrize("same", [3, 60, 200])
-def test_select_among_equals(sv, kind, shared, same):  # noqa: F811
-    """Equal scores go to the lower blocks: few of them, as many as fit the short path, and more; scores that
+@pytest.mark.parametrize("B,Q,blocks", [(2, 3, 260), (27, 3, 260), (80, 1, 260), (2, 3, 2100)])  # few lists, many, long ones
+def test_select_among_equals(sv, kind, shared, same, B, Q, blocks):  # noqa: F811
+    """Equal scores go to the lower blocks: few of them, as many as fit the short paths, and more; scores that
     differ by less than fp32 resolves keep their order."""
     rng = np.random.default_rng(same)
-    q, summary, table, base, new = select_case(rng, 2, 3, 4, 2, 64, 16, 260, kind == "bounds")
-    base[:] = 260 * 16
-    for b in range(2):
+    q, summary, table, base, new = select_case(rng, B, Q, 4, 2, 64, 16, blocks, kind == "bounds")
+    base[:] = blocks * 16
+    for b in range(B):
         for h in range(2):
             at = np.sort(rng.permutation(250)[:same] + 5)
             summary[table[b, at], h] = summary[table[b, at[0]], h]
@@ -159,13 +160,14 @@ def test_select_among_equals(sv, kind, shared, same):  # noqa: F811
 
 
 @pytest.mark.parametrize("kind", ["mean", "bounds"])
-def test_select_numbers_that_are_not_finite(sv, kind):  # noqa: F811
+@pytest.mark.parametrize("B", [1, 80])  # few lists, and many
+def test_select_numbers_that_are_not_finite(sv, kind, B):  # noqa: F811
     """NaN ranks below everything but holes; infinities rank where they belong; large numbers overflow nothing."""
     rng = np.random.default_rng(2)
     for case in range(5):
-        q, summary, table, base, _ = select_case(rng, 1, 2, 4, 1, 64, 16, 90, kind == "bounds")
+        q, summary, table, base, _ = select_case(rng, B, 2, 4, 1, 64, 16, 90, kind == "bounds")
         base[:] = 90 * 16
-        pages = table[0, :90]
+        pages = table[:, :90].T  # [block][row]
         if case == 0:
             summary[pages[10:80], 0, 5] = math.nan
         elif case == 1:
@@ -177,7 +179,7 @@ def test_select_numbers_that_are_not_finite(sv, kind):  # noqa: F811
             summary *= 2.0 ** 120
             q *= 2.0 ** 100
         else:
-            table[0, 3:85] = -1  # holes: fewer blocks left than are wanted
+            table[:, 3:85] = -1  # holes: fewer blocks left than are wanted
             table[0, 50] = 10 ** 6
         for top in (4, 12, 60):
             check_select(sv, q, summary, table, base, None, 16, top, kind, 1, 1, False)
@@ -451,6 +453,50 @@ def run_on(sv, c, stream):  # noqa: F811
     args = [ints(x) for x in (table, base, blocks, new)]
     torch.cuda.synchronize()
     return sv.spec_sparse_attention(q, k, v, *args[:3], new_len=args[3], want_lse=True, stream=stream)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("shared,Q", [(False, 5), (True, 5), (True, 70)])
+def test_rows_that_see_nothing_and_short_rows(sv, cache, shared, Q):  # noqa: F811
+    """Tables of holes alone, no context, no real query, a context of less than a block."""
+    rng = np.random.default_rng(11)
+    c = attention_case(rng, 5, Q, 8, 2, 64, 16, 400, 6, cache, True, False, shared)
+    table, base, new = c[5], c[6], c[7]
+    base[:], new[:] = [400, 0, 300, 7, 16], [Q, Q, 0, 1, 2]
+    c[9][1:] = -1
+    c[9][4, :, :, 0] = 0
+    table[0] = -1
+    got, lse = run(sv, c)
+    check_attention(got, lse, *c, 64 ** -0.5, 3.0)
+    assert (got[0] == 0).all() and (lse[0] == -math.inf).all() and (got[2] == 3).all()
+
+
+def test_offsets_beyond_32_bits(sv):  # noqa: F811
+    """Pages that lie more than 4 GB into the cache, against the same pages in a small one."""
+    import torch
+    P, H, ps, D, B, Q, n = 40000, 8, 64, 128, 2, 5, 9  # 131 KB a page: 5.2 GB of keys
+    if torch.cuda.mem_get_info()[0] < 24e9:
+        pytest.skip("needs 24 GB")
+    k, v = (torch.zeros((P, H, ps, D), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    summary = torch.zeros((P, H, 2 * D), dtype=torch.bfloat16, device="cuda")
+    used = torch.arange(P - 40, P, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    k[used], v[used] = (torch.randn((40, H, ps, D), generator=gen, device="cuda").to(torch.bfloat16) for _ in "kv")
+    small = [k[used].clone(), v[used].clone(), torch.zeros((40, H, 2 * D), dtype=torch.bfloat16, device="cuda")]
+    table = ints(np.random.default_rng(1).permutation(40).reshape(2, 20))
+    base, qkv = ints([1100, 700]), torch.randn((B, Q, 48, D), generator=gen, device="cuda").to(torch.bfloat16)
+    freq = sv.rotary_frequencies(D, device="cuda")
+    got = []
+    for kk, vv, mm, t in ((k, v, summary, table + (P - 40)), (*small, table)):
+        q = sv.spec_rotary_append(qkv[:, :, :32], qkv[:, :, 32:40], qkv[:, :, 40:], freq, kk, vv, t, base)
+        sv.spec_block_summary(kk, t, ints([0, 0]), 1105, kind="bounds", new_len=base + Q, summary=mm)
+        blocks = sv.spec_block_select(q, mm, t, base, ps, n, kind="bounds")
+        got.append((q, blocks, *sv.spec_sparse_attention(q, kk, vv, t, base, blocks, want_lse=True),
+                    *sv.spec_sparse_attention(q, kk, vv, t, base, blocks[:, :1].contiguous(), want_lse=True)))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    for big, few in zip((k, v, summary), small):
+        assert torch.equal(big[used], few)
 
 
 def test_refusals(sv):  # noqa: F811
