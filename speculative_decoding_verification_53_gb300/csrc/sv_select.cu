@@ -4,7 +4,9 @@
 //
 // Summaries are one pass over the keys, bound by memory: a warp (few blocks: all warps of a
 // CTA) takes one block and head, a group of lanes a key, eight elements each, and the groups
-// meet by shuffles at the end.
+// meet by shuffles at the end.  8 x up to 8192 positions of 8 heads of 128, pages of 64: bf16 means 16 us (84 MB,
+// floor 13), bounds in pages of 16 17; e4m3 bounds 17 (43 MB, floor 7: the codes' way to fp32 bounds it; compared in
+// fp32 instead of as pairs of bf16 18.4).
 //
 // Scores: score(i, j) = max over rows r of s_r . m_j, s_r . m_j = q_r . mean_j, or
 // q_r+ . max_j + q_r- . min_j with q+ = max(q, 0), q- = min(q, 0), both matrix products of the
@@ -56,57 +58,79 @@ struct SummaryArgs {
     uint16_t* out;
 };
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+// The larger, and the smaller, of two pairs of bf16; NaN stays.
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ float min_nan(float a, float b) {
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+__device__ __forceinline__ uint32_t min_pair(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-// What a lane keeps of its eight elements.
+// What a lane keeps of its eight elements: their sums, or their bounds as pairs of bf16.  (The largest of rounded
+// values is the largest one rounded, so e4m3 values are rounded as they come, two an instruction.)
 template <bool BOUNDS>
 struct Kept {
-    float a[8], b[BOUNDS ? 8 : 1];
+    uint32_t a[BOUNDS ? 4 : 8], b[BOUNDS ? 4 : 1];
     __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            a[k] = BOUNDS ? neg_inf() : 0.0f;
-            if (BOUNDS) b[BOUNDS ? k : 0] = pos_inf();
-        }
+        for (int k = 0; k < (BOUNDS ? 4 : 8); ++k) a[k] = BOUNDS ? 0xff80ff80u : 0u;
+#pragma unroll
+        for (int k = 0; k < (BOUNDS ? 4 : 1); ++k) b[k] = 0x7f807f80u;
     }
     __device__ __forceinline__ void add(const float x[8]) {
+        if (BOUNDS) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            a[k] = BOUNDS ? max_nan(a[k], x[k]) : a[k] + x[k];
-            if (BOUNDS) b[BOUNDS ? k : 0] = min_nan(b[BOUNDS ? k : 0], x[k]);
+            for (int k = 0; k < 4; ++k) pair(k, sv::bf16x2(x[2 * k], x[2 * k + 1]));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) a[BOUNDS ? 0 : k] = __float_as_uint(__uint_as_float(a[BOUNDS ? 0 : k]) + x[k]);
         }
     }
+    __device__ __forceinline__ void pair(int k, uint32_t w) {
+        a[k] = max_pair(a[k], w);
+        b[BOUNDS ? k : 0] = min_pair(b[BOUNDS ? k : 0], w);
+    }
     __device__ __forceinline__ void join(const Kept& o) {
+        if (BOUNDS) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            a[k] = BOUNDS ? max_nan(a[k], o.a[k]) : a[k] + o.a[k];
-            if (BOUNDS) b[BOUNDS ? k : 0] = min_nan(b[BOUNDS ? k : 0], o.b[BOUNDS ? k : 0]);
+            for (int k = 0; k < 4; ++k) {
+                a[k] = max_pair(a[k], o.a[k]);
+                b[BOUNDS ? k : 0] = min_pair(b[BOUNDS ? k : 0], o.b[BOUNDS ? k : 0]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) a[BOUNDS ? 0 : k] = __float_as_uint(__uint_as_float(a[BOUNDS ? 0 : k]) + __uint_as_float(o.a[BOUNDS ? 0 : k]));
         }
     }
     __device__ __forceinline__ Kept from(int mask) const {
         Kept o;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            o.a[k] = __shfl_xor_sync(0xffffffffu, a[k], mask);
-            if (BOUNDS) o.b[BOUNDS ? k : 0] = __shfl_xor_sync(0xffffffffu, b[BOUNDS ? k : 0], mask);
-        }
+        for (int k = 0; k < (BOUNDS ? 4 : 8); ++k) o.a[k] = __shfl_xor_sync(0xffffffffu, a[k], mask);
+#pragma unroll
+        for (int k = 0; k < (BOUNDS ? 4 : 1); ++k) o.b[k] = BOUNDS ? __shfl_xor_sync(0xffffffffu, b[k], mask) : 0u;
         return o;
     }
 };
 
+// Eight bf16 to a summary's row.
+__device__ __forceinline__ void store_pairs(uint16_t* row, int e0, int dim, const uint32_t w[4]) {
+    if (dim % 8 == 0) {
+        if (e0 < dim) *reinterpret_cast<uint4*>(row + e0) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (e0 + k < dim) row[e0 + k] = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
+    }
+}
+
 // grid: x over blocks * heads of one batch row, y the batch row.  WPU warps take one of them.
 template <int LPR, bool E4M3, bool BOUNDS, bool AL, int WPU>
 __global__ void __launch_bounds__(kThreads) block_summary_kernel(const __grid_constant__ SummaryArgs a) {
-    constexpr int G = 32 / LPR, FLY = E4M3 ? 8 : 4;  // keys of a warp at a time, and how many a lane has in flight
+    constexpr int G = 32 / LPR, FLY = E4M3 || BOUNDS ? 8 : 4;  // keys of a warp at a time, and how many a lane has in flight
     __shared__ Kept<BOUNDS> s_kept[WPU > 1 ? kWarps : 1][LPR];
     sv::pdl_trigger();
     sv::pdl_wait();
@@ -142,9 +166,17 @@ __global__ void __launch_bounds__(kThreads) block_summary_kernel(const __grid_co
 #pragma unroll
         for (int k = 0; k < FLY; ++k) {
             if (r0 + k * G * WPU >= count) break;
-            float f[8];
-            x[k].widen(scale[k], f);
-            kept.add(f);
+            if constexpr (BOUNDS && !E4M3 && AL) {
+                const uint4 w = x[k].b.w[0];
+                kept.pair(0, w.x);
+                kept.pair(1, w.y);
+                kept.pair(2, w.z);
+                kept.pair(3, w.w);
+            } else {
+                float f[8];
+                x[k].widen(scale[k], f);
+                kept.add(f);
+            }
         }
     }
     __syncwarp();
@@ -160,18 +192,15 @@ __global__ void __launch_bounds__(kThreads) block_summary_kernel(const __grid_co
     if (page < 0 || lane >= LPR) return;
     const int dim = a.c.dim;
     uint16_t* out = a.out + ((int64_t)page * heads + h) * (BOUNDS ? 2 * dim : dim);
-    if (!BOUNDS) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) kept.a[k] = kept.a[k] / (float)count;
-    }
-    if (dim % 8 == 0) sv::store_row8<uint16_t, true>(out, e0, dim, kept.a);
-    else sv::store_row8<uint16_t, false>(out, e0, dim, kept.a);
     if (BOUNDS) {
-        float low[8];
+        store_pairs(out, e0, dim, kept.a);
+        store_pairs(out + dim, e0, dim, kept.b);
+    } else {
+        uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) low[k] = kept.b[BOUNDS ? k : 0];
-        if (dim % 8 == 0) sv::store_row8<uint16_t, true>(out + dim, e0, dim, low);
-        else sv::store_row8<uint16_t, false>(out + dim, e0, dim, low);
+        for (int k = 0; k < 4; ++k)
+            w[k] = sv::bf16x2(__uint_as_float(kept.a[BOUNDS ? 0 : 2 * k]) / (float)count, __uint_as_float(kept.a[BOUNDS ? 0 : 2 * k + 1]) / (float)count);
+        store_pairs(out, e0, dim, w);
     }
 }
 
