@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_
     const int rest = (int)(at / part_rows), r = (int)(at - (int64_t)rest * part_rows);
     const sv::AttnPlace p = sv::attn_place(a, pairs, (unsigned)(a.whole + rest));
     sv::AttnRows rows_of;
-    if (!sv::attn_rows(a, p, tile_rows, rows_of)) return;
+    if (!sv::attn_rows<true>(a, p, tile_rows, rows_of)) return;
     const int64_t R = (int64_t)rows_of.r0 + r;
     if (R >= rows_of.r1) return;
     const int parts = sv::attn_parts(a, sv::attn_active(a, rows_of.end));

@@ -79,22 +79,24 @@ __host__ __device__ __forceinline__ int attn_tile_end(int base, int n, int group
     return base + last + 1;
 }
 
-// False where the tile has no rows, or its batch row is left untouched.
+// False where the tile has no rows, or its batch row is left untouched.  EACH: also the modes whose tiles
+// belong to certain queries (lists 2 and 3).
+template <bool EACH>
 __device__ __forceinline__ bool attn_rows(const AttnArgs& a, const AttnPlace& p, int tile_rows, AttnRows& r) {
-    const int i = a.lists == 2 ? p.mt / a.query_tiles : 0;
-    r.row = a.lists == 0 ? p.b : a.lists == 1 ? p.b * a.c.heads + p.h
-            : (p.b * (a.lists == 2 ? a.Q : a.m_tiles) + (a.lists == 2 ? i : p.mt)) * a.c.heads + p.h;
+    const int i = EACH && a.lists == 2 ? p.mt / a.query_tiles : 0;
+    r.row = a.lists ? p.b * a.c.heads + p.h : p.b;
+    if (EACH && a.lists >= 2) r.row = (p.b * (a.lists == 2 ? a.Q : a.m_tiles) + (a.lists == 2 ? i : p.mt)) * a.c.heads + p.h;
     r.base = __ldg(a.base + r.row);
     r.n = a.new_len ? __ldg(a.new_len + p.b) : a.Q;
     if (r.base < 0 || r.n < 0 || r.n > a.Q || (int64_t)r.base + r.n > (int64_t)a.c.max_pages * a.c.page_size) return false;
-    if (a.lists == 2) {
+    if (EACH && a.lists == 2) {
         if (i >= r.n) return false;
         r.r0 = i * a.group + (p.mt - i * a.query_tiles) * tile_rows;
         r.r1 = (i + 1) * a.group;
         r.end = a.tree_mask ? r.base + r.n : r.base + i + 1;
         return true;
     }
-    if (a.lists == 3) {
+    if (EACH && a.lists == 3) {
         const int first = p.mt * a.query_tiles, end = min(r.n, first + a.query_tiles);
         if (first >= r.n) return false;
         r.r0 = first * a.group;
@@ -107,6 +109,12 @@ __device__ __forceinline__ bool attn_rows(const AttnArgs& a, const AttnPlace& p,
     r.r1 = r.n * a.group;
     r.end = attn_tile_end(r.base, r.n, a.group, p.mt, tile_rows, a.tree_mask != nullptr);
     return true;
+}
+
+// AttnTile::row of the modes that the tcgen05 kernel runs (lists 0 and 1), made where it is needed: held
+// in a register it made that kernel spill (16 e4m3 trees of 61 over 8192 positions 158 -> 165 us).
+__device__ __forceinline__ int attn_table_row(const AttnArgs& a, const AttnTile& t) {
+    return a.lists ? t.b * a.c.heads + t.h : t.b;
 }
 
 // Splits of a row tile that have positions.
@@ -150,6 +158,7 @@ __device__ __forceinline__ int attn_sorted(const AttnArgs& a, int r) {
 
 // The work of CTA `id` (pairs: batch rows times cache heads; per: splits that a CTA takes);
 // false where it has none.
+template <bool EACH = true>
 __device__ __forceinline__ bool attn_tile(const AttnArgs& a, int pairs, unsigned id, int tile_rows, int per, AttnTile& t) {
     const bool whole = id < (unsigned)a.whole;
     const unsigned rest = id - (unsigned)a.whole, each = (unsigned)(a.splits / per);
@@ -166,7 +175,7 @@ __device__ __forceinline__ bool attn_tile(const AttnArgs& a, int pairs, unsigned
     t.split = whole ? 0 : (int)(rest % each) * per;
     t.part = whole ? 0 : ((int64_t)tile * each + rest % each) * a.part_rows;
     AttnRows r;
-    if (!attn_rows(a, p, tile_rows, r)) return false;
+    if (!attn_rows<EACH>(a, p, tile_rows, r)) return false;
     t.row = r.row;
     t.r0 = r.r0;
     t.r1 = r.r1;

@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
     pdl_trigger();
     pdl_wait();
     AttnTile t;
-    if (!sv::attn_tile(a, pairs, blockIdx.x, S::ROWS, DUAL ? 2 : 1, t)) return;
+    if (!sv::attn_tile<false>(a, pairs, blockIdx.x, S::ROWS, DUAL ? 2 : 1, t)) return;
     const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;  // queries, then the ring
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = a.c.dim, rows = t.n * a.group;
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                             }
                         } else {
                             int r;
-                            const int page = sv::paged_place(a.c, t.row, pos, r);
+                            const int page = sv::paged_place(a.c, sv::attn_table_row(a, t), pos, r);
                             if (page < 0) continue;
                             const int64_t at = page * a.c.page_stride + t.h * a.c.head_stride + r * a.c.row_stride;
                             const int64_t sc_at = ((int64_t)page * a.c.heads + t.h) * a.c.page_size + r;
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             const int pos = start(tile) + 32 * w + lane;
             if (box_rows || tile >= tiles || pos >= stop(tile)) return (int64_t)-1;
             int row;
-            const int page = sv::paged_place(a.c, t.row, pos, row);
+            const int page = sv::paged_place(a.c, sv::attn_table_row(a, t), pos, row);
             return page < 0 ? (int64_t)-1 : page * a.c.page_stride + row * a.c.row_stride;
         };
         bool bad = false;
@@ -1004,7 +1004,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                 page = a.c.num_pages;  // a page outside the cache reads as zeros
                 row = 0;
                 if (lane < boxes && tile < tiles && pos < stop(tile)) {
-                    const int p = sv::paged_place(a.c, t.row, pos, row);
+                    const int p = sv::paged_place(a.c, sv::attn_table_row(a, t), pos, row);
                     if (p >= 0) page = p;
                 }
             };
@@ -1069,7 +1069,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
             uint32_t largest_v = 0u, other_v = 0u, seen = 0u, other_seen = 0u;
             if (E4M3) {
                 int row;
-                const int page = sv::paged_place(a.c, t.row, open - 1, row);
+                const int page = sv::paged_place(a.c, sv::attn_table_row(a, t), open - 1, row);
                 if (page >= 0) {
                     const float s = fabsf(__ldg(a.c.v_scale + ((int64_t)page * a.c.heads + t.h) * a.c.page_size + row));
                     if (!sv::not_finite(s)) seen = other_seen = __float_as_uint(s);
@@ -1085,7 +1085,7 @@ __global__ void __launch_bounds__(MQ * 128 + 256, 1) paged_attention_tc_kernel(c
                     at[z] = -1;
                     if (tile < tiles && pos < stop(tile)) {
                         int row;
-                        const int page = sv::paged_place(a.c, t.row, pos, row);
+                        const int page = sv::paged_place(a.c, sv::attn_table_row(a, t), pos, row);
                         if (page >= 0) at[z] = ((int64_t)page * a.c.heads + t.h) * a.c.page_size + row;
                     }
                 }
