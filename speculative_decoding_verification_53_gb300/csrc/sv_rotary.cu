@@ -75,9 +75,8 @@ __device__ __forceinline__ bool token_position(const RotaryArgs& a, int b, int i
     return true;
 }
 
-// Cosine and sine of pos * (fh + fl) turns.
-__device__ __forceinline__ float2 turn(int64_t pos, float fh, float fl) {
-    const float rest = (float)(int)(pos & 4095), big = (float)(pos - (pos & 4095));
+// Cosine and sine of (big + rest) * (fh + fl) turns.
+__device__ __forceinline__ float2 turn(float big, float rest, float fh, float fl) {
     float x = big * fh, y = rest * fh;
     const float small = fmaf(big, fl, rest * fl) + fmaf(big, fh, -x) + fmaf(rest, fh, -y);
     x -= rintf(x);
@@ -125,10 +124,11 @@ struct Raw {
 // grid: x over tiles of tokens, y over chunks of a token's rows.  LPR lanes hold a row.
 template <typename T, int LPR, int MODE, bool AL, int PAIR>
 __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ RotaryArgs a) {
-    extern __shared__ uint4 s_raw[];  // AL: the ring; then [tile][R] cosines and sines
-    float2* s_turn = reinterpret_cast<float2*>(s_raw + (AL ? kDepth * ((int)sizeof(T) / 2) * kThreads : 0));
+    extern __shared__ uint4 s_raw[];  // AL: the ring; then of each token RP cosines, sines negated, sines
+    const int RP = (a.R + 3) & ~3;
+    float* s_turn = reinterpret_cast<float*>(s_raw + (AL ? kDepth * ((int)sizeof(T) / 2) * kThreads : 0));
     __shared__ float2 s_freq[kMaxFreq];
-    __shared__ int64_t s_pos[kMaxTokens];
+    __shared__ float2 s_pos[kMaxTokens];  // a multiple of 4096, and the rest
     __shared__ int s_first[kMaxTokens];  // the row's base; -1: token not written
     constexpr int G = 32 / LPR;
     sv::pdl_trigger();
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
         int first = -1;
         int64_t pos = 0;
         if (x < total && !token_position<MODE>(a, (int)(x / a.N), (int)(x % a.N), pos, first)) first = -1;
-        s_pos[tid] = pos;
+        s_pos[tid] = make_float2((float)(pos & ~(int64_t)4095), (float)((int)pos & 4095));
         s_first[tid] = first;
     }
     for (int j = tid; j < a.R; j += kThreads) {
@@ -179,12 +179,17 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
         s_freq[j] = make_float2(hi, (float)(f - (double)hi));
     }
     __syncthreads();
-    for (int x = tid; x < a.tile * a.R; x += kThreads) {
-        const int t = x / a.R;
-        const float2 f = s_freq[x - t * a.R], cs = turn(s_pos[t], f.x, f.y);
-        s_turn[x] = make_float2(cs.x * a.amplitude, a.inverse ? -(cs.y * a.amplitude) : cs.y * a.amplitude);
+    float* mine = s_turn + t * 3 * RP;
+    const float2 pos = s_pos[t];
+    for (int j = tid - t * each * 32; j < a.R; j += each * 32) {  // by the token's warps
+        const float2 f = s_freq[j], cs = turn(pos.x, pos.y, f.x, f.y);
+        const float sine = a.inverse ? -(cs.y * a.amplitude) : cs.y * a.amplitude;
+        mine[j] = cs.x * a.amplitude;
+        mine[RP + j] = -sine;
+        mine[2 * RP + j] = sine;
     }
-    __syncthreads();
+    if (each == 1) __syncwarp();
+    else __syncthreads();
     const int first = s_first[t];
     if (first < 0) {
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -193,10 +198,33 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     int page = -1, line = 0;
     if (MODE != DENSE) page = sv::paged_place(a.c, b, first + i, line);
 
-    // This lane's elements: own and partner's factors (elements that are copied: 1 and 0).
+    // This lane's elements: own and partner's factors.  Those of elements that are copied are not used, only read
+    // within the block's memory.
     const int R = a.R, turned = 2 * R;
     float2 c[4], s[4];
-    {
+    if (PAIR == BESIDE) {
+        const float* at = mine + (e0 < turned ? e0 >> 1 : 0);
+        const float4 cs = *reinterpret_cast<const float4*>(at), sn = *reinterpret_cast<const float4*>(at + 2 * RP);
+        c[0] = make_float2(cs.x, cs.x);
+        c[1] = make_float2(cs.y, cs.y);
+        c[2] = make_float2(cs.z, cs.z);
+        c[3] = make_float2(cs.w, cs.w);
+        s[0] = make_float2(-sn.x, sn.x);
+        s[1] = make_float2(-sn.y, sn.y);
+        s[2] = make_float2(-sn.z, sn.z);
+        s[3] = make_float2(-sn.w, sn.w);
+    } else if (PAIR == LANE) {
+        const float* at = mine + (e0 < R ? e0 : e0 < turned ? e0 - R : 0);
+        const float* from = at + (e0 < R ? RP : 2 * RP);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float4 cs = reinterpret_cast<const float4*>(at)[k], sn = reinterpret_cast<const float4*>(from)[k];
+            c[2 * k] = make_float2(cs.x, cs.y);
+            c[2 * k + 1] = make_float2(cs.z, cs.w);
+            s[2 * k] = make_float2(sn.x, sn.y);
+            s[2 * k + 1] = make_float2(sn.z, sn.w);
+        }
+    } else {
         float cc[8], ss[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -204,10 +232,8 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
             cc[k] = 1.0f;
             ss[k] = 0.0f;
             if (e < turned) {
-                const bool second = PAIR == BESIDE ? k & 1 : e >= R;
-                const float2 cs = s_turn[t * R + (PAIR == BESIDE ? e >> 1 : second ? e - R : e)];
-                cc[k] = cs.x;
-                ss[k] = second ? cs.y : -cs.y;
+                cc[k] = mine[e < R ? e : e - R];
+                ss[k] = mine[e < R ? RP + e : 2 * RP + e - R];
             }
         }
 #pragma unroll
@@ -324,7 +350,8 @@ cudaError_t launch_pair(RotaryArgs& a, cudaStream_t stream) {
     while (a.tile < kMaxTokens && tokens / (2 * a.tile) >= 6 * sms) a.tile *= 2;
     a.chunk = tokens >= 2 * sms ? a.groups[2] : kWarps;
     const dim3 grid((unsigned)((tokens + a.tile - 1) / a.tile), (unsigned)((a.groups[2] + a.chunk - 1) / a.chunk));
-    const size_t smem = (size_t)a.tile * a.R * sizeof(float2);
+    // Without pairs the factors are read all the same: eight floats behind the first of a plane.
+    const size_t smem = ((size_t)a.tile * 3 * ((a.R + 3) & ~3) + 8) * sizeof(float);
     constexpr size_t ring = AL ? kDepth * kThreads * sizeof(T) * 8 : 0;
     static sv::KernelLaunchCache cache;
     auto kern = rotary_kernel<T, LPR, MODE, AL, PAIR>;
