@@ -7,11 +7,14 @@
 // as in the cache's other kernels (sv_rows.cuh); a pair's other element is in the same lane
 // (neighbours paired), in another one (num_freq a multiple of 8: by shuffles), or anywhere in the
 // row, which lies in shared memory.  Rows in flight go through a ring there, since registers hold too
-// few: 4 x 6001 tokens, 32 + 8 heads of 128, bf16, a quarter of them in pairs: 89 us (5.5 TB/s) through the
-// ring, 95 with two rows ahead in registers, 132 with none; issue comes next (60 instructions a row of a
-// warp).  A warp decides on the kind of a group of rows as one: decided per row, 112 us.  fp32 198 us (5.0
-// TB/s); num_freq 10 129 us; few heads are bound by what a token costs a warp: 64 x 2000 tokens of 4 + 1 heads of 64
-// 90 us, four times their bytes' time.
+// few (4 x 6001 tokens, 32 + 8 heads of 128, bf16, a quarter of them in pairs: with two rows ahead in registers 6 us
+// more, with none 43).  A warp decides on the kind of a group of rows as one (decided per row: 23 us more).
+//
+// With the bytes in flight, instructions bound it.  160 a group of rows, most of them for 64-bit addresses and for
+// factors picked one by one, took 87 us in those 4 x 6001 tokens; factors read as vectors from planes of cosines
+// and sines 82; pointers that move on by their kind's stride, found anew only for another kind, 76 (5.9 TB/s).
+// fp32 201 us (4.9 TB/s), num_freq 10 105; 16 x 2048 tokens on their way into a cache of bf16 83 (floor 75), of e4m3 93.
+// Few heads pay for their tokens' sines and places: 64 x 2000 tokens of 4 + 1 heads of 64 61, their bytes' time 25.
 //
 // Angles: position * freq in fp32 would be off by whole radians at 10^7 positions.  Counted in
 // turns only the fraction matters: f = freq / 2 pi as hi + lo (fp32 each, from its 64 bits), the
@@ -29,12 +32,18 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxTokens = 8;  // of a block
+constexpr int kEach = 4;       // tokens of a warp, where tokens have few rows
 constexpr int kMaxFreq = 128;
 constexpr int kMaxB = 65535;
 constexpr int kMaxN = 1 << 20;
 constexpr int kDepth = 4;  // places of the ring: groups of rows in flight per warp, and the one read
 
 enum { DENSE, CACHE_BF16, CACHE_E4M3 };
+template <int K>
+struct Int {
+    static constexpr int value = K;
+};
+
 // Where a pair's other element is: beside it; in another lane (num_freq a multiple of 8); or anywhere.
 enum { BESIDE, LANE, ANYWHERE };
 
@@ -45,6 +54,8 @@ struct RotaryArgs {
     int64_t ss[3][3];    // element strides of the sources (batch, token, head)
     int64_t ds[2][3];    // and of the destinations
     int heads[3];        // of queries, keys, values
+    int64_t in_step[3];  // from a group of a warp to its next one: elements,
+    int64_t out_step[2]; // bytes (queries, keys and values)
     int groups[3];       // groups of rows of a token: [0, groups[0]) queries, then keys, then values
     const double* freq;
     const int32_t* depth;
@@ -121,15 +132,18 @@ struct Raw {
     }
 };
 
-// grid: x over tiles of tokens, y over chunks of a token's rows.  LPR lanes hold a row.
-template <typename T, int LPR, int MODE, bool AL, int PAIR>
+// grid: x over tiles of tokens, y over chunks of a token's rows.  LPR lanes hold a row.  A token is one warp's or
+// several warps'; MANY (DENSE, tokens of few rows): a warp takes kEach tokens, one after the other.
+template <typename T, int LPR, int MODE, bool AL, int PAIR, bool MANY>
 __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ RotaryArgs a) {
     extern __shared__ uint4 s_raw[];  // AL: the ring; then of each token RP cosines, sines negated, sines
     const int RP = (a.R + 3) & ~3;
     float* s_turn = reinterpret_cast<float*>(s_raw + (AL ? kDepth * ((int)sizeof(T) / 2) * kThreads : 0));
     __shared__ float2 s_freq[kMaxFreq];
-    __shared__ float2 s_pos[kMaxTokens];  // a multiple of 4096, and the rest
-    __shared__ int s_first[kMaxTokens];  // the row's base; -1: token not written
+    constexpr int EACH = MANY ? kEach : 1, TOKENS = kMaxTokens * EACH;
+    __shared__ float2 s_pos[TOKENS];             // a multiple of 4096, and the rest
+    __shared__ int s_first[TOKENS];              // the row's base; -1: token not written
+    __shared__ int2 s_token[MANY ? TOKENS : 1];  // batch row and index
     constexpr int G = 32 / LPR;
     sv::pdl_trigger();
     sv::pdl_wait();
@@ -138,34 +152,89 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     const int e0 = 8 * (lane % LPR);
     // This warp's token, and the groups of rows that it takes of it (a group is of one kind, so
     // the warp decides on it as one); the first ones are asked for ahead of the angles.
-    const int each = kWarps / a.tile, t = warp / each;
-    const unsigned token = blockIdx.x * (unsigned)a.tile + t;
-    const int b = token < total ? (int)(token / a.N) : 0, i = token < total ? (int)(token % a.N) : 0;
-    const int last = min(a.groups[2], (int)(blockIdx.y + 1) * a.chunk);
-    int at = blockIdx.y * a.chunk + (warp - t * each);
-    auto kind_of = [&](int group) { return group < a.groups[0] ? 0 : group < a.groups[1] ? 1 : 2; };
-    auto head_of = [&](int kind, int group) { return (kind ? group - a.groups[kind - 1] : group) * G + lane / LPR; };
-    auto row_of = [&](int kind, int h) { return static_cast<const T*>(a.src[kind]) + (b * a.ss[kind][0] + i * a.ss[kind][1]) + h * a.ss[kind][2]; };
+    const int each = MANY ? 1 : kWarps / a.tile;
+    int t = MANY ? warp * EACH : warp / each;
+    const int end_t = t + EACH;
+    const unsigned token = blockIdx.x * (unsigned)(MANY ? TOKENS : a.tile) + t + (MANY ? lane : 0);
+    int b = token < total ? (int)(token / a.N) : 0, i = token < total ? (int)(token % a.N) : 0;
+    const int last = MANY ? a.groups[2] : min(a.groups[2], (int)(blockIdx.y + 1) * a.chunk);
+    int at = MANY ? 0 : blockIdx.y * a.chunk + (warp - t * each);
+    if (MANY) {
+        if (lane < EACH) s_token[t + lane] = make_int2(b, i);
+        __syncwarp();
+    }
+    // Where a group's rows are read and written: found for its kind (and token), then moved on by its heads.
+    const int lane_row = lane / LPR, stride = each * G;
+    const int row_or_none = !AL || e0 < a.D ? lane_row : 1 << 20;  // lanes behind the row's end have none
+    auto to_kind = [&](int& kind, int& head) {
+        if (kind == 0 && head >= a.heads[0]) {
+            head -= a.groups[0] * G;
+            kind = 1;
+        }
+        if (MODE != DENSE && kind == 1 && head >= a.heads[1]) {
+            head -= (a.groups[1] - a.groups[0]) * G;
+            kind = 2;
+        }
+    };
+    int in_kind = 0, in_head = at * G, in_heads = 0;  // of the next group to ask for; in_head of its first row
+    const T* in_row = nullptr;
+    int64_t in_step = 0;
+    auto find_in = [&](int b, int i) {
+        to_kind(in_kind, in_head);
+        auto of = [&](auto k) {  // (by constants: their operands need no loads)
+            constexpr int K = decltype(k)::value;
+            in_heads = a.heads[K];
+            in_row = static_cast<const T*>(a.src[K]) + (b * a.ss[K][0] + i * a.ss[K][1]) + (in_head + lane_row) * a.ss[K][2] + (AL ? e0 : 0);
+            in_step = a.in_step[K];
+        };
+        if (in_kind == 0) of(Int<0>{});
+        else if (MODE == DENSE || in_kind == 1) of(Int<1>{});
+        else of(Int<2>{});
+    };
     // Groups in flight go through a ring in shared memory, kDepth deep.
     constexpr int PIECES = (int)sizeof(T) / 2;
     uint4* ring = reinterpret_cast<uint4*>(s_raw) + tid;
-    auto fetch = [&](int group, int slot) {
-        if (!AL) return;
-        if (group < last) {
-            const int kind = kind_of(group), h = head_of(kind, group);
-            const bool in = h < a.heads[kind] && e0 < a.D;
-            const T* from = row_of(kind, in ? h : 0) + (in ? e0 : 0);
+    if (AL && e0 >= a.D) {
 #pragma unroll
-            for (int k = 0; k < PIECES; ++k)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sv::smem_u32(ring + (slot * PIECES + k) * kThreads)),
-                             "l"(from + k * 4), "r"(in ? 16 : 0)
-                             : "memory");
+        for (int k = 0; k < kDepth * PIECES; ++k) ring[k * kThreads] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    int ahead_t = t, ahead = at;  // the next group to ask for
+    auto fetch = [&](int slot) {
+        if (!AL) return;
+        if (MANY ? ahead_t < end_t : ahead < last) {
+            if (in_head >= in_heads) {
+                const int2 of = MANY ? s_token[MANY ? ahead_t : 0] : make_int2(b, i);
+                find_in(of.x, of.y);
+            }
+            if (in_head + row_or_none < in_heads) {
+#pragma unroll
+                for (int k = 0; k < PIECES; ++k)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sv::smem_u32(ring + (slot * PIECES + k) * kThreads)),
+                                 "l"(in_row + k * 4)
+                                 : "memory");
+            }
+            in_row += in_step;
+            in_head += stride;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
+        ahead += each;
+        if (MANY && ahead >= last) {
+            ahead = 0;
+            ++ahead_t;
+            in_kind = in_head = in_heads = 0;
+        }
     };
 #pragma unroll
-    for (int k = 0; k < kDepth - 1; ++k) fetch(at + k * each, k);
-    if (tid < a.tile) {
+    for (int k = 0; k < kDepth - 1; ++k) fetch(k);
+    if (MANY) {
+        if (lane < EACH) {
+            int first = -1;
+            int64_t pos = 0;
+            if (token >= total || !token_position<MODE>(a, b, i, pos, first)) first = -1;
+            s_pos[t + lane] = make_float2((float)(pos & ~(int64_t)4095), (float)((int)pos & 4095));
+            s_first[t + lane] = first;
+        }
+    } else if (tid < a.tile) {
         const unsigned x = blockIdx.x * (unsigned)a.tile + tid;
         int first = -1;
         int64_t pos = 0;
@@ -179,75 +248,128 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
         s_freq[j] = make_float2(hi, (float)(f - (double)hi));
     }
     __syncthreads();
-    float* mine = s_turn + t * 3 * RP;
-    const float2 pos = s_pos[t];
-    for (int j = tid - t * each * 32; j < a.R; j += each * 32) {  // by the token's warps
-        const float2 f = s_freq[j], cs = turn(pos.x, pos.y, f.x, f.y);
-        const float sine = a.inverse ? -(cs.y * a.amplitude) : cs.y * a.amplitude;
-        mine[j] = cs.x * a.amplitude;
-        mine[RP + j] = -sine;
-        mine[2 * RP + j] = sine;
+    const float* mine = s_turn + t * 3 * RP;
+    for (int j = tid - t / EACH * each * 32; j < a.R; j += each * 32) {  // by the token's warps
+        const float2 f = s_freq[j];
+        for (int k = 0; k < EACH; ++k) {
+            const float2 pos = s_pos[t + k], cs = turn(pos.x, pos.y, f.x, f.y);
+            const float sine = a.inverse ? -(cs.y * a.amplitude) : cs.y * a.amplitude;
+            float* to = s_turn + (t + k) * 3 * RP + j;
+            to[0] = cs.x * a.amplitude;
+            to[RP] = -sine;
+            to[2 * RP] = sine;
+        }
     }
     if (each == 1) __syncwarp();
     else __syncthreads();
-    const int first = s_first[t];
+    const int first = MANY ? 0 : s_first[t];
     if (first < 0) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         return;
     }
     int page = -1, line = 0;
-    if (MODE != DENSE) page = sv::paged_place(a.c, b, first + i, line);
+    int64_t place = 0, scale_place = 0;  // of this lane's row of the first heads, in the keys and values
+    if (MODE != DENSE) {
+        page = sv::paged_place(a.c, b, first + i, line);
+        const int pg = max(page, 0);
+        place = pg * a.c.page_stride + line * a.c.row_stride + lane_row * a.c.head_stride;
+        if (MODE == CACHE_E4M3) scale_place = ((int64_t)pg * a.c.heads + lane_row) * a.c.page_size + line;
+    }
 
     // This lane's elements: own and partner's factors.  Those of elements that are copied are not used, only read
     // within the block's memory.
     const int R = a.R, turned = 2 * R;
     float2 c[4], s[4];
-    if (PAIR == BESIDE) {
-        const float* at = mine + (e0 < turned ? e0 >> 1 : 0);
-        const float4 cs = *reinterpret_cast<const float4*>(at), sn = *reinterpret_cast<const float4*>(at + 2 * RP);
-        c[0] = make_float2(cs.x, cs.x);
-        c[1] = make_float2(cs.y, cs.y);
-        c[2] = make_float2(cs.z, cs.z);
-        c[3] = make_float2(cs.w, cs.w);
-        s[0] = make_float2(-sn.x, sn.x);
-        s[1] = make_float2(-sn.y, sn.y);
-        s[2] = make_float2(-sn.z, sn.z);
-        s[3] = make_float2(-sn.w, sn.w);
-    } else if (PAIR == LANE) {
-        const float* at = mine + (e0 < R ? e0 : e0 < turned ? e0 - R : 0);
-        const float* from = at + (e0 < R ? RP : 2 * RP);
+    auto factors = [&]() {
+        if (PAIR == BESIDE) {
+            const float* at = mine + (e0 < turned ? e0 >> 1 : 0);
+            const float4 cs = *reinterpret_cast<const float4*>(at), sn = *reinterpret_cast<const float4*>(at + 2 * RP);
+            c[0] = make_float2(cs.x, cs.x);
+            c[1] = make_float2(cs.y, cs.y);
+            c[2] = make_float2(cs.z, cs.z);
+            c[3] = make_float2(cs.w, cs.w);
+            s[0] = make_float2(-sn.x, sn.x);
+            s[1] = make_float2(-sn.y, sn.y);
+            s[2] = make_float2(-sn.z, sn.z);
+            s[3] = make_float2(-sn.w, sn.w);
+        } else if (PAIR == LANE) {
+            const float* at = mine + (e0 < R ? e0 : e0 < turned ? e0 - R : 0);
+            const float* from = at + (e0 < R ? RP : 2 * RP);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float4 cs = reinterpret_cast<const float4*>(at)[k], sn = reinterpret_cast<const float4*>(from)[k];
-            c[2 * k] = make_float2(cs.x, cs.y);
-            c[2 * k + 1] = make_float2(cs.z, cs.w);
-            s[2 * k] = make_float2(sn.x, sn.y);
-            s[2 * k + 1] = make_float2(sn.z, sn.w);
-        }
-    } else {
-        float cc[8], ss[8];
+            for (int k = 0; k < 2; ++k) {
+                const float4 cs = reinterpret_cast<const float4*>(at)[k], sn = reinterpret_cast<const float4*>(from)[k];
+                c[2 * k] = make_float2(cs.x, cs.y);
+                c[2 * k + 1] = make_float2(cs.z, cs.w);
+                s[2 * k] = make_float2(sn.x, sn.y);
+                s[2 * k + 1] = make_float2(sn.z, sn.w);
+            }
+        } else {
+            float cc[8], ss[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int e = e0 + k;
-            cc[k] = 1.0f;
-            ss[k] = 0.0f;
-            if (e < turned) {
-                cc[k] = mine[e < R ? e : e - R];
-                ss[k] = mine[e < R ? RP + e : 2 * RP + e - R];
+            for (int k = 0; k < 8; ++k) {
+                const int e = e0 + k;
+                cc[k] = 1.0f;
+                ss[k] = 0.0f;
+                if (e < turned) {
+                    cc[k] = mine[e < R ? e : e - R];
+                    ss[k] = mine[e < R ? RP + e : 2 * RP + e - R];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                c[k] = make_float2(cc[2 * k], cc[2 * k + 1]);
+                s[k] = make_float2(ss[2 * k], ss[2 * k + 1]);
             }
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            c[k] = make_float2(cc[2 * k], cc[2 * k + 1]);
-            s[k] = make_float2(ss[2 * k], ss[2 * k + 1]);
-        }
-    }
+    };
+    if (!MANY) factors();
     const int mate = PAIR == LANE && e0 < turned ? lane + (e0 < R ? R / 8 : -(R / 8)) : lane;
     const int same = e0 >= turned ? 0 : min(turned - e0, 8);  // elements of this lane that are turned
 
-    for (int slot = 0; at < last; slot = slot + 1 == kDepth ? 0 : slot + 1) {
-        const int kind = kind_of(at), h = head_of(kind, at);
-        const bool in = h < a.heads[kind];
+    bool written = true;
+    int kind = 0, head = at * G, heads = 0;
+    unsigned char* to = nullptr;
+    float* scale = nullptr;
+    int64_t step = 0;
+    for (int slot = 0; MANY ? t < end_t : at < last; slot = slot + 1 == kDepth ? 0 : slot + 1) {
+        if (MANY && at == 0) {  // the next token
+            const int2 of = s_token[MANY ? t : 0];
+            b = of.x;
+            i = of.y;
+            written = s_first[t] >= 0;
+            mine = s_turn + t * 3 * RP;
+            kind = head = heads = 0;
+            factors();
+        }
+        if (head >= heads) {
+            to_kind(kind, head);
+            auto dense = [&](auto k) {
+                constexpr int K = decltype(k)::value;
+                heads = a.heads[K];
+                to = reinterpret_cast<unsigned char*>(static_cast<T*>(a.dst[K]) + (b * a.ds[K][0] + i * a.ds[K][1]) + (head + lane_row) * a.ds[K][2]);
+                step = a.out_step[K];
+            };
+            if (kind == 0) {
+                dense(Int<0>{});
+            } else if (MODE == DENSE) {
+                dense(Int<1>{});
+            } else {
+                heads = a.heads[1];
+                to = (kind == 2 ? a.c.v : a.c.k) + (place + head * a.c.head_stride);
+                step = a.out_step[1];
+                if (MODE == CACHE_E4M3) scale = (kind == 2 ? a.c.v_scale : a.c.k_scale) + (scale_place + head * a.c.page_size);
+            }
+        }
+        const bool in = head + row_or_none < heads && written;
+        const T* row = in_row;  // !AL: read here
+        if (!AL) {
+            if (in_head >= in_heads) {
+                find_in(b, i);
+                row = in_row;
+            }
+            in_row += in_step;
+            in_head += stride;
+        }
         Raw<T, AL> x;
         if (AL) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
@@ -261,12 +383,22 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
                 x.w[4 * k + 3] = w.w;
             }
         } else {
-            x.load(row_of(kind, in ? h : 0), e0, in ? a.D : 0);
+            x.load(row, e0, in ? a.D : 0);
         }
-        fetch(at + (kDepth - 1) * each, slot ? slot - 1 : kDepth - 1);  // into the place of the group before
+        fetch(slot ? slot - 1 : kDepth - 1);  // into the place of the group before
         at += each;
+        if (MANY && at >= last) {
+            at = 0;
+            ++t;
+        }
+        unsigned char* const dst = to;
+        float* const dst_scale = scale;
+        const int of_kind = kind;
+        to += step;
+        head += stride;
+        if (MODE == CACHE_E4M3) scale += (int64_t)stride * a.c.page_size;
         float v[8];
-        if (kind != 2) {
+        if (MODE == DENSE || of_kind != 2) {
             float p[8];
             if (PAIR == BESIDE) {
 #pragma unroll
@@ -279,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
                 for (int k = 0; k < 8; ++k) p[k] = y.at(k);
             } else {
                 // (AL: rows are whole in the ring, fp32 ones in two planes of four elements per lane)
-                const T* from = AL ? reinterpret_cast<const T*>(ring + slot * PIECES * kThreads - lane % LPR) : row_of(kind, in ? h : 0);
+                const T* from = AL ? reinterpret_cast<const T*>(ring + slot * PIECES * kThreads - lane % LPR) : row;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const int e = e0 + k, other = e < R ? e + R : e - R;
@@ -300,20 +432,14 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
                 for (int k = 0; k < 8; ++k)
                     if (k >= same) v[k] = x.at(k);
             }
-            if (MODE == DENSE || kind == 0) {
-                if (in) {
-                    T* to = static_cast<T*>(a.dst[kind]) + (b * a.ds[kind][0] + i * a.ds[kind][1]) + h * a.ds[kind][2];
-                    sv::store_row8<T, AL>(to, e0, a.D, v);
-                }
+            if (MODE == DENSE || of_kind == 0) {
+                if (in) sv::store_row8<T, AL>(reinterpret_cast<T*>(dst), e0, a.D, v);
                 continue;
             }
         }
         if constexpr (MODE != DENSE) {
             const bool live = in && page >= 0;
-            const int head = in ? h : 0, pg = live ? page : 0;
-            unsigned char* to = (kind == 2 ? a.c.v : a.c.k) + (pg * a.c.page_stride + line * a.c.row_stride) + head * a.c.head_stride;
-            float* scale = (kind == 2 ? a.c.v_scale : a.c.k_scale) + ((int64_t)pg * a.c.heads + head) * a.c.page_size + line;
-            if (kind == 2) {  // values as they are
+            if (of_kind == 2) {  // values as they are
                 sv::Eight<T, AL> f;
                 if constexpr (AL) {
 #pragma unroll
@@ -322,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
 #pragma unroll
                     for (int k = 0; k < 8; ++k) f.f[k] = x.at(k);
                 }
-                sv::store_cache_row<T, LPR, MODE == CACHE_E4M3, AL>(to, scale, e0, a.D, live, f);
+                sv::store_cache_row<T, LPR, MODE == CACHE_E4M3, AL>(dst, dst_scale, e0, a.D, live, f);
             } else {
                 sv::Eight<float, AL> f;
                 if constexpr (AL) {
@@ -333,33 +459,50 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
 #pragma unroll
                     for (int k = 0; k < 8; ++k) f.f[k] = v[k];
                 }
-                sv::store_cache_row<float, LPR, MODE == CACHE_E4M3, AL>(to, scale, e0, a.D, live, f);
+                sv::store_cache_row<float, LPR, MODE == CACHE_E4M3, AL>(dst, dst_scale, e0, a.D, live, f);
             }
         }
     }
 }
 
-template <typename T, int LPR, int MODE, bool AL, int PAIR>
-cudaError_t launch_pair(RotaryArgs& a, cudaStream_t stream) {
+template <typename T, int LPR, int MODE, bool AL, int PAIR, bool MANY>
+cudaError_t launch_rows(RotaryArgs& a, cudaStream_t stream) {
     const int64_t tokens = (int64_t)a.B * a.N;
     constexpr int sms = 152, G = 32 / LPR;
-    for (int k = 0, n = 0; k < 3; ++k) a.groups[k] = n += (a.heads[k] + G - 1) / G;
     // Tokens of a block: as many as leave six blocks per SM, since they share the frequencies;
     // a few tokens are spread over blocks by their rows instead, one pass of a block's warps each.
     a.tile = 1;
     while (a.tile < kMaxTokens && tokens / (2 * a.tile) >= 6 * sms) a.tile *= 2;
-    a.chunk = tokens >= 2 * sms ? a.groups[2] : kWarps;
+    if (MANY) a.tile = kMaxTokens * kEach;
+    const int64_t stride = (MANY ? 1 : kWarps / a.tile) * G;  // heads from a group of a warp to its next
+    for (int k = 0; k < 3; ++k) a.in_step[k] = stride * a.ss[k][2];
+    a.out_step[0] = stride * a.ds[0][2] * (int64_t)sizeof(T);
+    a.out_step[1] = stride * (MODE == DENSE ? a.ds[1][2] * (int64_t)sizeof(T) : a.c.head_stride);
+    a.chunk = MANY || tokens >= 2 * sms ? a.groups[2] : kWarps;
     const dim3 grid((unsigned)((tokens + a.tile - 1) / a.tile), (unsigned)((a.groups[2] + a.chunk - 1) / a.chunk));
     // Without pairs the factors are read all the same: eight floats behind the first of a plane.
     const size_t smem = ((size_t)a.tile * 3 * ((a.R + 3) & ~3) + 8) * sizeof(float);
     constexpr size_t ring = AL ? kDepth * kThreads * sizeof(T) * 8 : 0;
     static sv::KernelLaunchCache cache;
-    auto kern = rotary_kernel<T, LPR, MODE, AL, PAIR>;
+    auto kern = rotary_kernel<T, LPR, MODE, AL, PAIR, MANY>;
     int max_dyn = 0;
     const cudaError_t e = cache.setup((const void*)kern, &max_dyn);
     if (e != cudaSuccess) return e;
     if (ring + smem > (size_t)max_dyn) return cudaErrorInvalidValue;
     return sv::launch_serial(kern, grid, dim3(kThreads), ring + smem, stream, a);
+}
+
+template <typename T, int LPR, int MODE, bool AL, int PAIR>
+cudaError_t launch_pair(RotaryArgs& a, cudaStream_t stream) {
+    constexpr int G = 32 / LPR;
+    for (int k = 0, n = 0; k < 3; ++k) a.groups[k] = n += (a.heads[k] + G - 1) / G;
+    // Tokens of few rows, enough of them for a full wave of blocks (us, four tokens of a warp and one): 64 x 2000 of
+    // 4 + 1 heads of 64 (2 groups) 61 and 80, 32 x 2000 of 8 + 2 of 128 (5 groups) 58 and 64, of 14 + 2 (8 groups)
+    // 45 and 46; but 8 x 1000 of 4 + 1 12 and 8, fp32 35 and 30, on the way into a cache 41 and 35.
+    constexpr bool CAN = AL && PAIR != ANYWHERE && MODE == DENSE && sizeof(T) == 2;
+    if (CAN && a.groups[2] <= 8 && (int64_t)a.B * a.N >= 4 * 152 * kMaxTokens * kEach)
+        return launch_rows<T, LPR, MODE, AL, PAIR, CAN>(a, stream);
+    return launch_rows<T, LPR, MODE, AL, PAIR, false>(a, stream);
 }
 
 template <typename T, int LPR, int MODE, bool AL>
