@@ -21,10 +21,10 @@
 // fp32 score whatever is above T + 2 e is in, whatever is below T - 2 e out, and only what
 // lies between (one or two blocks as a rule) is summed again in 64 bits.  Where that are many
 // (equal summaries), the 64-bit scores are selected among by their upper bits, then the lower ones.
-// One GB300: 32 chains of 6 queries, 32 over 8 heads of 128, 256 to 1024 blocks, 64 of them by bounds 50 us, 30 of it
+// One GB300: 32 chains of 6 queries, 32 over 8 heads of 128, 256 to 1024 blocks, 64 of them by bounds 46 us, 28 of it
 // the scores (floor 13: 84 MB of summaries; a warp's loads one after the other - row, page, summary, query - and
-// 16 warps an SM are what it waits for), by means 41; one token over 1562 blocks 16 us; 16 trees of 61 over 128 to
-// 512 blocks 105 us, 116 where their queries share a list.
+// 16 warps an SM are what it waits for), by means 38; one token over 1562 blocks 16 us; 16 trees of 61 over 128 to
+// 512 blocks 90 us, 98 where their queries share a list.
 //
 // The error of an fp32 score: its (exact) products are summed in chains of four matrix products, each
 // of which sums 17 numbers, off by at most 17 units of 2^-23 of the largest partial sum, and up to
@@ -367,10 +367,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32, KC * (BOUNDS ? 2 : 1) > 8 ? 
                 for (int k = 0; k < 2; ++k) {
                     const int e = 32 * (k0 + k);
                     if (FULL) {
-                        q[t][k] = sv::ld_nc_v4(from[t] + e);
+                        q[t][k] = __ldg(reinterpret_cast<const uint4*>(from[t] + e));
                     } else {
                         q[t][k] = make_uint4(0u, 0u, 0u, 0u);
-                        if (e + 8 * t4 < D) q[t][k] = sv::ld_nc_v4(from[t] + e);
+                        if (e + 8 * t4 < D) q[t][k] = __ldg(reinterpret_cast<const uint4*>(from[t] + e));
                     }
                     if (count) norm[t] += magnitudes(q[t][k]);
                 }
@@ -464,6 +464,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, KC * (BOUNDS ? 2 : 1) > 8 ? 
 // ---------------------------------------------------------------- selection
 
 constexpr int kFew = 64;     // blocks next to the border whose 64-bit scores are compared with one another
+constexpr int kAtOnce = 4;   // query rows that a warp has in flight as it sums again (32 chains of 6: 46 us; one 47, eight 52)
 constexpr int kKept = 8192;  // blocks whose keys are kept in shared memory
 
 struct SelectShared {
@@ -503,46 +504,53 @@ __device__ __forceinline__ uint64_t exact_rows(const SelectArgs& a, float scale,
     }
     uint64_t best = 0;
     bool nan = false;
-#pragma unroll 2
-    for (int r = r0; r < rows; r += step) {
-        const uint16_t* q = a.q + b * a.q_sb + (i0 + r / a.g) * a.q_st + (int64_t)(h * a.g + r % a.g) * a.q_sh;
-        uint32_t x[4];
+    for (int r1 = r0; r1 < rows; r1 += kAtOnce * step) {  // rows whose loads are in flight together
+        uint32_t rows_x[kAtOnce][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = 2 * lane + 64 * k < a.D ? two(q + 2 * lane + 64 * k) : 0u;
-        auto factors = [&](int e, float& u, float& w) {  // q_d and m_d of the lane's element e
-            u = e & 1 ? sv::bf16_hi(x[e / 2]) : sv::bf16_lo(x[e / 2]);
-            const uint32_t y = BOUNDS && !(u >= 0.0f) ? lo[BOUNDS ? e / 2 : 0] : hi[e / 2];
-            w = e & 1 ? sv::bf16_hi(y) : sv::bf16_lo(y);
-        };
-        uint64_t key;
-        if (scale != 0.0f) {
-            int upper = 0, lower = 0;
+        for (int f = 0; f < kAtOnce; ++f) {
+            const int r = r1 + f * step < rows ? r1 + f * step : r1;  // (a row twice does no harm)
+            const uint16_t* q = a.q + b * a.q_sb + (i0 + r / a.g) * a.q_st + (int64_t)(h * a.g + r % a.g) * a.q_sh;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float u, w;
-                factors(e, u, w);
-                const float p = u * w * scale;
-                const int n = __float2int_rn(p);
-                upper += n;
-                lower += __float2int_rn((p - (float)n) * 0x1p22f);
-            }
-            upper = __reduce_add_sync(0xffffffffu, upper);
-            lower = __reduce_add_sync(0xffffffffu, lower);
-            key = (uint64_t)((int64_t)upper * (1 << 22) + lower) ^ 0x8000000000000000ull;
-        } else {
-            double s = 0.0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float u, w;
-                factors(e, u, w);
-                if (2 * lane + 64 * (e / 2) < a.D) s = fma((double)u, (double)w, s);
-            }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (s != s) nan = true;
-            key = key64(s == 0.0 ? 0.0 : s);  // -0 is 0
+            for (int k = 0; k < 4; ++k) rows_x[f][k] = 2 * lane + 64 * k < a.D ? two(q + 2 * lane + 64 * k) : 0u;
         }
-        if (key > best) best = key;
+#pragma unroll
+        for (int f = 0; f < kAtOnce; ++f) {
+            const uint32_t (&x)[4] = rows_x[f];
+            auto factors = [&](int e, float& u, float& w) {  // q_d and m_d of the lane's element e
+                u = e & 1 ? sv::bf16_hi(x[e / 2]) : sv::bf16_lo(x[e / 2]);
+                const uint32_t y = BOUNDS && !(u >= 0.0f) ? lo[BOUNDS ? e / 2 : 0] : hi[e / 2];
+                w = e & 1 ? sv::bf16_hi(y) : sv::bf16_lo(y);
+            };
+            uint64_t key;
+            if (scale != 0.0f) {
+                int upper = 0, lower = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float u, w;
+                    factors(e, u, w);
+                    const float p = u * w * scale;
+                    const int n = __float2int_rn(p);
+                    upper += n;
+                    lower += __float2int_rn((p - (float)n) * 0x1p22f);
+                }
+                upper = __reduce_add_sync(0xffffffffu, upper);
+                lower = __reduce_add_sync(0xffffffffu, lower);
+                key = (uint64_t)((int64_t)upper * (1 << 22) + lower) ^ 0x8000000000000000ull;
+            } else {
+                double s = 0.0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float u, w;
+                    factors(e, u, w);
+                    if (2 * lane + 64 * (e / 2) < a.D) s = fma((double)u, (double)w, s);
+                }
+#pragma unroll
+                for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (s != s) nan = true;
+                key = key64(s == 0.0 ? 0.0 : s);  // -0 is 0
+            }
+            if (key > best) best = key;
+        }
     }
     return nan ? ~0ull : best;
 }
@@ -1070,7 +1078,7 @@ cudaError_t run_select(SelectArgs& a, int B, int64_t lists, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     // A warp per list, all in registers, where its blocks fit there, no list has many rows to sum again, and the
-    // lists are more than the SMs: 1536 lists of up to 1024 blocks 50 us (with the scores) against 65 by a
+    // lists are more than the SMs: 1536 lists of up to 1024 blocks 46 us (with the scores) against 61 by a
     // CTA each, 8 lists of 1562 17.3 against 16.3.
     if (a.max_pages <= 2048 && lists > 152 && (a.lists > 1 ? 1 : a.Q) * a.g <= 32) {
         const dim3 grid((unsigned)((lists + 3) / 4));
