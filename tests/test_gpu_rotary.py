@@ -84,6 +84,35 @@ def test_matches_the_plain_form(sv, shape):  # noqa: F811
     assert a.data_ptr() == wide.data_ptr() and torch.equal(wide[:, :, :Hq], first) and torch.equal(wide[:, :, Hq:], first_k)
 
 
+@pytest.mark.parametrize("B,N,Hq,Hk,D,R,interleaved", [
+    (5, 4001, 3, 1, 64, 32, False), (7, 2801, 2, 1, 128, 20, True), (5, 4001, 1, 2, 256, 128, False),
+    (19999, 1, 9, 0, 96, 16, False), (3, 7000, 32, 0, 40, 8, True)])
+def test_many_tokens_of_few_rows(sv, B, N, Hq, Hk, D, R, interleaved):  # noqa: F811
+    """A warp takes several tokens, across batch rows, some of which are not written; alike in place."""
+    import torch
+    rng = np.random.default_rng([B, N, D])
+    q, k = make(rng, B, N, Hq, D, "bf16"), make(rng, B, N, Hk, D, "bf16") if Hk else None
+    freq = 10000.0 ** (-np.arange(R) / R)
+    base, new = rng.integers(0, 100000, B), rng.integers(0, N + 1, B)
+    base[1], new[0], new[2] = -1, N, 0
+    f, kw = torch.from_numpy(freq).cuda(), dict(interleaved=interleaved, new_len=ints(new))
+    live = (np.arange(N) < new[:, None]) & (base >= 0)[:, None]
+    pos = context.positions(base, N)
+    outs = [torch.full(x.shape, 9.0, dtype=x.dtype, device="cuda") if x is not None else None for x in (q, k)]
+    sv.spec_rotary(q, f, ints(base), key=k, out=outs[0], out_key=outs[1], **kw)
+    for x, out in zip((q, k), outs):
+        if x is None:
+            continue
+        got, want = host(out), context.rotary(host(x), freq, pos, interleaved)
+        assert (got[~live] == 9).all()
+        close(got[live], want[live], reach(host(x), R, interleaved)[live], "bf16")
+        assert torch.equal(out[..., 2 * R:][torch.from_numpy(live).cuda()], x[..., 2 * R:][torch.from_numpy(live).cuda()])
+    q2 = q.clone()
+    sv.spec_rotary(q2, f, ints(base), key=k, out=q2, out_key=k, **kw)
+    keep = torch.from_numpy(live).cuda()[..., None, None]
+    assert torch.equal(q2, torch.where(keep, outs[0], q))
+
+
 def test_turning_back(sv):  # noqa: F811
     """The inverse is the transpose: <turn(x), y> = <x, turn back(y)> for every x and y, as a gradient needs."""
     import torch
