@@ -13,8 +13,9 @@
 // With the bytes in flight, instructions bound it.  160 a group of rows, most of them for 64-bit addresses and for
 // factors picked one by one, took 87 us in those 4 x 6001 tokens; factors read as vectors from planes of cosines
 // and sines 82; pointers that move on by their kind's stride, found anew only for another kind, 76 (5.9 TB/s).
-// fp32 201 us (4.9 TB/s), num_freq 10 105; 16 x 2048 tokens on their way into a cache of bf16 83 (floor 75), of e4m3 93.
-// Few heads pay for their tokens' sines and places: 64 x 2000 tokens of 4 + 1 heads of 64 61, their bytes' time 25.
+// fp32 198 us (5.0 TB/s), num_freq 10 104; 16 x 2048 tokens on their way into a cache of bf16 83 (floor 75), of e4m3 92.
+// Tokens of few rows pay for their sines, places and idle lanes, so a warp takes four of them at once (rotary_few_kernel):
+// 64 x 2000 tokens of 4 + 1 heads of 64 43 us (80 without; their bytes' time 24), into a cache of bf16 49 (89; 18).
 //
 // Angles: position * freq in fp32 would be off by whole radians at 10^7 positions.  Counted in
 // turns only the fraction matters: f = freq / 2 pi as hi + lo (fp32 each, from its 64 bits), the
@@ -56,6 +57,7 @@ struct RotaryArgs {
     int heads[3];        // of queries, keys, values
     int64_t in_step[3];  // from a group of a warp to its next one: elements,
     int64_t out_step[2]; // bytes (queries, keys and values)
+    int magic[3];        // 2^16 / heads, rounded up (kernel for few rows)
     int groups[3];       // groups of rows of a token: [0, groups[0]) queries, then keys, then values
     const double* freq;
     const int32_t* depth;
@@ -67,6 +69,9 @@ struct RotaryArgs {
     int tile;   // tokens of a block: 1, 2, 4 or 8
     int chunk;  // groups of a token that a block does
 };
+
+// n strides (n >= 0): two instructions, where the product of a signed number takes four.
+__device__ __forceinline__ int64_t times(int n, int64_t stride) { return (int64_t)((uint64_t)(uint32_t)n * (uint64_t)stride); }
 
 // Position of token i of row b; false where the token is not written.
 template <int MODE>
@@ -98,6 +103,62 @@ __device__ __forceinline__ float2 turn(float big, float rest, float fh, float fl
     float s, c;
     sincospif(2.0f * r, &s, &c);
     return make_float2(c, s);
+}
+
+// A token's cosine, negated sine and sine of one frequency, in planes of RP.
+__device__ __forceinline__ void put_turn(float* to, int RP, float2 pos, float2 f, float amplitude, int inverse) {
+    const float2 cs = turn(pos.x, pos.y, f.x, f.y);
+    const float sine = inverse ? -(cs.y * amplitude) : cs.y * amplitude;
+    to[0] = cs.x * amplitude;
+    to[RP] = -sine;
+    to[2 * RP] = sine;
+}
+
+// The factors of a lane's elements e0 .. e0 + 7: of their own (c), and of their partners (s).  Those of elements that
+// are copied are not used, only read within the block's memory.
+template <int PAIR>
+__device__ __forceinline__ void row_factors(const float* planes, int RP, int R, int e0, float2 c[4], float2 s[4]) {
+    const int turned = 2 * R;
+    if (PAIR == BESIDE) {
+        const float* at = planes + (e0 < turned ? e0 >> 1 : 0);
+        const float4 cs = *reinterpret_cast<const float4*>(at), sn = *reinterpret_cast<const float4*>(at + 2 * RP);
+        c[0] = make_float2(cs.x, cs.x);
+        c[1] = make_float2(cs.y, cs.y);
+        c[2] = make_float2(cs.z, cs.z);
+        c[3] = make_float2(cs.w, cs.w);
+        s[0] = make_float2(-sn.x, sn.x);
+        s[1] = make_float2(-sn.y, sn.y);
+        s[2] = make_float2(-sn.z, sn.z);
+        s[3] = make_float2(-sn.w, sn.w);
+    } else if (PAIR == LANE) {
+        const float* at = planes + (e0 < R ? e0 : e0 < turned ? e0 - R : 0);
+        const float* from = at + (e0 < R ? RP : 2 * RP);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float4 cs = reinterpret_cast<const float4*>(at)[k], sn = reinterpret_cast<const float4*>(from)[k];
+            c[2 * k] = make_float2(cs.x, cs.y);
+            c[2 * k + 1] = make_float2(cs.z, cs.w);
+            s[2 * k] = make_float2(sn.x, sn.y);
+            s[2 * k + 1] = make_float2(sn.z, sn.w);
+        }
+    } else {
+        float cc[8], ss[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int e = e0 + k;
+            cc[k] = 1.0f;
+            ss[k] = 0.0f;
+            if (e < turned) {
+                cc[k] = planes[e < R ? e : e - R];
+                ss[k] = planes[e < R ? RP + e : 2 * RP + e - R];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            c[k] = make_float2(cc[2 * k], cc[2 * k + 1]);
+            s[k] = make_float2(ss[2 * k], ss[2 * k + 1]);
+        }
+    }
 }
 
 // Eight elements of a row as they lie in memory (AL), or widened one by one; zero where there is no row.
@@ -133,17 +194,15 @@ struct Raw {
 };
 
 // grid: x over tiles of tokens, y over chunks of a token's rows.  LPR lanes hold a row.  A token is one warp's or
-// several warps'; MANY (DENSE, tokens of few rows): a warp takes kEach tokens, one after the other.
-template <typename T, int LPR, int MODE, bool AL, int PAIR, bool MANY>
+// several warps'.
+template <typename T, int LPR, int MODE, bool AL, int PAIR>
 __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ RotaryArgs a) {
     extern __shared__ uint4 s_raw[];  // AL: the ring; then of each token RP cosines, sines negated, sines
     const int RP = (a.R + 3) & ~3;
     float* s_turn = reinterpret_cast<float*>(s_raw + (AL ? kDepth * ((int)sizeof(T) / 2) * kThreads : 0));
     __shared__ float2 s_freq[kMaxFreq];
-    constexpr int EACH = MANY ? kEach : 1, TOKENS = kMaxTokens * EACH;
-    __shared__ float2 s_pos[TOKENS];             // a multiple of 4096, and the rest
-    __shared__ int s_first[TOKENS];              // the row's base; -1: token not written
-    __shared__ int2 s_token[MANY ? TOKENS : 1];  // batch row and index
+    __shared__ float2 s_pos[kMaxTokens];  // a multiple of 4096, and the rest
+    __shared__ int s_first[kMaxTokens];   // the row's base; -1: token not written
     constexpr int G = 32 / LPR;
     sv::pdl_trigger();
     sv::pdl_wait();
@@ -152,18 +211,12 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     const int e0 = 8 * (lane % LPR);
     // This warp's token, and the groups of rows that it takes of it (a group is of one kind, so
     // the warp decides on it as one); the first ones are asked for ahead of the angles.
-    const int each = MANY ? 1 : kWarps / a.tile;
-    int t = MANY ? warp * EACH : warp / each;
-    const int end_t = t + EACH;
-    const unsigned token = blockIdx.x * (unsigned)(MANY ? TOKENS : a.tile) + t + (MANY ? lane : 0);
-    int b = token < total ? (int)(token / a.N) : 0, i = token < total ? (int)(token % a.N) : 0;
-    const int last = MANY ? a.groups[2] : min(a.groups[2], (int)(blockIdx.y + 1) * a.chunk);
-    int at = MANY ? 0 : blockIdx.y * a.chunk + (warp - t * each);
-    if (MANY) {
-        if (lane < EACH) s_token[t + lane] = make_int2(b, i);
-        __syncwarp();
-    }
-    // Where a group's rows are read and written: found for its kind (and token), then moved on by its heads.
+    const int each = kWarps / a.tile, t = warp / each;
+    const unsigned token = blockIdx.x * (unsigned)a.tile + t;
+    const int b = token < total ? (int)(token / a.N) : 0, i = token < total ? (int)(token % a.N) : 0;
+    const int last = min(a.groups[2], (int)(blockIdx.y + 1) * a.chunk);
+    int at = blockIdx.y * a.chunk + (warp - t * each);
+    // Where a group's rows are read and written: found for its kind, then moved on by its heads.
     const int lane_row = lane / LPR, stride = each * G;
     const int row_or_none = !AL || e0 < a.D ? lane_row : 1 << 20;  // lanes behind the row's end have none
     auto to_kind = [&](int& kind, int& head) {
@@ -179,12 +232,12 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     int in_kind = 0, in_head = at * G, in_heads = 0;  // of the next group to ask for; in_head of its first row
     const T* in_row = nullptr;
     int64_t in_step = 0;
-    auto find_in = [&](int b, int i) {
+    auto find_in = [&]() {
         to_kind(in_kind, in_head);
         auto of = [&](auto k) {  // (by constants: their operands need no loads)
             constexpr int K = decltype(k)::value;
             in_heads = a.heads[K];
-            in_row = static_cast<const T*>(a.src[K]) + (b * a.ss[K][0] + i * a.ss[K][1]) + (in_head + lane_row) * a.ss[K][2] + (AL ? e0 : 0);
+            in_row = static_cast<const T*>(a.src[K]) + (times(b, a.ss[K][0]) + times(i, a.ss[K][1]) + times(in_head + lane_row, a.ss[K][2]) + (AL ? e0 : 0));
             in_step = a.in_step[K];
         };
         if (in_kind == 0) of(Int<0>{});
@@ -198,14 +251,11 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
 #pragma unroll
         for (int k = 0; k < kDepth * PIECES; ++k) ring[k * kThreads] = make_uint4(0u, 0u, 0u, 0u);
     }
-    int ahead_t = t, ahead = at;  // the next group to ask for
+    int ahead = at;  // the next group to ask for
     auto fetch = [&](int slot) {
         if (!AL) return;
-        if (MANY ? ahead_t < end_t : ahead < last) {
-            if (in_head >= in_heads) {
-                const int2 of = MANY ? s_token[MANY ? ahead_t : 0] : make_int2(b, i);
-                find_in(of.x, of.y);
-            }
+        if (ahead < last) {
+            if (in_head >= in_heads) find_in();
             if (in_head + row_or_none < in_heads) {
 #pragma unroll
                 for (int k = 0; k < PIECES; ++k)
@@ -218,23 +268,10 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         ahead += each;
-        if (MANY && ahead >= last) {
-            ahead = 0;
-            ++ahead_t;
-            in_kind = in_head = in_heads = 0;
-        }
     };
 #pragma unroll
     for (int k = 0; k < kDepth - 1; ++k) fetch(k);
-    if (MANY) {
-        if (lane < EACH) {
-            int first = -1;
-            int64_t pos = 0;
-            if (token >= total || !token_position<MODE>(a, b, i, pos, first)) first = -1;
-            s_pos[t + lane] = make_float2((float)(pos & ~(int64_t)4095), (float)((int)pos & 4095));
-            s_first[t + lane] = first;
-        }
-    } else if (tid < a.tile) {
+    if (tid < a.tile) {
         const unsigned x = blockIdx.x * (unsigned)a.tile + tid;
         int first = -1;
         int64_t pos = 0;
@@ -248,21 +285,14 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
         s_freq[j] = make_float2(hi, (float)(f - (double)hi));
     }
     __syncthreads();
-    const float* mine = s_turn + t * 3 * RP;
-    for (int j = tid - t / EACH * each * 32; j < a.R; j += each * 32) {  // by the token's warps
-        const float2 f = s_freq[j];
-        for (int k = 0; k < EACH; ++k) {
-            const float2 pos = s_pos[t + k], cs = turn(pos.x, pos.y, f.x, f.y);
-            const float sine = a.inverse ? -(cs.y * a.amplitude) : cs.y * a.amplitude;
-            float* to = s_turn + (t + k) * 3 * RP + j;
-            to[0] = cs.x * a.amplitude;
-            to[RP] = -sine;
-            to[2 * RP] = sine;
-        }
+    float* mine = s_turn + t * 3 * RP;
+    const float2 pos = s_pos[t];
+    for (int j = tid - t * each * 32; j < a.R; j += each * 32) {  // by the token's warps
+        put_turn(mine + j, RP, pos, s_freq[j], a.amplitude, a.inverse);
     }
     if (each == 1) __syncwarp();
     else __syncthreads();
-    const int first = MANY ? 0 : s_first[t];
+    const int first = s_first[t];
     if (first < 0) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         return;
@@ -272,81 +302,27 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     if (MODE != DENSE) {
         page = sv::paged_place(a.c, b, first + i, line);
         const int pg = max(page, 0);
-        place = pg * a.c.page_stride + line * a.c.row_stride + lane_row * a.c.head_stride;
+        place = times(pg, a.c.page_stride) + times(line, a.c.row_stride) + times(lane_row, a.c.head_stride);
         if (MODE == CACHE_E4M3) scale_place = ((int64_t)pg * a.c.heads + lane_row) * a.c.page_size + line;
     }
 
-    // This lane's elements: own and partner's factors.  Those of elements that are copied are not used, only read
-    // within the block's memory.
     const int R = a.R, turned = 2 * R;
     float2 c[4], s[4];
-    auto factors = [&]() {
-        if (PAIR == BESIDE) {
-            const float* at = mine + (e0 < turned ? e0 >> 1 : 0);
-            const float4 cs = *reinterpret_cast<const float4*>(at), sn = *reinterpret_cast<const float4*>(at + 2 * RP);
-            c[0] = make_float2(cs.x, cs.x);
-            c[1] = make_float2(cs.y, cs.y);
-            c[2] = make_float2(cs.z, cs.z);
-            c[3] = make_float2(cs.w, cs.w);
-            s[0] = make_float2(-sn.x, sn.x);
-            s[1] = make_float2(-sn.y, sn.y);
-            s[2] = make_float2(-sn.z, sn.z);
-            s[3] = make_float2(-sn.w, sn.w);
-        } else if (PAIR == LANE) {
-            const float* at = mine + (e0 < R ? e0 : e0 < turned ? e0 - R : 0);
-            const float* from = at + (e0 < R ? RP : 2 * RP);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float4 cs = reinterpret_cast<const float4*>(at)[k], sn = reinterpret_cast<const float4*>(from)[k];
-                c[2 * k] = make_float2(cs.x, cs.y);
-                c[2 * k + 1] = make_float2(cs.z, cs.w);
-                s[2 * k] = make_float2(sn.x, sn.y);
-                s[2 * k + 1] = make_float2(sn.z, sn.w);
-            }
-        } else {
-            float cc[8], ss[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int e = e0 + k;
-                cc[k] = 1.0f;
-                ss[k] = 0.0f;
-                if (e < turned) {
-                    cc[k] = mine[e < R ? e : e - R];
-                    ss[k] = mine[e < R ? RP + e : 2 * RP + e - R];
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                c[k] = make_float2(cc[2 * k], cc[2 * k + 1]);
-                s[k] = make_float2(ss[2 * k], ss[2 * k + 1]);
-            }
-        }
-    };
-    if (!MANY) factors();
+    row_factors<PAIR>(mine, RP, R, e0, c, s);
     const int mate = PAIR == LANE && e0 < turned ? lane + (e0 < R ? R / 8 : -(R / 8)) : lane;
     const int same = e0 >= turned ? 0 : min(turned - e0, 8);  // elements of this lane that are turned
 
-    bool written = true;
     int kind = 0, head = at * G, heads = 0;
     unsigned char* to = nullptr;
     float* scale = nullptr;
     int64_t step = 0;
-    for (int slot = 0; MANY ? t < end_t : at < last; slot = slot + 1 == kDepth ? 0 : slot + 1) {
-        if (MANY && at == 0) {  // the next token
-            const int2 of = s_token[MANY ? t : 0];
-            b = of.x;
-            i = of.y;
-            written = s_first[t] >= 0;
-            mine = s_turn + t * 3 * RP;
-            kind = head = heads = 0;
-            factors();
-        }
+    for (int slot = 0; at < last; slot = slot + 1 == kDepth ? 0 : slot + 1) {
         if (head >= heads) {
             to_kind(kind, head);
             auto dense = [&](auto k) {
                 constexpr int K = decltype(k)::value;
                 heads = a.heads[K];
-                to = reinterpret_cast<unsigned char*>(static_cast<T*>(a.dst[K]) + (b * a.ds[K][0] + i * a.ds[K][1]) + (head + lane_row) * a.ds[K][2]);
+                to = reinterpret_cast<unsigned char*>(static_cast<T*>(a.dst[K]) + (times(b, a.ds[K][0]) + times(i, a.ds[K][1]) + times(head + lane_row, a.ds[K][2])));
                 step = a.out_step[K];
             };
             if (kind == 0) {
@@ -355,16 +331,16 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
                 dense(Int<1>{});
             } else {
                 heads = a.heads[1];
-                to = (kind == 2 ? a.c.v : a.c.k) + (place + head * a.c.head_stride);
+                to = (kind == 2 ? a.c.v : a.c.k) + (place + times(head, a.c.head_stride));
                 step = a.out_step[1];
                 if (MODE == CACHE_E4M3) scale = (kind == 2 ? a.c.v_scale : a.c.k_scale) + (scale_place + head * a.c.page_size);
             }
         }
-        const bool in = head + row_or_none < heads && written;
+        const bool in = head + row_or_none < heads;
         const T* row = in_row;  // !AL: read here
         if (!AL) {
             if (in_head >= in_heads) {
-                find_in(b, i);
+                find_in();
                 row = in_row;
             }
             in_row += in_step;
@@ -387,10 +363,6 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
         }
         fetch(slot ? slot - 1 : kDepth - 1);  // into the place of the group before
         at += each;
-        if (MANY && at >= last) {
-            at = 0;
-            ++t;
-        }
         unsigned char* const dst = to;
         float* const dst_scale = scale;
         const int of_kind = kind;
@@ -465,26 +437,197 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     }
 }
 
-template <typename T, int LPR, int MODE, bool AL, int PAIR, bool MANY>
+// Tokens of few rows (bf16): a warp takes kEach tokens, and a group of rows may be of several of them, since the rows of
+// each kind are taken together, token by token.  What a token costs (its place, a warp's start and the lanes that a
+// group leaves idle) is shared; the factors are read for each group.  grid: x over tiles of kWarps * kEach tokens.
+template <int LPR, int MODE, int PAIR>
+__global__ void __launch_bounds__(kThreads, 4) rotary_few_kernel(const __grid_constant__ RotaryArgs a) {
+    extern __shared__ uint4 s_raw[];  // the ring; then of each token RP cosines, sines negated, sines
+    const int RP = (a.R + 3) & ~3;
+    float* s_turn = reinterpret_cast<float*>(s_raw + kDepth * kThreads);
+    constexpr int G = 32 / LPR, TOKENS = kWarps * kEach;
+    __shared__ float2 s_freq[kMaxFreq];
+    __shared__ float2 s_pos[TOKENS];
+    __shared__ int s_state[TOKENS];                            // 2: written, 1: but its page is a hole, 0: not written
+    __shared__ int64_t s_in[3][TOKENS], s_out[2][TOKENS];      // offsets of a token's first row
+    __shared__ int64_t s_scale[MODE == CACHE_E4M3 ? TOKENS : 1];
+    sv::pdl_trigger();
+    sv::pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), t0 = warp * kEach;
+    const unsigned total = (unsigned)a.B * (unsigned)a.N, token = blockIdx.x * (unsigned)TOKENS + t0 + lane;
+    const bool real = lane < kEach && token < total;
+    const int b = real ? (int)(token / a.N) : 0, i = real ? (int)(token % a.N) : 0;
+    const int e0 = 8 * (lane % LPR), lane_row = lane / LPR;
+    if (lane < kEach) {
+#pragma unroll
+        for (int k = 0; k < (MODE == DENSE ? 2 : 3); ++k) s_in[k][t0 + lane] = times(b, a.ss[k][0]) + times(i, a.ss[k][1]);
+#pragma unroll
+        for (int k = 0; k < (MODE == DENSE ? 2 : 1); ++k) s_out[k][t0 + lane] = times(b, a.ds[k][0]) + times(i, a.ds[k][1]);
+    }
+    uint4* ring = s_raw + tid;
+    if (e0 >= a.D) {
+#pragma unroll
+        for (int k = 0; k < kDepth; ++k) ring[k * kThreads] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __syncwarp();
+    // Group x: its kind, and this lane's token of the warp (kEach: none) and head.
+    auto row_of = [&](int x, int& kind, int& tt, int& h) {
+        kind = x < a.groups[0] ? 0 : MODE == DENSE || x < a.groups[1] ? 1 : 2;
+        const int r = (x - (kind == 0 ? 0 : kind == 1 ? a.groups[0] : a.groups[1])) * G + lane_row;
+        const int heads = a.heads[MODE != DENSE && kind == 2 ? 1 : kind];
+        tt = (int)((unsigned)r * (unsigned)a.magic[MODE != DENSE && kind == 2 ? 1 : kind] >> 16);
+        h = r - tt * heads;
+    };
+    auto fetch = [&](int x, int slot) {
+        if (x < a.groups[2]) {
+            int kind, tt, h;
+            row_of(x, kind, tt, h);
+            if (tt < kEach && e0 < a.D) {
+                const uint16_t* from = static_cast<const uint16_t*>(a.src[kind]) + (s_in[kind][t0 + tt] + times(h, a.ss[kind][2]) + e0);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sv::smem_u32(ring + slot * kThreads)), "l"(from) : "memory");
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int k = 0; k < kDepth - 1; ++k) fetch(k, k);
+    if (lane < kEach) {
+        int first = -1, state = 0;
+        int64_t pos = 0;
+        if (real && token_position<MODE>(a, b, i, pos, first)) {
+            state = 2;
+            if (MODE != DENSE) {
+                int line;
+                const int page = sv::paged_place(a.c, b, first + i, line);
+                if (page < 0) state = 1;
+                else s_out[1][t0 + lane] = times(page, a.c.page_stride) + times(line, a.c.row_stride);
+                if (MODE == CACHE_E4M3) s_scale[MODE == CACHE_E4M3 ? t0 + lane : 0] = times(max(page, 0), (int64_t)a.c.heads * a.c.page_size) + line;
+            }
+        }
+        s_pos[t0 + lane] = make_float2((float)(pos & ~(int64_t)4095), (float)((int)pos & 4095));
+        s_state[t0 + lane] = state;
+    }
+    for (int j = tid; j < a.R; j += kThreads) {
+        const double f = a.freq[j] * 0.15915494309189533577;
+        const float hi = (float)f;
+        s_freq[j] = make_float2(hi, (float)(f - (double)hi));
+    }
+    __syncthreads();
+    for (int j = lane; j < a.R; j += 32) {
+        const float2 f = s_freq[j];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) put_turn(s_turn + (t0 + k) * 3 * RP + j, RP, s_pos[t0 + k], f, a.amplitude, a.inverse);
+    }
+    __syncwarp();
+    const int R = a.R, turned = 2 * R;
+    const int mate = PAIR == LANE && e0 < turned ? lane + (e0 < R ? R / 8 : -(R / 8)) : lane;
+    const int same = e0 >= turned ? 0 : min(turned - e0, 8);  // elements of this lane that are turned
+    for (int x = 0, slot = 0; x < a.groups[2]; ++x, slot = slot + 1 == kDepth ? 0 : slot + 1) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+        Raw<uint16_t, true> w;
+        const uint4 raw = ring[slot * kThreads];
+        w.w[0] = raw.x;
+        w.w[1] = raw.y;
+        w.w[2] = raw.z;
+        w.w[3] = raw.w;
+        fetch(x + kDepth - 1, slot ? slot - 1 : kDepth - 1);  // into the place of the group before
+        int kind, tt, h;
+        row_of(x, kind, tt, h);
+        const int t = t0 + min(tt, kEach - 1), state = tt < kEach ? s_state[t] : 0;
+        float v[8];
+        if (MODE == DENSE || kind != 2) {
+            float2 c[4], s[4];
+            row_factors<PAIR>(s_turn + t * 3 * RP, RP, R, e0, c, s);
+            Raw<uint16_t, true> y;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y.w[k] = PAIR == LANE ? __shfl_sync(0xffffffffu, w.w[k], mate) : __byte_perm(w.w[k], 0u, 0x1032);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 f = sv::ffma2(make_float2(w.at(2 * k), w.at(2 * k + 1)), c[k], sv::fmul2(make_float2(y.at(2 * k), y.at(2 * k + 1)), s[k]));
+                v[2 * k] = f.x;
+                v[2 * k + 1] = f.y;
+            }
+            if (same < 8) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k >= same) v[k] = w.at(k);
+            }
+            if (MODE == DENSE || kind == 0) {
+                const int K = MODE == DENSE ? kind : 0;
+                if (state) sv::store_row8<uint16_t, true>(static_cast<uint16_t*>(a.dst[K]) + (s_out[K][t] + times(h, a.ds[K][2])), e0, a.D, v);
+                continue;
+            }
+        }
+        if constexpr (MODE != DENSE) {
+            unsigned char* to = (kind == 2 ? a.c.v : a.c.k) + (s_out[1][t] + times(h, a.c.head_stride));
+            float* scale = MODE == CACHE_E4M3 ? (kind == 2 ? a.c.v_scale : a.c.k_scale) + (s_scale[t] + h * a.c.page_size) : nullptr;
+            const bool live = state == 2 && e0 < a.D;
+            if (kind == 2) {
+                sv::Eight<uint16_t, true> f;
+                f.w[0] = raw;
+                sv::store_cache_row<uint16_t, LPR, MODE == CACHE_E4M3, true>(to, scale, e0, a.D, live, f);
+            } else {
+                sv::Eight<float, true> f;
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    f.w[k] = make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3]));
+                sv::store_cache_row<float, LPR, MODE == CACHE_E4M3, true>(to, scale, e0, a.D, live, f);
+            }
+        }
+    }
+}
+
+// Whether that kernel is the faster one: where kEach tokens' rows fill 12 groups or fewer and the tokens a full wave of
+// blocks.  In us, this one and the other: 64 x 2000 tokens of 4 + 1 heads of 64 43 and 80, on the way into a cache
+// 49 and 89; 1 + 1 heads of 128 into e4m3 65 and 125; 32 x 2000 of 4 + 1 heads of 128 into e4m3 (12 groups) 51 and 66,
+// 20 x 1000 of 2 + 2 into bf16 (12) 19.6 and 18.5; but 32 x 2000 of 8 + 2 of 128 (20 groups) 74 and 64, and 8 x 1000 tokens of
+// 4 + 1 10.7 and 8.
+template <int LPR, int MODE>
+bool few_rows(const RotaryArgs& a) {
+    constexpr int G = 32 / LPR;
+    int n = 0;
+    for (int k = 0; k < 3; ++k) n += (kEach * a.heads[k] + G - 1) / G;
+    return n <= 12 && (int64_t)a.B * a.N >= 4 * 152 * kWarps * kEach;
+}
+
+template <int LPR, int MODE, int PAIR>
+cudaError_t launch_few(RotaryArgs& a, cudaStream_t stream) {
+    constexpr int G = 32 / LPR, TOKENS = kWarps * kEach;
+    for (int k = 0, n = 0; k < 3; ++k) {
+        a.groups[k] = n += (kEach * a.heads[k] + G - 1) / G;
+        a.magic[k] = a.heads[k] ? (65536 + a.heads[k] - 1) / a.heads[k] : 0;
+    }
+    const int64_t tokens = (int64_t)a.B * a.N;
+    const size_t smem = kDepth * kThreads * sizeof(uint4) + ((size_t)TOKENS * 3 * ((a.R + 3) & ~3) + 8) * sizeof(float);
+    static sv::KernelLaunchCache cache;
+    auto kern = rotary_few_kernel<LPR, MODE, PAIR>;
+    int max_dyn = 0;
+    const cudaError_t e = cache.setup((const void*)kern, &max_dyn);
+    if (e != cudaSuccess) return e;
+    if (smem > (size_t)max_dyn) return cudaErrorInvalidValue;
+    return sv::launch_serial(kern, dim3((unsigned)((tokens + TOKENS - 1) / TOKENS)), dim3(kThreads), smem, stream, a);
+}
+
+template <typename T, int LPR, int MODE, bool AL, int PAIR>
 cudaError_t launch_rows(RotaryArgs& a, cudaStream_t stream) {
     const int64_t tokens = (int64_t)a.B * a.N;
     constexpr int sms = 152, G = 32 / LPR;
+    for (int k = 0, n = 0; k < 3; ++k) a.groups[k] = n += (a.heads[k] + G - 1) / G;
     // Tokens of a block: as many as leave six blocks per SM, since they share the frequencies;
     // a few tokens are spread over blocks by their rows instead, one pass of a block's warps each.
     a.tile = 1;
     while (a.tile < kMaxTokens && tokens / (2 * a.tile) >= 6 * sms) a.tile *= 2;
-    if (MANY) a.tile = kMaxTokens * kEach;
-    const int64_t stride = (MANY ? 1 : kWarps / a.tile) * G;  // heads from a group of a warp to its next
+    const int64_t stride = (kWarps / a.tile) * G;  // heads from a group of a warp to its next
     for (int k = 0; k < 3; ++k) a.in_step[k] = stride * a.ss[k][2];
     a.out_step[0] = stride * a.ds[0][2] * (int64_t)sizeof(T);
     a.out_step[1] = stride * (MODE == DENSE ? a.ds[1][2] * (int64_t)sizeof(T) : a.c.head_stride);
-    a.chunk = MANY || tokens >= 2 * sms ? a.groups[2] : kWarps;
+    a.chunk = tokens >= 2 * sms ? a.groups[2] : kWarps;
     const dim3 grid((unsigned)((tokens + a.tile - 1) / a.tile), (unsigned)((a.groups[2] + a.chunk - 1) / a.chunk));
     // Without pairs the factors are read all the same: eight floats behind the first of a plane.
     const size_t smem = ((size_t)a.tile * 3 * ((a.R + 3) & ~3) + 8) * sizeof(float);
     constexpr size_t ring = AL ? kDepth * kThreads * sizeof(T) * 8 : 0;
     static sv::KernelLaunchCache cache;
-    auto kern = rotary_kernel<T, LPR, MODE, AL, PAIR, MANY>;
+    auto kern = rotary_kernel<T, LPR, MODE, AL, PAIR>;
     int max_dyn = 0;
     const cudaError_t e = cache.setup((const void*)kern, &max_dyn);
     if (e != cudaSuccess) return e;
@@ -494,15 +637,9 @@ cudaError_t launch_rows(RotaryArgs& a, cudaStream_t stream) {
 
 template <typename T, int LPR, int MODE, bool AL, int PAIR>
 cudaError_t launch_pair(RotaryArgs& a, cudaStream_t stream) {
-    constexpr int G = 32 / LPR;
-    for (int k = 0, n = 0; k < 3; ++k) a.groups[k] = n += (a.heads[k] + G - 1) / G;
-    // Tokens of few rows, enough of them for a full wave of blocks (us, four tokens of a warp and one): 64 x 2000 of
-    // 4 + 1 heads of 64 (2 groups) 61 and 80, 32 x 2000 of 8 + 2 of 128 (5 groups) 58 and 64, of 14 + 2 (8 groups)
-    // 45 and 46; but 8 x 1000 of 4 + 1 12 and 8, fp32 35 and 30, on the way into a cache 41 and 35.
-    constexpr bool CAN = AL && PAIR != ANYWHERE && MODE == DENSE && sizeof(T) == 2;
-    if (CAN && a.groups[2] <= 8 && (int64_t)a.B * a.N >= 4 * 152 * kMaxTokens * kEach)
-        return launch_rows<T, LPR, MODE, AL, PAIR, CAN>(a, stream);
-    return launch_rows<T, LPR, MODE, AL, PAIR, false>(a, stream);
+    if constexpr (AL && PAIR != ANYWHERE && sizeof(T) == 2)
+        if (few_rows<LPR, MODE>(a)) return launch_few<LPR, MODE, PAIR>(a, stream);
+    return launch_rows<T, LPR, MODE, AL, PAIR>(a, stream);
 }
 
 template <typename T, int LPR, int MODE, bool AL>

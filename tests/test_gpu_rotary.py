@@ -88,7 +88,8 @@ def test_matches_the_plain_form(sv, shape):  # noqa: F811
     (5, 4001, 3, 1, 64, 32, False), (7, 2801, 2, 1, 128, 20, True), (5, 4001, 1, 2, 256, 128, False),
     (19999, 1, 9, 0, 96, 16, False), (3, 7000, 32, 0, 40, 8, True)])
 def test_many_tokens_of_few_rows(sv, B, N, Hq, Hk, D, R, interleaved):  # noqa: F811
-    """A warp takes several tokens, across batch rows, some of which are not written; alike in place."""
+    """A warp takes several tokens (but for the last two shapes, whose rows are too many), across batch rows, some of which are
+    not written; alike in place."""
     import torch
     rng = np.random.default_rng([B, N, D])
     q, k = make(rng, B, N, Hq, D, "bf16"), make(rng, B, N, Hk, D, "bf16") if Hk else None
@@ -234,6 +235,15 @@ def test_append(sv, cache, B, N, Hq, H, D, R, ps, dtype, interleaved, tree, nhd)
                 p, r = paged.place(table, b, int(base[b]) + int(i), P, ps)
                 if p >= 0:
                     close(got[p, :, r], want[b, i], size[b, i], "bf16")
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("shape", [
+    (5, 4001, 3, 1, 64, 32, 16, "bf16", False, True, True), (7, 2801, 1, 1, 128, 20, 24, "bf16", True, False, False),
+    (3, 7000, 0, 1, 256, 128, 32, "bf16", False, False, True), (9, 2300, 5, 2, 40, 8, 8, "bf16", False, False, False)])
+def test_append_many_tokens_of_few_rows(sv, cache, shape):  # noqa: F811
+    """A warp takes several tokens; the last shape's rows are as many as one does not."""
+    test_append(sv, cache, *shape)
 
 
 def test_captured(sv):  # noqa: F811
