@@ -327,18 +327,23 @@ __global__ void __launch_bounds__(THREADS, NQ == 4 ? 2 : 3)
                 s[n][3] = see1 & col[n][1] ? w.y : neg_inf();
                 grow |= fmaxf(s[n][0], s[n][2]) > lim[n][0] || fmaxf(s[n][1], s[n][3]) > lim[n][1];
             }
-            if (__any_sync(0xffffffffu, grow)) {  // the maximum moves: all columns of the warp
+            // The maximum moves, but only in the columns that outgrew it: what a column does hangs on its own scores
+            // alone, so keys that its query does not see move no bit of it.
+            if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
-                        float top = fmaxf(fmaxf(s[n][z], s[n][2 + z]), lim[n][z] == neg_inf() ? neg_inf() : mx[n][z]);
+                        float top = fmaxf(s[n][z], s[n][2 + z]);
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        const float fac = lim[n][z] == neg_inf() ? 1.0f : sv::ex2(mx[n][z] - top);  // nothing to scale yet
-                        lim[n][z] = top + RESCALE;
-                        mx[n][z] = top == neg_inf() ? 0.0f : top;
+                        const bool moves = top > lim[n][z];  // alike in the column's lanes; never to -infinity
+                        const float fac = moves && lim[n][z] != neg_inf() ? sv::ex2(mx[n][z] - top) : 1.0f;
+                        if (moves) {
+                            lim[n][z] = top + RESCALE;
+                            mx[n][z] = top;
+                        }
                         l[n][z] *= fac;
 #pragma unroll
                         for (int d = 0; d < DP / 16; ++d) {
