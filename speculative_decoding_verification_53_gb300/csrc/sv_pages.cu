@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(kThreads) page_resize_kernel(const __grid_cons
 
     // Rows' new state; pages and count are read no more.
     auto fine = [&](int b) {
-        const int u = b * a.parts;
-        return s_change[u] != kBad && (s_take[u] == s_take[u + a.parts] || s_take[u + a.parts] <= top);
+        const int u = b * a.parts;  // (sums may have saturated; the first part of a row that lacks pages takes some)
+        return s_change[u] != kBad && (s_change[u] <= 0 || s_take[u + a.parts] <= top);
     };
     const int all = ranks * kThreads;
     uint32_t taken = 0u;  // by the rows that found enough: they come before those that did not
