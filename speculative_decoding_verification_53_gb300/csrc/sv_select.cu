@@ -29,6 +29,8 @@
 // The error of an fp32 score: its (exact) products are summed in chains of four matrix products, each
 // of which sums 17 numbers, off by at most 17 units of 2^-23 of the largest partial sum, and up to
 // eight such chains by fp32 additions.  |q|_1 max|m| bounds every partial sum: 4 * 17 * 2^-23 + 8 * 2^-24 < 2^-16.
+// fp32's smallest steps are not in that, so scores count only where |q|_1 max|m| is 2^-100 or more (256 products off by
+// 2^-126 each are 2^-18 of it); below, as beyond 2^120, all are summed again.
 #include <cstdint>
 
 #include "spec_sparse.h"
@@ -476,6 +478,11 @@ struct SelectShared {
     uint32_t biggest[kWarps], sums[kWarps];
 };
 
+// Whether every score is zero.  (Not where the product is: that of 2^-80 and 2^-80 is, in fp32.)
+__device__ __forceinline__ bool all_scores_zero(float norm, float biggest) {
+    return (norm == 0.0f && biggest < pos_inf()) || (biggest == 0.0f && norm < pos_inf());
+}
+
 // What the sums in 64 bits go by: 2^a with |q|_1 max|m| 2^a below 2^30, or 0 where that bound is not finite, or
 // so large or small that products may leave fp32's range.
 __device__ __forceinline__ float fixed_scale(float reach) {
@@ -673,9 +680,10 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const __grid_con
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) biggest = max(biggest, sh.biggest[w]);
         const float reach = norm * __uint_as_float(biggest);  // |q|_1 max|m|
+        const bool all_zero = all_scores_zero(norm, __uint_as_float(biggest));
         const float err = reach * 0x1p-16f;
         const float scale = fixed_scale(reach);
-        const bool sure = reach < 0x1p120f;  // else (NaN among them) every score is summed again
+        const bool sure = reach >= 0x1p-100f && reach < 0x1p120f;  // else (NaN among them) every score is summed again
         const float t = from_key32(edge.key);
         const float low = __fadd_rd(t, -2.0f * err), high = __fadd_ru(t, 2.0f * err);
         uint32_t in = 0u, unsure = 0u;
@@ -707,7 +715,7 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const __grid_con
         uint32_t some = sh.unsure;
         const int i0 = a.lists > 1 ? i : 0, i1 = a.lists > 1 ? i + 1 : n;
         auto open = [&](int w) { return s_unsure[w]; };
-        const bool again = edge.key != 0u && reach != 0.0f;  // (holes are all alike; no reach: all scores are 0)
+        const bool again = edge.key != 0u && !all_zero;  // (holes are all alike)
         if (want < some && again && some <= kFew) {
             for (int w = tid; w < words; w += kThreads)
                 for (uint32_t bits = s_unsure[w]; bits; bits &= bits - 1u)
@@ -925,9 +933,10 @@ __global__ void __launch_bounds__(128) block_select_warp_kernel(const __grid_con
         };
         const uint32_t edge = search(want, true);
         const float reach = norm * __uint_as_float(biggest);  // |q|_1 max|m|
+        const bool all_zero = all_scores_zero(norm, __uint_as_float(biggest));
         const float err = reach * 0x1p-16f, t = from_key32(edge);
         const float scale = fixed_scale(reach);
-        const bool sure = reach < 0x1p120f;  // else (NaN among them) every score is summed again
+        const bool sure = reach >= 0x1p-100f && reach < 0x1p120f;  // else (NaN among them) every score is summed again
         int some;
         if (edge == 0u) {  // fewer blocks than wanted are in no hole: holes follow, the lowest first
             some = sort_out(1u, 0u);
@@ -942,7 +951,7 @@ __global__ void __launch_bounds__(128) block_select_warp_kernel(const __grid_con
             some = sure ? sort_out(key32(__fadd_rd(t, -2.0f * err)), key32(__fadd_ru(t, 2.0f * err))) : sort_out(1u, ~0u);
         }
         const int i0 = a.lists > 1 ? i : 0, i1 = a.lists > 1 ? i + 1 : n;
-        if (want < some && reach != 0.0f) {  // (no reach: all are 0)
+        if (want < some && !all_zero) {
             if (some <= 32) {
                 int mine = -1, x = 0;  // lane x has the x-th open block
                 uint64_t best = 0;
