@@ -471,7 +471,7 @@ constexpr int kKept = 8192;  // blocks whose keys are kept in shared memory
 
 struct SelectShared {
     uint32_t hist[4][256];
-    uint32_t in, unsure, few_n;
+    uint32_t in, unsure, few_n, lost;
     int few[kFew];
     uint64_t few_key[kFew];
     uint64_t best[kWarps];
@@ -491,12 +491,12 @@ __device__ __forceinline__ float fixed_scale(float reach) {
 
 // The key of score(i, j) in 64 bits over rows r0, r0 + step, ... of the list's (i1 - i0) * g, by one warp, the
 // result in all lanes; ~0 where one of them is NaN.  A product has 16 bits and is exact in fp32; it is added
-// up in fixed point, 30 bits and 22 more behind them, each in integers of 32 bits.  What a product has
-// below that is under 2^-53 of |q|_1 max|m|, which is what a rounding of a 64-bit float sum may lose, and the order of
-// additions does not matter.  Where products may leave fp32's range the sums are of doubles, of which the SM
-// adds two a clock: with them throughout, 1536 lists of up to 1024 blocks took 27 us longer.
+// up in fixed point, 30 bits and 22 more behind them, each in integers of 32 bits: exact in any order, and as a
+// sum of doubles would be, as long as no product has bits below those.  One that may, below 2^-37 of |q|_1 max|m|,
+// sets `lost` in its lane, and the list is summed again by doubles (scale 0), as where products may leave fp32's
+// range.  The SM adds two of them a clock: with them throughout, 1536 lists of up to 1024 blocks took 27 us longer.
 template <bool BOUNDS>
-__device__ __forceinline__ uint64_t exact_rows(const SelectArgs& a, float scale, int b, int i0, int i1, int h, int j, int r0, int step) {
+__device__ __forceinline__ uint64_t exact_rows(const SelectArgs& a, float scale, int b, int i0, int i1, int h, int j, int r0, int step, bool& lost) {
     const int lane = threadIdx.x & 31;
     const int page = __ldg(a.table + (int64_t)b * a.max_pages + j);
     const uint16_t* m = a.summary + ((int64_t)page * a.H + h) * (a.D * (BOUNDS ? 2 : 1));
@@ -536,6 +536,7 @@ __device__ __forceinline__ uint64_t exact_rows(const SelectArgs& a, float scale,
                     float u, w;
                     factors(e, u, w);
                     const float p = u * w * scale;
+                    lost |= fabsf(p) < 0x1p-7f && u != 0.0f && w != 0.0f;
                     const int n = __float2int_rn(p);
                     upper += n;
                     lower += __float2int_rn((p - (float)n) * 0x1p22f);
@@ -564,14 +565,14 @@ __device__ __forceinline__ uint64_t exact_rows(const SelectArgs& a, float scale,
 
 // Over all rows; NaN has key 1.  By one warp, or by all of the CTA's.
 template <bool BOUNDS>
-__device__ __forceinline__ uint64_t exact_key(const SelectArgs& a, float scale, int b, int i0, int i1, int h, int j) {
-    const uint64_t best = exact_rows<BOUNDS>(a, scale, b, i0, i1, h, j, 0, 1);
+__device__ __forceinline__ uint64_t exact_key(const SelectArgs& a, float scale, int b, int i0, int i1, int h, int j, bool& lost) {
+    const uint64_t best = exact_rows<BOUNDS>(a, scale, b, i0, i1, h, j, 0, 1, lost);
     return best == ~0ull ? 1 : best;
 }
 template <bool BOUNDS>
-__device__ __forceinline__ uint64_t exact_key_together(const SelectArgs& a, SelectShared& sh, float scale, int b, int i0, int i1, int h, int j) {
+__device__ __forceinline__ uint64_t exact_key_together(const SelectArgs& a, SelectShared& sh, float scale, int b, int i0, int i1, int h, int j, bool& lost) {
     const int warp = threadIdx.x >> 5;
-    uint64_t best = exact_rows<BOUNDS>(a, scale, b, i0, i1, h, j, warp, kWarps);
+    uint64_t best = exact_rows<BOUNDS>(a, scale, b, i0, i1, h, j, warp, kWarps, lost);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) sh.best[warp] = best;
     __syncthreads();
@@ -638,8 +639,9 @@ __device__ __forceinline__ Edge radix_select(SelectShared& sh, const uint32_t* k
 }
 
 // One CTA per list.  A warp takes 32 blocks at a time, so that what it decides on them is a word of a bitmap.
+// (Three CTAs an SM, 80 registers: left to itself the compiler takes 64 for bounds and spills.)
 template <bool BOUNDS>
-__global__ void __launch_bounds__(kThreads) block_select_kernel(const __grid_constant__ SelectArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) block_select_kernel(const __grid_constant__ SelectArgs a) {
     extern __shared__ uint32_t s_bits[];  // [words] blocks that are in, [words] not yet decided, then keys
     __shared__ SelectShared sh;
     sv::pdl_trigger();
@@ -675,7 +677,7 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const __grid_con
         }
         biggest = __reduce_max_sync(0xffffffffu, biggest);
         if (lane == 0) sh.biggest[warp] = biggest;
-        if (tid == 0) sh.in = sh.unsure = sh.few_n = 0u;
+        if (tid == 0) sh.in = sh.unsure = sh.few_n = sh.lost = 0u;
         Edge edge = radix_select(sh, keys, words, want, candidates);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) biggest = max(biggest, sh.biggest[w]);
@@ -721,18 +723,23 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const __grid_con
                 for (uint32_t bits = s_unsure[w]; bits; bits &= bits - 1u)
                     sh.few[atomicAdd(&sh.few_n, 1u)] = 32 * w + __ffs(bits) - 1;  // in any order: ranked by key and index
             __syncthreads();
-            if ((i1 - i0) * a.g <= 2 * kWarps) {
-                for (uint32_t x = warp; x < some; x += kWarps) {
-                    const uint64_t k = exact_key<BOUNDS>(a, scale, b, i0, i1, h, sh.few[x]);
-                    if (lane == 0) sh.few_key[x] = k;
+            for (float by = scale;; by = 0.0f) {
+                bool lost = false;
+                if ((i1 - i0) * a.g <= 2 * kWarps) {
+                    for (uint32_t x = warp; x < some; x += kWarps) {
+                        const uint64_t k = exact_key<BOUNDS>(a, by, b, i0, i1, h, sh.few[x], lost);
+                        if (lane == 0) sh.few_key[x] = k;
+                    }
+                } else {
+                    for (uint32_t x = 0; x < some; ++x) {
+                        const uint64_t k = exact_key_together<BOUNDS>(a, sh, by, b, i0, i1, h, sh.few[x], lost);
+                        if (tid == 0) sh.few_key[x] = k;
+                    }
                 }
-            } else {
-                for (uint32_t x = 0; x < some; ++x) {
-                    const uint64_t k = exact_key_together<BOUNDS>(a, sh, scale, b, i0, i1, h, sh.few[x]);
-                    if (tid == 0) sh.few_key[x] = k;
-                }
+                if (lost) sh.lost = 1u;
+                __syncthreads();
+                if (by == 0.0f || !sh.lost) break;
             }
-            __syncthreads();
             if (tid < (int)some) {
                 const uint64_t k = sh.few_key[tid];
                 const int j = sh.few[tid];
@@ -742,13 +749,24 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const __grid_con
             }
             want = 0u;
         } else if (want < some && again) {
+            float by = scale;
             for (int half = 0; half < 2 && want < some; ++half) {
+                bool lost = false;
                 for (int w = 0; w < words; ++w) {
                     for (uint32_t bits = s_unsure[w]; bits; bits &= bits - 1u) {
                         const int j = 32 * w + __ffs(bits) - 1;
                         if (j % kWarps != warp) continue;
-                        const uint64_t k = exact_key<BOUNDS>(a, scale, b, i0, i1, h, j);
+                        const uint64_t k = exact_key<BOUNDS>(a, by, b, i0, i1, h, j, lost);
                         if (lane == 0) keys[j] = half ? (uint32_t)k : (uint32_t)(k >> 32);
+                    }
+                }
+                if (by != 0.0f && half == 0) {
+                    if (lost) sh.lost = 1u;
+                    __syncthreads();
+                    if (sh.lost) {  // from the start, by doubles
+                        by = 0.0f;
+                        half = -1;
+                        continue;
                     }
                 }
                 edge = radix_select(sh, keys, words, want, open);
@@ -953,21 +971,26 @@ __global__ void __launch_bounds__(128) block_select_warp_kernel(const __grid_con
         const int i0 = a.lists > 1 ? i : 0, i1 = a.lists > 1 ? i + 1 : n;
         if (want < some && !all_zero) {
             if (some <= 32) {
-                int mine = -1, x = 0;  // lane x has the x-th open block
+                int mine = -1;  // lane x has the x-th open block
                 uint64_t best = 0;
+                for (float by = scale;; by = 0.0f) {
+                    bool lost = false;
+                    int x = 0;
 #pragma unroll
-                for (int w = 0; w < WPL; ++w)
-                    for (uint32_t left = __ballot_sync(0xffffffffu, maybe[w] != 0u); left; left &= left - 1u) {
-                        const int l = __ffs(left) - 1;
-                        for (uint32_t bits = __shfl_sync(0xffffffffu, maybe[w], l); bits; bits &= bits - 1u, ++x) {
-                            const int j = 32 * (32 * w + l) + __ffs(bits) - 1;
-                            const uint64_t k = exact_key<BOUNDS>(a, scale, b, i0, i1, h, j);
-                            if (lane == x) {
-                                mine = j;
-                                best = k;
+                    for (int w = 0; w < WPL; ++w)
+                        for (uint32_t left = __ballot_sync(0xffffffffu, maybe[w] != 0u); left; left &= left - 1u) {
+                            const int l = __ffs(left) - 1;
+                            for (uint32_t bits = __shfl_sync(0xffffffffu, maybe[w], l); bits; bits &= bits - 1u, ++x) {
+                                const int j = 32 * (32 * w + l) + __ffs(bits) - 1;
+                                const uint64_t k = exact_key<BOUNDS>(a, by, b, i0, i1, h, j, lost);
+                                if (lane == x) {
+                                    mine = j;
+                                    best = k;
+                                }
                             }
                         }
-                    }
+                    if (by == 0.0f || !__any_sync(0xffffffffu, lost)) break;
+                }
                 int before = 0;
                 for (int y = 0; y < some; ++y) {
                     const uint64_t k = __shfl_sync(0xffffffffu, best, y);
@@ -985,17 +1008,24 @@ __global__ void __launch_bounds__(128) block_select_warp_kernel(const __grid_con
                 want = 0;
             } else {
                 // by thirds of the 64 bits, each made larger than 0
+                float by = scale;
                 for (int third = 0; third < 3 && want < some; ++third) {
+                    bool lost = false;
 #pragma unroll
                     for (int w = 0; w < WPL; ++w)
                         for (uint32_t left = __ballot_sync(0xffffffffu, maybe[w] != 0u); left; left &= left - 1u) {
                             const int l = __ffs(left) - 1;
                             for (uint32_t bits = __shfl_sync(0xffffffffu, maybe[w], l); bits; bits &= bits - 1u) {
                                 const int j = 32 * (32 * w + l) + __ffs(bits) - 1;
-                                const uint64_t k = exact_key<BOUNDS>(a, scale, b, i0, i1, h, j);
+                                const uint64_t k = exact_key<BOUNDS>(a, by, b, i0, i1, h, j, lost);
                                 if (lane == 0) keys[j] = 1u + (third == 0 ? (uint32_t)(k >> 42) : third == 1 ? (uint32_t)(k >> 21) & 0x1fffffu : (uint32_t)k & 0x1fffffu);
                             }
                         }
+                    if (third == 0 && by != 0.0f && __any_sync(0xffffffffu, lost)) {  // from the start, by doubles
+                        by = 0.0f;
+                        third = -1;
+                        continue;
+                    }
                     __syncwarp();
 #pragma unroll
                     for (int x = 0; x < KPL; ++x) {

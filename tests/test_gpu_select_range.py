@@ -1,5 +1,5 @@
-"""Block selection where scores are small: lists are those of scores summed in 64 bits, equal to the plain form's.
-The scores of different blocks differ by far more than the sums' last bits.
+"""Block selection where scores are small, or small beside |q|_1 max|m|: lists are those of scores summed in 64
+bits, equal to the plain form's.  The scores of different blocks differ by far more than the sums' last bits.
 """
 import numpy as np
 import pytest
@@ -27,3 +27,20 @@ def test_small_magnitudes(sv, kind, shared, B, blocks, of_q, of_m):  # noqa: F81
         check_select(sv, q, summary, table, base, None, 16, top, kind, 1, 1, shared)
     summary.zero_()  # and true zeros are all alike
     check_select(sv, q, summary, table, base, None, 16, 12, kind, 1, 1, shared)
+
+
+@pytest.mark.parametrize("kind", ["mean", "bounds"])
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("B,Q,blocks", [(1, 2, 90), (1, 9, 90), (80, 2, 90), (2, 2, 2100)])
+@pytest.mark.parametrize("far", [30, 60, 90])
+def test_large_elements_that_meet_zeros(sv, kind, shared, B, Q, blocks, far):  # noqa: F811
+    """An element of the queries, or of the summaries, far above the others whose partner is zero: |q|_1 max|m| is
+    2 ** far times what the scores are, and they keep their order."""
+    rng = np.random.default_rng(4)
+    for side in ("query", "summary"):
+        q, summary, table, base, _ = select_case(rng, B, Q, 4, 1, 64, 16, blocks, kind == "bounds")
+        base[:] = blocks * 16
+        q[..., 0] = 2.0 ** far if side == "query" else 0
+        summary[..., 0::64] = 0 if side == "query" else 2.0 ** far
+        for top in (4, 33, 60):
+            check_select(sv, q, summary, table, base, None, 16, top, kind, 1, 1, shared)
