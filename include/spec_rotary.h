@@ -67,8 +67,8 @@ SV_API sv_status spec_rotary(const void *q, const int64_t *q_stride, int num_q_h
  *   q, out_q     as above (out_q_stride alike); q may be NULL with num_q_heads 0.
  *   key, value   device [B][N][cache->num_heads][cache->head_dim], element strides
  *                kv_stride[0..2], which both share.
- * Other arguments, rows that are left untouched and errors as spec_rotary and
- * spec_kv_append; N < 2^31 / (num_q_heads + 2 num_heads).
+ * Other arguments, rows that are left untouched, limits and errors as spec_rotary and
+ * spec_kv_append (0 <= num_q_heads <= 65536).
  */
 SV_API sv_status spec_rotary_append(const void *q, const int64_t *q_stride, int num_q_heads, const void *key,
                                     const void *value, const int64_t *kv_stride, sv_dtype dt, const sv_rotary *rotary,
