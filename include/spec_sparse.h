@@ -38,8 +38,9 @@ typedef enum {
  *   cache        as spec_kv_append; values and their scales are not read (v_pages may equal
  *                k_pages).
  *   summary      device bf16 [num_pages][num_heads][head_dim or 2 * head_dim], dense: a page's
- *                summary lies at the page.  Sums are fp32 and rounded once, bounds are rounded to
- *                nearest (bf16 pages: exact).  NaN among an element's values makes it NaN.
+ *                summary lies at the page.  Sums and means are fp32, means are rounded to bf16
+ *                once; bounds are rounded to nearest (bf16 pages: exact; e4m3 pages: off by up to
+ *                half a step to either side).  NaN among an element's values makes it NaN.
  * Blocks in holes are passed over, and so are rows that spec_kv_append leaves untouched.  A
  * page that two rows hold must have the same positions in both.
  * 0 <= N <= 2^30.  Errors: SV_ERR_INVALID_ARG for a bad size, kind, pointer or stride
@@ -58,7 +59,9 @@ SV_API sv_status spec_block_summary(const sv_paged_cache *cache, const int32_t *
  *                spec_paged_attention.
  * A block's score for a query is the largest, over the heads that share the cache head (and
  * over the row's real queries where shared), of sum_d q_d m_d (mean m), or of
- * sum_d (q_d >= 0 ? q_d max_d : q_d min_d): no key of the block has a larger product with q.
+ * sum_d (q_d >= 0 ? q_d max_d : q_d min_d).  On bf16 pages no key of the block has a larger
+ * product with q; on e4m3 pages, whose bounds are rounded, none has one that is larger by more
+ * than 2^-8 sum_d |q_d| |m_d|, m_d the bound that the sum took.
  * Selected are the first `sink` context blocks, the last `recent` ones, and of the others
  * those with the largest scores, top_k in all (all of them where there are no more).  The
  * order is that of the scores summed in 64 bits; of equal ones the lower block comes first;

@@ -1098,8 +1098,8 @@ def spec_block_select(q, summary, page_table, base, page_size: int, top_k: int, 
                       recent: int = 1, shared: bool = False, new_len=None, out=None, workspace="auto", stream=None):
     """The top_k blocks of the context (the base[b] // page_size whole blocks before the chunk)
     that each query attends to: the first `sink`, the last `recent`, and those with the largest
-    scores, q . mean or, for bounds, the largest product any key within them could have with q;
-    the largest over the heads that share a cache head and, where shared, over the row's queries.
+    scores, q . mean or, for bounds, the largest product any key within them could have with q (e4m3
+    pages: but for the rounding of their bounds to bf16); the largest over the heads that share a cache head and, where shared, over the row's queries.
     q bf16 [B][Q][q_heads][head_dim] as spec_paged_attention; summary bf16 [pages][heads][head_dim
     or 2 head_dim] from spec_block_summary; page_table, base, new_len as spec_paged_attention.
     Scores are compared as sums in 64 bits, equal ones go to the lower block.  Returns int32
