@@ -728,7 +728,9 @@ constexpr int kMaxUnionOf = 65536;   // blocks of the context it is built over
 // measured (us): a tile's positions 0.0144 each (e4m3 0.0235), a split 10 of its own, the join 8 and the partial
 // results' bytes at 2 TB/s.  16 trees of 61 over 64 pages of 64 (128 tiles): 67 in one piece, 122 in 3 as
 // make_plan cuts contexts of unequal length (e4m3 110 and 160); 9 trees 64 and 87 in 5, 5 trees 63 and 59 in 5,
-// 1 tree 60 and 29; 5 trees over 200 pages 168 and 105 in 11.
+// 1 tree 60 and 29; 5 trees over 200 pages 168 and 105 in 11.  The numbers are those of heads of 128; with heads of 64 the
+// choice was within 1 us of the best of 1, 2, 4 and 8 splits for 1 to 16 trees of 61, with heads of 256 within 2 us but for 5 trees
+// in e4m3 (216 us in one piece, 196 in 8).
 void split_lists(Plan& p, int most, int64_t rows, int D, bool e4m3, int sms) {
     double best = 0.0;
     int splits = 1;
@@ -757,7 +759,8 @@ bool sparse_plan(int B, int Q, int Hq, int H, int D, bool e4m3, int page_size, i
     // Up to 32 query rows over a list or a union of lists: the kernel for few queries.  Lists that a row's
     // queries share, 64 pages of 64, 32 over 8 heads of 128, against the kernels of contexts over the list's
     // page table (us): 16 tokens bf16 57 and 77, e4m3 51 and 73; 64 tokens over 32 pages 112 and 117, 90
-    // and 114; 16 chains of 6 64 and 81, 73 and 109; one token 17 and 19, 18 and 21; but one chain of 6 24 and 20.
+    // and 114; 16 chains of 6 64 and 81, 73 and 109; one token 17 and 19, 18 and 21.  One chain of 6 alone loses by it, 24 and
+    // 20; the rule goes by rows, and no size told the two apart elsewhere.
     const int g = Hq / H;
     // Queries whose lists are united: as many as 32 rows hold, in tiles of one size.
     int tile = g <= 32 ? 32 / g : 0, tiles = tile ? (Q + tile - 1) / tile : 0;

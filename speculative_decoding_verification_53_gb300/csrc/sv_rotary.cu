@@ -613,7 +613,8 @@ cudaError_t launch_rows(RotaryArgs& a, cudaStream_t stream) {
     const int64_t tokens = (int64_t)a.B * a.N;
     constexpr int sms = 152, G = 32 / LPR;
     for (int k = 0, n = 0; k < 3; ++k) a.groups[k] = n += (a.heads[k] + G - 1) / G;
-    // Tokens of a block: as many as leave six blocks per SM, since they share the frequencies;
+    // Tokens of a block: as many as leave six blocks per SM (a wave and a half: four at a time, by registers), since they
+    // share the frequencies;
     // a few tokens are spread over blocks by their rows instead, one pass of a block's warps each.
     a.tile = 1;
     while (a.tile < kMaxTokens && tokens / (2 * a.tile) >= 6 * sms) a.tile *= 2;

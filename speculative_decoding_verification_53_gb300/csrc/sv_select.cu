@@ -24,11 +24,11 @@
 // One GB300: 32 chains of 6 queries, 32 over 8 heads of 128, 256 to 1024 blocks, 64 of them by bounds 46 us, 28 of it
 // the scores (floor 13: 84 MB of summaries; a warp's loads one after the other - row, page, summary, query - and
 // 16 warps an SM are what it waits for), by means 38; one token over 1562 blocks 16 us; 16 trees of 61 over 128 to
-// 512 blocks 90 us, 98 where their queries share a list.
+// 512 blocks 91 us, 103 where their queries share a list.
 //
 // The error of an fp32 score: its (exact) products are summed in chains of four matrix products, each
-// of which sums 17 numbers, off by at most 17 units of 2^-23 of the largest partial sum, and up to
-// eight such chains by fp32 additions.  |q|_1 max|m| bounds every partial sum: 4 * 17 * 2^-23 + 8 * 2^-24 < 2^-16.
+// of which sums 17 numbers, taken to be off by at most 17 units of 2^-23 of the largest partial sum (how the hardware
+// aligns and cuts them is not documented), and up to eight such chains by fp32 additions.  |q|_1 max|m| bounds every partial sum: 4 * 17 * 2^-23 + 8 * 2^-24 < 2^-16.
 // fp32's smallest steps are not in that, so scores count only where |q|_1 max|m| is 2^-100 or more (256 products off by
 // 2^-126 each are 2^-18 of it); below, as beyond 2^120, all are summed again.
 #include <cstdint>
