@@ -759,8 +759,8 @@ bool sparse_plan(int B, int Q, int Hq, int H, int D, bool e4m3, int page_size, i
     // Up to 32 query rows over a list or a union of lists: the kernel for few queries.  Lists that a row's
     // queries share, 64 pages of 64, 32 over 8 heads of 128, against the kernels of contexts over the list's
     // page table (us): 16 tokens bf16 57 and 77, e4m3 51 and 73; 64 tokens over 32 pages 112 and 117, 90
-    // and 114; 16 chains of 6 64 and 81, 73 and 109; one token 17 and 19, 18 and 21.  One chain of 6 alone loses by it, 24 and
-    // 20; the rule goes by rows, and no size told the two apart elsewhere.
+    // and 114; 16 chains of 6 64 and 81, 73 and 109; one token 17 and 19, 18 and 21.  One chain of 6 loses by it, 24 and 20:
+    // the rule goes by rows alone, not by how many rows of the batch there are.
     const int g = Hq / H;
     // Queries whose lists are united: as many as 32 rows hold, in tiles of one size.
     int tile = g <= 32 ? 32 / g : 0, tiles = tile ? (Q + tile - 1) / tile : 0;
